@@ -15,11 +15,20 @@ Space Models"):
               between chunks (exactly the full-length SSM; 16-bit activations
               pass the state every 64 samples, fp32 convolve chunks of T by FFT)
   h3_mix      out = q * (f * (shift(k) * v) + D * shift(k) * v)
+
+and the layers and loss of a language model with input-dependent state spaces:
+  short_conv      y = silu(bias + sum_i w_i x_{t-i}), with short_conv_bwd and,
+                  for one token per sequence, short_conv_step
+  selective_scan  x_t = exp(d_t A) x_{t-1} + d_t B_t u_t, y = (C_t x_t + D u) silu(z),
+                  with selective_scan_bwd and selective_step
+  linear_xent     cross entropy of x w^T without the logits in memory, with
+                  linear_xent_bwd
 """
 from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -34,12 +43,17 @@ OP_FFT_CONV, OP_STATE_PASS, OP_H3_MIX, OP_H3_MIX_MH = 0, 1, 2, 3
 MAX_FUSED_N = 8192
 MAX_FUSED_N_16BIT = 16384
 MAX_STATE = 64
+MAX_TAPS = 4
 
 _IO = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _lib = None
 
 EXPORTS = ("h3conv_fft_conv", "h3conv_fft_conv_bidir", "h3conv_fft_conv_bwd", "h3conv_ssm_filter", "h3conv_state_pass", "h3conv_state_pass_noalloc",
-           "h3conv_ssm_step", "h3conv_h3_mix", "h3conv_h3_mix_mh", "h3conv_workspace_size", "h3conv_status_string", "h3conv_version")
+           "h3conv_ssm_step", "h3conv_h3_mix", "h3conv_h3_mix_mh", "h3conv_workspace_size", "h3conv_status_string", "h3conv_version",
+           "h3conv_short_conv", "h3conv_short_conv_bwd", "h3conv_short_conv_bwd_workspace_size", "h3conv_short_conv_step",
+           "h3conv_selective_scan", "h3conv_selective_saved_size", "h3conv_selective_scan_bwd",
+           "h3conv_selective_scan_bwd_workspace_size", "h3conv_selective_step",
+           "h3conv_linear_xent", "h3conv_linear_xent_bwd", "h3conv_linear_xent_workspace_size")
 NOALLOC_WORKSPACE_BYTES = 128 * 1024 * 1024
 
 
@@ -76,6 +90,24 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     for name in ("h3conv_fft_conv", "h3conv_fft_conv_bidir", "h3conv_fft_conv_bwd", "h3conv_ssm_filter", "h3conv_state_pass", "h3conv_state_pass_noalloc",
                  "h3conv_ssm_step", "h3conv_h3_mix", "h3conv_h3_mix_mh"):
         getattr(lib, name).restype = I
+    lib.h3conv_short_conv.argtypes = [P] * 7 + [I64] * 4 + [I, I, P]
+    lib.h3conv_short_conv_bwd.argtypes = [P] * 11 + [I64] * 4 + [I, I, P, SZ, P]
+    lib.h3conv_short_conv_step.argtypes = [P] * 7 + [I64] * 4 + [I, I, P]
+    lib.h3conv_selective_scan.argtypes = [P] * 13 + [I64] * 5 + [I, I, P]
+    lib.h3conv_selective_scan_bwd.argtypes = [P] * 21 + [I64] * 5 + [I, I, P, SZ, P]
+    lib.h3conv_selective_step.argtypes = [P] * 12 + [I64] * 5 + [I, I, P]
+    lib.h3conv_linear_xent.argtypes = [P, P, P, I64, P, P, I64, I64, I64, I, P, SZ, P]
+    lib.h3conv_linear_xent_bwd.argtypes = [P, P, P, I64, P, P, P, P, I64, I64, I64, I, P, SZ, P]
+    for name in ("h3conv_short_conv", "h3conv_short_conv_bwd", "h3conv_short_conv_step", "h3conv_selective_scan",
+                 "h3conv_selective_scan_bwd", "h3conv_selective_step", "h3conv_linear_xent", "h3conv_linear_xent_bwd"):
+        getattr(lib, name).restype = I
+    lib.h3conv_short_conv_bwd_workspace_size.argtypes = [I64] * 4
+    lib.h3conv_selective_saved_size.argtypes = [I64] * 4
+    lib.h3conv_selective_scan_bwd_workspace_size.argtypes = [I64] * 5
+    lib.h3conv_linear_xent_workspace_size.argtypes = [I64, I64, I64, I, I]
+    for name in ("h3conv_short_conv_bwd_workspace_size", "h3conv_selective_saved_size",
+                 "h3conv_selective_scan_bwd_workspace_size", "h3conv_linear_xent_workspace_size"):
+        getattr(lib, name).restype = SZ
     _lib = lib
     return lib
 
@@ -389,3 +421,281 @@ def h3_mix_mh(q, k, v, w, f, D, dh: int, out=None, workspace=None):
                                    io, _ptr(ws), ws.numel() * ws.element_size(), _stream()),
            "h3conv_h3_mix_mh")
     return o
+
+
+# ---------------------------------------------------------------------------
+# Layers and loss of a language model with input-dependent state spaces.
+
+def _size(name: str, *args) -> int:
+    n = getattr(load(), name)(*args)
+    if n == ctypes.c_size_t(-1).value:
+        raise H3ConvError(ERR_UNSUPPORTED, name)
+    return int(n)
+
+
+def _scratch(workspace, need: int, device) -> torch.Tensor:
+    """The caller's workspace where it is large enough, else a new one."""
+    if workspace is not None and workspace.numel() * workspace.element_size() >= need:
+        return workspace
+    return torch.empty(max(need, 1), device=device, dtype=torch.uint8)
+
+
+def _arg(t, name: str, dtype, shape, optional: bool = True):
+    """One tensor argument; None passes where it is optional."""
+    if t is None:
+        if not optional:
+            raise TypeError("%s is required" % name)
+        return
+    _need(t, name, dtype, shape)
+
+
+def _conv_args(x, w, bias, dims: int):
+    _need(x, "x")
+    io = _io(x, "x")
+    if x.dim() != dims:
+        raise ValueError("x must be %s, got %s" % ("[B,H,N]" if dims == 3 else "[B,H]", tuple(x.shape)))
+    H = x.shape[1]
+    _need(w, "w", torch.float32)
+    if w.dim() != 2 or w.shape[0] != H or w.shape[1] < 1:
+        raise ValueError("w must be [H,W] with H = %d, got %s" % (H, tuple(w.shape)))
+    _arg(bias, "bias", torch.float32, (H,))
+    return io, H, w.shape[1]
+
+
+def short_conv(x, w, bias=None, silu: bool = True, x_in=None, lengths=None, return_state: bool = False, out=None):
+    """y[b,h,t] = silu(bias[h] + sum_i w[h,i] x[b,h,t-i]) (without ``silu`` the sum itself).
+
+    x [B,H,N] f32/f16/bf16; w [H,W] f32, W <= MAX_TAPS; bias [H] f32; x_in
+    [B,H,W-1] like x, the inputs before the row, oldest first (zeros if None);
+    lengths [B] int32, valid steps of every row.  Returns y, or (y, x_out) with
+    the last W-1 inputs of every row if ``return_state``."""
+    io, H, W = _conv_args(x, w, bias, 3)
+    B, N = x.shape[0], x.shape[2]
+    _arg(x_in, "x_in", x.dtype, (B, H, W - 1))
+    _arg(lengths, "lengths", torch.int32, (B,))
+    _arg(out, "out", x.dtype, (B, H, N))
+    _same_device(x=x, w=w, bias=bias, x_in=x_in, lengths=lengths, out=out)
+    y = torch.empty_like(x) if out is None else out
+    x_out = torch.empty(B, H, W - 1, device=x.device, dtype=x.dtype) if return_state else None
+    _check(load().h3conv_short_conv(_ptr(x), _ptr(w), _ptr(bias), _ptr(x_in), _ptr(lengths), _ptr(y), _ptr(x_out),
+                                    B, H, N, W, int(bool(silu)), io, _stream()),
+           "h3conv_short_conv")
+    return (y, x_out) if return_state else y
+
+
+def short_conv_bwd(x, w, dy, bias=None, silu: bool = True, x_in=None, lengths=None, dx_out=None, workspace=None):
+    """Gradients of y (and x_out) = short_conv(x, w, bias, ...) for dy [B,H,N] and dx_out [B,H,W-1] (or None).
+
+    Returns (dx [B,H,N], dw [H,W] f32, dbias [H] f32, dx_in [B,H,W-1]); dbias
+    is None without a bias, dx_in without an x_in."""
+    io, H, W = _conv_args(x, w, bias, 3)
+    B, N = x.shape[0], x.shape[2]
+    _arg(dy, "dy", x.dtype, (B, H, N), optional=False)
+    _arg(x_in, "x_in", x.dtype, (B, H, W - 1))
+    _arg(lengths, "lengths", torch.int32, (B,))
+    _arg(dx_out, "dx_out", x.dtype, (B, H, W - 1))
+    if workspace is not None:
+        _need(workspace, "workspace")
+    _same_device(x=x, w=w, dy=dy, bias=bias, x_in=x_in, lengths=lengths, dx_out=dx_out, workspace=workspace)
+    dx = torch.empty_like(x)
+    dw = torch.empty_like(w)
+    dbias = torch.empty_like(bias) if bias is not None else None
+    dx_in = torch.empty_like(x_in) if x_in is not None else None
+    ws = _scratch(workspace, _size("h3conv_short_conv_bwd_workspace_size", B, H, N, W), x.device)
+    _check(load().h3conv_short_conv_bwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(x_in), _ptr(lengths), _ptr(dy),
+                                        _ptr(dx_out), _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(dx_in), B, H, N, W,
+                                        int(bool(silu)), io, _ptr(ws), ws.numel() * ws.element_size(), _stream()),
+           "h3conv_short_conv_bwd")
+    return dx, dw, dbias, dx_in
+
+
+def short_conv_step(x, w, state, bias=None, silu: bool = True, slots=None, state_out=None, out=None):
+    """short_conv for one token of each sequence.
+
+    x [B,H]; state [P,H,W-1] like x, a pool of saved inputs, updated in place
+    (or into ``state_out``, of which only the slots in use are written); slots
+    [B] int32, the slot of each sequence (sequence b in slot b if None).  A
+    slot outside the pool marks an idle row: its output is zero.  Returns y [B,H]."""
+    io, H, W = _conv_args(x, w, bias, 2)
+    B = x.shape[0]
+    P = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() == 3 else 0
+    _arg(state, "state", x.dtype, (P, H, W - 1), optional=False)
+    _arg(state_out, "state_out", x.dtype, (P, H, W - 1))
+    _arg(slots, "slots", torch.int32, (B,))
+    _arg(out, "out", x.dtype, (B, H))
+    _same_device(x=x, w=w, bias=bias, slots=slots, state=state, state_out=state_out, out=out)
+    y = torch.empty_like(x) if out is None else out
+    to = state if state_out is None else state_out
+    _check(load().h3conv_short_conv_step(_ptr(x), _ptr(w), _ptr(bias), _ptr(slots), _ptr(state), _ptr(to), _ptr(y),
+                                         B, H, P, W, int(bool(silu)), io, _stream()),
+           "h3conv_short_conv_step")
+    return y
+
+
+def _scan_args(u, dt, A, Bm, C, D, z, dt_bias, dims: int):
+    _need(u, "u")
+    io = _io(u, "u")
+    if u.dim() != dims:
+        raise ValueError("u must be %s, got %s" % ("[B,H,N]" if dims == 3 else "[B,H]", tuple(u.shape)))
+    B, H = u.shape[:2]
+    _arg(dt, "dt", u.dtype, u.shape, optional=False)
+    _need(A, "A", torch.float32)
+    if A.dim() != 2 or A.shape[0] != H or A.shape[1] < 1:
+        raise ValueError("A must be [H,S] with H = %d, got %s" % (H, tuple(A.shape)))
+    S = A.shape[1]
+    _need(Bm, "Bm", u.dtype)
+    if Bm.dim() != dims + 1 or Bm.shape[1] < 1 or H % Bm.shape[1] != 0:
+        raise ValueError("Bm must be %s with G dividing H = %d, got %s"
+                         % ("[B,G,S,N]" if dims == 3 else "[B,G,S]", H, tuple(Bm.shape)))
+    G = Bm.shape[1]
+    bc = (B, G, S) + tuple(u.shape[2:])
+    _need(Bm, "Bm", u.dtype, bc)
+    _arg(C, "C", u.dtype, bc, optional=False)
+    _arg(D, "D", torch.float32, (H,))
+    _arg(z, "z", u.dtype, u.shape)
+    _arg(dt_bias, "dt_bias", torch.float32, (H,))
+    return io, B, H, S, G
+
+
+def selective_scan(u, dt, A, Bm, C, D=None, z=None, dt_bias=None, softplus: bool = True, x_in=None, lengths=None,
+                   return_state: bool = False, return_saved: bool = False, out=None):
+    """Selective state-space scan: d_t = softplus(dt_t + dt_bias), x_t = exp(d_t A) x_{t-1} + d_t B_t u_t,
+    y_t = (C_t . x_t + D u_t) silu(z_t).
+
+    u, dt, z [B,H,N] f32/f16/bf16; A [H,S] f32; Bm, C [B,G,S,N] like u, shared
+    by the H/G channels of a group; D, dt_bias [H] f32; x_in [B,H,S] f32;
+    lengths [B] int32, valid steps of every row.  Returns y, followed by the
+    final state [B,H,S] f32 if ``return_state`` and by the saved states that
+    selective_scan_bwd needs if ``return_saved``."""
+    io, B, H, S, G = _scan_args(u, dt, A, Bm, C, D, z, dt_bias, 3)
+    N = u.shape[2]
+    _arg(x_in, "x_in", torch.float32, (B, H, S))
+    _arg(lengths, "lengths", torch.int32, (B,))
+    _arg(out, "out", u.dtype, (B, H, N))
+    _same_device(u=u, dt=dt, A=A, Bm=Bm, C=C, D=D, z=z, dt_bias=dt_bias, x_in=x_in, lengths=lengths, out=out)
+    y = torch.empty_like(u) if out is None else out
+    x_out = torch.empty(B, H, S, device=u.device, dtype=torch.float32) if return_state else None
+    saved = None
+    if return_saved:
+        saved = torch.empty(_size("h3conv_selective_saved_size", B, H, N, S) // 4, device=u.device, dtype=torch.float32)
+    _check(load().h3conv_selective_scan(_ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias),
+                                        _ptr(x_in), _ptr(lengths), _ptr(y), _ptr(x_out), _ptr(saved), B, H, N, S, G,
+                                        int(bool(softplus)), io, _stream()),
+           "h3conv_selective_scan")
+    if not (return_state or return_saved):
+        return y
+    return (y,) + ((x_out,) if return_state else ()) + ((saved,) if return_saved else ())
+
+
+class SelectiveScanGrads(NamedTuple):
+    """Gradients of selective_scan; None for an input that was not given."""
+    du: torch.Tensor
+    ddt: torch.Tensor
+    dA: torch.Tensor
+    dB: torch.Tensor
+    dC: torch.Tensor
+    dD: Optional[torch.Tensor]
+    dz: Optional[torch.Tensor]
+    ddt_bias: Optional[torch.Tensor]
+    dx_in: torch.Tensor
+
+
+def selective_scan_bwd(u, dt, A, Bm, C, dy, saved, D=None, z=None, dt_bias=None, softplus: bool = True, lengths=None,
+                       dx_out=None, workspace=None) -> SelectiveScanGrads:
+    """Gradients of selective_scan (same arguments, ``saved`` as it returned it) for dy [B,H,N] and
+    dx_out [B,H,S] f32 (upstream of the final state, or None)."""
+    io, B, H, S, G = _scan_args(u, dt, A, Bm, C, D, z, dt_bias, 3)
+    N = u.shape[2]
+    _arg(dy, "dy", u.dtype, (B, H, N), optional=False)
+    _arg(saved, "saved", torch.float32, (_size("h3conv_selective_saved_size", B, H, N, S) // 4,), optional=False)
+    _arg(lengths, "lengths", torch.int32, (B,))
+    _arg(dx_out, "dx_out", torch.float32, (B, H, S))
+    if workspace is not None:
+        _need(workspace, "workspace")
+    _same_device(u=u, dt=dt, A=A, Bm=Bm, C=C, D=D, z=z, dt_bias=dt_bias, dy=dy, saved=saved, lengths=lengths,
+                 dx_out=dx_out, workspace=workspace)
+    g = SelectiveScanGrads(
+        torch.empty_like(u), torch.empty_like(dt), torch.empty_like(A), torch.empty_like(Bm), torch.empty_like(C),
+        None if D is None else torch.empty_like(D), None if z is None else torch.empty_like(z),
+        None if dt_bias is None else torch.empty_like(dt_bias),
+        torch.empty(B, H, S, device=u.device, dtype=torch.float32))
+    ws = _scratch(workspace, _size("h3conv_selective_scan_bwd_workspace_size", B, H, N, S, G), u.device)
+    _check(load().h3conv_selective_scan_bwd(
+        _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(lengths), _ptr(saved),
+        _ptr(dy), _ptr(dx_out), _ptr(g.du), _ptr(g.ddt), _ptr(g.dA), _ptr(g.dB), _ptr(g.dC), _ptr(g.dD), _ptr(g.dz),
+        _ptr(g.ddt_bias), _ptr(g.dx_in), B, H, N, S, G, int(bool(softplus)), io, _ptr(ws),
+        ws.numel() * ws.element_size(), _stream()),
+        "h3conv_selective_scan_bwd")
+    return g
+
+
+def selective_step(u, dt, A, Bm, C, x, D=None, z=None, dt_bias=None, softplus: bool = True, slots=None, x_out=None,
+                   out=None):
+    """selective_scan for one token of each sequence.
+
+    u, dt, z [B,H]; Bm, C [B,G,S]; x [P,H,S] f32, a pool of states, updated in
+    place (or into ``x_out``, of which only the slots in use are written);
+    slots [B] int32, the slot of each sequence (sequence b in slot b if None).
+    A slot outside the pool marks an idle row: its output is zero.  Returns y [B,H]."""
+    io, B, H, S, G = _scan_args(u, dt, A, Bm, C, D, z, dt_bias, 2)
+    P = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 3 else 0
+    _arg(x, "x", torch.float32, (P, H, S), optional=False)
+    _arg(x_out, "x_out", torch.float32, (P, H, S))
+    _arg(slots, "slots", torch.int32, (B,))
+    _arg(out, "out", u.dtype, (B, H))
+    _same_device(u=u, dt=dt, A=A, Bm=Bm, C=C, D=D, z=z, dt_bias=dt_bias, slots=slots, x=x, x_out=x_out, out=out)
+    y = torch.empty_like(u) if out is None else out
+    to = x if x_out is None else x_out
+    _check(load().h3conv_selective_step(_ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias),
+                                        _ptr(slots), _ptr(x), _ptr(to), _ptr(y), B, H, P, S, G, int(bool(softplus)),
+                                        io, _stream()),
+           "h3conv_selective_step")
+    return y
+
+
+def _xent_args(x, w, labels):
+    _need(x, "x")
+    io = _io(x, "x")
+    if x.dim() != 2 or x.shape[1] < 1:
+        raise ValueError("x must be [T,D], got %s" % (tuple(x.shape),))
+    T, D = x.shape
+    _need(w, "w", x.dtype)
+    if w.dim() != 2 or w.shape[1] != D or w.shape[0] < 1:
+        raise ValueError("w must be [V,D] with D = %d, got %s" % (D, tuple(w.shape)))
+    _arg(labels, "labels", torch.int64, (T,), optional=False)
+    return io, T, D, w.shape[0]
+
+
+def linear_xent(x, w, labels, ignore_index: int = -100, return_lse: bool = False, workspace=None):
+    """Cross entropy of the logits x w^T per token, without the logits in memory.
+
+    x [T,D], w [V,D] f32/f16/bf16; labels [T] int64.  Returns loss [T] f32 (0
+    where the label is ignore_index or outside 0 .. V-1), or (loss, lse)."""
+    io, T, D, V = _xent_args(x, w, labels)
+    if workspace is not None:
+        _need(workspace, "workspace")
+    _same_device(x=x, w=w, labels=labels, workspace=workspace)
+    loss = torch.empty(T, device=x.device, dtype=torch.float32)
+    lse = torch.empty(T, device=x.device, dtype=torch.float32)
+    ws = _scratch(workspace, _size("h3conv_linear_xent_workspace_size", T, D, V, io, 0), x.device)
+    _check(load().h3conv_linear_xent(_ptr(x), _ptr(w), _ptr(labels), int(ignore_index), _ptr(loss), _ptr(lse), T, D, V,
+                                     io, _ptr(ws), ws.numel() * ws.element_size(), _stream()),
+           "h3conv_linear_xent")
+    return (loss, lse) if return_lse else loss
+
+
+def linear_xent_bwd(x, w, labels, lse, dloss, ignore_index: int = -100, workspace=None):
+    """Gradients (dx [T,D], dw [V,D], like x) of linear_xent for dloss [T] f32; lse [T] as it returned it."""
+    io, T, D, V = _xent_args(x, w, labels)
+    _arg(lse, "lse", torch.float32, (T,), optional=False)
+    _arg(dloss, "dloss", torch.float32, (T,), optional=False)
+    if workspace is not None:
+        _need(workspace, "workspace")
+    _same_device(x=x, w=w, labels=labels, lse=lse, dloss=dloss, workspace=workspace)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    ws = _scratch(workspace, _size("h3conv_linear_xent_workspace_size", T, D, V, io, 1), x.device)
+    _check(load().h3conv_linear_xent_bwd(_ptr(x), _ptr(w), _ptr(labels), int(ignore_index), _ptr(lse), _ptr(dloss),
+                                         _ptr(dx), _ptr(dw), T, D, V, io, _ptr(ws), ws.numel() * ws.element_size(),
+                                         _stream()),
+           "h3conv_linear_xent_bwd")
+    return dx, dw

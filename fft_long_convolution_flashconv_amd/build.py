@@ -1,6 +1,6 @@
 """Build the gfx950 HIP library ``libh3conv.so`` in-tree with hipcc.
 
-Every ``csrc/*.hip`` file is compiled to an object in parallel, then linked
+Every ``.hip`` file under ``csrc/`` is compiled to an object in parallel, then linked
 into one shared library next to this file.  The build always runs when
 called, also where a built library exists; loaders only load what exists.
 """
@@ -51,7 +51,7 @@ def _compile(src: str, sanitize: bool = False) -> str:
 
 def build(verbose: bool = True, sanitize: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
-    srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
+    srcs = sorted(glob.glob(os.path.join(CSRC, "**", "*.hip"), recursive=True))
     jobs = min(len(srcs), int(os.environ.get("MAX_JOBS", "8")))
     with cf.ThreadPoolExecutor(max_workers=max(1, jobs)) as ex:
         objs = list(ex.map(lambda p: _compile(p, sanitize), srcs))

@@ -295,6 +295,168 @@ h3conv_status h3conv_h3_mix_mh(const void *q, const void *k, const void *v, cons
                                void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Layers of a language model with input-dependent (selective) state spaces,
+ * and its loss.  The recurrence is that of the SSM above (the blog's section
+ * "Background: What Are State Space Models?") with real modes and a step
+ * size, B and C that vary with the input.  Stream, ownership and errors are as
+ * above; tensors of the convolution and the scan need only the alignment of
+ * their elements (a row or token of a larger tensor may start anywhere),
+ * saved states, workspaces and all arguments of the loss 16 bytes.  With a zero-sized batch or length, what does not depend on it is
+ * still written: final states (the initial ones) and gradients (zeros, and
+ * dx_in = dx_out).
+ * ---------------------------------------------------------------------------
+ */
+
+/* Largest number of taps of the short convolution. */
+#define H3CONV_MAX_TAPS 4
+
+/*
+ * Short causal depthwise convolution with bias and SiLU:
+ *     p[b,h,t] = bias[h] + sum_{i<W} w[h,i] x[b,h,t-i],   y = silu(p), or p if !silu
+ * with the tap order of h3conv_h3_mix (w[h,0] on the current input).
+ *
+ *   x, y     [B,H,N]    io dtype
+ *   w, bias  [H,W], [H] fp32     bias may be NULL (zero)
+ *   x_in     [B,H,W-1]  io dtype the W-1 inputs before the row, oldest first; NULL = zeros
+ *   lengths  [B]        int32    valid steps of every row (clamped to 0 .. N), or NULL = N;
+ *                                inputs past them are not read into any result, outputs
+ *                                past them are zero
+ *   x_out    [B,H,W-1]  io dtype the last W-1 inputs of every row (reaching back into x_in),
+ *                                the x_in of what follows; may be NULL
+ * Supported: 1 <= W <= H3CONV_MAX_TAPS, B*H <= 2^30, B*H*N <= 2^40; any N.
+ */
+h3conv_status h3conv_short_conv(const void *x, const float *w, const float *bias, const void *x_in,
+                                const int32_t *lengths, void *y, void *x_out, int64_t B, int64_t H, int64_t N,
+                                int64_t W, int silu, int io, void *stream);
+
+/*
+ * Backward pass of h3conv_short_conv for upstream gradients dy of y and
+ * dx_out of x_out (NULL = none): with dp = dy silu'(p),
+ *     dx_s = sum_i w_i dp_{s+i},  dw_i = sum_{b,t} dp_t x_{t-i},  dbias = sum_{b,t} dp_t
+ * dx [B,H,N] and dx_in [B,H,W-1] (may be NULL) have the io dtype; dw [H,W] and
+ * dbias [H] (may be NULL) are fp32, written, summed in a fixed order.  Steps past a row's length
+ * get zero.  ws: at least h3conv_short_conv_bwd_workspace_size bytes.
+ */
+h3conv_status h3conv_short_conv_bwd(const void *x, const float *w, const float *bias, const void *x_in,
+                                    const int32_t *lengths, const void *dy, const void *dx_out, void *dx, float *dw,
+                                    float *dbias, void *dx_in, int64_t B, int64_t H, int64_t N, int64_t W, int silu,
+                                    int io, void *ws, size_t ws_bytes, void *stream);
+size_t h3conv_short_conv_bwd_workspace_size(int64_t B, int64_t H, int64_t N, int64_t W);
+
+/*
+ * h3conv_short_conv for one token of each of B sequences, whose saved inputs
+ * are kept in a pool of P slots.
+ *
+ *   x, y       [B,H]      io dtype
+ *   slots      [B]        int32    the slot of each sequence, or NULL (sequence b in slot b,
+ *                                  P >= B).  A slot outside 0 .. P-1 marks an idle row: its y
+ *                                  is zero and no state changes.  Slots in use must differ.
+ *   state_in, state_out [P,H,W-1] io dtype  the last W-1 inputs; state_out is state_in
+ *                                  (updated in place) or a separate pool, of which only the
+ *                                  slots in use are written
+ * Supported: as h3conv_short_conv, B <= 65535.
+ */
+h3conv_status h3conv_short_conv_step(const void *x, const float *w, const float *bias, const int32_t *slots,
+                                     const void *state_in, void *state_out, void *y, int64_t B, int64_t H, int64_t P,
+                                     int64_t W, int silu, int io, void *stream);
+
+/*
+ * Selective state-space scan, real modes:
+ *     d_t    = softplus(dt_t + dt_bias), or dt_t + dt_bias if !softplus
+ *     x_t[j] = exp(d_t A[j]) x_{t-1}[j] + d_t B_t[j] u_t
+ *     y_t    = (sum_j C_t[j] x_t[j] + D u_t) silu(z_t)
+ * per row (b,h); B_t and C_t are shared by the H/G consecutive channels of a
+ * group.
+ *
+ *   u, dt, y  [B,H,N]    io dtype
+ *   z         [B,H,N]    io dtype  gate, or NULL (none)
+ *   A         [H,S]      fp32      decay rates (negative for stable modes)
+ *   Bm, C     [B,G,S,N]  io dtype
+ *   D, dt_bias [H]       fp32      NULL = zeros
+ *   x_in      [B,H,S]    fp32      initial state, or NULL for zero
+ *   lengths   [B]        int32     valid steps of every row (clamped to 0 .. N), or NULL = N:
+ *                                  later steps leave the state alone, their y is zero and
+ *                                  their inputs are not read into any result
+ *   x_out     [B,H,S]    fp32      state after the last valid step, or NULL
+ *   saved     states inside the rows for h3conv_selective_scan_bwd,
+ *             h3conv_selective_saved_size bytes, or NULL
+ * Supported: 1 <= S <= H3CONV_MAX_STATE, G divides H, B*H <= 2^30,
+ * B*H*N <= 2^40, B*G*S*N <= 2^38; any N.  The recurrence runs in fp32.
+ */
+h3conv_status h3conv_selective_scan(const void *u, const void *dt, const float *A, const void *Bm, const void *C,
+                                    const float *D, const void *z, const float *dt_bias, const float *x_in,
+                                    const int32_t *lengths, void *y, float *x_out, float *saved, int64_t B, int64_t H,
+                                    int64_t N, int64_t S, int64_t G, int softplus, int io, void *stream);
+size_t h3conv_selective_saved_size(int64_t B, int64_t H, int64_t N, int64_t S);
+
+/*
+ * Backward pass of h3conv_selective_scan (same u, dt, A, Bm, C, D, z, dt_bias
+ * and lengths; `saved` as that call wrote it) for upstream gradients dy of y
+ * and dx_out [B,H,S] of x_out (NULL = none).
+ *
+ *   du, ddt   [B,H,N]    io dtype;  dz likewise, given exactly if z is
+ *   dB, dC    [B,G,S,N]  io dtype   summed over the channels of the group
+ *   dA        [H,S]      fp32       summed over batch and time
+ *   dD, ddt_bias [H]     fp32       likewise; may be NULL
+ *   dx_in     [B,H,S]    fp32       may be NULL
+ *   ws        at least h3conv_selective_scan_bwd_workspace_size bytes
+ * Gradients are written, not accumulated into; all sums run in a fixed order.
+ */
+h3conv_status h3conv_selective_scan_bwd(const void *u, const void *dt, const float *A, const void *Bm, const void *C,
+                                        const float *D, const void *z, const float *dt_bias, const int32_t *lengths,
+                                        const float *saved, const void *dy, const float *dx_out, void *du, void *ddt,
+                                        float *dA, void *dB, void *dC, float *dD, void *dz, float *ddt_bias,
+                                        float *dx_in, int64_t B, int64_t H, int64_t N, int64_t S, int64_t G,
+                                        int softplus, int io, void *ws, size_t ws_bytes, void *stream);
+size_t h3conv_selective_scan_bwd_workspace_size(int64_t B, int64_t H, int64_t N, int64_t S, int64_t G);
+
+/*
+ * h3conv_selective_scan for one token of each of B sequences, whose states
+ * are kept in a pool of P slots (slots and the pool as in
+ * h3conv_short_conv_step).
+ *
+ *   u, dt, z, y [B,H]    io dtype    Bm, C [B,G,S]  io dtype
+ *   x_in, x_out [P,H,S]  fp32        the same pool (updated in place) or separate ones
+ * Supported: as h3conv_selective_scan, B <= 65535.
+ */
+h3conv_status h3conv_selective_step(const void *u, const void *dt, const float *A, const void *Bm, const void *C,
+                                    const float *D, const void *z, const float *dt_bias, const int32_t *slots,
+                                    const float *x_in, float *x_out, void *y, int64_t B, int64_t H, int64_t P,
+                                    int64_t S, int64_t G, int softplus, int io, void *stream);
+
+/*
+ * Softmax cross entropy of a linear output layer, without the logits in
+ * memory:
+ *     l[t,v] = sum_d x[t,d] w[v,d],  lse[t] = log sum_v exp(l[t,v]),
+ *     loss[t] = lse[t] - l[t,labels[t]]
+ *
+ *   x [T,D], w [V,D]  io dtype     labels [T] int64
+ *   loss, lse [T]     fp32         loss is 0 where labels[t] is ignore_index or outside 0 .. V-1
+ *   ws   at least h3conv_linear_xent_workspace_size(T, D, V, io, 0) bytes
+ * Supported: D <= 2^20, V <= 2^22, T <= 2^30, T*D and V*D <= 2^40.
+ * Products of 16-bit elements are summed in fp32 on the matrix cores; fp32
+ * elements use the fp32 matrix cores.
+ */
+h3conv_status h3conv_linear_xent(const void *x, const void *w, const int64_t *labels, int64_t ignore_index,
+                                 float *loss, float *lse, int64_t T, int64_t D, int64_t V, int io, void *ws,
+                                 size_t ws_bytes, void *stream);
+
+/*
+ * Gradients of h3conv_linear_xent for an upstream gradient dloss [T] fp32 of
+ * loss (lse as that call wrote it):
+ *     G[t,v] = (exp(l[t,v] - lse[t]) - [v == labels[t]]) dloss[t]   (0 on ignored tokens)
+ *     dx = G w  [T,D],   dw = G^T x  [V,D]     io dtype, written
+ * The vocabulary is taken in pieces; G of one piece is held in the workspace
+ * in the io dtype (fp16: scaled by a power of two from the largest |dloss|),
+ * ws: at least h3conv_linear_xent_workspace_size(T, D, V, io, 1) bytes.
+ */
+h3conv_status h3conv_linear_xent_bwd(const void *x, const void *w, const int64_t *labels, int64_t ignore_index,
+                                     const float *lse, const float *dloss, void *dx, void *dw, int64_t T, int64_t D,
+                                     int64_t V, int io, void *ws, size_t ws_bytes, void *stream);
+size_t h3conv_linear_xent_workspace_size(int64_t T, int64_t D, int64_t V, int io, int bwd);
+
+/*
  * Workspace bytes an operation needs for the given sizes (0 if none).
  * `op` is an h3conv_op; unused size arguments are ignored.  For
  * H3CONV_OP_H3_MIX, H is the model width Dm and the size is that of the
