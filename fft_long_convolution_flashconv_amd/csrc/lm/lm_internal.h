@@ -26,7 +26,7 @@ hipError_t launch_short_conv_step(const void *x, const float *w, const float *bi
 
 // -------------------------------------------------------- selective_scan
 // Samples between two saved states of a training pass.
-constexpr int kSelChunk = 256;
+constexpr int kSelChunk = 128;
 
 struct SelArgs {
     const void *u, *dt, *Bm, *C, *z;                 // [B,H,N] (z may be null), [B,G,S,N]

@@ -39,41 +39,19 @@ __device__ __forceinline__ float dpp_rows(float old, float v) {
                                                                  CTRL, RMASK, 0xf, false));
 }
 
-// The maps x -> P x + Q of consecutive lanes, composed: on return (P, Q) is
-// the composition of all lanes before this one (the identity for lane 0).
-__device__ __forceinline__ void prefix_maps(float &P, float &Q, int lane) {
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) {
-        const float p = __shfl_up(P, k), q = __shfl_up(Q, k);
-        if (lane >= k) {
-            Q = fmaf(P, q, Q);
-            P *= p;
-        }
-    }
-    P = __shfl_up(P, 1);
-    Q = __shfl_up(Q, 1);
-    if (lane == 0) { P = 1.f; Q = 0.f; }
+// Sum over the 16 lanes of a DPP row, in every lane of it.
+__device__ __forceinline__ float row_sum(float v) {
+    v += dpp0<0xb1>(v);   // quad_perm [1,0,3,2]
+    v += dpp0<0x4e>(v);   // quad_perm [2,3,0,1]
+    v += dpp0<0x141>(v);  // row_half_mirror
+    v += dpp0<0x140>(v);  // row_mirror
+    return v;
 }
-
-// The same from the last lane down: the composition of all lanes after this
-// one.
-__device__ __forceinline__ void suffix_maps(float &P, float &Q, int lane) {
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) {
-        const float p = __shfl_down(P, k), q = __shfl_down(Q, k);
-        if (lane + k < 64) {
-            Q = fmaf(P, q, Q);
-            P *= p;
-        }
-    }
-    P = __shfl_down(P, 1);
-    Q = __shfl_down(Q, 1);
-    if (lane == 63) { P = 1.f; Q = 0.f; }
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
+// Sum over the wave, in its last lane.
+__device__ __forceinline__ float wave_sum_last(float v) {
+    v = row_sum(v);
+    v += dpp_rows<0x142, 0xa>(0.f, v);  // row_bcast:15
+    v += dpp_rows<0x143, 0xc>(0.f, v);  // row_bcast:31
     return v;
 }
 
@@ -377,12 +355,16 @@ __global__ __launch_bounds__(256, 2) void k_sel_scan(const SelK<typename io_elem
 //   dA = sum_t g_t (a_t x_{t-1}) d_t          dD = sum dr u,  dz = dy r silu'(z)
 // One block takes one batch row and a set of channels of one group, and walks
 // the row's pieces of kSelChunk steps from the end, with the states at each
-// piece's start as the forward pass saved them.  Wave w owns the modes 4w ..
-// 4w+3 of a block of 16: their dB and dC over the block's channels stay in
-// its registers, so no sum needs an atomic.  Channels go through in fours:
-// wave w prepares channel w (softplus, gate) for all waves in LDS, and joins
-// the waves' sums over modes for it.
-constexpr int kModes = 16, kSetMax = 64, kJT = kSelChunk / 64;
+// piece's start as the forward pass saved them.  A wave takes the set's
+// channels w, w + 8, ... alone: its four DPP rows of 16 lanes hold four modes
+// at a time (row r: modes 4r .. 4r+3 of a block of 16, in four rounds), lane l
+// of a row kJT steps.  So dB and dC of every mode and step stay in one lane's
+// registers over all the wave's channels (no atomics), the scans over time
+// stay within a DPP row, and the sums over modes are two exchanges between
+// rows.  A lane prepares and finishes a quarter of its steps (softplus, gate)
+// and the rows share them through LDS.
+constexpr int kModes = 16, kJT = kSelChunk / 16, kQ = kJT / 4, kWaves = 8, kPerWave = 16;
+static_assert(kJT == 8 && 2 * kModes * kSelChunk == kWaves * 64 * 8, "one 8-step load of B or C per thread and piece");
 
 struct SelBwdWs {
     float *dB, *dC;        // [sets][B][G][S][N]
@@ -392,195 +374,314 @@ struct SelBwdWs {
     int sets, per;         // sets per group, channels per set
 };
 
+// As scan_states<16>, from the last lane of a DPP row down.
+__device__ __forceinline__ void scan_back(float P, float &Q) {
+    Q = fmaf(P, dpp0<0x101>(Q), Q);  // row_shl:1
+    P *= dpp0<0x101>(P);
+    Q = fmaf(P, dpp0<0x102>(Q), Q);
+    P *= dpp0<0x102>(P);
+    Q = fmaf(P, dpp0<0x104>(Q), Q);
+    P *= dpp0<0x104>(P);
+    Q = fmaf(P, dpp0<0x108>(Q), Q);
+}
+
+// Sums over the wave's four DPP rows of v[0 .. 7]; row r gets those of
+// v[2r], v[2r+1].
+__device__ __forceinline__ void sum_rows(const float (&v)[kJT], float (&o)[kQ]) {
+    float h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // rows 0, 1 keep i, rows 2, 3 keep i + 4
+        const auto x = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, v[i]),
+                                                        __builtin_bit_cast(unsigned, v[i + 4]), false, false);
+        h[i] = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const auto x = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, h[i]),
+                                                        __builtin_bit_cast(unsigned, h[i + 2]), false, false);
+        o[i] = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+    }
+}
+
+__device__ __forceinline__ void get8(const float4 *p, int step, float (&v)[8]) {
+    const float4 x = p[0], y = p[step];
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+}
+
+// What a lane loads of one channel and piece ahead of its use.
 template <int IO>
-__global__ __launch_bounds__(256) void k_sel_bwd(const SelK<typename io_elem<IO>::T> k,
-                                                 const float *__restrict__ saved,
-                                                 const typename io_elem<IO>::T *__restrict__ dy,
-                                                 const float *__restrict__ dx_out,
-                                                 typename io_elem<IO>::T *__restrict__ du,
-                                                 typename io_elem<IO>::T *__restrict__ ddt,
-                                                 typename io_elem<IO>::T *__restrict__ dz, float *__restrict__ dx_in,
-                                                 const SelBwdWs ws, int64_t nchunk, int n0, int last_block) {
-    __shared__ float pre[4][3][kSelChunk];
-    __shared__ float part[4][4][3][kSelChunk];
-    __shared__ float carry[kSetMax][kModes], sumA[kSetMax][kModes], sumDb[kSetMax][2];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+struct BwdIn {
+    Raw<IO, kQ> u, p, z, gy;
+    float A[4], x[4];
+};
+
+template <int IO>
+__global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
+    const SelK<typename io_elem<IO>::T> k, const float *__restrict__ saved,
+    const typename io_elem<IO>::T *__restrict__ dy, const float *__restrict__ dx_out,
+    typename io_elem<IO>::T *__restrict__ du, typename io_elem<IO>::T *__restrict__ ddt,
+    typename io_elem<IO>::T *__restrict__ dz, float *__restrict__ dx_in, const SelBwdWs ws, int64_t nchunk, int n0,
+    int last_block) {
+    constexpr int F4 = kSelChunk / 4;  // float4 per row of steps
+    // B and C of the piece, then the rows' exchange; both over again as the
+    // buffer that joins the waves' dB and dC
+    __shared__ float4 lds[2048];
+    __shared__ float4 carry[kWaves][kPerWave][4], sumA[kWaves][kPerWave][4];
+    __shared__ float sumDb[kWaves][kPerWave][2];
+    float4(*const BC)[kModes][F4] = (float4(*)[kModes][F4])lds;
+    const int tid = threadIdx.x, lane = tid & 63, row = lane >> 4, l = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // (scalar: so are the rows' base addresses)
+    float4(*const mine)[F4] = (float4(*)[F4])(lds + 2 * kModes * F4) + 3 * wave;
     const int64_t N = k.N, Hg = k.H / k.G;
     const int set = (int)(blockIdx.x % ws.sets);
     const int64_t bg = blockIdx.x / ws.sets, g = bg % k.G, b = bg / k.G;
     const int64_t len = row_len(k.lengths, b, N);
-    const int64_t h0 = g * Hg + (int64_t)set * ws.per;
-    const int64_t left = Hg - (int64_t)set * ws.per;
-    const int nch = (int)(left < ws.per ? left : ws.per);
-    for (int i = threadIdx.x; i < nch * kModes; i += 256) {
-        const int c = i / kModes, n = n0 + i % kModes;
-        sumA[c][i % kModes] = 0.f;
-        carry[c][i % kModes] = (dx_out && n < k.S) ? dx_out[(b * k.H + h0 + c) * k.S + n] : 0.f;
-    }
-    for (int i = threadIdx.x; i < nch * 2; i += 256) sumDb[i / 2][i & 1] = 0.f;
-    __syncthreads();
-    for (int64_t ch = nchunk - 1; ch >= 0; --ch) {
-        const int64_t t0 = ch * kSelChunk + lane * kJT, valid = len - t0;
-        float Bv[4][kJT], Cv[4][kJT], aB[4][kJT], aC[4][kJT];
+    const int64_t left = Hg - (int64_t)set * ws.per, h0 = g * Hg + (int64_t)set * ws.per;
+    const int nset = (int)(left < ws.per ? left : ws.per);
+    const int nch = nset > wave ? (nset - wave + kWaves - 1) / kWaves : 0;  // this wave's channels
+    const int m0 = n0 + 4 * row;                                            // this row's modes
+    for (int c = 0; c < nch; ++c)
+        if (l < 4) {
+            const int64_t h = h0 + wave + kWaves * c;
+            (&carry[wave][c][row].x)[l] = (dx_out && m0 + l < k.S) ? dx_out[(b * k.H + h) * k.S + m0 + l] : 0.f;
+            (&sumA[wave][c][row].x)[l] = 0.f;
+            if (row == 0 && l < 2) sumDb[wave][c][l] = 0.f;
+        }
+    // this thread's eight steps of B or C in LDS: matrix, mode, steps
+    const int cm = tid >> 8, cn = (tid >> 4) & 15, ct = tid & 15;
+    const typename io_elem<IO>::T *const bc = (cm ? k.C : k.Bm) + (bg * k.S + (n0 + cn < k.S ? n0 + cn : 0)) * N + ct * 8;
+    // valid steps of a piece, and those from step `from` of it on
+    const auto steps = [&](int64_t ch, int64_t end) {
+        const int64_t n = end - ch * kSelChunk;
+        return (int)(n < 0 ? 0 : (n < kSelChunk ? n : kSelChunk));
+    };
+    const auto load_bc = [&](int64_t ch) {
+        return ld_raw<IO, 8, false>(bc + ch * kSelChunk, n0 + cn < k.S ? steps(ch, len) - ct * 8 : 0);
+    };
+    const int tq = l * kJT + row * kQ;  // this lane's own steps within a piece
+    BwdIn<IO> f;
+    const auto load_in = [&](int64_t ch, int c) {
+        const int64_t h = h0 + wave + kWaves * c, r = b * k.H + h, o = r * N + ch * kSelChunk;
+        const int valid = steps(ch, len) - tq;
+        f.u = ld_raw<IO, kQ, false>(k.u + o + tq, valid);
+        f.p = ld_raw<IO, kQ, false>(k.dt + o + tq, valid);
+        f.gy = ld_raw<IO, kQ, false>(dy + o + tq, valid);
+        if (k.z) f.z = ld_raw<IO, kQ, false>(k.z + o + tq, valid);
+        const float *const Ah = k.A + h * k.S, *const xh = saved + (r * nchunk + ch) * k.S;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int n = n0 + wave * 4 + q;
-            const int64_t bc = ((b * k.G + g) * k.S + (n < k.S ? n : 0)) * N + t0;
-            ld_row<IO, kJT>(k.Bm + bc, Bv[q], valid);
-            ld_row<IO, kJT>(k.C + bc, Cv[q], valid);
+            const bool in = m0 + q < k.S;
+            f.A[q] = in ? Ah[m0 + q] : 0.f;
+            f.x[q] = in ? xh[m0 + q] : 0.f;
+        }
+    };
+    Raw<IO, 8> rbc;
+    if (nchunk > 0) {
+        rbc = load_bc(nchunk - 1);
+        if (nch > 0) load_in(nchunk - 1, 0);
+    }
+    for (int64_t ch = nchunk - 1; ch >= 0; --ch) {
+        const int valid = steps(ch, len) - tq, keep = steps(ch, N) - tq;  // this lane's steps: valid, and in the row
+        {
+            // steps 4j .. 4j+3 at (j % 2) * 16 + j / 2: a lane's two reads are
+            // consecutive over the lanes of a row
+            float v[8];
+            unpack<IO, 8>(rbc, v);
+            BC[cm][cn][ct] = make_float4(v[0], v[1], v[2], v[3]);
+            BC[cm][cn][16 + ct] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+        __syncthreads();
+        if (ch > 0) rbc = load_bc(ch - 1);
+        float aB[4][kJT], aC[4][kJT];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
             for (int i = 0; i < kJT; ++i) aB[q][i] = aC[q][i] = 0.f;
-        }
-        for (int c0 = 0; c0 < nch; c0 += 4) {
-            const int mine = c0 + wave;
-            const int64_t h = h0 + mine, r = b * k.H + h;
-            float u[kJT], p[kJT], z[kJT], gy[kJT], d[kJT], dr[kJT];
-            if (mine < nch) {
-                const float bias = k.dt_bias ? k.dt_bias[h] : 0.f;
-                ld_row<IO, kJT>(k.u + r * N + t0, u, valid);
-                ld_row<IO, kJT>(k.dt + r * N + t0, p, valid);
-                ld_row<IO, kJT>(dy + r * N + t0, gy, valid);
-                if (k.z) ld_row<IO, kJT>(k.z + r * N + t0, z, valid);
+        for (int c = 0; c < nch; ++c) {
+            const int64_t h = h0 + wave + kWaves * c, r = b * k.H + h, o0 = r * N + ch * kSelChunk;
+            const float bias = k.dt_bias ? k.dt_bias[h] : 0.f, Dh = k.D ? k.D[h] : 0.f;
+            float u[kQ], p[kQ], z[kQ], gy[kQ], d[kQ], dr[kQ], A[4], xs[4];
+            unpack<IO, kQ>(f.u, u);
+            unpack<IO, kQ>(f.p, p);
+            unpack<IO, kQ>(f.gy, gy);
+            if (k.z) unpack<IO, kQ>(f.z, z);
 #pragma unroll
-                for (int i = 0; i < kJT; ++i) {
-                    p[i] += bias;
-                    d[i] = k.softplus ? softplus(p[i]) : p[i];
-                    if (i >= valid) d[i] = 0.f;
-                    dr[i] = k.z ? gy[i] * z[i] * sigmoid(z[i]) : gy[i];
-                    pre[wave][0][lane * kJT + i] = d[i];
-                    pre[wave][1][lane * kJT + i] = d[i] * u[i];
-                    pre[wave][2][lane * kJT + i] = dr[i];
+            for (int q = 0; q < 4; ++q) {
+                A[q] = f.A[q];
+                xs[q] = f.x[q];
+            }
+            if (c + 1 < nch) load_in(ch, c + 1);
+            else if (ch > 0) load_in(ch - 1, 0);
+#pragma unroll
+            for (int i = 0; i < kQ; ++i) {
+                p[i] += bias;
+                d[i] = k.softplus ? softplus(p[i]) : p[i];
+                if (i >= valid) d[i] = 0.f;
+                dr[i] = k.z ? gy[i] * z[i] * sigmoid(z[i]) : gy[i];
+            }
+            {
+                const int at = 4 * ((row >> 1) * 16 + l) + 2 * (row & 1);
+                float *const to0 = &mine[0][0].x + at, *const to1 = &mine[1][0].x + at, *const to2 = &mine[2][0].x + at;
+#pragma unroll
+                for (int i = 0; i < kQ; ++i) {
+                    to0[i] = d[i];
+                    to1[i] = d[i] * u[i];
+                    to2[i] = dr[i];
                 }
             }
-            __syncthreads();
-            for (int j = 0; j < 4 && c0 + j < nch; ++j) {
-                const int c = c0 + j;
-                const int64_t rc = b * k.H + h0 + c;
-                float dd[kJT], bu[kJT], rr[kJT], sr[kJT], sb[kJT], sk[kJT];
+            __builtin_amdgcn_wave_barrier();
+            float dd[kJT], bu[kJT], rr[kJT], sr[kJT], sb[kJT], sk[kJT], sum = 0.f;
+            get8(mine[0] + l, 16, dd);
+            get8(mine[1] + l, 16, bu);
+            get8(mine[2] + l, 16, rr);
 #pragma unroll
-                for (int i = 0; i < kJT; ++i) {
-                    dd[i] = pre[j][0][lane * kJT + i];
-                    bu[i] = pre[j][1][lane * kJT + i];
-                    rr[i] = pre[j][2][lane * kJT + i];
-                    sr[i] = sb[i] = sk[i] = 0.f;
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int m = wave * 4 + q, n = n0 + m;
-                    if (n >= k.S) break;
-                    const float A = k.A[(h0 + c) * k.S + n], A2 = A * kLog2e;
-                    float a[kJT], ax[kJT], P = 1.f, Q = 0.f;
-#pragma unroll
-                    for (int i = 0; i < kJT; ++i) {
-                        a[i] = exp2_(dd[i] * A2);
-                        P *= a[i];
-                        Q = fmaf(a[i], Q, bu[i] * Bv[q][i]);
-                    }
-                    const float Pl = P;
-                    prefix_maps(P, Q, lane);
-                    float x = fmaf(P, saved[(rc * nchunk + ch) * k.S + n], Q);
-#pragma unroll
-                    for (int i = 0; i < kJT; ++i) {
-                        ax[i] = a[i] * x;
-                        x = fmaf(bu[i], Bv[q][i], ax[i]);
-                        sr[i] = fmaf(Cv[q][i], x, sr[i]);
-                        aC[q][i] = fmaf(rr[i], x, aC[q][i]);
-                    }
-                    P = Pl;
-                    Q = 0.f;
-#pragma unroll
-                    for (int i = kJT - 1; i >= 0; --i) Q = a[i] * fmaf(Cv[q][i], rr[i], Q);
-                    suffix_maps(P, Q, lane);
-                    float e = fmaf(P, carry[c][m], Q), sA = 0.f;
-#pragma unroll
-                    for (int i = kJT - 1; i >= 0; --i) {
-                        const float gx = fmaf(Cv[q][i], rr[i], e), w = gx * ax[i];
-                        aB[q][i] = fmaf(gx, bu[i], aB[q][i]);
-                        sb[i] = fmaf(gx, Bv[q][i], sb[i]);
-                        sk[i] = fmaf(w, A, sk[i]);
-                        sA = fmaf(w, dd[i], sA);
-                        e = a[i] * gx;
-                    }
-                    sA = wave_sum(sA);
-                    if (lane == 0) {
-                        carry[c][m] = e;
-                        sumA[c][m] += sA;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kJT; ++i) {
-                    part[j][wave][0][lane * kJT + i] = sr[i];
-                    part[j][wave][1][lane * kJT + i] = sb[i];
-                    part[j][wave][2][lane * kJT + i] = sk[i];
-                }
+            for (int i = 0; i < kJT; ++i) {
+                sum += dd[i];
+                sr[i] = sb[i] = sk[i] = 0.f;
             }
-            __syncthreads();
-            if (mine < nch) {
-                const float Dh = k.D ? k.D[h] : 0.f;
-                const int64_t plane = k.B * k.H * N, keep = N - t0;
-                float o0[kJT], o1[kJT], o2[kJT], sD = 0.f, sp = 0.f;
+            const float4 cy4 = carry[wave][c][row];
+            const float cy[4] = {cy4.x, cy4.y, cy4.z, cy4.w};
+            float out[4], sA[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float A2 = A[q] * kLog2e, P = exp2_(sum * A2);
+                float Bv[kJT], Cv[kJT], a[kJT], ax[kJT];
+                get8(BC[0][4 * row + q] + l, 16, Bv);
+                const float in = l == 0 ? xs[q] : 0.f;
+                float Q = in;
 #pragma unroll
                 for (int i = 0; i < kJT; ++i) {
-                    float s[3];
+                    a[i] = exp2_(dd[i] * A2);
+                    ax[i] = bu[i] * Bv[i];
+                    Q = fmaf(a[i], Q, ax[i]);
+                }
+                scan_states<16>(P, Q);
+                float x = dpp0<0x111>(Q) + in;
+                get8(BC[1][4 * row + q] + l, 16, Cv);
 #pragma unroll
-                    for (int f = 0; f < 3; ++f) {
-                        s[f] = 0.f;
+                for (int i = 0; i < kJT; ++i) {
+                    const float w = ax[i];
+                    ax[i] = a[i] * x;
+                    x = ax[i] + w;
+                    sr[i] = fmaf(Cv[i], x, sr[i]);
+                    aC[q][i] = fmaf(rr[i], x, aC[q][i]);
+                    Cv[i] *= rr[i];
+                }
+                const float back = l == 15 ? cy[q] : 0.f;
+                Q = back;
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) s[f] += part[wave][w][f][lane * kJT + i];
-                        if (ws.acc && i < keep) {
-                            float *q = ws.acc + f * plane + r * N + t0 + i;
-                            if (n0 > 0) s[f] += *q;
-                            if (!last_block) *q = s[f];
+                for (int i = kJT - 1; i >= 0; --i) Q = a[i] * (Q + Cv[i]);
+                scan_back(P, Q);
+                out[q] = Q;  // what lane 0 hands to the piece before
+                float e = dpp0<0x101>(Q) + back;
+                sA[q] = 0.f;
+#pragma unroll
+                for (int i = kJT - 1; i >= 0; --i) {
+                    const float gx = Cv[i] + e, w = gx * ax[i];
+                    aB[q][i] = fmaf(gx, bu[i], aB[q][i]);
+                    sb[i] = fmaf(gx, Bv[i], sb[i]);
+                    sk[i] = fmaf(w, A[q], sk[i]);
+                    sA[q] = fmaf(w, dd[i], sA[q]);
+                    e = a[i] * gx;
+                }
+                // one round's registers at a time
+                hold(aC[q]);
+                hold(aB[q]);
+                hold(sr);
+                hold(sb);
+                hold(sk);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sA[q] = row_sum(sA[q]);
+            if (l == 0) {
+                carry[wave][c][row] = make_float4(out[0], out[1], out[2], out[3]);
+                float4 t = sumA[wave][c][row];
+                t.x += sA[0], t.y += sA[1], t.z += sA[2], t.w += sA[3];
+                sumA[wave][c][row] = t;
+            }
+            float s3[3][kQ], o[3][kQ], sD = 0.f, sp = 0.f;
+            sum_rows(sr, s3[0]);
+            sum_rows(sb, s3[1]);
+            sum_rows(sk, s3[2]);
+            if (ws.acc) {
+                const int64_t plane = k.B * k.H * N;
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+#pragma unroll
+                    for (int i = 0; i < kQ; ++i)
+                        if (i < keep) {
+                            float *q = ws.acc + j * plane + o0 + tq + i;
+                            if (n0 > 0) s3[j][i] += *q;
+                            if (!last_block) *q = s3[j][i];
                         }
-                    }
-                    const float raw = fmaf(Dh, u[i], s[0]);
-                    o0[i] = fmaf(d[i], s[1], Dh * dr[i]);
-                    o1[i] = fmaf(u[i], s[1], s[2]);
-                    if (k.softplus) o1[i] *= sigmoid(p[i]);
+            }
+            if (last_block) {
+#pragma unroll
+                for (int i = 0; i < kQ; ++i) {
+                    const float raw = fmaf(Dh, u[i], s3[0][i]);
+                    o[0][i] = fmaf(d[i], s3[1][i], Dh * dr[i]);
+                    o[1][i] = fmaf(u[i], s3[1][i], s3[2][i]);
+                    if (k.softplus) o[1][i] *= sigmoid(p[i]);
                     if (k.z) {
                         const float sg = sigmoid(z[i]);
-                        o2[i] = gy[i] * raw * sg * (1.f + z[i] * (1.f - sg));
+                        o[2][i] = gy[i] * raw * sg * (1.f + z[i] * (1.f - sg));
                     }
-                    if (i >= valid) o0[i] = o1[i] = o2[i] = 0.f;
+                    if (i >= valid) o[0][i] = o[1][i] = o[2][i] = 0.f;
                     sD = fmaf(dr[i], u[i], sD);
-                    sp += o1[i];
+                    sp += o[1][i];
                 }
-                if (last_block) {
-                    st_row<IO, kJT>(du + r * N + t0, o0, keep);
-                    st_row<IO, kJT>(ddt + r * N + t0, o1, keep);
-                    if (dz) st_row<IO, kJT>(dz + r * N + t0, o2, keep);
-                    sD = wave_sum(sD);
-                    sp = wave_sum(sp);
-                    if (lane == 0) {
-                        sumDb[mine][0] += sD;
-                        sumDb[mine][1] += sp;
-                    }
+                st_row<IO, kQ>(du + o0 + tq, o[0], keep);
+                st_row<IO, kQ>(ddt + o0 + tq, o[1], keep);
+                if (dz) st_row<IO, kQ>(dz + o0 + tq, o[2], keep);
+                sD = wave_sum_last(sD);
+                sp = wave_sum_last(sp);
+                if (lane == 63) {
+                    sumDb[wave][c][0] += sD;
+                    sumDb[wave][c][1] += sp;
                 }
             }
         }
+        // dB, dC of the piece: the waves' sums, in order, two rounds at a time;
+        // thread t joins steps 8 (t % 16) .. of matrix t / 256, DPP row
+        // (t / 16) % 4 of round (t / 128) % 2 ... as values v of a lane
+        __syncthreads();
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int n = n0 + wave * 4 + q;
-            if (n >= k.S) break;
-            const int64_t o = ((((int64_t)set * k.B + b) * k.G + g) * k.S + n) * N + t0;
+            float4(*const buf)[4][64] = (float4(*)[4][64])lds;  // [wave][quarter of the 16 values][lane]
+            buf[wave][0][lane] = make_float4(aB[q][0], aB[q][1], aB[q][2], aB[q][3]);
+            buf[wave][1][lane] = make_float4(aB[q][4], aB[q][5], aB[q][6], aB[q][7]);
+            buf[wave][2][lane] = make_float4(aC[q][0], aC[q][1], aC[q][2], aC[q][3]);
+            buf[wave][3][lane] = make_float4(aC[q][4], aC[q][5], aC[q][6], aC[q][7]);
+            __syncthreads();
+            // thread: quarter v, lane ll of the waves' values
+            const int half = tid & 1, ll = (tid >> 1) & 63, v = tid >> 7;
+            float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < kJT; ++i)
-                if (t0 + i < N) {
-                    ws.dB[o + i] = aB[q][i];
-                    ws.dC[o + i] = aC[q][i];
-                }
+            for (int w = 0; w < kWaves; ++w) {
+                const float *x = &buf[w][v][ll].x + 2 * half;
+                s.x += x[0];
+                s.y += x[1];
+            }
+            const int n = n0 + 4 * (ll >> 4) + q;
+            const int t = (ll & 15) * kJT + (v & 1) * 4 + half * 2;
+            if (n < k.S) {
+                float *o = (v < 2 ? ws.dB : ws.dC) + ((((int64_t)set * k.B + b) * k.G + g) * k.S + n) * N + ch * kSelChunk + t;
+                if (t < steps(ch, N)) o[0] = s.x;
+                if (t + 1 < steps(ch, N)) o[1] = s.y;
+            }
+            __syncthreads();
         }
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < nch * kModes; i += 256) {
-        const int c = i / kModes, m = i % kModes, n = n0 + m;
-        if (n >= k.S) continue;
-        const int64_t o = (b * k.H + h0 + c) * k.S + n;
-        ws.dA[o] = sumA[c][m];
-        if (dx_in) dx_in[o] = carry[c][m];
+    for (int c = 0; c < nch; ++c) {
+        const int64_t h = h0 + wave + kWaves * c, o = (b * k.H + h) * k.S + m0;
+        if (l < 4 && m0 + l < k.S) {
+            ws.dA[o + l] = (&sumA[wave][c][row].x)[l];
+            if (dx_in) dx_in[o + l] = (&carry[wave][c][row].x)[l];
+        }
+        if (last_block && lane < 2) ws.dDb[(b * k.H + h) * 2 + lane] = sumDb[wave][c][lane];
     }
-    if (last_block)
-        for (int i = threadIdx.x; i < nch * 2; i += 256) ws.dDb[(b * k.H + h0) * 2 + i] = sumDb[i / 2][i & 1];
 }
 
 // dB, dC: the sets' sums, in order; M = B*G*S*N values each.
@@ -680,14 +781,14 @@ SelK<typename io_elem<IO>::T> pack_args(const SelArgs &a) {
                    a.dt_bias, a.x_in, a.lengths, a.B, a.H, a.N, a.S, a.G, a.softplus};
 }
 
-// Sets of channels per group: enough blocks to fill the chip twice, sets of
-// at most kSetMax channels.
+// Sets of channels per group.  A compute unit holds one block of eight waves:
+// 256 blocks fill the chip, more channels per block mean fewer partial sums of
+// dB and dC (written and read once per set).
 void bwd_sets(int64_t B, int64_t H, int64_t G, int *sets, int *per) {
-    const int64_t Hg = H / G;
-    const int64_t want = B > 0 ? (512 + B * G - 1) / (B * G) : 1;
+    const int64_t Hg = H / G, want = B > 0 ? (256 + B * G - 1) / (B * G) : 1;
     int64_t p = (Hg + want - 1) / want;
-    p = (p + 3) / 4 * 4;
-    if (p > kSetMax) p = kSetMax;
+    p = (p + kWaves - 1) / kWaves * kWaves;
+    if (p > kWaves * kPerWave) p = kWaves * kPerWave;
     *per = (int)p;
     *sets = (int)((Hg + p - 1) / p);
 }
@@ -738,7 +839,7 @@ hipError_t bwd_io(const SelArgs &a, const float *saved, const void *dy, const fl
     const dim3 grid((unsigned)(a.B * a.G * w.sets));
     for (int n0 = 0; n0 < a.S && a.B > 0; n0 += kModes) {
         const hipError_t e =
-            launch(k_sel_bwd<IO>, grid, dim3(256), 0, s, pack_args<IO>(a), saved, (const T *)dy, dx_out, (T *)g.du,
+            launch(k_sel_bwd<IO>, grid, dim3(kWaves * 64), 0, s, pack_args<IO>(a), saved, (const T *)dy, dx_out, (T *)g.du,
                    (T *)g.ddt, (T *)g.dz, g.dx_in, w, chunks(a.N), n0, n0 + kModes >= a.S ? 1 : 0);
         if (e != hipSuccess) return e;
     }
