@@ -79,23 +79,46 @@ struct Raw {
     uint32_t w[kWords];
 };
 
-// FULL: all n are valid; else elements from `valid` on are zero.
+// Elements off .. off + n - 1 of p.  FULL: all n are valid; else elements from
+// `valid` on are zero: a lane with some of them loads the n elements that end
+// at its last valid one (still in the tensor unless at its very start) and
+// shifts them down.
 template <int IO, int n, bool FULL>
-__device__ __forceinline__ Raw<IO, n> ld_raw(const typename io_elem<IO>::T *p, int64_t valid) {
+__device__ __forceinline__ Raw<IO, n> ld_raw(const typename io_elem<IO>::T *p, int64_t off, int64_t valid) {
     using T = typename io_elem<IO>::T;
+    constexpr int W = Raw<IO, n>::kWords, E = 4 / (int)sizeof(T);
     Raw<IO, n> r;
     if (FULL || valid >= n) {
-        const Pack<T, n> q = *reinterpret_cast<const Pack<T, n> *>(p);
+        const Pack<T, n> q = *reinterpret_cast<const Pack<T, n> *>(p + off);
         __builtin_memcpy(&r, &q, sizeof(r));
+        return r;
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) r.w[i] = 0;
+    if (valid <= 0) return r;
+    if (off + valid >= n) {
+        const Pack<T, n> q = *reinterpret_cast<const Pack<T, n> *>(p + off + valid - n);
+        __builtin_memcpy(&r, &q, sizeof(r));
+        const int s = n - (int)valid;  // elements to drop, 1 .. n - 1
+        if (E == 2) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const uint32_t hi = i + 1 < W ? r.w[i + 1] : 0u;
+                r.w[i] = (s & 1) ? (r.w[i] >> 16 | hi << 16) : r.w[i];
+            }
+        }
+#pragma unroll
+        for (int k = 1; k < W; k *= 2)
+#pragma unroll
+            for (int i = 0; i < W; ++i) r.w[i] = (s & (E * k)) ? (i + k < W ? r.w[i + k] : 0u) : r.w[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < Raw<IO, n>::kWords; ++i) {
-            if constexpr (sizeof(T) == 4) {
-                r.w[i] = i < valid ? __builtin_bit_cast(uint32_t, p[i]) : 0u;
+        for (int i = 0; i < W; ++i) {
+            if constexpr (E == 1) {
+                if (i < valid) r.w[i] = __builtin_bit_cast(uint32_t, p[off + i]);
             } else {
-                const uint32_t lo = 2 * i < valid ? __builtin_bit_cast(uint16_t, p[2 * i]) : 0u;
-                const uint32_t hi = 2 * i + 1 < valid ? __builtin_bit_cast(uint16_t, p[2 * i + 1]) : 0u;
-                r.w[i] = lo | hi << 16;
+                if (2 * i < valid) r.w[i] = __builtin_bit_cast(uint16_t, p[off + 2 * i]);
+                if (2 * i + 1 < valid) r.w[i] |= (uint32_t)__builtin_bit_cast(uint16_t, p[off + 2 * i + 1]) << 16;
             }
         }
     }
@@ -229,8 +252,8 @@ __device__ __forceinline__ void scan_piece(const SelK<typename io_elem<IO>::T> &
     constexpr int IT = kIT, AH = kAhead;
     const int last = k.S - 1;
     Raw<IO, IT> rB[AH], rC[AH];
-    const auto loadB = [&](int n) { return ld_raw<IO, IT, FULL>(k.Bm + p.bc + (n < last ? n : last) * k.N, p.valid); };
-    const auto loadC = [&](int n) { return ld_raw<IO, IT, FULL>(k.C + p.bc + (n < last ? n : last) * k.N, p.valid); };
+    const auto loadB = [&](int n) { return ld_raw<IO, IT, FULL>(k.Bm, p.bc + (n < last ? n : last) * k.N, p.valid); };
+    const auto loadC = [&](int n) { return ld_raw<IO, IT, FULL>(k.C, p.bc + (n < last ? n : last) * k.N, p.valid); };
 #pragma unroll
     for (int j = 0; j < AH; ++j) {
         rB[j] = loadB(j);
@@ -273,7 +296,7 @@ __device__ __forceinline__ void scan_piece(const SelK<typename io_elem<IO>::T> &
     }
     if (k.z) {
         float z[IT];
-        unpack<IO, IT>(ld_raw<IO, IT, FULL>(k.z + p.row, p.valid), z);
+        unpack<IO, IT>(ld_raw<IO, IT, FULL>(k.z, p.row, p.valid), z);
 #pragma unroll
         for (int i = 0; i < IT; ++i) o[i] *= z[i] * sigmoid(z[i]);
     }
@@ -320,15 +343,15 @@ __global__ __launch_bounds__(256, 2) void k_sel_scan(const SelK<typename io_elem
     int64_t base = 0;
     if (__all(len >= PIECE)) {  // the pieces that are full in every row of the wave
         Lane p = piece(0);
-        ru = ld_raw<IO, IT, true>(k.u + p.row, 0);
-        rd = ld_raw<IO, IT, true>(k.dt + p.row, 0);
+        ru = ld_raw<IO, IT, true>(k.u, p.row, 0);
+        rd = ld_raw<IO, IT, true>(k.dt, p.row, 0);
         bool more;
         do {
             more = __all(len >= base + 2 * PIECE);
             scan_piece<IO, LPR, WPR, true>(k, p, ru, rd, Ap, Dh, bias, st, l, live, maps, y, sv, [&] {
                 const int64_t o = more ? p.row + PIECE : p.row;
-                ru = ld_raw<IO, IT, true>(k.u + o, 0);
-                rd = ld_raw<IO, IT, true>(k.dt + o, 0);
+                ru = ld_raw<IO, IT, true>(k.u, o, 0);
+                rd = ld_raw<IO, IT, true>(k.dt, o, 0);
             });
             __builtin_amdgcn_wave_barrier();
             base += PIECE;
@@ -337,8 +360,8 @@ __global__ __launch_bounds__(256, 2) void k_sel_scan(const SelK<typename io_elem
     }
     for (; base < N; base += PIECE) {
         const Lane p = piece(base);
-        ru = ld_raw<IO, IT, false>(k.u + p.row, p.valid);
-        rd = ld_raw<IO, IT, false>(k.dt + p.row, p.valid);
+        ru = ld_raw<IO, IT, false>(k.u, p.row, p.valid);
+        rd = ld_raw<IO, IT, false>(k.dt, p.row, p.valid);
         scan_piece<IO, LPR, WPR, false>(k, p, ru, rd, Ap, Dh, bias, st, l, live, maps, y, sv, [] {});
         __builtin_amdgcn_wave_barrier();
     }
@@ -450,24 +473,25 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
         }
     // this thread's eight steps of B or C in LDS: matrix, mode, steps
     const int cm = tid >> 8, cn = (tid >> 4) & 15, ct = tid & 15;
-    const typename io_elem<IO>::T *const bc = (cm ? k.C : k.Bm) + (bg * k.S + (n0 + cn < k.S ? n0 + cn : 0)) * N + ct * 8;
+    const typename io_elem<IO>::T *const bc = cm ? k.C : k.Bm;
+    const int64_t bc0 = (bg * k.S + (n0 + cn < k.S ? n0 + cn : 0)) * N + ct * 8;
     // valid steps of a piece, and those from step `from` of it on
     const auto steps = [&](int64_t ch, int64_t end) {
         const int64_t n = end - ch * kSelChunk;
         return (int)(n < 0 ? 0 : (n < kSelChunk ? n : kSelChunk));
     };
     const auto load_bc = [&](int64_t ch) {
-        return ld_raw<IO, 8, false>(bc + ch * kSelChunk, n0 + cn < k.S ? steps(ch, len) - ct * 8 : 0);
+        return ld_raw<IO, 8, false>(bc, bc0 + ch * kSelChunk, n0 + cn < k.S ? steps(ch, len) - ct * 8 : 0);
     };
     const int tq = l * kJT + row * kQ;  // this lane's own steps within a piece
     BwdIn<IO> f;
     const auto load_in = [&](int64_t ch, int c) {
         const int64_t h = h0 + wave + kWaves * c, r = b * k.H + h, o = r * N + ch * kSelChunk;
         const int valid = steps(ch, len) - tq;
-        f.u = ld_raw<IO, kQ, false>(k.u + o + tq, valid);
-        f.p = ld_raw<IO, kQ, false>(k.dt + o + tq, valid);
-        f.gy = ld_raw<IO, kQ, false>(dy + o + tq, valid);
-        if (k.z) f.z = ld_raw<IO, kQ, false>(k.z + o + tq, valid);
+        f.u = ld_raw<IO, kQ, false>(k.u, o + tq, valid);
+        f.p = ld_raw<IO, kQ, false>(k.dt, o + tq, valid);
+        f.gy = ld_raw<IO, kQ, false>(dy, o + tq, valid);
+        if (k.z) f.z = ld_raw<IO, kQ, false>(k.z, o + tq, valid);
         const float *const Ah = k.A + h * k.S, *const xh = saved + (r * nchunk + ch) * k.S;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
