@@ -433,32 +433,63 @@ def _size(name: str, *args) -> int:
     return int(n)
 
 
-def _scratch(workspace, need: int, device) -> torch.Tensor:
+def _scratch(workspace, need: int, like) -> torch.Tensor:
     """The caller's workspace where it is large enough, else a new one."""
-    if workspace is not None and workspace.numel() * workspace.element_size() >= need:
-        return workspace
-    return torch.empty(max(need, 1), device=device, dtype=torch.uint8)
+    if workspace is not None:
+        _need(workspace, "workspace")
+        _same_device(workspace=workspace)
+        if workspace.numel() * workspace.element_size() >= need:
+            return workspace
+    return torch.empty(max(need, 1), device=like.device, dtype=torch.uint8)
 
 
-def _arg(t, name: str, dtype, shape, optional: bool = True):
-    """One tensor argument; None passes where it is optional."""
-    if t is None:
-        if not optional:
-            raise TypeError("%s is required" % name)
-        return
-    _need(t, name, dtype, shape)
+def _tensors(dev: int, *specs) -> None:
+    """Checks (name, tensor, dtype, shape) of every argument; None passes where an
+    argument is optional, its name then ends in "?".  One pass over plain
+    attributes (a token's step takes a few microseconds on the GPU); _need and
+    _same_device find the words for what is wrong."""
+    for name, t, dtype, shape in specs:
+        if t is None:
+            if name[-1] != "?":
+                raise TypeError("%s is required" % name)
+        elif not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                  and t.get_device() == dev and t.is_cuda):
+            name = name.rstrip("?")
+            _need(t, name, dtype, shape)
+            _same_device(**{name: t})
+            raise ValueError("%s is on %s, the first argument on cuda:%d" % (name, t.device, dev))
 
 
-def _conv_args(x, w, bias, dims: int):
-    _need(x, "x")
+def _device_of(t, name: str) -> int:
+    """The index of a tensor's device, which has to be the current one."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    dev = t.get_device()
+    if not t.is_cuda or dev != torch.cuda.current_device():
+        _same_device(**{name: t})
+    return dev
+
+
+def _at(t):
+    """A tensor's address, as ctypes takes it."""
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _conv_args(x, w, dims: int):
     io = _io(x, "x")
     if x.dim() != dims:
         raise ValueError("x must be %s, got %s" % ("[B,H,N]" if dims == 3 else "[B,H]", tuple(x.shape)))
     H = x.shape[1]
-    _need(w, "w", torch.float32)
+    if not isinstance(w, torch.Tensor):
+        raise TypeError("w must be a torch.Tensor")
     if w.dim() != 2 or w.shape[0] != H or w.shape[1] < 1:
         raise ValueError("w must be [H,W] with H = %d, got %s" % (H, tuple(w.shape)))
-    _arg(bias, "bias", torch.float32, (H,))
     return io, H, w.shape[1]
 
 
@@ -469,16 +500,16 @@ def short_conv(x, w, bias=None, silu: bool = True, x_in=None, lengths=None, retu
     [B,H,W-1] like x, the inputs before the row, oldest first (zeros if None);
     lengths [B] int32, valid steps of every row.  Returns y, or (y, x_out) with
     the last W-1 inputs of every row if ``return_state``."""
-    io, H, W = _conv_args(x, w, bias, 3)
-    B, N = x.shape[0], x.shape[2]
-    _arg(x_in, "x_in", x.dtype, (B, H, W - 1))
-    _arg(lengths, "lengths", torch.int32, (B,))
-    _arg(out, "out", x.dtype, (B, H, N))
-    _same_device(x=x, w=w, bias=bias, x_in=x_in, lengths=lengths, out=out)
+    dev = _device_of(x, "x")
+    io, H, W = _conv_args(x, w, 3)
+    B, _, N = x.shape
+    _tensors(dev, ("w", w, torch.float32, (H, W)), ("bias?", bias, torch.float32, (H,)),
+             ("x_in?", x_in, x.dtype, (B, H, W - 1)), ("lengths?", lengths, torch.int32, (B,)),
+             ("out?", out, x.dtype, (B, H, N)))
     y = torch.empty_like(x) if out is None else out
-    x_out = torch.empty(B, H, W - 1, device=x.device, dtype=x.dtype) if return_state else None
-    _check(load().h3conv_short_conv(_ptr(x), _ptr(w), _ptr(bias), _ptr(x_in), _ptr(lengths), _ptr(y), _ptr(x_out),
-                                    B, H, N, W, int(bool(silu)), io, _stream()),
+    x_out = torch.empty((B, H, W - 1), device=x.device, dtype=x.dtype) if return_state else None
+    _check(load().h3conv_short_conv(_at(x), _at(w), _at(bias), _at(x_in), _at(lengths), _at(y), _at(x_out), B, H, N, W,
+                                    1 if silu else 0, io, _raw_stream(dev)),
            "h3conv_short_conv")
     return (y, x_out) if return_state else y
 
@@ -488,23 +519,20 @@ def short_conv_bwd(x, w, dy, bias=None, silu: bool = True, x_in=None, lengths=No
 
     Returns (dx [B,H,N], dw [H,W] f32, dbias [H] f32, dx_in [B,H,W-1]); dbias
     is None without a bias, dx_in without an x_in."""
-    io, H, W = _conv_args(x, w, bias, 3)
-    B, N = x.shape[0], x.shape[2]
-    _arg(dy, "dy", x.dtype, (B, H, N), optional=False)
-    _arg(x_in, "x_in", x.dtype, (B, H, W - 1))
-    _arg(lengths, "lengths", torch.int32, (B,))
-    _arg(dx_out, "dx_out", x.dtype, (B, H, W - 1))
-    if workspace is not None:
-        _need(workspace, "workspace")
-    _same_device(x=x, w=w, dy=dy, bias=bias, x_in=x_in, lengths=lengths, dx_out=dx_out, workspace=workspace)
+    dev = _device_of(x, "x")
+    io, H, W = _conv_args(x, w, 3)
+    B, _, N = x.shape
+    _tensors(dev, ("w", w, torch.float32, (H, W)), ("dy", dy, x.dtype, (B, H, N)), ("bias?", bias, torch.float32, (H,)),
+             ("x_in?", x_in, x.dtype, (B, H, W - 1)), ("lengths?", lengths, torch.int32, (B,)),
+             ("dx_out?", dx_out, x.dtype, (B, H, W - 1)))
+    ws = _scratch(workspace, _size("h3conv_short_conv_bwd_workspace_size", B, H, N, W), x)
     dx = torch.empty_like(x)
     dw = torch.empty_like(w)
     dbias = torch.empty_like(bias) if bias is not None else None
     dx_in = torch.empty_like(x_in) if x_in is not None else None
-    ws = _scratch(workspace, _size("h3conv_short_conv_bwd_workspace_size", B, H, N, W), x.device)
-    _check(load().h3conv_short_conv_bwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(x_in), _ptr(lengths), _ptr(dy),
-                                        _ptr(dx_out), _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(dx_in), B, H, N, W,
-                                        int(bool(silu)), io, _ptr(ws), ws.numel() * ws.element_size(), _stream()),
+    _check(load().h3conv_short_conv_bwd(_at(x), _at(w), _at(bias), _at(x_in), _at(lengths), _at(dy), _at(dx_out),
+                                        _at(dx), _at(dw), _at(dbias), _at(dx_in), B, H, N, W, 1 if silu else 0, io,
+                                        _at(ws), ws.numel() * ws.element_size(), _raw_stream(dev)),
            "h3conv_short_conv_bwd")
     return dx, dw, dbias, dx_in
 
@@ -516,45 +544,35 @@ def short_conv_step(x, w, state, bias=None, silu: bool = True, slots=None, state
     (or into ``state_out``, of which only the slots in use are written); slots
     [B] int32, the slot of each sequence (sequence b in slot b if None).  A
     slot outside the pool marks an idle row: its output is zero.  Returns y [B,H]."""
-    io, H, W = _conv_args(x, w, bias, 2)
-    B = x.shape[0]
+    dev = _device_of(x, "x")
+    io, H, W = _conv_args(x, w, 2)
+    B, t = x.shape[0], x.dtype
     P = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() == 3 else 0
-    _arg(state, "state", x.dtype, (P, H, W - 1), optional=False)
-    _arg(state_out, "state_out", x.dtype, (P, H, W - 1))
-    _arg(slots, "slots", torch.int32, (B,))
-    _arg(out, "out", x.dtype, (B, H))
-    _same_device(x=x, w=w, bias=bias, slots=slots, state=state, state_out=state_out, out=out)
+    _tensors(dev, ("w", w, torch.float32, (H, W)), ("state", state, t, (P, H, W - 1)),
+             ("bias?", bias, torch.float32, (H,)), ("slots?", slots, torch.int32, (B,)),
+             ("state_out?", state_out, t, (P, H, W - 1)), ("out?", out, t, (B, H)))
     y = torch.empty_like(x) if out is None else out
-    to = state if state_out is None else state_out
-    _check(load().h3conv_short_conv_step(_ptr(x), _ptr(w), _ptr(bias), _ptr(slots), _ptr(state), _ptr(to), _ptr(y),
-                                         B, H, P, W, int(bool(silu)), io, _stream()),
+    _check(load().h3conv_short_conv_step(_at(x), _at(w), _at(bias), _at(slots), _at(state),
+                                         _at(state if state_out is None else state_out), _at(y), B, H, P, W,
+                                         1 if silu else 0, io, _raw_stream(dev)),
            "h3conv_short_conv_step")
     return y
 
 
-def _scan_args(u, dt, A, Bm, C, D, z, dt_bias, dims: int):
-    _need(u, "u")
+def _scan_args(u, A, Bm, dims: int):
     io = _io(u, "u")
     if u.dim() != dims:
         raise ValueError("u must be %s, got %s" % ("[B,H,N]" if dims == 3 else "[B,H]", tuple(u.shape)))
     B, H = u.shape[:2]
-    _arg(dt, "dt", u.dtype, u.shape, optional=False)
-    _need(A, "A", torch.float32)
+    for t, name in ((A, "A"), (Bm, "Bm")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % name)
     if A.dim() != 2 or A.shape[0] != H or A.shape[1] < 1:
         raise ValueError("A must be [H,S] with H = %d, got %s" % (H, tuple(A.shape)))
-    S = A.shape[1]
-    _need(Bm, "Bm", u.dtype)
     if Bm.dim() != dims + 1 or Bm.shape[1] < 1 or H % Bm.shape[1] != 0:
         raise ValueError("Bm must be %s with G dividing H = %d, got %s"
                          % ("[B,G,S,N]" if dims == 3 else "[B,G,S]", H, tuple(Bm.shape)))
-    G = Bm.shape[1]
-    bc = (B, G, S) + tuple(u.shape[2:])
-    _need(Bm, "Bm", u.dtype, bc)
-    _arg(C, "C", u.dtype, bc, optional=False)
-    _arg(D, "D", torch.float32, (H,))
-    _arg(z, "z", u.dtype, u.shape)
-    _arg(dt_bias, "dt_bias", torch.float32, (H,))
-    return io, B, H, S, G
+    return io, B, H, A.shape[1], Bm.shape[1]
 
 
 def selective_scan(u, dt, A, Bm, C, D=None, z=None, dt_bias=None, softplus: bool = True, x_in=None, lengths=None,
@@ -567,20 +585,20 @@ def selective_scan(u, dt, A, Bm, C, D=None, z=None, dt_bias=None, softplus: bool
     lengths [B] int32, valid steps of every row.  Returns y, followed by the
     final state [B,H,S] f32 if ``return_state`` and by the saved states that
     selective_scan_bwd needs if ``return_saved``."""
-    io, B, H, S, G = _scan_args(u, dt, A, Bm, C, D, z, dt_bias, 3)
-    N = u.shape[2]
-    _arg(x_in, "x_in", torch.float32, (B, H, S))
-    _arg(lengths, "lengths", torch.int32, (B,))
-    _arg(out, "out", u.dtype, (B, H, N))
-    _same_device(u=u, dt=dt, A=A, Bm=Bm, C=C, D=D, z=z, dt_bias=dt_bias, x_in=x_in, lengths=lengths, out=out)
+    dev = _device_of(u, "u")
+    io, B, H, S, G = _scan_args(u, A, Bm, 3)
+    N, t, row, bc, f32 = u.shape[2], u.dtype, u.shape, (B, G, S, u.shape[2]), torch.float32
+    _tensors(dev, ("dt", dt, t, row), ("A", A, f32, (H, S)), ("Bm", Bm, t, bc), ("C", C, t, bc), ("D?", D, f32, (H,)),
+             ("z?", z, t, row), ("dt_bias?", dt_bias, f32, (H,)), ("x_in?", x_in, f32, (B, H, S)),
+             ("lengths?", lengths, torch.int32, (B,)), ("out?", out, t, row))
     y = torch.empty_like(u) if out is None else out
-    x_out = torch.empty(B, H, S, device=u.device, dtype=torch.float32) if return_state else None
+    x_out = torch.empty((B, H, S), device=u.device, dtype=f32) if return_state else None
     saved = None
     if return_saved:
-        saved = torch.empty(_size("h3conv_selective_saved_size", B, H, N, S) // 4, device=u.device, dtype=torch.float32)
-    _check(load().h3conv_selective_scan(_ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias),
-                                        _ptr(x_in), _ptr(lengths), _ptr(y), _ptr(x_out), _ptr(saved), B, H, N, S, G,
-                                        int(bool(softplus)), io, _stream()),
+        saved = torch.empty(_size("h3conv_selective_saved_size", B, H, N, S) // 4, device=u.device, dtype=f32)
+    _check(load().h3conv_selective_scan(_at(u), _at(dt), _at(A), _at(Bm), _at(C), _at(D), _at(z), _at(dt_bias), _at(x_in),
+                                        _at(lengths), _at(y), _at(x_out), _at(saved), B, H, N, S, G,
+                                        1 if softplus else 0, io, _raw_stream(dev)),
            "h3conv_selective_scan")
     if not (return_state or return_saved):
         return y
@@ -604,27 +622,23 @@ def selective_scan_bwd(u, dt, A, Bm, C, dy, saved, D=None, z=None, dt_bias=None,
                        dx_out=None, workspace=None) -> SelectiveScanGrads:
     """Gradients of selective_scan (same arguments, ``saved`` as it returned it) for dy [B,H,N] and
     dx_out [B,H,S] f32 (upstream of the final state, or None)."""
-    io, B, H, S, G = _scan_args(u, dt, A, Bm, C, D, z, dt_bias, 3)
-    N = u.shape[2]
-    _arg(dy, "dy", u.dtype, (B, H, N), optional=False)
-    _arg(saved, "saved", torch.float32, (_size("h3conv_selective_saved_size", B, H, N, S) // 4,), optional=False)
-    _arg(lengths, "lengths", torch.int32, (B,))
-    _arg(dx_out, "dx_out", torch.float32, (B, H, S))
-    if workspace is not None:
-        _need(workspace, "workspace")
-    _same_device(u=u, dt=dt, A=A, Bm=Bm, C=C, D=D, z=z, dt_bias=dt_bias, dy=dy, saved=saved, lengths=lengths,
-                 dx_out=dx_out, workspace=workspace)
+    dev = _device_of(u, "u")
+    io, B, H, S, G = _scan_args(u, A, Bm, 3)
+    N, t, row, bc, f32 = u.shape[2], u.dtype, u.shape, (B, G, S, u.shape[2]), torch.float32
+    _tensors(dev, ("dt", dt, t, row), ("A", A, f32, (H, S)), ("Bm", Bm, t, bc), ("C", C, t, bc), ("D?", D, f32, (H,)),
+             ("z?", z, t, row), ("dt_bias?", dt_bias, f32, (H,)), ("dy", dy, t, row),
+             ("saved", saved, f32, (_size("h3conv_selective_saved_size", B, H, N, S) // 4,)),
+             ("lengths?", lengths, torch.int32, (B,)), ("dx_out?", dx_out, f32, (B, H, S)))
+    ws = _scratch(workspace, _size("h3conv_selective_scan_bwd_workspace_size", B, H, N, S, G), u)
     g = SelectiveScanGrads(
         torch.empty_like(u), torch.empty_like(dt), torch.empty_like(A), torch.empty_like(Bm), torch.empty_like(C),
         None if D is None else torch.empty_like(D), None if z is None else torch.empty_like(z),
-        None if dt_bias is None else torch.empty_like(dt_bias),
-        torch.empty(B, H, S, device=u.device, dtype=torch.float32))
-    ws = _scratch(workspace, _size("h3conv_selective_scan_bwd_workspace_size", B, H, N, S, G), u.device)
+        None if dt_bias is None else torch.empty_like(dt_bias), torch.empty((B, H, S), device=u.device, dtype=f32))
     _check(load().h3conv_selective_scan_bwd(
-        _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(lengths), _ptr(saved),
-        _ptr(dy), _ptr(dx_out), _ptr(g.du), _ptr(g.ddt), _ptr(g.dA), _ptr(g.dB), _ptr(g.dC), _ptr(g.dD), _ptr(g.dz),
-        _ptr(g.ddt_bias), _ptr(g.dx_in), B, H, N, S, G, int(bool(softplus)), io, _ptr(ws),
-        ws.numel() * ws.element_size(), _stream()),
+        _at(u), _at(dt), _at(A), _at(Bm), _at(C), _at(D), _at(z), _at(dt_bias), _at(lengths), _at(saved), _at(dy),
+        _at(dx_out), _at(g.du), _at(g.ddt), _at(g.dA), _at(g.dB), _at(g.dC), _at(g.dD), _at(g.dz), _at(g.ddt_bias),
+        _at(g.dx_in), B, H, N, S, G, 1 if softplus else 0, io, _at(ws), ws.numel() * ws.element_size(),
+        _raw_stream(dev)),
         "h3conv_selective_scan_bwd")
     return g
 
@@ -637,33 +651,34 @@ def selective_step(u, dt, A, Bm, C, x, D=None, z=None, dt_bias=None, softplus: b
     place (or into ``x_out``, of which only the slots in use are written);
     slots [B] int32, the slot of each sequence (sequence b in slot b if None).
     A slot outside the pool marks an idle row: its output is zero.  Returns y [B,H]."""
-    io, B, H, S, G = _scan_args(u, dt, A, Bm, C, D, z, dt_bias, 2)
+    dev = _device_of(u, "u")
+    io, B, H, S, G = _scan_args(u, A, Bm, 2)
     P = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 3 else 0
-    _arg(x, "x", torch.float32, (P, H, S), optional=False)
-    _arg(x_out, "x_out", torch.float32, (P, H, S))
-    _arg(slots, "slots", torch.int32, (B,))
-    _arg(out, "out", u.dtype, (B, H))
-    _same_device(u=u, dt=dt, A=A, Bm=Bm, C=C, D=D, z=z, dt_bias=dt_bias, slots=slots, x=x, x_out=x_out, out=out)
+    t, row, bc, f32 = u.dtype, u.shape, (B, G, S), torch.float32
+    _tensors(dev, ("dt", dt, t, row), ("A", A, f32, (H, S)), ("Bm", Bm, t, bc), ("C", C, t, bc), ("x", x, f32, (P, H, S)),
+             ("D?", D, f32, (H,)), ("z?", z, t, row), ("dt_bias?", dt_bias, f32, (H,)),
+             ("slots?", slots, torch.int32, (B,)), ("x_out?", x_out, f32, (P, H, S)), ("out?", out, t, row))
     y = torch.empty_like(u) if out is None else out
-    to = x if x_out is None else x_out
-    _check(load().h3conv_selective_step(_ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias),
-                                        _ptr(slots), _ptr(x), _ptr(to), _ptr(y), B, H, P, S, G, int(bool(softplus)),
-                                        io, _stream()),
+    _check(load().h3conv_selective_step(_at(u), _at(dt), _at(A), _at(Bm), _at(C), _at(D), _at(z), _at(dt_bias),
+                                        _at(slots), _at(x), _at(x if x_out is None else x_out), _at(y), B, H, P, S, G,
+                                        1 if softplus else 0, io, _raw_stream(dev)),
            "h3conv_selective_step")
     return y
 
 
 def _xent_args(x, w, labels):
-    _need(x, "x")
+    dev = _device_of(x, "x")
     io = _io(x, "x")
     if x.dim() != 2 or x.shape[1] < 1:
         raise ValueError("x must be [T,D], got %s" % (tuple(x.shape),))
     T, D = x.shape
-    _need(w, "w", x.dtype)
+    if not isinstance(w, torch.Tensor):
+        raise TypeError("w must be a torch.Tensor")
     if w.dim() != 2 or w.shape[1] != D or w.shape[0] < 1:
         raise ValueError("w must be [V,D] with D = %d, got %s" % (D, tuple(w.shape)))
-    _arg(labels, "labels", torch.int64, (T,), optional=False)
-    return io, T, D, w.shape[0]
+    V = w.shape[0]
+    _tensors(dev, ("w", w, x.dtype, (V, D)), ("labels", labels, torch.int64, (T,)))
+    return dev, io, T, D, V
 
 
 def linear_xent(x, w, labels, ignore_index: int = -100, return_lse: bool = False, workspace=None):
@@ -671,31 +686,24 @@ def linear_xent(x, w, labels, ignore_index: int = -100, return_lse: bool = False
 
     x [T,D], w [V,D] f32/f16/bf16; labels [T] int64.  Returns loss [T] f32 (0
     where the label is ignore_index or outside 0 .. V-1), or (loss, lse)."""
-    io, T, D, V = _xent_args(x, w, labels)
-    if workspace is not None:
-        _need(workspace, "workspace")
-    _same_device(x=x, w=w, labels=labels, workspace=workspace)
+    dev, io, T, D, V = _xent_args(x, w, labels)
+    ws = _scratch(workspace, _size("h3conv_linear_xent_workspace_size", T, D, V, io, 0), x)
     loss = torch.empty(T, device=x.device, dtype=torch.float32)
     lse = torch.empty(T, device=x.device, dtype=torch.float32)
-    ws = _scratch(workspace, _size("h3conv_linear_xent_workspace_size", T, D, V, io, 0), x.device)
-    _check(load().h3conv_linear_xent(_ptr(x), _ptr(w), _ptr(labels), int(ignore_index), _ptr(loss), _ptr(lse), T, D, V,
-                                     io, _ptr(ws), ws.numel() * ws.element_size(), _stream()),
+    _check(load().h3conv_linear_xent(_at(x), _at(w), _at(labels), int(ignore_index), _at(loss), _at(lse), T, D, V, io,
+                                     _at(ws), ws.numel() * ws.element_size(), _raw_stream(dev)),
            "h3conv_linear_xent")
     return (loss, lse) if return_lse else loss
 
 
 def linear_xent_bwd(x, w, labels, lse, dloss, ignore_index: int = -100, workspace=None):
     """Gradients (dx [T,D], dw [V,D], like x) of linear_xent for dloss [T] f32; lse [T] as it returned it."""
-    io, T, D, V = _xent_args(x, w, labels)
-    _arg(lse, "lse", torch.float32, (T,), optional=False)
-    _arg(dloss, "dloss", torch.float32, (T,), optional=False)
-    if workspace is not None:
-        _need(workspace, "workspace")
-    _same_device(x=x, w=w, labels=labels, lse=lse, dloss=dloss, workspace=workspace)
+    dev, io, T, D, V = _xent_args(x, w, labels)
+    _tensors(dev, ("lse", lse, torch.float32, (T,)), ("dloss", dloss, torch.float32, (T,)))
+    ws = _scratch(workspace, _size("h3conv_linear_xent_workspace_size", T, D, V, io, 1), x)
     dx, dw = torch.empty_like(x), torch.empty_like(w)
-    ws = _scratch(workspace, _size("h3conv_linear_xent_workspace_size", T, D, V, io, 1), x.device)
-    _check(load().h3conv_linear_xent_bwd(_ptr(x), _ptr(w), _ptr(labels), int(ignore_index), _ptr(lse), _ptr(dloss),
-                                         _ptr(dx), _ptr(dw), T, D, V, io, _ptr(ws), ws.numel() * ws.element_size(),
-                                         _stream()),
+    _check(load().h3conv_linear_xent_bwd(_at(x), _at(w), _at(labels), int(ignore_index), _at(lse), _at(dloss), _at(dx),
+                                         _at(dw), T, D, V, io, _at(ws), ws.numel() * ws.element_size(),
+                                         _raw_stream(dev)),
            "h3conv_linear_xent_bwd")
     return dx, dw
