@@ -40,6 +40,187 @@ __device__ __forceinline__ f4 mfma16(u4 a, u4 b, f4 c) {
     }
 }
 
+// ------------------------------------------------------- 16-bit tile products
+//
+// One block forms a BM x BN tile of A B^T, its waves WM x WN parts of it.  An
+// operand is K-contiguous (row m of A holds its k elements) or K-major (row k
+// holds the m elements; read back transposed by ds_read_b64_tr_b16).  Slabs of
+// KS elements of k go straight from memory to LDS, NS of them in a ring; the
+// fragments of the next k step are read while the matrix cores work on this
+// one, so the only wait is for a slab that was requested NS - 1 slabs earlier.
+// LDS positions are permuted in units of 16 (32) bytes on the way in, by
+// choosing the address each lane loads, so that fragment reads meet no bank
+// twice.
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s4 lds_s4;
+typedef __attribute__((address_space(3))) void lds_void;
+typedef const __attribute__((address_space(1))) void glb_void;
+
+// ROWS x KS of one operand.  mem: its element (0, 0) of the tile's rows;
+// ld: bytes per memory row.  rows: valid rows (K-contiguous) or row bytes
+// (K-major), k: valid k; what lies beyond repeats the last valid one.
+template <int ROWS, int KS, int NT, bool KMAJOR>
+struct Operand {
+    static constexpr int kBytes = ROWS * KS * 2, kLoads = kBytes / 16 / NT;
+    static constexpr int kRowChunks = KMAJOR ? ROWS / 8 : KS / 8;  // 16-byte chunks per LDS row
+    const char *mem;
+    int64_t ld, k;
+    int32_t off[kLoads];  // (the shim keeps 256 rows within 31 bits)
+
+    __device__ __forceinline__ static int slot(int krow) { return (krow & 3) | ((krow >> 3) & 1) << 2; }
+    __device__ __forceinline__ static int turn(int row) { return (row >> (KS == 32 ? 1 : 0)) & (KS / 8 - 1); }
+
+    __device__ __forceinline__ void init(const char *m, int64_t ld_, int64_t rows, int64_t k_) {
+        mem = m;
+        ld = ld_;
+        k = k_;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int q = i * NT + (int)threadIdx.x, row = q / kRowChunks, pos = q % kRowChunks;
+            if constexpr (KMAJOR) {
+                const int c = ((pos >> 1) ^ slot(row)) * 2 + (pos & 1);
+                const int64_t last = rows / 16 - 1;
+                off[i] = (int32_t)((c < last ? c : last) * 16);
+            } else {
+                const int64_t r = row < rows ? row : rows - 1;
+                off[i] = (int32_t)(r * ld + (pos ^ turn(row)) * 16);
+            }
+        }
+    }
+    // slab s into the LDS bytes at `to`
+    __device__ __forceinline__ void load(int64_t s, char *to) const {
+        const char *base = mem + s * (KMAJOR ? KS * ld : (int64_t)KS * 2);
+        const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            int32_t o = off[i];
+            if constexpr (KMAJOR) {
+                // rows past the end read the last valid one, which lies behind
+                // `base` where the whole slab is past it
+                const int row = (i * NT + (int)threadIdx.x) / kRowChunks;
+                const int64_t last = k - 1 - s * KS;
+                o += (row < last ? row : (int)last) * (int32_t)ld;
+            }
+            __builtin_amdgcn_global_load_lds((glb_void *)(base + o), (lds_void *)(to + (i * NT + wave * 64) * 16), 16, 0, 0);
+        }
+    }
+    // fragment of the 16 rows from `m`, k step s of the slab
+    __device__ __forceinline__ static u4 frag(const char *from, int m, int s) {
+        const int l = threadIdx.x & 63, g = l >> 4, i = l & 15;
+        if constexpr (KMAJOR) {
+            typedef int i2 __attribute__((ext_vector_type(2)));
+            i2 h[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int kr = s * 32 + g * 8 + q * 4 + (i >> 2);
+                const char *p = from + kr * (ROWS * 2) + (((m >> 4) ^ slot(kr)) * 32) + (i & 3) * 8;
+                h[q] = __builtin_bit_cast(i2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)p));
+            }
+            return u4{(uint32_t)h[0].x, (uint32_t)h[0].y, (uint32_t)h[1].x, (uint32_t)h[1].y};
+        } else {
+            const int row = m + i, c = s * 4 + g;
+            return *(const u4 *)(from + row * (KS * 2) + ((c ^ turn(row)) * 16));
+        }
+    }
+};
+
+template <int IO, int BM_, int BN_, int WM, int WN, int KS_, int NS, bool AK, bool BK>
+struct Tile {
+    static constexpr int BM = BM_, BN = BN_, KS = KS_, NT = WM * WN * 64, TM = BM / WM / 16, TN = BN / WN / 16;
+    using OA = Operand<BM, KS, NT, AK>;
+    using OB = Operand<BN, KS, NT, BK>;
+    static constexpr int kStage = OA::kBytes + OB::kBytes, kLds = NS * kStage, NK = KS / 32;
+    static constexpr int kLoads = OA::kLoads + OB::kLoads;
+    f4 acc[TM][TN];
+
+    __device__ __forceinline__ static int wave() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6); }
+    __device__ __forceinline__ static int row0() { return wave() / WN * (BM / WM); }
+    __device__ __forceinline__ static int col0() { return wave() % WN * (BN / WN); }
+
+    __device__ __forceinline__ static void read(const char *stage, int s, u4 (&a)[TM], u4 (&b)[TN]) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) a[i] = OA::frag(stage, row0() + i * 16, s);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) b[j] = OB::frag(stage + OA::kBytes, col0() + j * 16, s);
+    }
+    __device__ __forceinline__ void mul(const u4 (&a)[TM], const u4 (&b)[TN]) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = mfma16<IO>(a[i], b[j], acc[i][j]);
+    }
+    // Slab s + 1 has landed for every wave, and every wave has read its last
+    // fragment of slab s: its place takes slab s + NS.
+    __device__ __forceinline__ static void turn(const OA &a, const OB &b, char *lds, int64_t s, int64_t slabs) {
+        // this thread's loads of slabs s + 2 .. s + NS - 1 may still be out
+        if (s + NS - 1 < slabs) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NS - 2) * kLoads) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (s + NS < slabs) {
+            char *to = lds + (s % NS) * kStage;
+            a.load(s + NS, to);
+            b.load(s + NS, to + OA::kBytes);
+        }
+    }
+    // acc = A B^T over `slabs` slabs
+    __device__ __forceinline__ void run(const OA &a, const OB &b, int64_t slabs, char *lds) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+            if (s < slabs) {
+                a.load(s, lds + s * kStage);
+                b.load(s, lds + s * kStage + OA::kBytes);
+            }
+        // slab 0 has landed: all loads but those of the slabs after it
+        if (slabs >= NS) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 1) * kLoads) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        u4 fa[2][TM], fb[2][TN];
+        read(lds, 0, fa[0], fb[0]);
+        int64_t s = 0;
+        int st = 0;  // s % NS
+        if constexpr (NK == 2) {
+            for (; s + 1 < slabs; ++s) {
+                const int nx = st + 1 == NS ? 0 : st + 1;
+                read(lds + st * kStage, 1, fa[1], fb[1]);
+                __builtin_amdgcn_sched_barrier(0);
+                mul(fa[0], fb[0]);
+                turn(a, b, lds, s, slabs);
+                read(lds + nx * kStage, 0, fa[0], fb[0]);
+                __builtin_amdgcn_sched_barrier(0);
+                mul(fa[1], fb[1]);
+                st = nx;
+            }
+            read(lds + st * kStage, 1, fa[1], fb[1]);
+            mul(fa[0], fb[0]);
+            mul(fa[1], fb[1]);
+        } else {
+            static_assert(NK == 1, "one or two k steps per slab");
+            // two slabs per turn of the loop (slabs is even: k is padded to 64)
+            for (; s + 2 < slabs; s += 2) {
+                const int n1 = st + 1 == NS ? 0 : st + 1, n2 = n1 + 1 == NS ? 0 : n1 + 1;
+                turn(a, b, lds, s, slabs);
+                read(lds + n1 * kStage, 0, fa[1], fb[1]);
+                mul(fa[0], fb[0]);
+                turn(a, b, lds, s + 1, slabs);
+                read(lds + n2 * kStage, 0, fa[0], fb[0]);
+                mul(fa[1], fb[1]);
+                st = n2;
+            }
+            const int n1 = st + 1 == NS ? 0 : st + 1;
+            turn(a, b, lds, s, slabs);
+            read(lds + n1 * kStage, 0, fa[1], fb[1]);
+            mul(fa[0], fb[0]);
+            mul(fa[1], fb[1]);
+        }
+    }
+};
+
 constexpr int kSlab = 128;  // bytes of k per step and row: operands are padded to whole slabs
 constexpr int BM = 128, BN = 128;
 
@@ -178,27 +359,37 @@ __global__ __launch_bounds__(256) void k_xent_stats(const char *x, int64_t ldx, 
     }
 }
 
-// One thread per token joins the tiles' pairs in order.
-__global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ part, const float *__restrict__ hit,
-                                                   const Labels lab, float *__restrict__ loss,
-                                                   float *__restrict__ lse, int64_t T, int64_t tiles) {
-    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (t >= T) return;
-    float m = -INFINITY, s = 0.f;
-    for (int64_t i = 0; i < tiles; ++i) {
-        const float2 p = part[i * T + t];
-        const float n = fmaxf(m, p.x), nn = n == -INFINITY ? 0.f : n;
-        s = s * __builtin_amdgcn_exp2f((m - nn) * kLog2e) + p.y * __builtin_amdgcn_exp2f((p.x - nn) * kLog2e);
-        m = n;
+// Joins the tiles' pairs of 64 tokens per block: 16 threads per token take
+// every 16th tile, then one joins those, both in order.
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+    const float m = fmaxf(a.x, b.x), mm = m == -INFINITY ? 0.f : m;
+    return make_float2(m, a.y * __builtin_amdgcn_exp2f((a.x - mm) * kLog2e) + b.y * __builtin_amdgcn_exp2f((b.x - mm) * kLog2e));
+}
+__global__ __launch_bounds__(1024) void k_xent_join(const float2 *__restrict__ part, const float *__restrict__ hit,
+                                                    const Labels lab, float *__restrict__ loss,
+                                                    float *__restrict__ lse, int64_t T, int64_t tiles) {
+    __shared__ float2 red[16][64];
+    const int64_t t = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+    const int g = threadIdx.x >> 6;
+    float2 a = make_float2(-INFINITY, 0.f);
+    if (t < T)
+        for (int64_t i = g; i < tiles; i += 16) a = join(a, part[i * T + t]);
+    red[g][threadIdx.x & 63] = a;
+    __syncthreads();
+    if (g == 0 && t < T) {
+        for (int i = 1; i < 16; ++i) a = join(a, red[i][threadIdx.x]);
+        const float l = a.x + logf(a.y);
+        lse[t] = l;
+        loss[t] = lab.of(t) >= 0 ? l - hit[t] : 0.f;
     }
-    const float l = m + logf(s);
-    lse[t] = l;
-    loss[t] = lab.of(t) >= 0 ? l - hit[t] : 0.f;
 }
 
-// fp16 holds G as a share of the largest |dloss|, times 2^15: probabilities
-// down to 2^-29 stay normal numbers.  scale[0] is the power of two that G is
-// multiplied by, scale[1] its inverse.
+// G is held as a share of the largest |dloss| of a token that counts: with the
+// usual equal weights the entry of a label, -(1 - p), is then held almost
+// exactly, and it dominates its row.  fp16 multiplies by 2^15 more, so that
+// probabilities down to 2^-29 stay normal numbers.  scale[0]: the divisor,
+// scale[1]: what undoes both in the fp32 sums.
+template <int IO>
 __global__ __launch_bounds__(1024) void k_xent_scale(const float *__restrict__ dloss, const Labels lab,
                                                      float *__restrict__ scale, int64_t T) {
     __shared__ float red[16];
@@ -211,12 +402,15 @@ __global__ __launch_bounds__(1024) void k_xent_scale(const float *__restrict__ d
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int i = 1; i < 16; ++i) m = fmaxf(m, red[i]);
-        int e = 0;
-        if (m > 0.f && m < INFINITY) frexpf(m, &e);   // m = f 2^e, f < 1
-        e = e > 100 ? 100 : (e < -100 ? -100 : e);
-        scale[0] = ldexpf(1.f, 15 - e);
-        scale[1] = ldexpf(1.f, e - 15);
+        if (!(m > 0.f && m < INFINITY)) m = 1.f;
+        scale[0] = m;
+        scale[1] = IO == IO_F16 ? m * 0x1p-15f : m;
     }
+}
+// this token's weight in G
+template <int IO>
+__device__ __forceinline__ float weight(float dloss, float divisor) {
+    return dloss / divisor * (IO == IO_F16 ? 0x1p15f : 1.f);
 }
 
 // G of the vocabulary piece [v0, v0 + nv): g[t][v - v0] (row stride ldg
@@ -236,7 +430,7 @@ __global__ __launch_bounds__(256) void k_xent_grad(const char *x, int64_t ldx, c
     tile_product<IO>(x, ldx, T, w + v0 * ldw, ldw, nv, k, m0, n0, sA, sB, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-    const float up = IO == IO_F16 ? scale[0] : 1.f;
+    const float top = scale[0];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int64_t t = m0 + wm + i * 16 + (lane >> 4) * 4;
@@ -246,7 +440,7 @@ __global__ __launch_bounds__(256) void k_xent_grad(const char *x, int64_t ldx, c
         for (int e = 0; e < 4; ++e) {
             lb[e] = t + e < T ? lab.of(t + e) : -1;
             ls[e] = t + e < T ? lse[t + e] : 0.f;
-            dl[e] = lb[e] >= 0 ? dloss[t + e] * up : 0.f;
+            dl[e] = lb[e] >= 0 ? weight<IO>(dloss[t + e], top) : 0.f;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -278,7 +472,7 @@ __global__ __launch_bounds__(256) void k_xent_product(const char *a, int64_t lda
     tile_product<IO>(a, lda, M, bt, ldb, N, k, m0, n0, sA, sB, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-    const float down = IO == IO_F16 ? scale[1] : 1.f;
+    const float down = scale[1];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -292,6 +486,263 @@ __global__ __launch_bounds__(256) void k_xent_product(const char *a, int64_t lda
                 if (last) out[m * N + n] = from_f<IO>(v * down);
                 else accum[m * N + n] = v;
             }
+}
+
+// ------------------------------------------------------------ 16-bit kernels
+
+// Blocks go to the eight XCDs in turn; each XCD takes one stretch of the
+// tiles, so that neighbours in memory meet in its L2.
+__device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t n) {
+    const int64_t x = id & 7, per = n >> 3, more = n & 7;
+    return x * per + (x < more ? x : more) + (id >> 3);
+}
+// Tile `id` of rows x cols tiles: groups of four rows go through all columns.
+__device__ __forceinline__ void tile_of(int64_t id, int64_t rows, int64_t cols, int64_t &r, int64_t &c) {
+    const int64_t g = id / (4 * cols), left = rows - 4 * g, h = left < 4 ? left : 4, k = id - 4 * g * cols;
+    c = k / h;
+    r = 4 * g + k - c * h;
+}
+
+template <int IO>
+using LogitTile = Tile<IO, 256, 256, 2, 4, 64, 2, false, false>;
+template <int IO, bool G_KMAJOR>
+using GradTile = Tile<IO, 256, 256, 2, 4, 64, 2, true, G_KMAJOR>;
+template <int IO>
+constexpr int kGradThreads = GradTile<IO, false>::NT;
+
+// As k_xent_stats with w's rows as the tile's rows and tokens as its columns:
+// a lane holds four consecutive rows of w for a token.
+template <int IO>
+__global__ __launch_bounds__(LogitTile<IO>::NT, 1) void k_xent_stats16(const char *x, const char *w, int64_t ld,
+                                                                       const Labels lab, float2 *__restrict__ part,
+                                                                       float *__restrict__ hit, int64_t T, int64_t V) {
+    using L = LogitTile<IO>;
+    __shared__ __align__(16) char lds[L::kLds];
+    const int64_t rows = (V + L::BM - 1) / L::BM, cols = (T + L::BN - 1) / L::BN;
+    int64_t rt, ct;
+    tile_of(xcd_order(blockIdx.x, rows * cols), rows, cols, rt, ct);
+    const int64_t v0 = rt * L::BM, t0 = ct * L::BN;
+    typename L::OA a;
+    typename L::OB b;
+    a.init(w + v0 * ld, ld, V - v0, 0);
+    b.init(x + t0 * ld, ld, T - t0, 0);
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    int lr[L::TN];  // the labels' rows in this tile, or -1; loaded ahead of the products
+#pragma unroll
+    for (int j = 0; j < L::TN; ++j) {
+        const int64_t t = t0 + L::col0() + j * 16 + (lane & 15), lb = (t < T ? lab.of(t) : -1) - v0;
+        lr[j] = lb >= 0 && lb < L::BM ? (int)lb : -1;
+        asm volatile("" : "+v"(lr[j]));
+    }
+    L tile;
+    tile.run(a, b, ld / 2 / L::KS, lds);
+    __syncthreads();
+    float2(*const red)[L::BN] = (float2(*)[L::BN])lds;  // [wave row][token]
+    const bool whole = v0 + L::BM <= V;
+#pragma unroll
+    for (int j = 0; j < L::TN; ++j) {
+        const int col = L::col0() + j * 16 + (lane & 15);
+        float m = -INFINITY, s = 0.f;
+#pragma unroll
+        for (int i = 0; i < L::TM; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = L::row0() + i * 16 + g * 4 + e;
+                if (!whole && v0 + row >= V) tile.acc[i][j][e] = -INFINITY;
+                m = fmaxf(m, tile.acc[i][j][e]);
+            }
+        if (__any(lr[j] >= 0)) {
+            float found = 0.f;
+#pragma unroll
+            for (int i = 0; i < L::TM; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (L::row0() + i * 16 + g * 4 + e == lr[j]) found = tile.acc[i][j][e];
+            if (lr[j] >= L::row0() && lr[j] < L::row0() + L::TM * 16 && (lr[j] >> 2 & 3) == g) hit[t0 + col] = found;
+        }
+        m = fmaxf(m, __shfl_xor(m, 16));
+        m = fmaxf(m, __shfl_xor(m, 32));
+        const float mm = m == -INFINITY ? 0.f : m * kLog2e;
+#pragma unroll
+        for (int i = 0; i < L::TM; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f(fmaf(tile.acc[i][j][e], kLog2e, -mm));
+        s += __shfl_xor(s, 16);
+        s += __shfl_xor(s, 32);
+        if (g == 0) red[L::row0() / (L::TM * 16)][col] = make_float2(m, s);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < L::BN; c += L::NT) {
+        float2 q = red[0][c];
+#pragma unroll
+        for (int r = 1; r < L::BM / (L::TM * 16); ++r) q = join(q, red[r][c]);
+        if (t0 + c < T) part[rt * T + t0 + c] = q;
+    }
+}
+
+// G of the vocabulary piece [v0, v0 + nv): g[t][v - v0], rows of ldg elements;
+// zero for nv <= v - v0 < ldg and for T <= t < Tp.
+template <int IO>
+__global__ __launch_bounds__(LogitTile<IO>::NT, 1) void k_xent_grad16(const char *x, const char *w, int64_t ld,
+                                                                      const Labels lab, const float *__restrict__ lse,
+                                                                      const float *__restrict__ dloss,
+                                                                      const float *__restrict__ scale,
+                                                                      typename io_elem<IO>::T *__restrict__ gout,
+                                                                      int64_t ldg, int64_t T, int64_t Tp, int64_t v0,
+                                                                      int64_t nv) {
+    using L = LogitTile<IO>;
+    using E = typename io_elem<IO>::T;
+    __shared__ __align__(16) char lds[L::kLds];
+    const int64_t rows = (nv + L::BM - 1) / L::BM, cols = (T + L::BN - 1) / L::BN;
+    int64_t rt, ct;
+    tile_of(xcd_order(blockIdx.x, rows * cols), rows, cols, rt, ct);
+    const int64_t r0 = rt * L::BM, t0 = ct * L::BN;
+    typename L::OA a;
+    typename L::OB b;
+    a.init(w + (v0 + r0) * ld, ld, nv - r0, 0);
+    b.init(x + t0 * ld, ld, T - t0, 0);
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    const float top = scale[0];
+    const bool whole = r0 + L::BM <= nv;
+    // of this lane's tokens, loaded ahead of the products: the label's row in
+    // the tile (or -1), the log-sum, the weight (0 where the token does not count)
+    int lr[L::TN];
+    float ls[L::TN], dl[L::TN];
+    bool on[L::TN];
+#pragma unroll
+    for (int j = 0; j < L::TN; ++j) {
+        const int64_t t = t0 + L::col0() + j * 16 + (lane & 15), label = t < T ? lab.of(t) : -1, lb = label - v0 - r0;
+        on[j] = label >= 0;
+        lr[j] = lb >= 0 && lb < L::BM ? (int)lb : -1;
+        ls[j] = t < T ? lse[t] * kLog2e : 0.f;
+        dl[j] = on[j] ? weight<IO>(dloss[t], top) : 0.f;
+        asm volatile("" : "+v"(lr[j]), "+v"(ls[j]), "+v"(dl[j]));
+    }
+    L tile;
+    tile.run(a, b, ld / 2 / L::KS, lds);
+#pragma unroll
+    for (int j = 0; j < L::TN; ++j) {
+        const int64_t t = t0 + L::col0() + j * 16 + (lane & 15);
+        const bool any = __any(lr[j] >= 0);
+#pragma unroll
+        for (int i = 0; i < L::TM; ++i) {
+            const int row = L::row0() + i * 16 + g * 4;
+            float q[4];
+            Pack<E, 4> o;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q[e] = __builtin_amdgcn_exp2f(fmaf(tile.acc[i][j][e], kLog2e, -ls[j]));
+            if (any) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (row + e == lr[j]) q[e] -= 1.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                q[e] = on[j] ? q[e] * dl[j] : 0.f;
+                if (!whole && r0 + row + e >= nv) q[e] = 0.f;
+                o.v[e] = from_f<IO>(q[e]);
+            }
+            if (t < Tp && r0 + row < ldg) *reinterpret_cast<Pack<E, 4> *>(gout + t * ldg + r0 + row) = o;
+        }
+    }
+}
+
+// dx and dw of a piece in one launch: blocks 0 .. ndx-1 form dx[t][d] +=
+// sum_v G[t][v] w[v][d], the others dw[v][d] = sum_t G[t][v] x[t][d].  The
+// tile's rows are d (so that a lane stores four consecutive values), its
+// columns t or v.  dx has few tiles where D is small: the piece's v are cut
+// into `splits` ranges of kx, each with a sum of its own in accum over all
+// pieces; without a cut and with one piece dx is stored at once.
+template <int IO>
+__global__ __launch_bounds__(kGradThreads<IO>, 1) void k_xent_products16(
+    const char *x, const char *w, int64_t ld, const char *g, int64_t ldg, typename io_elem<IO>::T *__restrict__ dx,
+    typename io_elem<IO>::T *__restrict__ dw, float *__restrict__ accum, const float *__restrict__ scale, int64_t T,
+    int64_t Tp, int64_t D, int64_t nv, int64_t kv, int64_t kx, int splits, int64_t ndx, int first, int whole) {
+    using E = typename io_elem<IO>::T;
+    using PX = GradTile<IO, false>;
+    using PW = GradTile<IO, true>;
+    __shared__ __align__(16) char lds[PX::kLds];
+    const int64_t rows = (D + PX::BM - 1) / PX::BM;
+    const int lane = threadIdx.x & 63;
+    const float down = scale[1];
+    int64_t rt, ct;
+    if ((int64_t)blockIdx.x < ndx) {
+        const int64_t cols = ndx / rows / splits, id = xcd_order(blockIdx.x, ndx), part = id / (rows * cols);
+        tile_of(id - part * rows * cols, rows, cols, rt, ct);
+        const int64_t d0 = rt * PX::BM, t0 = ct * PX::BN, k0 = part * kx, kn = kv - k0 < kx ? kv - k0 : kx;
+        typename PX::OA a;
+        typename PX::OB b;
+        a.init(w + k0 * ld + d0 * 2, ld, ld - d0 * 2, nv - k0);
+        b.init(g + t0 * ldg * 2 + k0 * 2, ldg * 2, T - t0, 0);
+        PX tile;
+        tile.run(a, b, kn / PX::KS, lds);
+        float *const sum = accum + part * T * D;
+#pragma unroll
+        for (int i = 0; i < PX::TM; ++i)
+#pragma unroll
+            for (int j = 0; j < PX::TN; ++j) {
+                const int64_t d = d0 + PX::row0() + i * 16 + (lane >> 4) * 4;
+                const int64_t t = t0 + PX::col0() + j * 16 + (lane & 15);
+                if (t >= T || d >= D) continue;
+                float q[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) q[e] = tile.acc[i][j][e];
+                if (whole) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) q[e] *= down;
+                    st_row<IO, 4>(dx + t * D + d, q, D - d);
+                    continue;
+                }
+                if (!first) {
+                    float o[4];
+                    ld_row<IO_F32, 4>(sum + t * D + d, o, D - d);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) q[e] += o[e];
+                }
+                st_row<IO_F32, 4>(sum + t * D + d, q, D - d);
+            }
+    } else {
+        const int64_t n = (int64_t)gridDim.x - ndx, cols = n / rows;
+        tile_of(xcd_order(blockIdx.x - ndx, n), rows, cols, rt, ct);
+        const int64_t d0 = rt * PW::BM, c0 = ct * PW::BN;
+        typename PW::OA a;
+        typename PW::OB b;
+        a.init(x + d0 * 2, ld, ld - d0 * 2, T);
+        b.init(g + c0 * 2, ldg * 2, (ldg - c0) * 2, Tp);
+        PW tile;
+        tile.run(a, b, Tp / PW::KS, lds);
+#pragma unroll
+        for (int i = 0; i < PW::TM; ++i)
+#pragma unroll
+            for (int j = 0; j < PW::TN; ++j) {
+                const int64_t d = d0 + PW::row0() + i * 16 + (lane >> 4) * 4;
+                const int64_t v = c0 + PW::col0() + j * 16 + (lane & 15);
+                if (v >= nv || d >= D) continue;
+                float q[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) q[e] = tile.acc[i][j][e] * down;
+                st_row<IO, 4>(dw + v * D + d, q, D - d);
+            }
+    }
+}
+
+// dx from the sums of its ranges, in order; n values each.
+template <int IO>
+__global__ __launch_bounds__(256) void k_xent_dx(const float *__restrict__ accum, const float *__restrict__ scale,
+                                                 typename io_elem<IO>::T *__restrict__ dx, int64_t n, int splits) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    float s[4];
+    ld_row<IO_F32, 4>(accum + i, s, n - i);
+    for (int k = 1; k < splits; ++k) {
+        float o[4];
+        ld_row<IO_F32, 4>(accum + k * n + i, o, n - i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += o[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] *= scale[1];
+    st_row<IO, 4>(dx + i, s, n - i);
 }
 
 // dst[r][c] = src[r][c] for c < C, zero up to ldd.
@@ -327,17 +778,40 @@ int64_t ceil_to(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
 struct Plan {
     int64_t kD;            // elements of a padded row of x and w
-    int64_t Tp;            // elements of a padded row of x^T and G^T
-    int64_t piece, pieces; // vocabulary rows per piece (a multiple of BN)
+    int64_t Tp;            // padded tokens: rows of G (16-bit), columns of x^T and G^T (fp32)
+    int64_t piece, pieces; // vocabulary rows per piece
+    int64_t tiles;         // pairs per token of the forward pass
+    int64_t range, ranges; // vocabulary rows whose part of dx is summed apart, such parts of a piece (16-bit)
     char *xp, *wp, *xt, *wt, *g, *gt;
     float *accum, *scale, *hit;
     float2 *part;
     size_t bytes;
 };
 
+// The time of a first-come schedule on the chip's 256 compute units of n tiles
+// of length a, then m of length b.
+int64_t makespan(int64_t n, int64_t a, int64_t m, int64_t b) {
+    constexpr int kUnits = 256;
+    const int64_t full = n / kUnits, more = n % kUnits;  // `more` units finish one a later
+    int64_t early = full * a, late = more ? early + a : early, ne = kUnits - more, nl = more;
+    while (m > 0) {  // whole rows of equal units at a time
+        if (ne > 0 && (nl == 0 || early <= late)) {
+            if (m < ne) return early + b > late ? early + b : late;
+            m -= ne;
+            early += b;
+        } else {
+            if (m < nl) return late + b > early ? late + b : early;
+            m -= nl;
+            late += b;
+        }
+    }
+    return early > late ? early : late;
+}
+
 Plan plan(int64_t T, int64_t D, int64_t V, int io, bool bwd, char *base) {
     Plan p = {};
-    const int64_t e = io == IO_F32 ? 4 : 2, slab = kSlab / e;
+    const bool wide = io == IO_F32;
+    const int64_t e = wide ? 4 : 2, slab = kSlab / e, rows = wide ? BN : LogitTile<IO_F16>::BM;
     p.kD = ceil_to(D, slab);
     p.Tp = ceil_to(T, slab);
     size_t at = 0;
@@ -348,21 +822,39 @@ Plan plan(int64_t T, int64_t D, int64_t V, int io, bool bwd, char *base) {
     };
     p.xp = take(p.kD != D ? T * p.kD * e : 0);
     p.wp = take(p.kD != D ? V * p.kD * e : 0);
+    p.tiles = (V + rows - 1) / rows;
     if (!bwd) {
-        p.part = (float2 *)take((V + BN - 1) / BN * T * 8);
+        p.part = (float2 *)take(p.tiles * T * 8);
         p.hit = (float *)take(T * 4);
     } else {
-        // G and G^T of a piece: up to 256 MiB each
-        int64_t most = ((int64_t)256 << 20) / (p.Tp * e) / BN * BN;
-        if (most < BN) most = BN;
+        // G of a piece (fp32: and G^T): up to 512 MiB
+        int64_t most = ((int64_t)512 << 20) / (p.Tp * e) / rows * rows;
+        if (most > (int64_t)1 << 21) most = (int64_t)1 << 21;  // (256 rows of G within 31 bits)
+        if (most < rows) most = rows;
         const int64_t n = (V + most - 1) / most;
-        p.piece = ceil_to((V + n - 1) / n, BN);
+        p.piece = ceil_to((V + n - 1) / n, rows);
         p.pieces = (V + p.piece - 1) / p.piece;
-        p.xt = take(D * p.Tp * e);
-        p.wt = take(D * p.piece * e);
-        p.g = take(T * p.piece * e);
-        p.gt = take(p.piece * p.Tp * e);
-        p.accum = (float *)take(p.pieces > 1 ? T * D * 4 : 0);
+        p.xt = take(wide ? D * p.Tp * e : 0);
+        p.wt = take(wide ? D * p.piece * e : 0);
+        p.g = take(p.Tp * p.piece * e);
+        p.gt = take(wide ? p.piece * p.Tp * e : 0);
+        // the number of ranges that fills the chip best with a piece's tiles
+        // (one more range: one more sum to write and read)
+        int64_t splits = 1;
+        if (!wide) {
+            using G = GradTile<IO_F16, false>;
+            const int64_t rows_d = (D + G::BM - 1) / G::BM, ndx = rows_d * ((T + G::BN - 1) / G::BN);
+            const int64_t ndw = rows_d * ((p.piece + G::BN - 1) / G::BN), kv = ceil_to(p.piece, 64) / 64;
+            int64_t best = makespan(ndx, kv, ndw, p.Tp / 64);
+            for (int64_t k = 2; k <= 8 && k * 8 <= kv; ++k) {
+                const int64_t m = makespan(ndx * k, (kv + k - 1) / k, ndw, p.Tp / 64);
+                if (m * 20 < best * 19) best = m, splits = k;
+            }
+        }
+        const int64_t k0 = ceil_to(V < p.piece ? V : p.piece, 64);  // the longest piece's
+        p.range = ceil_to((k0 + splits - 1) / splits, 64);
+        p.ranges = (k0 + p.range - 1) / p.range;
+        p.accum = (float *)take(p.pieces > 1 || p.ranges > 1 ? p.ranges * T * D * 4 : 0);
         p.scale = (float *)take(8);
     }
     p.bytes = at;
@@ -389,12 +881,17 @@ hipError_t fwd_io(const void *x, const void *w, const Labels &lab, float *loss, 
     const char *xr, *wr;
     hipError_t e = padded<IO>(x, p.xp, T, D, p.kD, &xr, s);
     if (e == hipSuccess) e = padded<IO>(w, p.wp, V, D, p.kD, &wr, s);
-    if (e == hipSuccess)
+    if (e != hipSuccess) return e;
+    if constexpr (IO == IO_F32) {
         e = launch(k_xent_stats<IO>, dim3(blocks(T, BM), blocks(V, BN)), dim3(256), 0, s, xr, ld, wr, ld, lab, p.part,
                    p.hit, T, V, ld);
+    } else {
+        using L = LogitTile<IO>;
+        e = launch(k_xent_stats16<IO>, dim3(blocks(V, L::BM) * blocks(T, L::BN)), dim3(L::NT), 0, s, xr, wr, ld,
+                   lab, p.part, p.hit, T, V);
+    }
     if (e != hipSuccess) return e;
-    return launch(k_xent_join, dim3(blocks(T, 256)), dim3(256), 0, s, p.part, p.hit, lab, loss, lse, T,
-                  (int64_t)blocks(V, BN));
+    return launch(k_xent_join, dim3(blocks(T, 64)), dim3(1024), 0, s, p.part, p.hit, lab, loss, lse, T, p.tiles);
 }
 
 template <int IO>
@@ -408,24 +905,45 @@ hipError_t bwd_io(const void *x, const void *w, const Labels &lab, const float *
     const char *xr, *wr;
     hipError_t e = padded<IO>(x, p.xp, T, D, p.kD, &xr, s);
     if (e == hipSuccess) e = padded<IO>(w, p.wp, V, D, p.kD, &wr, s);
-    if (e == hipSuccess && IO == IO_F16) e = launch(k_xent_scale, dim3(1), dim3(1024), 0, s, dloss, lab, p.scale, T);
-    if (e == hipSuccess)
-        e = launch(k_xent_transpose<E>, dim3(blocks(p.Tp, 64), blocks(D, 64)), dim3(256), 0, s, (const E *)x,
-                   (E *)p.xt, T, D, p.Tp);
+    if (e == hipSuccess) e = launch(k_xent_scale<IO>, dim3(1), dim3(1024), 0, s, dloss, lab, p.scale, T);
+    if constexpr (IO == IO_F32) {
+        if (e == hipSuccess)
+            e = launch(k_xent_transpose<E>, dim3(blocks(p.Tp, 64), blocks(D, 64)), dim3(256), 0, s, (const E *)x,
+                       (E *)p.xt, T, D, p.Tp);
+    }
     for (int64_t i = 0; i < p.pieces && e == hipSuccess; ++i) {
-        const int64_t v0 = i * p.piece, nv = V - v0 < p.piece ? V - v0 : p.piece, kv = ceil_to(nv, BN);
+        const int64_t v0 = i * p.piece, nv = V - v0 < p.piece ? V - v0 : p.piece;
         const int first = i == 0, last = i + 1 == p.pieces;
-        e = launch(k_xent_transpose<E>, dim3(blocks(kv, 64), blocks(D, 64)), dim3(256), 0, s,
-                   (const E *)w + v0 * D, (E *)p.wt, nv, D, kv);
-        if (e != hipSuccess) break;
-        e = launch(k_xent_grad<IO>, dim3(blocks(T, BM), blocks(nv, BN)), dim3(256), 0, s, xr, ld, wr, ld, lab, lse,
-                   dloss, p.scale, (E *)p.g, kv, (E *)p.gt, p.Tp, T, v0, nv, ld);
-        if (e != hipSuccess) break;
-        e = launch(k_xent_product<IO>, dim3(blocks(nv, BM), blocks(D, BN)), dim3(256), 0, s, p.gt, p.Tp * es, nv,
-                   p.xt, p.Tp * es, D, p.Tp * es, (E *)dw + v0 * D, (float *)nullptr, 1, 1, p.scale);
-        if (e != hipSuccess) break;
-        e = launch(k_xent_product<IO>, dim3(blocks(T, BM), blocks(D, BN)), dim3(256), 0, s, p.g, kv * es, T, p.wt,
-                   kv * es, D, kv * es, (E *)dx, p.accum, first, last, p.scale);
+        if constexpr (IO == IO_F32) {
+            const int64_t kv = ceil_to(nv, BN);
+            e = launch(k_xent_transpose<E>, dim3(blocks(kv, 64), blocks(D, 64)), dim3(256), 0, s,
+                       (const E *)w + v0 * D, (E *)p.wt, nv, D, kv);
+            if (e != hipSuccess) break;
+            e = launch(k_xent_grad<IO>, dim3(blocks(T, BM), blocks(nv, BN)), dim3(256), 0, s, xr, ld, wr, ld, lab,
+                       lse, dloss, p.scale, (E *)p.g, kv, (E *)p.gt, p.Tp, T, v0, nv, ld);
+            if (e != hipSuccess) break;
+            e = launch(k_xent_product<IO>, dim3(blocks(nv, BM), blocks(D, BN)), dim3(256), 0, s, p.gt, p.Tp * es, nv,
+                       p.xt, p.Tp * es, D, p.Tp * es, (E *)dw + v0 * D, (float *)nullptr, 1, 1, p.scale);
+            if (e != hipSuccess) break;
+            e = launch(k_xent_product<IO>, dim3(blocks(T, BM), blocks(D, BN)), dim3(256), 0, s, p.g, kv * es, T, p.wt,
+                       kv * es, D, kv * es, (E *)dx, p.accum, first, last, p.scale);
+        } else {
+            using L = LogitTile<IO>;
+            using G = GradTile<IO, false>;
+            const int64_t kv = ceil_to(nv, 64);
+            e = launch(k_xent_grad16<IO>, dim3(blocks(nv, L::BM) * blocks(T, L::BN)), dim3(L::NT), 0, s, xr, wr,
+                       ld, lab, lse, dloss, p.scale, (E *)p.g, kv, T, p.Tp, v0, nv);
+            if (e != hipSuccess) break;
+            // ranges of whole slabs, as long as the first piece's (a shorter last piece has fewer)
+            const int64_t kx = p.range, parts = (kv + kx - 1) / kx;
+            const int64_t rows = blocks(D, G::BM), ndx = rows * blocks(T, G::BN) * parts, ndw = rows * blocks(nv, G::BN);
+            e = launch(k_xent_products16<IO>, dim3((unsigned)(ndx + ndw)), dim3(G::NT), 0, s, xr, wr + v0 * ld, ld, p.g,
+                       kv, (E *)dx, (E *)dw + v0 * D, p.accum, p.scale, T, p.Tp, D, nv, kv, kx, (int)parts, ndx, first,
+                       p.accum ? 0 : 1);
+            if (e == hipSuccess && last && p.accum)
+                e = launch(k_xent_dx<IO>, dim3(blocks(T * D, 1024)), dim3(256), 0, s, p.accum, p.scale, (E *)dx, T * D,
+                           (int)p.ranges);
+        }
     }
     return e;
 }

@@ -143,3 +143,9 @@ def test_xent_refusals():
         pkg.linear_xent_bwd(x, w, labels, dloss, dloss[:3].contiguous())
     with pytest.raises(TypeError):
         pkg.linear_xent_bwd(x, w, labels, None, dloss)
+
+
+@pytest.mark.parametrize("T,D,V", [(512, 64, 9000), (300, 40, 4545), (130, 128, 12300)])
+def test_gradient_ranges(T, D, V):
+    """dx of few tokens and few columns over many rows: summed over ranges of the vocabulary."""
+    _check("bf16", *_make("bf16", T, D, V, 21))
