@@ -86,7 +86,9 @@ bool scan_sizes_ok(int64_t B, int64_t H, int64_t N, int64_t S, int64_t G) {
 }
 bool xent_sizes_ok(int64_t T, int64_t D, int64_t V) {
     return T <= ((int64_t)1 << 30) && D <= ((int64_t)1 << 20) && V <= ((int64_t)1 << 22) &&
-           product_ok({T, D}, kElems) && product_ok({V, D}, kElems);
+           product_ok({T, D}, kElems) && product_ok({V, D}, kElems) &&
+           product_ok({T / 64 + 1, V / 64 + 1}, (int64_t)1 << 31) &&                       // tiles of one dispatch
+           product_ok({(T > V ? T : V) / 64 + 2, D / 64 + 1}, (int64_t)1 << 27);
 }
 
 }  // namespace

@@ -15,7 +15,7 @@ namespace h3c {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTaps = 4;  // taps and halo are held for the largest W; missing taps are zero
+constexpr int kTaps = 4;  // the largest W
 
 // Threads of a block along one row (a power of two), the others take rows.
 __host__ __device__ inline int threads_per_row(int64_t nvec) {
@@ -32,64 +32,70 @@ __device__ __forceinline__ int64_t row_len(const int32_t *lengths, int64_t b, in
 
 // x at position p of a row that starts at p = -(W-1), the first W-1 from the
 // saved inputs
-template <int IO>
+template <int IO, int W>
 __device__ __forceinline__ float at_ext(const typename io_elem<IO>::T *x, const typename io_elem<IO>::T *xin,
-                                        int64_t p, int W) {
+                                        int64_t p) {
     if (p >= 0) return to_f<IO>(x[p]);
-    return (xin && p >= -(int64_t)(W - 1)) ? to_f<IO>(xin[p + W - 1]) : 0.f;
+    return (xin && p >= -(W - 1)) ? to_f<IO>(xin[p + W - 1]) : 0.f;
 }
 
-__device__ __forceinline__ void load_taps(const float *w, int64_t h, int W, float (&tap)[kTaps]) {
+// The W - 1 elements of x before step t0, oldest first; what lies at or past
+// `len` is zero.
+template <int IO, int W>
+__device__ __forceinline__ void before(const typename io_elem<IO>::T *x, const typename io_elem<IO>::T *xin, int64_t t0,
+                                       int64_t len, float *v) {
+    if constexpr (W > 1) {
+        if (t0 > 0) {  // (t0 is a multiple of the vector: at least four elements come before it)
+            float near[4];
+            ld_row<IO, 4>(x + t0 - 4, near, len - t0 + 4);
 #pragma unroll
-    for (int i = 0; i < kTaps; ++i) tap[i] = i < W ? w[h * W + i] : 0.f;
+            for (int j = 0; j < W - 1; ++j) v[j] = near[j + 5 - W];
+        } else {
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) v[j] = at_ext<IO, W>(x, xin, j - (W - 1));
+        }
+    }
 }
 
-template <int IO>
+// A count of steps as a small int: at most V matter.
+__device__ __forceinline__ int few(int64_t n) { return (int)(n < 0 ? 0 : (n > 64 ? 64 : n)); }
+
+template <int IO, int W>
 __global__ __launch_bounds__(kThreads) void k_short_conv(const typename io_elem<IO>::T *__restrict__ x,
                                                          const typename io_elem<IO>::T *__restrict__ x_in,
                                                          const float *__restrict__ w, const float *__restrict__ bias,
                                                          const int32_t *__restrict__ lengths,
                                                          typename io_elem<IO>::T *__restrict__ y,
                                                          typename io_elem<IO>::T *__restrict__ x_out, int64_t B,
-                                                         int64_t H, int64_t N, int W, int silu, int tpr) {
+                                                         int64_t H, int64_t N, int silu, int tpr) {
     using T = typename io_elem<IO>::T;
     constexpr int V = 16 / (int)sizeof(T);
-    const int64_t r = (int64_t)blockIdx.x * (kThreads / tpr) + threadIdx.x / tpr;
-    if (r >= B * H) return;
-    const int64_t b = r / H, h = r - b * H;
-    const int64_t len = row_len(lengths, b, N);
+    const uint32_t row = blockIdx.x * (uint32_t)(kThreads / tpr) + threadIdx.x / (uint32_t)tpr;
+    if (row >= (uint32_t)(B * H)) return;
+    const uint32_t b = row / (uint32_t)H, h = row - b * (uint32_t)H;
+    const int64_t r = row, len = row_len(lengths, b, N);
     const T *xr = x + r * N, *xi = x_in ? x_in + r * (W - 1) : nullptr;
     const int tl = (int)threadIdx.x % tpr;
-    float tap[kTaps];
-    load_taps(w, h, W, tap);
+    float tap[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) tap[k] = w[(int64_t)h * W + k];
     const float bs = bias ? bias[h] : 0.f;
     if (x_out && blockIdx.y == 0)
-        for (int j = tl; j < W - 1; j += tpr) x_out[r * (W - 1) + j] = from_f<IO>(at_ext<IO>(xr, xi, len - (W - 1) + j, W));
+        for (int j = tl; j < W - 1; j += tpr) x_out[r * (W - 1) + j] = from_f<IO>(at_ext<IO, W>(xr, xi, len - (W - 1) + j));
     for (int64_t t0 = ((int64_t)blockIdx.y * tpr + tl) * V; t0 < N; t0 += (int64_t)gridDim.y * tpr * V) {
-        float v[V + kTaps - 1], o[V];
-        {
-            float cur[V];
-            ld_row<IO, V>(xr + t0, cur, len - t0);
+        float v[V + W - 1], cur[V], o[V];
+        ld_row<IO, V>(xr + t0, cur, len - t0);
+        before<IO, W>(xr, xi, t0, len, v);
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i + kTaps - 1] = cur[i];
-        }
-        if (t0 >= V && t0 < len) {
-            float pre[V];
-            ld_row<IO, V>(xr + t0 - V, pre);
-#pragma unroll
-            for (int i = 0; i < kTaps - 1; ++i) v[i] = pre[V - (kTaps - 1) + i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < kTaps - 1; ++i) v[i] = t0 < len ? at_ext<IO>(xr, xi, t0 - (kTaps - 1) + i, W) : 0.f;
-        }
+        for (int i = 0; i < V; ++i) v[i + W - 1] = cur[i];
+        const int valid = few(len - t0);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float p = bs;
 #pragma unroll
-            for (int k = 0; k < kTaps; ++k)
-                if (k < W) p = fmaf(tap[k], v[i + kTaps - 1 - k], p);
+            for (int k = 0; k < W; ++k) p = fmaf(tap[k], v[i + W - 1 - k], p);
             if (silu) p *= sigmoid(p);
-            o[i] = t0 + i < len ? p : 0.f;
+            o[i] = i < valid ? p : 0.f;
         }
         st_row<IO, V>(y + r * N + t0, o, N - t0);
     }
@@ -99,75 +105,101 @@ __global__ __launch_bounds__(kThreads) void k_short_conv(const typename io_elem<
 __device__ __forceinline__ float act_bwd(float p, float dy, int silu) {
     if (!silu) return dy;
     const float s = sigmoid(p);
-    return dy * s * (1.f + p * (1.f - s));
+    return dy * fmaf(p * s, 1.f - s, s);
 }
 
 // Backward pass of one channel: block (h, k) takes the tasks k, k + K, ... of
 // the channel's B rows cut into pieces, so the sums over batch and time stay
 // in one block's registers and are joined in a fixed order:
 //   dx_s = sum_i w_i dp_{s+i},  dw_i = sum_{b,t} dp_t x_{t-i},  dbias = sum dp.
-template <int IO>
+// A thread forms dp of its own steps and of the W - 1 after them.
+template <int IO, int W>
 __global__ __launch_bounds__(kThreads) void k_short_conv_bwd(
     const typename io_elem<IO>::T *__restrict__ x, const typename io_elem<IO>::T *__restrict__ x_in,
     const float *__restrict__ w, const float *__restrict__ bias, const int32_t *__restrict__ lengths,
     const typename io_elem<IO>::T *__restrict__ dy, const typename io_elem<IO>::T *__restrict__ dx_out,
     typename io_elem<IO>::T *__restrict__ dx, typename io_elem<IO>::T *__restrict__ dx_in, float *__restrict__ part,
-    int64_t B, int64_t H, int64_t N, int W, int silu, int tpr, int64_t pieces) {
+    float *__restrict__ dw, float *__restrict__ dbias, int64_t B, int64_t H, int64_t N, int silu, int tpr,
+    int64_t pieces) {
     using T = typename io_elem<IO>::T;
-    constexpr int V = 16 / (int)sizeof(T), E = V + kTaps - 1;
+    constexpr int V = 16 / (int)sizeof(T), E = V + W - 1;
     const int64_t h = blockIdx.x;
-    const int rpb = kThreads / tpr, tl = (int)threadIdx.x % tpr;
-    float tap[kTaps];
-    load_taps(w, h, W, tap);
+    const int rpb = kThreads / tpr, tl = (int)threadIdx.x % tpr, sub = (int)threadIdx.x / tpr;
+    float tap[W], sw[W], sb = 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        tap[k] = w[h * W + k];
+        sw[k] = 0.f;
+    }
     const float bs = bias ? bias[h] : 0.f;
-    float sw[kTaps] = {0.f, 0.f, 0.f, 0.f}, sb = 0.f;
     const int64_t tasks = (B + rpb - 1) / rpb * pieces;
     for (int64_t task = blockIdx.y; task < tasks; task += gridDim.y) {
-        const int64_t b = task / pieces * rpb + threadIdx.x / tpr, t0 = (task % pieces * tpr + tl) * V;
+        const int64_t bg = task / pieces, b = bg * rpb + sub, t0 = ((task - bg * pieces) * tpr + tl) * V;
         if (b >= B || (t0 >= N && t0 > 0)) continue;  // (step 0 of an empty row: dx_in alone)
         const int64_t r = b * H + h, len = row_len(lengths, b, N);
         const T *xr = x + r * N, *xi = x_in ? x_in + r * (W - 1) : nullptr, *gr = dy + r * N;
-        // v[j]: x at t0 - (kTaps-1) + j, for the steps t0 .. t0 + V + kTaps - 2
-        float v[E + kTaps - 1], g[E], dp[E], o[V];
+        // v[j]: x at t0 - (W-1) + j, g[j]: dy at t0 + j; the neighbours'
+        // elements come from the caches
+        float v[E + W - 1], g[E], dp[E], o[V];
+        {
+            float cur[V], gc[V], near[4], gn[4];
+            ld_row<IO, V>(xr + t0, cur, len - t0);
+            ld_row<IO, V>(gr + t0, gc, len - t0);
+            if constexpr (W > 1) {
+                ld_row<IO, 4>(xr + t0 + V, near, len - t0 - V);
+                ld_row<IO, 4>(gr + t0 + V, gn, len - t0 - V);
+            }
+            before<IO, W>(xr, xi, t0, len, v);
 #pragma unroll
-        for (int j = 0; j < E + kTaps - 1; ++j) {
-            const int64_t p = t0 - (kTaps - 1) + j;
-            v[j] = p < len ? at_ext<IO>(xr, xi, p, W) : 0.f;
+            for (int j = 0; j < V; ++j) {
+                v[j + W - 1] = cur[j];
+                g[j] = gc[j];
+            }
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) {
+                v[j + V + W - 1] = near[j];
+                g[j + V] = gn[j];
+            }
         }
-#pragma unroll
-        for (int j = 0; j < E; ++j) g[j] = t0 + j < len ? to_f<IO>(gr[t0 + j]) : 0.f;
+        const int valid = few(len - t0);
 #pragma unroll
         for (int j = 0; j < E; ++j) {
             float p = bs;
 #pragma unroll
-            for (int k = 0; k < kTaps; ++k)
-                if (k < W) p = fmaf(tap[k], v[j + kTaps - 1 - k], p);
-            dp[j] = t0 + j < len ? act_bwd(p, g[j], silu) : 0.f;
+            for (int k = 0; k < W; ++k) p = fmaf(tap[k], v[j + W - 1 - k], p);
+            dp[j] = j < valid ? act_bwd(p, g[j], silu) : 0.f;
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             float a = 0.f;
 #pragma unroll
-            for (int k = 0; k < kTaps; ++k)
-                if (k < W) a = fmaf(tap[k], dp[j + k], a);
-            // the saved last inputs are inputs len-(W-1) .. len-1
-            const int64_t q = t0 + j - (len - (W - 1));
-            if (dx_out && q >= 0 && q < W - 1) a += to_f<IO>(dx_out[r * (W - 1) + q]);
-            o[j] = t0 + j < len ? a : 0.f;
+            for (int k = 0; k < W; ++k) a = fmaf(tap[k], dp[j + k], a);
+            o[j] = a;
             sb += dp[j];
 #pragma unroll
-            for (int k = 0; k < kTaps; ++k) sw[k] = fmaf(dp[j], v[j + kTaps - 1 - k], sw[k]);
+            for (int k = 0; k < W; ++k) sw[k] = fmaf(dp[j], v[j + W - 1 - k], sw[k]);
         }
+        // the saved last inputs are inputs len-(W-1) .. len-1
+        if (dx_out && valid < V + W) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int q = j - (valid - (W - 1));
+                if (q >= 0 && q < W - 1) o[j] += to_f<IO>(dx_out[r * (W - 1) + q]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j >= valid) o[j] = 0.f;
         st_row<IO, V>(dx + r * N + t0, o, N - t0);
         if (dx_in && t0 == 0) {
             // saved input j stands at position j - (W-1): it meets the steps
             // 0 .. j through the taps W-1-j .. W-1; with len < W-1 it is also
             // kept as the saved input j - len of the next piece
+#pragma unroll
             for (int j = 0; j < W - 1; ++j) {
                 float a = 0.f;
 #pragma unroll
-                for (int k = 0; k < kTaps - 1; ++k)
-                    if (k <= j && W - 1 - j + k < W) a = fmaf(w[h * W + W - 1 - j + k], dp[k], a);
+                for (int k = 0; k <= j; ++k) a = fmaf(tap[W - 1 - j + k], dp[k], a);
                 if (dx_out && j >= len) a += to_f<IO>(dx_out[r * (W - 1) + j - len]);
                 dx_in[r * (W - 1) + j] = from_f<IO>(a);
             }
@@ -176,17 +208,20 @@ __global__ __launch_bounds__(kThreads) void k_short_conv_bwd(
     // joined over the block in a fixed order
     __shared__ float red[kTaps + 1][kThreads / 64];
 #pragma unroll
-    for (int k = 0; k <= kTaps; ++k) {
-        float s = k < kTaps ? sw[k] : sb;
+    for (int k = 0; k <= W; ++k) {
+        float s = k < W ? sw[k < W ? k : 0] : sb;
 #pragma unroll
         for (int m = 32; m >= 1; m >>= 1) s += __shfl_xor(s, m);
         if ((threadIdx.x & 63) == 0) red[k][threadIdx.x >> 6] = s;
     }
     __syncthreads();
-    if (threadIdx.x <= kTaps) {
+    if (threadIdx.x <= W) {
         float s = 0.f;
         for (int i = 0; i < kThreads / 64; ++i) s += red[threadIdx.x][i];
-        part[((int64_t)blockIdx.y * H + h) * (kTaps + 1) + threadIdx.x] = s;
+        const int k = threadIdx.x;
+        if (gridDim.y > 1) part[((int64_t)blockIdx.y * H + h) * (kTaps + 1) + k] = s;
+        else if (k < W) dw[h * W + k] = s;
+        else if (dbias) dbias[h] = s;
     }
 }
 
@@ -195,11 +230,11 @@ __global__ void k_short_conv_sums(const float *__restrict__ part, float *__restr
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int64_t h = i / (kTaps + 1);
     const int k = (int)(i - h * (kTaps + 1));
-    if (h >= H) return;
+    if (h >= H || k > W) return;
     float s = 0.f;
     for (int j = 0; j < K; ++j) s += part[((int64_t)j * H + h) * (kTaps + 1) + k];
     if (k < W) dw[h * W + k] = s;
-    else if (k == kTaps && dbias) dbias[h] = s;
+    else if (dbias) dbias[h] = s;
 }
 
 // One token per sequence: the saved inputs of slot slots[b] move on by one.
@@ -257,8 +292,8 @@ size_t short_conv_bwd_workspace(int64_t B, int64_t H, int64_t N, int W) {
     return (size_t)(k16 > k32 ? k16 : k32) * (size_t)H * (kTaps + 1) * 4;
 }
 
-template <int IO>
-static hipError_t short_conv_io(const ShortConvArgs &a, void *y, void *x_out, hipStream_t s) {
+template <int IO, int W>
+static hipError_t short_conv_taps(const ShortConvArgs &a, void *y, void *x_out, hipStream_t s) {
     using T = typename io_elem<IO>::T;
     constexpr int V = 16 / (int)sizeof(T);
     const int64_t nvec = (a.N + V - 1) / V, R = a.B * a.H;
@@ -266,8 +301,19 @@ static hipError_t short_conv_io(const ShortConvArgs &a, void *y, void *x_out, hi
     const int64_t rows = (R + kThreads / tpr - 1) / (kThreads / tpr);
     int64_t gy = (nvec + tpr - 1) / tpr;
     gy = gy < 1 ? 1 : (gy > 4096 ? 4096 : gy);
-    return launch(k_short_conv<IO>, dim3((unsigned)rows, (unsigned)gy), dim3(kThreads), 0, s, (const T *)a.x,
-                  (const T *)a.x_in, a.w, a.bias, a.lengths, (T *)y, (T *)x_out, a.B, a.H, a.N, a.W, a.silu, tpr);
+    return launch(k_short_conv<IO, W>, dim3((unsigned)rows, (unsigned)gy), dim3(kThreads), 0, s, (const T *)a.x,
+                  (const T *)a.x_in, a.w, a.bias, a.lengths, (T *)y, (T *)x_out, a.B, a.H, a.N, a.silu, tpr);
+}
+
+template <int IO>
+static hipError_t short_conv_io(const ShortConvArgs &a, void *y, void *x_out, hipStream_t s) {
+    switch (a.W) {
+        case 1: return short_conv_taps<IO, 1>(a, y, x_out, s);
+        case 2: return short_conv_taps<IO, 2>(a, y, x_out, s);
+        case 3: return short_conv_taps<IO, 3>(a, y, x_out, s);
+        case 4: return short_conv_taps<IO, 4>(a, y, x_out, s);
+        default: return hipErrorInvalidValue;
+    }
 }
 
 hipError_t launch_short_conv(const ShortConvArgs &a, void *y, void *x_out, int io, hipStream_t s) {
@@ -279,19 +325,32 @@ hipError_t launch_short_conv(const ShortConvArgs &a, void *y, void *x_out, int i
     }
 }
 
-template <int IO>
-static hipError_t short_conv_bwd_io(const ShortConvArgs &a, const void *dy, const void *dx_out, void *dx, float *dw,
-                                    float *dbias, void *dx_in, float *part, hipStream_t s) {
+template <int IO, int W>
+static hipError_t short_conv_bwd_taps(const ShortConvArgs &a, const void *dy, const void *dx_out, void *dx, float *dw,
+                                      float *dbias, void *dx_in, float *part, hipStream_t s) {
     using T = typename io_elem<IO>::T;
     int64_t pieces;
     int tpr;
     const int K = bwd_splits(a.B, a.H, a.N, &pieces, &tpr, 16 / (int)sizeof(T));
-    hipError_t e = launch(k_short_conv_bwd<IO>, dim3((unsigned)a.H, (unsigned)K), dim3(kThreads), 0, s,
-                          (const T *)a.x, (const T *)a.x_in, a.w, a.bias, a.lengths, (const T *)dy, (const T *)dx_out,
-                          (T *)dx, (T *)dx_in, part, a.B, a.H, a.N, a.W, a.silu, tpr, pieces);
-    if (e != hipSuccess) return e;
+    const hipError_t e = launch(k_short_conv_bwd<IO, W>, dim3((unsigned)a.H, (unsigned)K), dim3(kThreads), 0, s,
+                                (const T *)a.x, (const T *)a.x_in, a.w, a.bias, a.lengths, (const T *)dy,
+                                (const T *)dx_out, (T *)dx, (T *)dx_in, part, dw, dbias, a.B, a.H, a.N, a.silu, tpr,
+                                pieces);
+    if (e != hipSuccess || K == 1) return e;
     return launch(k_short_conv_sums, dim3((unsigned)((a.H * (kTaps + 1) + 255) / 256)), dim3(256), 0, s, part, dw,
-                  dbias, a.H, a.W, K);
+                  dbias, a.H, W, K);
+}
+
+template <int IO>
+static hipError_t short_conv_bwd_io(const ShortConvArgs &a, const void *dy, const void *dx_out, void *dx, float *dw,
+                                    float *dbias, void *dx_in, float *part, hipStream_t s) {
+    switch (a.W) {
+        case 1: return short_conv_bwd_taps<IO, 1>(a, dy, dx_out, dx, dw, dbias, dx_in, part, s);
+        case 2: return short_conv_bwd_taps<IO, 2>(a, dy, dx_out, dx, dw, dbias, dx_in, part, s);
+        case 3: return short_conv_bwd_taps<IO, 3>(a, dy, dx_out, dx, dw, dbias, dx_in, part, s);
+        case 4: return short_conv_bwd_taps<IO, 4>(a, dy, dx_out, dx, dw, dbias, dx_in, part, s);
+        default: return hipErrorInvalidValue;
+    }
 }
 
 hipError_t launch_short_conv_bwd(const ShortConvArgs &a, const void *dy, const void *dx_out, void *dx, float *dw,

@@ -221,69 +221,84 @@ struct Tile {
     }
 };
 
-constexpr int kSlab = 128;  // bytes of k per step and row: operands are padded to whole slabs
-constexpr int BM = 128, BN = 128;
+// ------------------------------------------------------------ fp32 tile products
+//
+// 64 x 64 tiles on the fp32 matrix cores (a sixteenth of the 16-bit rate, so
+// LDS and caches keep up with small tiles, and small problems fill the chip).
+// Rows may start at any element and have any length: operands are loaded
+// through registers, what lies past the end is zero.
+constexpr int BM = 64, BN = 64, KS32 = 32;
 
-// acc[i][j] of this wave's 64 x 64 part of the tile (m0, n0) of A B^T; A has
-// M rows of lda bytes, B has N rows of ldb bytes, k bytes each (k a multiple
-// of kSlab).  Rows past the end read the last row; their results are dropped
-// by the epilogue.
-template <int IO>
-__device__ __forceinline__ void tile_product(const char *A, int64_t lda, int64_t M, const char *Bt, int64_t ldb,
-                                             int64_t N, int64_t k, int64_t m0, int64_t n0, u4 (&sA)[BM * 8],
-                                             u4 (&sB)[BN * 8], f4 (&acc)[4][4]) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-    const char *pa[4], *pb[4];
-    int at[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int id = tid + i * 256, row = id >> 3, c = id & 7;
-        int64_t ra = m0 + row, rb = n0 + row;
-        ra = ra < M ? ra : M - 1;
-        rb = rb < N ? rb : N - 1;
-        pa[i] = A + ra * lda + c * 16;
-        pb[i] = Bt + rb * ldb + c * 16;
-        at[i] = row * 8 + (c ^ (row & 7));
+// An operand of a tile: K-contiguous (rows of the tile are memory rows) or
+// K-major (memory rows are k).  ld: elements per memory row.
+template <bool KMAJOR>
+struct Operand32 {
+    const float *mem;
+    int64_t ld, rows, k;  // rows: of the operand, from the tile's first; k: valid k
+
+    // chunk `id` (of 512) of the slab from k0: four k of a row, or four rows at one k
+    __device__ __forceinline__ f4 load(int64_t k0, int id) const {
+        const int64_t r = KMAJOR ? k0 + (id >> 4) : id >> 3, c = KMAJOR ? (id & 15) * 4 : k0 + (id & 7) * 4;
+        const int64_t left = (KMAJOR ? rows : k) - c;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (r < (KMAJOR ? k : rows)) ld_row<IO_F32, 4>(mem + r * ld + c, v, left);
+        return f4{v[0], v[1], v[2], v[3]};
     }
+    // where element (row, k) of the slab is kept: fragment reads (16 rows, one
+    // chunk of four k) and transposed writes both spread over the banks
+    __device__ __forceinline__ static int at(int row, int chunk) { return row * 8 + (chunk ^ ((row ^ row >> 2) & 7)); }
+    __device__ __forceinline__ static void keep(f4 *s, int id, f4 v) {
+        if constexpr (KMAJOR) {
+            const int kr = id >> 4, m = (id & 15) * 4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
-    u4 ga[4], gb[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        ga[i] = *(const u4 *)pa[i];
-        gb[i] = *(const u4 *)pb[i];
+            for (int j = 0; j < 4; ++j) ((float *)&s[at(m + j, kr >> 2)])[kr & 3] = v[j];
+        } else {
+            s[at(id >> 3, id & 7)] = v;
+        }
     }
-    for (int64_t kk = 0; kk < k; kk += kSlab) {
+};
+
+// acc[i][j] of this wave's 32 x 32 part of A B^T over k elements.
+template <bool AK, bool BK>
+__device__ __forceinline__ void product32(const Operand32<AK> &a, const Operand32<BK> &b, int64_t k, f4 *sA, f4 *sB,
+                                          f4 (&acc)[2][2]) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
+    f4 ga[2], gb[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+        ga[i] = a.load(0, tid + i * 256);
+        gb[i] = b.load(0, tid + i * 256);
+    }
+    for (int64_t k0 = 0; k0 < k; k0 += KS32) {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            sA[at[i]] = ga[i];
-            sB[at[i]] = gb[i];
+        for (int i = 0; i < 2; ++i) {
+            a.keep(sA, tid + i * 256, ga[i]);
+            b.keep(sB, tid + i * 256, gb[i]);
         }
         __syncthreads();
-        if (kk + kSlab < k) {
+        if (k0 + KS32 < k) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                ga[i] = *(const u4 *)(pa[i] + kk + kSlab);
-                gb[i] = *(const u4 *)(pb[i] + kk + kSlab);
+            for (int i = 0; i < 2; ++i) {
+                ga[i] = a.load(k0 + KS32, tid + i * 256);
+                gb[i] = b.load(k0 + KS32, tid + i * 256);
             }
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            u4 fa[4], fb[4];
+            u4 fa[2], fb[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int ra = wm + i * 16 + (lane & 15), rb = wn + i * 16 + (lane & 15), c = s * 4 + (lane >> 4);
-                fa[i] = sA[ra * 8 + (c ^ (ra & 7))];
-                fb[i] = sB[rb * 8 + (c ^ (rb & 7))];
+            for (int i = 0; i < 2; ++i) {
+                const int c = s * 4 + (lane >> 4);
+                fa[i] = __builtin_bit_cast(u4, sA[Operand32<AK>::at(wm + i * 16 + (lane & 15), c)]);
+                fb[i] = __builtin_bit_cast(u4, sB[Operand32<BK>::at(wn + i * 16 + (lane & 15), c)]);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = mfma16<IO>(fa[i], fb[j], acc[i][j]);
+                for (int j = 0; j < 2; ++j) acc[i][j] = mfma16<IO_F32>(fa[i], fb[j], acc[i][j]);
         }
     }
 }
@@ -298,29 +313,30 @@ struct Labels {
     }
 };
 
-// Per row of the tile: (maximum, sum of e^{l - maximum}) over the tile's
-// columns to part[tile][t], and the label's logit where it is one of them.
-template <int IO>
-__global__ __launch_bounds__(256) void k_xent_stats(const char *x, int64_t ldx, const char *w, int64_t ldw,
-                                                    const Labels lab, float2 *__restrict__ part,
-                                                    float *__restrict__ hit, int64_t T, int64_t V, int64_t k) {
-    __shared__ u4 sA[BM * 8], sB[BN * 8];
+__device__ __forceinline__ float2 join(float2 a, float2 b);
+
+// Per token of the tile (its rows): (maximum, sum of e^{l - maximum}) over the
+// tile's columns to part[tile][t], and the label's logit where it is one of them.
+__global__ __launch_bounds__(256) void k_xent_stats32(const float *x, const float *w, const Labels lab,
+                                                      float2 *__restrict__ part, float *__restrict__ hit, int64_t T,
+                                                      int64_t D, int64_t V) {
+    __shared__ f4 sA[BM * 8], sB[BN * 8];
     __shared__ float2 half[BM];
-    f4 acc[4][4];
-    const int64_t m0 = (int64_t)blockIdx.x * BM, n0 = (int64_t)blockIdx.y * BN;
-    tile_product<IO>(x, ldx, T, w, ldw, V, k, m0, n0, sA, sB, acc);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-    float2 st[4][4];
+    f4 acc[2][2];
+    const int64_t tiles = (T + BM - 1) / BM, tile = blockIdx.x / tiles;  // of the vocabulary; tokens run first
+    const int64_t m0 = (blockIdx.x - tile * tiles) * BM, n0 = tile * BN;
+    product32(Operand32<false>{x + m0 * D, D, T - m0, D}, Operand32<false>{w + n0 * D, D, V - n0, D}, D, sA, sB, acc);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
+    float2 st[2][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int64_t t = m0 + wm + i * 16 + (lane >> 4) * 4 + e;
             const int64_t l = t < T ? lab.of(t) : -1;
             float m = -INFINITY, s = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2; ++j) {
                 const int64_t v = n0 + wn + j * 16 + (lane & 15);
                 if (v < V) m = fmaxf(m, acc[i][j][e]);
                 if (v < V && v == l) hit[t] = acc[i][j][e];
@@ -329,32 +345,21 @@ __global__ __launch_bounds__(256) void k_xent_stats(const char *x, int64_t ldx, 
             for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
             const float mm = m == -INFINITY ? 0.f : m;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t v = n0 + wn + j * 16 + (lane & 15);
-                if (v < V) s += __builtin_amdgcn_exp2f((acc[i][j][e] - mm) * kLog2e);
-            }
+            for (int j = 0; j < 2; ++j)
+                if (n0 + wn + j * 16 + (lane & 15) < V) s += __builtin_amdgcn_exp2f((acc[i][j][e] - mm) * kLog2e);
 #pragma unroll
             for (int d = 1; d < 16; d <<= 1) s += __shfl_xor(s, d);
             st[i][e] = make_float2(m, s);
+            if ((wave & 1) && (lane & 15) == 0) half[wm + i * 16 + (lane >> 4) * 4 + e] = st[i][e];
         }
-    if ((wave & 1) && (lane & 15) == 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) half[wm + i * 16 + (lane >> 4) * 4 + e] = st[i][e];
-    }
     __syncthreads();
     if (!(wave & 1) && (lane & 15) == 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int row = wm + i * 16 + (lane >> 4) * 4 + e;
-                const float2 o = half[row], q = st[i][e];
-                const float m = fmaxf(o.x, q.x), mm = m == -INFINITY ? 0.f : m;
-                const float s = o.y * __builtin_amdgcn_exp2f((o.x - mm) * kLog2e) +
-                                q.y * __builtin_amdgcn_exp2f((q.x - mm) * kLog2e);
-                if (m0 + row < T) part[(int64_t)blockIdx.y * T + m0 + row] = make_float2(m, s);
+                if (m0 + row < T) part[tile * T + m0 + row] = join(st[i][e], half[row]);
             }
     }
 }
@@ -413,78 +418,66 @@ __device__ __forceinline__ float weight(float dloss, float divisor) {
     return dloss / divisor * (IO == IO_F16 ? 0x1p15f : 1.f);
 }
 
-// G of the vocabulary piece [v0, v0 + nv): g[t][v - v0] (row stride ldg
-// elements) and its transpose gt[v - v0][t] (row stride ldt >= T, the columns
-// past T zero); columns past the piece's end are zero up to ldg.
-template <int IO>
-__global__ __launch_bounds__(256) void k_xent_grad(const char *x, int64_t ldx, const char *w, int64_t ldw,
-                                                   const Labels lab, const float *__restrict__ lse,
-                                                   const float *__restrict__ dloss, const float *__restrict__ scale,
-                                                   typename io_elem<IO>::T *__restrict__ g, int64_t ldg,
-                                                   typename io_elem<IO>::T *__restrict__ gt, int64_t ldt, int64_t T,
-                                                   int64_t v0, int64_t nv, int64_t k) {
-    using E = typename io_elem<IO>::T;
-    __shared__ u4 sA[BM * 8], sB[BN * 8];
-    f4 acc[4][4];
-    const int64_t m0 = (int64_t)blockIdx.x * BM, n0 = (int64_t)blockIdx.y * BN;
-    tile_product<IO>(x, ldx, T, w + v0 * ldw, ldw, nv, k, m0, n0, sA, sB, acc);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+// G of the vocabulary piece [v0, v0 + nv): g[t][v - v0], rows of nv.
+__global__ __launch_bounds__(256) void k_xent_grad32(const float *x, const float *w, const Labels lab,
+                                                     const float *__restrict__ lse, const float *__restrict__ dloss,
+                                                     const float *__restrict__ scale, float *__restrict__ g, int64_t T,
+                                                     int64_t D, int64_t v0, int64_t nv) {
+    __shared__ f4 sA[BM * 8], sB[BN * 8];
+    f4 acc[2][2];
+    const int64_t tiles = (T + BM - 1) / BM, tile = blockIdx.x / tiles;  // of the vocabulary; tokens run first
+    const int64_t m0 = (blockIdx.x - tile * tiles) * BM, n0 = tile * BN;
+    product32(Operand32<false>{x + m0 * D, D, T - m0, D}, Operand32<false>{w + (v0 + n0) * D, D, nv - n0, D}, D, sA, sB,
+              acc);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
     const float top = scale[0];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t t = m0 + wm + i * 16 + (lane >> 4) * 4;
-        float ls[4], dl[4];
-        int64_t lb[4];
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            lb[e] = t + e < T ? lab.of(t + e) : -1;
-            ls[e] = t + e < T ? lse[t + e] : 0.f;
-            dl[e] = lb[e] >= 0 ? weight<IO>(dloss[t + e], top) : 0.f;
-        }
+            const int64_t t = m0 + wm + i * 16 + (lane >> 4) * 4 + e;
+            if (t >= T) continue;
+            const int64_t l = lab.of(t);
+            const float ls = lse[t], dl = l >= 0 ? weight<IO_F32>(dloss[t], top) : 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t c = n0 + wn + j * 16 + (lane & 15);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float q = __builtin_amdgcn_exp2f((acc[i][j][e] - ls[e]) * kLog2e);
-                if (v0 + c == lb[e]) q -= 1.f;
-                q = (c < nv && lb[e] >= 0) ? q * dl[e] : 0.f;
-                const E o = from_f<IO>(q);
-                if (t + e < T && c < ldg) g[(t + e) * ldg + c] = o;
-                if (t + e < ldt && c < ldg) gt[c * ldt + t + e] = o;
+            for (int j = 0; j < 2; ++j) {
+                const int64_t c = n0 + wn + j * 16 + (lane & 15);
+                float q = __builtin_amdgcn_exp2f((acc[i][j][e] - ls) * kLog2e);
+                if (v0 + c == l) q -= 1.f;
+                if (c < nv) g[t * nv + c] = l >= 0 ? q * dl : 0.f;
             }
         }
-    }
 }
 
-// out = A B^T times scale, added to acc (fp32, row stride D) where there is
-// an earlier piece; to acc where a later one follows, else rounded to out.
-template <int IO>
-__global__ __launch_bounds__(256) void k_xent_product(const char *a, int64_t lda, int64_t M, const char *bt,
-                                                      int64_t ldb, int64_t N, int64_t k,
-                                                      typename io_elem<IO>::T *__restrict__ out,
-                                                      float *__restrict__ accum, int first, int last,
-                                                      const float *__restrict__ scale) {
-    __shared__ u4 sA[BM * 8], sB[BN * 8];
-    f4 acc[4][4];
-    const int64_t m0 = (int64_t)blockIdx.x * BM, n0 = (int64_t)blockIdx.y * BN;
-    tile_product<IO>(a, lda, M, bt, ldb, N, k, m0, n0, sA, sB, acc);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+// dx and dw of a piece in one launch, tiles of 64 x 64: first those of
+// dx[t][d] += sum_v G[t][v] w[v][d], then those of dw[v][d] = sum_t G[t][v] x[t][d].
+__global__ __launch_bounds__(256) void k_xent_products32(const float *x, const float *w, const float *g,
+                                                         float *__restrict__ dx, float *__restrict__ dw,
+                                                         const float *__restrict__ scale, int64_t T, int64_t D,
+                                                         int64_t nv, int64_t ndx, int first) {
+    __shared__ f4 sA[BM * 8], sB[BN * 8];
+    f4 acc[2][2];
+    const int64_t cols = (D + BN - 1) / BN;
+    const bool is_dx = (int64_t)blockIdx.x < ndx;
+    const int64_t id = is_dx ? blockIdx.x : blockIdx.x - ndx, m0 = id / cols * BM, n0 = id % cols * BN;
+    if (is_dx)
+        product32(Operand32<false>{g + m0 * nv, nv, T - m0, nv}, Operand32<true>{w + n0, D, D - n0, nv}, nv, sA, sB, acc);
+    else
+        product32(Operand32<true>{g + m0, nv, nv - m0, T}, Operand32<true>{x + n0, D, D - n0, T}, T, sA, sB, acc);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
     const float down = scale[1];
+    const int64_t M = is_dx ? T : nv;
+    float *const out = is_dx ? dx : dw;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int64_t m = m0 + wm + i * 16 + (lane >> 4) * 4 + e, n = n0 + wn + j * 16 + (lane & 15);
-                if (m >= M || n >= N) continue;
-                float v = acc[i][j][e];
-                if (!first) v += accum[m * N + n];
-                if (last) out[m * N + n] = from_f<IO>(v * down);
-                else accum[m * N + n] = v;
+                if (m >= M || n >= D) continue;
+                const float q = acc[i][j][e] * down;
+                out[m * D + n] = is_dx && !first ? out[m * D + n] + q : q;
             }
 }
 
@@ -658,7 +651,6 @@ __global__ __launch_bounds__(kGradThreads<IO>, 1) void k_xent_products16(
     const char *x, const char *w, int64_t ld, const char *g, int64_t ldg, typename io_elem<IO>::T *__restrict__ dx,
     typename io_elem<IO>::T *__restrict__ dw, float *__restrict__ accum, const float *__restrict__ scale, int64_t T,
     int64_t Tp, int64_t D, int64_t nv, int64_t kv, int64_t kx, int splits, int64_t ndx, int first, int whole) {
-    using E = typename io_elem<IO>::T;
     using PX = GradTile<IO, false>;
     using PW = GradTile<IO, true>;
     __shared__ __align__(16) char lds[PX::kLds];
@@ -753,20 +745,6 @@ __global__ __launch_bounds__(256) void k_xent_pad(const E *__restrict__ src, E *
     if (r < R) dst[i] = c < C ? src[r * C + c] : (E)0;
 }
 
-// dst[c][r] = src[r][c], zero for R <= r < ldd.
-template <class E>
-__global__ __launch_bounds__(256) void k_xent_transpose(const E *__restrict__ src, E *__restrict__ dst, int64_t R,
-                                                        int64_t C, int64_t ldd) {
-    __shared__ E tile[64][65];
-    const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
-    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-    for (int i = y; i < 64; i += 4)
-        tile[i][x] = (r0 + i < R && c0 + x < C) ? src[(r0 + i) * C + c0 + x] : (E)0;
-    __syncthreads();
-    for (int i = y; i < 64; i += 4)
-        if (c0 + i < C && r0 + x < ldd) dst[(c0 + i) * ldd + r0 + x] = tile[x][i];
-}
-
 template <class E>
 __global__ __launch_bounds__(256) void k_xent_zero(E *__restrict__ p, int64_t n) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -778,11 +756,11 @@ int64_t ceil_to(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
 struct Plan {
     int64_t kD;            // elements of a padded row of x and w
-    int64_t Tp;            // padded tokens: rows of G (16-bit), columns of x^T and G^T (fp32)
+    int64_t Tp;            // tokens, padded (16-bit): rows of G
     int64_t piece, pieces; // vocabulary rows per piece
     int64_t tiles;         // pairs per token of the forward pass
     int64_t range, ranges; // vocabulary rows whose part of dx is summed apart, such parts of a piece (16-bit)
-    char *xp, *wp, *xt, *wt, *g, *gt;
+    char *xp, *wp, *g;
     float *accum, *scale, *hit;
     float2 *part;
     size_t bytes;
@@ -811,7 +789,7 @@ int64_t makespan(int64_t n, int64_t a, int64_t m, int64_t b) {
 Plan plan(int64_t T, int64_t D, int64_t V, int io, bool bwd, char *base) {
     Plan p = {};
     const bool wide = io == IO_F32;
-    const int64_t e = wide ? 4 : 2, slab = kSlab / e, rows = wide ? BN : LogitTile<IO_F16>::BM;
+    const int64_t e = wide ? 4 : 2, slab = wide ? 1 : LogitTile<IO_F16>::KS, rows = wide ? BN : LogitTile<IO_F16>::BM;
     p.kD = ceil_to(D, slab);
     p.Tp = ceil_to(T, slab);
     size_t at = 0;
@@ -827,17 +805,14 @@ Plan plan(int64_t T, int64_t D, int64_t V, int io, bool bwd, char *base) {
         p.part = (float2 *)take(p.tiles * T * 8);
         p.hit = (float *)take(T * 4);
     } else {
-        // G of a piece (fp32: and G^T): up to 512 MiB
+        // G of a piece: up to 512 MiB
         int64_t most = ((int64_t)512 << 20) / (p.Tp * e) / rows * rows;
         if (most > (int64_t)1 << 21) most = (int64_t)1 << 21;  // (256 rows of G within 31 bits)
         if (most < rows) most = rows;
         const int64_t n = (V + most - 1) / most;
         p.piece = ceil_to((V + n - 1) / n, rows);
         p.pieces = (V + p.piece - 1) / p.piece;
-        p.xt = take(wide ? D * p.Tp * e : 0);
-        p.wt = take(wide ? D * p.piece * e : 0);
         p.g = take(p.Tp * p.piece * e);
-        p.gt = take(wide ? p.piece * p.Tp * e : 0);
         // the number of ranges that fills the chip best with a piece's tiles
         // (one more range: one more sum to write and read)
         int64_t splits = 1;
@@ -854,7 +829,7 @@ Plan plan(int64_t T, int64_t D, int64_t V, int io, bool bwd, char *base) {
         const int64_t k0 = ceil_to(V < p.piece ? V : p.piece, 64);  // the longest piece's
         p.range = ceil_to((k0 + splits - 1) / splits, 64);
         p.ranges = (k0 + p.range - 1) / p.range;
-        p.accum = (float *)take(p.pieces > 1 || p.ranges > 1 ? p.ranges * T * D * 4 : 0);
+        p.accum = (float *)take(!wide && (p.pieces > 1 || p.ranges > 1) ? p.ranges * T * D * 4 : 0);
         p.scale = (float *)take(8);
     }
     p.bytes = at;
@@ -883,8 +858,8 @@ hipError_t fwd_io(const void *x, const void *w, const Labels &lab, float *loss, 
     if (e == hipSuccess) e = padded<IO>(w, p.wp, V, D, p.kD, &wr, s);
     if (e != hipSuccess) return e;
     if constexpr (IO == IO_F32) {
-        e = launch(k_xent_stats<IO>, dim3(blocks(T, BM), blocks(V, BN)), dim3(256), 0, s, xr, ld, wr, ld, lab, p.part,
-                   p.hit, T, V, ld);
+        e = launch(k_xent_stats32, dim3(blocks(T, BM) * blocks(V, BN)), dim3(256), 0, s, (const float *)x, (const float *)w,
+                   lab, p.part, p.hit, T, D, V);
     } else {
         using L = LogitTile<IO>;
         e = launch(k_xent_stats16<IO>, dim3(blocks(V, L::BM) * blocks(T, L::BN)), dim3(L::NT), 0, s, xr, wr, ld,
@@ -906,27 +881,17 @@ hipError_t bwd_io(const void *x, const void *w, const Labels &lab, const float *
     hipError_t e = padded<IO>(x, p.xp, T, D, p.kD, &xr, s);
     if (e == hipSuccess) e = padded<IO>(w, p.wp, V, D, p.kD, &wr, s);
     if (e == hipSuccess) e = launch(k_xent_scale<IO>, dim3(1), dim3(1024), 0, s, dloss, lab, p.scale, T);
-    if constexpr (IO == IO_F32) {
-        if (e == hipSuccess)
-            e = launch(k_xent_transpose<E>, dim3(blocks(p.Tp, 64), blocks(D, 64)), dim3(256), 0, s, (const E *)x,
-                       (E *)p.xt, T, D, p.Tp);
-    }
     for (int64_t i = 0; i < p.pieces && e == hipSuccess; ++i) {
         const int64_t v0 = i * p.piece, nv = V - v0 < p.piece ? V - v0 : p.piece;
         const int first = i == 0, last = i + 1 == p.pieces;
         if constexpr (IO == IO_F32) {
-            const int64_t kv = ceil_to(nv, BN);
-            e = launch(k_xent_transpose<E>, dim3(blocks(kv, 64), blocks(D, 64)), dim3(256), 0, s,
-                       (const E *)w + v0 * D, (E *)p.wt, nv, D, kv);
+            const float *const wv = (const float *)w + v0 * D;
+            const int64_t ndx = (int64_t)blocks(T, BM) * blocks(D, BN), ndw = (int64_t)blocks(nv, BM) * blocks(D, BN);
+            e = launch(k_xent_grad32, dim3(blocks(T, BM) * blocks(nv, BN)), dim3(256), 0, s, (const float *)x,
+                       (const float *)w, lab, lse, dloss, p.scale, (float *)p.g, T, D, v0, nv);
             if (e != hipSuccess) break;
-            e = launch(k_xent_grad<IO>, dim3(blocks(T, BM), blocks(nv, BN)), dim3(256), 0, s, xr, ld, wr, ld, lab,
-                       lse, dloss, p.scale, (E *)p.g, kv, (E *)p.gt, p.Tp, T, v0, nv, ld);
-            if (e != hipSuccess) break;
-            e = launch(k_xent_product<IO>, dim3(blocks(nv, BM), blocks(D, BN)), dim3(256), 0, s, p.gt, p.Tp * es, nv,
-                       p.xt, p.Tp * es, D, p.Tp * es, (E *)dw + v0 * D, (float *)nullptr, 1, 1, p.scale);
-            if (e != hipSuccess) break;
-            e = launch(k_xent_product<IO>, dim3(blocks(T, BM), blocks(D, BN)), dim3(256), 0, s, p.g, kv * es, T, p.wt,
-                       kv * es, D, kv * es, (E *)dx, p.accum, first, last, p.scale);
+            e = launch(k_xent_products32, dim3((unsigned)(ndx + ndw)), dim3(256), 0, s, (const float *)x, wv,
+                       (const float *)p.g, (float *)dx, (float *)dw + v0 * D, p.scale, T, D, nv, ndx, first);
         } else {
             using L = LogitTile<IO>;
             using G = GradTile<IO, false>;

@@ -434,7 +434,8 @@ h3conv_status h3conv_selective_step(const void *u, const void *dt, const float *
  *   x [T,D], w [V,D]  io dtype     labels [T] int64
  *   loss, lse [T]     fp32         loss is 0 where labels[t] is ignore_index or outside 0 .. V-1
  *   ws   at least h3conv_linear_xent_workspace_size(T, D, V, io, 0) bytes
- * Supported: D <= 2^20, V <= 2^22, T <= 2^30, T*D and V*D <= 2^40.
+ * Supported: D <= 2^20, V <= 2^22, T <= 2^30, and the tiles of one dispatch:
+ * (T/64 + 1) (V/64 + 1) <= 2^31, (max(T, V)/64 + 2) (D/64 + 1) <= 2^27.
  * Products of 16-bit elements are summed in fp32 on the matrix cores; fp32
  * elements use the fp32 matrix cores.
  */
