@@ -371,8 +371,8 @@ __global__ __launch_bounds__(256, 2) void k_sel_scan(const SelK<typename io_elem
 
 // ------------------------------------------------------------------ backward
 
-// With dr = dy silu(z), x the states and e_t = a_t g_t (a_t = exp(d_t A)):
-//   g_t = C_t dr_t + e_{t+1}                  gradient of x_t
+// With dr = dy silu(z), x the states and a_t = exp(d_t A):
+//   g_t = C_t dr_t + a_{t+1} g_{t+1}          gradient of x_t
 //   dC_t = sum_h dr_t x_t                     dB_t = sum_h g_t d_t u_t
 //   du_t = D dr_t + d_t sum_j g_t B_t         dd_t = sum_j g_t (a_t x_{t-1}) A + u_t sum_j g_t B_t
 //   dA = sum_t g_t (a_t x_{t-1}) d_t          dD = sum dr u,  dz = dy r silu'(z)
@@ -439,7 +439,10 @@ struct BwdIn {
     float A[4], x[4];
 };
 
-template <int IO>
+// WHOLE: exactly kModes modes, the common case: no mode is missing, and one
+// launch has all of them (else: a launch per kModes modes, whose sums over modes
+// pass through ws.acc).
+template <int IO, bool WHOLE>
 __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
     const SelK<typename io_elem<IO>::T> k, const float *__restrict__ saved,
     const typename io_elem<IO>::T *__restrict__ dy, const float *__restrict__ dx_out,
@@ -463,47 +466,65 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
     const int64_t left = Hg - (int64_t)set * ws.per, h0 = g * Hg + (int64_t)set * ws.per;
     const int nset = (int)(left < ws.per ? left : ws.per);
     const int nch = nset > wave ? (nset - wave + kWaves - 1) / kWaves : 0;  // this wave's channels
-    const int m0 = n0 + 4 * row;                                            // this row's modes
+    const int S = WHOLE ? kModes : k.S, m0 = WHOLE ? 4 * row : n0 + 4 * row;  // this row's modes
+    // channel c of this wave: row r0 + kWaves c of the batch, channel hw + kWaves c
+    const int64_t hw = h0 + wave, r0 = b * k.H + hw;
     for (int c = 0; c < nch; ++c)
         if (l < 4) {
-            const int64_t h = h0 + wave + kWaves * c;
-            (&carry[wave][c][row].x)[l] = (dx_out && m0 + l < k.S) ? dx_out[(b * k.H + h) * k.S + m0 + l] : 0.f;
+            (&carry[wave][c][row].x)[l] = (dx_out && m0 + l < S) ? dx_out[(r0 + kWaves * c) * S + m0 + l] : 0.f;
             (&sumA[wave][c][row].x)[l] = 0.f;
             if (row == 0 && l < 2) sumDb[wave][c][l] = 0.f;
         }
     // this thread's eight steps of B or C in LDS: matrix, mode, steps
     const int cm = tid >> 8, cn = (tid >> 4) & 15, ct = tid & 15;
     const typename io_elem<IO>::T *const bc = cm ? k.C : k.Bm;
-    const int64_t bc0 = (bg * k.S + (n0 + cn < k.S ? n0 + cn : 0)) * N + ct * 8;
+    const bool mode = WHOLE || n0 + cn < S;
+    const int64_t bc0 = (bg * S + (mode ? (WHOLE ? 0 : n0) + cn : 0)) * N + ct * 8;
     // valid steps of a piece, and those from step `from` of it on
     const auto steps = [&](int64_t ch, int64_t end) {
         const int64_t n = end - ch * kSelChunk;
         return (int)(n < 0 ? 0 : (n < kSelChunk ? n : kSelChunk));
     };
     const auto load_bc = [&](int64_t ch) {
-        return ld_raw<IO, 8, false>(bc, bc0 + ch * kSelChunk, n0 + cn < k.S ? steps(ch, len) - ct * 8 : 0);
+        return ld_raw<IO, 8, false>(bc, bc0 + ch * kSelChunk, mode ? steps(ch, len) - ct * 8 : 0);
     };
     const int tq = l * kJT + row * kQ;  // this lane's own steps within a piece
     BwdIn<IO> f;
-    const auto load_in = [&](int64_t ch, int c) {
-        const int64_t h = h0 + wave + kWaves * c, r = b * k.H + h, o = r * N + ch * kSelChunk;
-        const int valid = steps(ch, len) - tq;
-        f.u = ld_raw<IO, kQ, false>(k.u, o + tq, valid);
-        f.p = ld_raw<IO, kQ, false>(k.dt, o + tq, valid);
-        f.gy = ld_raw<IO, kQ, false>(dy, o + tq, valid);
-        if (k.z) f.z = ld_raw<IO, kQ, false>(k.z, o + tq, valid);
-        const float *const Ah = k.A + h * k.S, *const xh = saved + (r * nchunk + ch) * k.S;
+    // the next channel and piece to load: offsets of its row's steps, states
+    // and decay rates
+    int64_t on = 0, xn = 0;
+    const float *An = nullptr;
+    const auto start = [&](int64_t ch) {
+        on = r0 * N + ch * kSelChunk;
+        xn = (r0 * nchunk + ch) * S;
+        An = k.A + hw * S;
+    };
+    const auto load_in = [&](int valid) {
+        f.u = ld_raw<IO, kQ, false>(k.u, on + tq, valid);
+        f.p = ld_raw<IO, kQ, false>(k.dt, on + tq, valid);
+        f.gy = ld_raw<IO, kQ, false>(dy, on + tq, valid);
+        if (k.z) f.z = ld_raw<IO, kQ, false>(k.z, on + tq, valid);
+        const float *const xh = saved + xn;
+        if constexpr (WHOLE) {
+            const float4 a = *(const float4 *)(An + m0), x = *(const float4 *)(xh + m0);
+            f.A[0] = a.x, f.A[1] = a.y, f.A[2] = a.z, f.A[3] = a.w;
+            f.x[0] = x.x, f.x[1] = x.y, f.x[2] = x.z, f.x[3] = x.w;
+        } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const bool in = m0 + q < k.S;
-            f.A[q] = in ? Ah[m0 + q] : 0.f;
-            f.x[q] = in ? xh[m0 + q] : 0.f;
+            for (int q = 0; q < 4; ++q) {
+                const bool in = m0 + q < S;
+                f.A[q] = in ? An[m0 + q] : 0.f;
+                f.x[q] = in ? xh[m0 + q] : 0.f;
+            }
         }
     };
     Raw<IO, 8> rbc;
     if (nchunk > 0) {
         rbc = load_bc(nchunk - 1);
-        if (nch > 0) load_in(nchunk - 1, 0);
+        if (nch > 0) {
+            start(nchunk - 1);
+            load_in(steps(nchunk - 1, len) - tq);
+        }
     }
     for (int64_t ch = nchunk - 1; ch >= 0; --ch) {
         const int valid = steps(ch, len) - tq, keep = steps(ch, N) - tq;  // this lane's steps: valid, and in the row
@@ -523,7 +544,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
 #pragma unroll
             for (int i = 0; i < kJT; ++i) aB[q][i] = aC[q][i] = 0.f;
         for (int c = 0; c < nch; ++c) {
-            const int64_t h = h0 + wave + kWaves * c, r = b * k.H + h, o0 = r * N + ch * kSelChunk;
+            const int64_t h = hw + kWaves * c, o0 = on;
             const float bias = k.dt_bias ? k.dt_bias[h] : 0.f, Dh = k.D ? k.D[h] : 0.f;
             float u[kQ], p[kQ], z[kQ], gy[kQ], d[kQ], dr[kQ], A[4], xs[4];
             unpack<IO, kQ>(f.u, u);
@@ -535,8 +556,15 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
                 A[q] = f.A[q];
                 xs[q] = f.x[q];
             }
-            if (c + 1 < nch) load_in(ch, c + 1);
-            else if (ch > 0) load_in(ch - 1, 0);
+            if (c + 1 < nch) {
+                on += kWaves * N;
+                xn += kWaves * nchunk * S;
+                An += kWaves * S;
+                load_in(valid);
+            } else if (ch > 0) {
+                start(ch - 1);
+                load_in(steps(ch - 1, len) - tq);
+            }
 #pragma unroll
             for (int i = 0; i < kQ; ++i) {
                 p[i] += bias;
@@ -592,22 +620,25 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
                     aC[q][i] = fmaf(rr[i], x, aC[q][i]);
                     Cv[i] *= rr[i];
                 }
+                // g_t = C_t dr_t + a_{t+1} g_{t+1}, and a g of a lane's first
+                // step goes to the lane before
                 const float back = l == 15 ? cy[q] : 0.f;
-                Q = back;
+                float gx = Cv[kJT - 1] + back;
 #pragma unroll
-                for (int i = kJT - 1; i >= 0; --i) Q = a[i] * (Q + Cv[i]);
+                for (int i = kJT - 2; i >= 0; --i) gx = fmaf(a[i + 1], gx, Cv[i]);
+                Q = a[0] * gx;
                 scan_back(P, Q);
                 out[q] = Q;  // what lane 0 hands to the piece before
-                float e = dpp0<0x101>(Q) + back;
+                gx = Cv[kJT - 1] + (dpp0<0x101>(Q) + back);
                 sA[q] = 0.f;
 #pragma unroll
                 for (int i = kJT - 1; i >= 0; --i) {
-                    const float gx = Cv[i] + e, w = gx * ax[i];
+                    const float w = gx * ax[i];
                     aB[q][i] = fmaf(gx, bu[i], aB[q][i]);
                     sb[i] = fmaf(gx, Bv[i], sb[i]);
                     sk[i] = fmaf(w, A[q], sk[i]);
                     sA[q] = fmaf(w, dd[i], sA[q]);
-                    e = a[i] * gx;
+                    if (i > 0) gx = fmaf(a[i], gx, Cv[i - 1]);
                 }
                 // one round's registers at a time
                 hold(aC[q]);
@@ -629,7 +660,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
             sum_rows(sr, s3[0]);
             sum_rows(sb, s3[1]);
             sum_rows(sk, s3[2]);
-            if (ws.acc) {
+            if constexpr (!WHOLE) if (ws.acc) {
                 const int64_t plane = k.B * k.H * N;
 #pragma unroll
                 for (int j = 0; j < 3; ++j)
@@ -641,7 +672,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
                             if (!last_block) *q = s3[j][i];
                         }
             }
-            if (last_block) {
+            if (WHOLE || last_block) {
 #pragma unroll
                 for (int i = 0; i < kQ; ++i) {
                     const float raw = fmaf(Dh, u[i], s3[0][i]);
@@ -688,10 +719,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
                 s.x += x[0];
                 s.y += x[1];
             }
-            const int n = n0 + 4 * (ll >> 4) + q;
+            const int n = (WHOLE ? 0 : n0) + 4 * (ll >> 4) + q;
             const int t = (ll & 15) * kJT + (v & 1) * 4 + half * 2;
-            if (n < k.S) {
-                float *o = (v < 2 ? ws.dB : ws.dC) + ((((int64_t)set * k.B + b) * k.G + g) * k.S + n) * N + ch * kSelChunk + t;
+            if (WHOLE || n < S) {
+                float *o = (v < 2 ? ws.dB : ws.dC) + ((((int64_t)set * k.B + b) * k.G + g) * S + n) * N + ch * kSelChunk + t;
                 if (t < steps(ch, N)) o[0] = s.x;
                 if (t + 1 < steps(ch, N)) o[1] = s.y;
             }
@@ -699,12 +730,12 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
         }
     }
     for (int c = 0; c < nch; ++c) {
-        const int64_t h = h0 + wave + kWaves * c, o = (b * k.H + h) * k.S + m0;
-        if (l < 4 && m0 + l < k.S) {
+        const int64_t r = r0 + kWaves * c, o = r * S + m0;
+        if (l < 4 && (WHOLE || m0 + l < S)) {
             ws.dA[o + l] = (&sumA[wave][c][row].x)[l];
             if (dx_in) dx_in[o + l] = (&carry[wave][c][row].x)[l];
         }
-        if (last_block && lane < 2) ws.dDb[(b * k.H + h) * 2 + lane] = sumDb[wave][c][lane];
+        if ((WHOLE || last_block) && lane < 2) ws.dDb[r * 2 + lane] = sumDb[wave][c][lane];
     }
 }
 
@@ -861,10 +892,13 @@ hipError_t bwd_io(const SelArgs &a, const float *saved, const void *dy, const fl
     SelBwdWs w;
     bwd_layout(a.B, a.H, a.N, a.S, a.G, ws, &w);
     const dim3 grid((unsigned)(a.B * a.G * w.sets));
+    // (float4 loads of decay rates: A may start at any element)
+    const bool whole = a.S == kModes && ((uintptr_t)a.A & 15) == 0;
     for (int n0 = 0; n0 < a.S && a.B > 0; n0 += kModes) {
         const hipError_t e =
-            launch(k_sel_bwd<IO>, grid, dim3(kWaves * 64), 0, s, pack_args<IO>(a), saved, (const T *)dy, dx_out, (T *)g.du,
-                   (T *)g.ddt, (T *)g.dz, g.dx_in, w, chunks(a.N), n0, n0 + kModes >= a.S ? 1 : 0);
+            launch(whole ? k_sel_bwd<IO, true> : k_sel_bwd<IO, false>, grid, dim3(kWaves * 64), 0, s, pack_args<IO>(a),
+                   saved, (const T *)dy, dx_out, (T *)g.du, (T *)g.ddt, (T *)g.dz, g.dx_in, w, chunks(a.N), n0,
+                   n0 + kModes >= a.S ? 1 : 0);
         if (e != hipSuccess) return e;
     }
     const int64_t M = a.B * a.G * a.S * a.N;
