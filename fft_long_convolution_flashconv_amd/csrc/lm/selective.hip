@@ -9,6 +9,9 @@
 // state passes them unchanged.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+#include <cstdlib>
+
 #include "lm_device.h"
 #include "lm_internal.h"
 
@@ -180,21 +183,51 @@ struct Sums {
     float lane, before, wave;
 };
 
-// One mode of one piece: o += C x.  WPR == 1: the state `in` enters the first
-// lane, and the state that leaves the row's last lane is kept in *st.
-// WPR == 4: the block's four waves hold four pieces in a row of one row; they
+// How a piece lies in its rows.
+enum Fit {
+    kFull,  // every lane has kIT valid steps
+    kTail,  // some lane has fewer: a lane that would read past its row's end reads
+            // the row's last kIT steps instead and passes over those of others (so
+            // every load is one in-row vector, whatever the length)
+    kShort  // as kTail, of rows with fewer than kIT steps: element loads
+};
+
+// Steps at .. at + n - 1 of the kIT at p + off.
+template <int IO, int n, Fit F>
+__device__ __forceinline__ Raw<IO, n> ld_steps(const typename io_elem<IO>::T *p, int64_t off, int at, int64_t N) {
+    if constexpr (F != kShort) return ld_raw<IO, n, true>(p, off + at, 0);
+    typename io_elem<IO>::T v[n];
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = p[off + (at + i < N ? at + i : N - 1)];
+    Raw<IO, n> r;
+    __builtin_memcpy(&r, v, sizeof(r));
+    return r;
+}
+
+// How the four waves of a block share their rows.
+enum Share {
+    kOwnRows,  // each wave has rows of its own
+    kTime,     // four pieces in a row of one row
+    kModeMod4  // the same pieces of the same rows; wave w has modes w, w + 4, ...
+};
+
+// One mode of one piece: o += C x.  The state `in` enters the first lane, and
+// the state that leaves the row's last lane is kept in *st.  kTime: the waves
 // exchange the maps of their pieces through `maps` (one barrier), and every
 // wave keeps in its own *st the state before the first and then after the
-// last.  B and C arrive as
-// loaded; nextB() and nextC() load a later mode's into the same registers once
-// they are unpacked.
-template <int IO, int LPR, int WPR, class NextB, class NextC>
+// last.  B and C arrive as loaded; nextB() and nextC() load a later mode's
+// into the same registers once they are unpacked.
+template <int IO, int LPR, Share SH, Fit F, class NextB, class NextC>
 __device__ __forceinline__ void scan_mode(Raw<IO, kIT> &rB, Raw<IO, kIT> &rC, float A2, float in,
                                           const float (&d)[kIT], const float (&u)[kIT], const Sums &sum,
                                           float (&o)[kIT], float *st, int l, float2 (*maps)[4], float *saved,
-                                          const NextB &nextB, const NextC &nextC) {
+                                          const Raw<IO, kIT> &own, const NextB &nextB, const NextC &nextC) {
     constexpr int IT = kIT;
-    float a[IT], w[IT], c[IT], P = exp2_(sum.lane * A2), Q = WPR == 1 ? in : 0.f;
+    float a[IT], w[IT], c[IT], P = exp2_(sum.lane * A2), Q = SH != kTime ? in : 0.f;
+    if (F != kFull) {
+#pragma unroll
+        for (int i = 0; i < Raw<IO, IT>::kWords; ++i) rB.w[i] &= own.w[i];  // (what is passed over may be NaN)
+    }
     unpack<IO, IT>(rB, w);
     hold(w);
     nextB();
@@ -206,7 +239,7 @@ __device__ __forceinline__ void scan_mode(Raw<IO, kIT> &rB, Raw<IO, kIT> &rC, fl
     }
     scan_states<LPR>(P, Q);
     float x0 = dpp0<LPR == 64 ? 0x138 : 0x111>(Q);  // from the lane before
-    if constexpr (WPR == 1) {
+    if constexpr (SH != kTime) {
         x0 += in;
     } else {
         const int wave = threadIdx.x >> 6;
@@ -214,7 +247,7 @@ __device__ __forceinline__ void scan_mode(Raw<IO, kIT> &rB, Raw<IO, kIT> &rC, fl
         __syncthreads();
         float x = *st, enter = x;
 #pragma unroll
-        for (int i = 0; i < WPR; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const float2 m = (*maps)[i];
             x = fmaf(m.x, x, m.y);
             if (i + 1 == wave) enter = x;
@@ -235,45 +268,57 @@ __device__ __forceinline__ void scan_mode(Raw<IO, kIT> &rB, Raw<IO, kIT> &rC, fl
     if (saved) *saved = x0;
 }
 
-// The steps of one lane in one piece: the first, how many are valid, and the
-// offsets of the first in u, dt, z, y and in mode 0 of B and C.
+// The steps of one lane in one piece: its first is t0; it loads kIT of them at
+// offset `row` of u and dt and `bc` of mode 0 of B and C, and has loaded steps
+// lo .. hi - 1 for its own.
 struct Lane {
-    int64_t t0, valid, row, bc;
+    int64_t t0, row, bc;
+    int lo, hi;
 };
 
 // One piece of LPR*IT steps of each of the wave's rows, from its u and dt as
-// loaded; reload() loads the next piece's into the same registers.  FULL:
-// every lane's steps are valid.
-template <int IO, int LPR, int WPR, bool FULL, class Reload>
+// loaded; reload() loads the next piece's into the same registers.
+template <int IO, int LPR, Share SH, Fit F, class Reload>
 __device__ __forceinline__ void scan_piece(const SelK<typename io_elem<IO>::T> &k, const Lane &p, Raw<IO, kIT> &ru,
                                            Raw<IO, kIT> &rd, const float *Ap, float Dh, float bias, float *st, int l,
-                                           bool live, float2 (*maps)[4], typename io_elem<IO>::T *y, float *saved,
-                                           const Reload &reload) {
-    constexpr int IT = kIT, AH = kAhead;
-    const int last = k.S - 1;
+                                           bool live, float2 (*maps)[4], float (*part)[kIT][64],
+                                           typename io_elem<IO>::T *y, float *saved, const Reload &reload) {
+    constexpr int IT = kIT, AH = kAhead, MS = SH == kModeMod4 ? 4 : 1;
+    const int last = k.S - 1, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), first = MS > 1 ? wave : 0;
     Raw<IO, IT> rB[AH], rC[AH];
-    const auto loadB = [&](int n) { return ld_raw<IO, IT, FULL>(k.Bm, p.bc + (n < last ? n : last) * k.N, p.valid); };
-    const auto loadC = [&](int n) { return ld_raw<IO, IT, FULL>(k.C, p.bc + (n < last ? n : last) * k.N, p.valid); };
+    const auto loadB = [&](int n) { return ld_steps<IO, IT, F>(k.Bm, p.bc + (n < last ? n : last) * k.N, 0, k.N); };
+    const auto loadC = [&](int n) { return ld_steps<IO, IT, F>(k.C, p.bc + (n < last ? n : last) * k.N, 0, k.N); };
 #pragma unroll
     for (int j = 0; j < AH; ++j) {
-        rB[j] = loadB(j);
-        rC[j] = loadC(j);
+        rB[j] = loadB(first + MS * j);
+        rC[j] = loadC(first + MS * j);
     }
     float u[IT], d[IT], o[IT];
     Sums sum = {0.f, 0.f, 0.f};
+    Raw<IO, IT> own;
+    if (F != kFull) {
+        constexpr int E = 4 / (int)sizeof(typename io_elem<IO>::T);
+#pragma unroll
+        for (int i = 0; i < Raw<IO, IT>::kWords; ++i) {
+            const auto in = [&](int t) { return t >= p.lo && t < p.hi; };
+            if (E == 1) own.w[i] = in(i) ? ~0u : 0u;
+            else own.w[i] = (in(2 * i) ? 0xffffu : 0u) | (in(2 * i + 1) ? 0xffff0000u : 0u);
+            ru.w[i] &= own.w[i];
+        }
+    }
     unpack<IO, IT>(ru, u);
     unpack<IO, IT>(rd, d);
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         d[i] += bias;
         if (k.softplus) d[i] = softplus(d[i]);
-        if (!FULL && i >= p.valid) d[i] = 0.f;
-        o[i] = Dh * u[i];
+        if (F != kFull && (i < p.lo || i >= p.hi)) d[i] = 0.f;
+        o[i] = first == 0 ? Dh * u[i] : 0.f;
         u[i] *= d[i];
         sum.lane += d[i];
     }
-    if (WPR > 1) {
-            float s = sum.lane;
+    if (SH == kTime) {
+        float s = sum.lane;
         scan_states<64>(1.f, s);
         sum.before = dpp0<0x138>(s);
         sum.wave = lane_of(s, 63);
@@ -281,29 +326,51 @@ __device__ __forceinline__ void scan_piece(const SelK<typename io_elem<IO>::T> &
     reload();
     // a lane's first step is where a state is saved
     float *sv = saved && live && p.t0 < k.N && p.t0 % kSelChunk == 0 ? saved + p.t0 / kSelChunk * k.S : nullptr;
-    float A = Ap[0], in = st[0];
-    for (int n0 = 0; n0 < k.S; n0 += AH) {
+    float A = Ap[first < last ? first : last], in = st[first];
+    for (int n0 = first; n0 < k.S; n0 += MS * AH) {
 #pragma unroll
         for (int j = 0; j < AH; ++j) {
-            const int n = n0 + j;
+            const int n = n0 + MS * j, next = n + MS < last ? n + MS : last;
             if (AH > 1 && n >= k.S) break;
             const float A2 = A * kLog2e, in0 = l == 0 ? in : 0.f;
-            A = Ap[n < last ? n + 1 : last];
-            in = st[n < last ? n + 1 : last];
-            scan_mode<IO, LPR, WPR>(rB[j], rC[j], A2, in0, d, u, sum, o, st + n, l, maps + (n & 1), sv ? sv + n : nullptr,
-                               [&] { rB[j] = loadB(n + AH); }, [&] { rC[j] = loadC(n + AH); });
+            A = Ap[next];
+            in = st[next];
+            scan_mode<IO, LPR, SH, F>(rB[j], rC[j], A2, in0, d, u, sum, o, st + n, l, maps + (n & 1), sv ? sv + n : nullptr,
+                               own, [&] { rB[j] = loadB(n + MS * AH); }, [&] { rC[j] = loadC(n + MS * AH); });
         }
     }
-    if (k.z) {
-        float z[IT];
-        unpack<IO, IT>(ld_raw<IO, IT, FULL>(k.z, p.row, p.valid), z);
+    // y of the lane: all of its steps, or with the modes' waves a quarter each
+    constexpr int OT = IT / MS;
+    const int at = OT * first;
+    float out[OT];
+    if constexpr (MS > 1) {
+        const int lane = threadIdx.x & 63;
 #pragma unroll
-        for (int i = 0; i < IT; ++i) o[i] *= z[i] * sigmoid(z[i]);
+        for (int i = 0; i < IT; ++i) part[wave][i][lane] = o[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < OT; ++i)
+            out[i] = (part[0][at + i][lane] + part[1][at + i][lane]) + (part[2][at + i][lane] + part[3][at + i][lane]);
+        __syncthreads();
+    } else {
+#pragma unroll
+        for (int i = 0; i < OT; ++i) out[i] = o[i];
     }
+    if (k.z) {
+        float z[OT];
+        unpack<IO, OT>(ld_steps<IO, OT, F>(k.z, p.row, at, k.N), z);
 #pragma unroll
-    for (int i = 0; i < IT; ++i)
-        if (!FULL && i >= p.valid) o[i] = 0.f;
-    if (live) st_row<IO, IT>(y + p.row, o, FULL ? IT : k.N - p.t0);
+        for (int i = 0; i < OT; ++i) out[i] *= z[i] * sigmoid(z[i]);
+    }
+    if (!live) return;
+    if (F == kFull || (p.lo <= at && p.hi >= at + OT)) {
+        st_row<IO, OT>(y + p.row + at, out, OT);
+    } else {
+#pragma unroll
+        for (int i = 0; i < OT; ++i)
+            if (at + i >= p.lo && (F != kShort || at + i < k.N))
+                y[p.row + at + i] = from_f<IO>(at + i < p.hi ? out[i] : 0.f);
+    }
 }
 
 // LPR lanes per row (b, h), 64 / LPR rows per wave; lane l of a row holds
@@ -312,19 +379,20 @@ __device__ __forceinline__ void scan_piece(const SelK<typename io_elem<IO>::T> &
 // composed by a scan over the row's lanes, and each lane runs its steps again
 // from the state that enters it: two multiply-adds per (step, mode) instead
 // of one, and no state leaves the chip between pieces.
-template <int IO, int LPR, int WPR>
-__global__ __launch_bounds__(256, 2) void k_sel_scan(const SelK<typename io_elem<IO>::T> k,
+template <int IO, int LPR, Share SH>
+__global__ __launch_bounds__(256, IO == IO_F32 || LPR == 16 ? 2 : 3) void k_sel_scan(const SelK<typename io_elem<IO>::T> k,
                                                      typename io_elem<IO>::T *__restrict__ y,
                                                      float *__restrict__ x_out, float *__restrict__ saved,
                                                      int64_t nchunk) {
-    constexpr int IT = kIT, RPW = 64 / LPR, PIECE = WPR * LPR * IT;
-    static_assert(WPR == 1 || (WPR == 4 && LPR == 64), "");
+    constexpr int IT = kIT, RPW = 64 / LPR, PIECE = (SH == kTime ? 4 : 1) * LPR * IT;
+    static_assert(SH != kTime || LPR == 64, "");
     static_assert(kSelChunk % IT == 0, "saved states fall on a lane's first step");
     __shared__ float state[4][RPW][kMaxModes];
     __shared__ float2 maps[2][4];
+    __shared__ float part[SH == kModeMod4 ? 4 : 1][kIT][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane / LPR, l = lane % LPR;
     const uint32_t R = (uint32_t)(k.B * k.H), H = (uint32_t)k.H;
-    const uint32_t r = WPR == 1 ? (blockIdx.x * 4 + wave) * RPW + sub : blockIdx.x;
+    const uint32_t r = (SH == kOwnRows ? blockIdx.x * 4 + wave : blockIdx.x) * RPW + sub;
     if (r - sub >= R) return;  // (the whole wave)
     const bool live = r < R;
     const uint32_t rr = live ? r : R - 1, b = rr / H, h = rr - b * H, g = h / (H / (uint32_t)k.G);
@@ -336,37 +404,45 @@ __global__ __launch_bounds__(256, 2) void k_sel_scan(const SelK<typename io_elem
     __builtin_amdgcn_wave_barrier();
     float *sv = saved ? saved + (int64_t)rr * nchunk * k.S : nullptr;
     const auto piece = [&](int64_t base) {
-        const int64_t t0 = base + (WPR == 1 ? 0 : wave * 64 * IT) + l * IT;
-        return Lane{t0, len - t0, rr * N + t0, (int64_t)(b * (uint32_t)k.G + g) * k.S * N + t0};
+        const int64_t t0 = base + (SH == kTime ? wave * 64 * IT : 0) + l * IT;
+        const int64_t w0 = t0 <= N - IT ? t0 : (N > IT ? N - IT : 0);  // the first step loaded
+        const int lo = (int)(t0 - w0 < IT ? t0 - w0 : IT), hi = (int)(len - w0 < IT ? (len > w0 ? len - w0 : 0) : IT);
+        return Lane{t0, rr * N + w0, (int64_t)(b * (uint32_t)k.G + g) * k.S * N + w0, lo, hi > lo ? hi : lo};
     };
     Raw<IO, IT> ru, rd;
     int64_t base = 0;
     if (__all(len >= PIECE)) {  // the pieces that are full in every row of the wave
         Lane p = piece(0);
-        ru = ld_raw<IO, IT, true>(k.u, p.row, 0);
-        rd = ld_raw<IO, IT, true>(k.dt, p.row, 0);
+        ru = ld_steps<IO, IT, kFull>(k.u, p.row, 0, N);
+        rd = ld_steps<IO, IT, kFull>(k.dt, p.row, 0, N);
         bool more;
         do {
             more = __all(len >= base + 2 * PIECE);
-            scan_piece<IO, LPR, WPR, true>(k, p, ru, rd, Ap, Dh, bias, st, l, live, maps, y, sv, [&] {
+            scan_piece<IO, LPR, SH, kFull>(k, p, ru, rd, Ap, Dh, bias, st, l, live, maps, part, y, sv, [&] {
                 const int64_t o = more ? p.row + PIECE : p.row;
-                ru = ld_raw<IO, IT, true>(k.u, o, 0);
-                rd = ld_raw<IO, IT, true>(k.dt, o, 0);
+                ru = ld_steps<IO, IT, kFull>(k.u, o, 0, N);
+                rd = ld_steps<IO, IT, kFull>(k.dt, o, 0, N);
             });
             __builtin_amdgcn_wave_barrier();
             base += PIECE;
             p = piece(base);
         } while (more);
     }
-    for (; base < N; base += PIECE) {
-        const Lane p = piece(base);
-        ru = ld_raw<IO, IT, false>(k.u, p.row, p.valid);
-        rd = ld_raw<IO, IT, false>(k.dt, p.row, p.valid);
-        scan_piece<IO, LPR, WPR, false>(k, p, ru, rd, Ap, Dh, bias, st, l, live, maps, y, sv, [] {});
-        __builtin_amdgcn_wave_barrier();
-    }
-    if (x_out && live && (WPR == 1 || wave == 0))
-        for (int n = l; n < k.S; n += LPR) x_out[(int64_t)rr * k.S + n] = st[n];
+    const auto rest = [&](auto fit) {
+        constexpr Fit F = decltype(fit)::value;
+        for (; base < N; base += PIECE) {
+            const Lane p = piece(base);
+            ru = ld_steps<IO, IT, F>(k.u, p.row, 0, N);
+            rd = ld_steps<IO, IT, F>(k.dt, p.row, 0, N);
+            scan_piece<IO, LPR, SH, F>(k, p, ru, rd, Ap, Dh, bias, st, l, live, maps, part, y, sv, [] {});
+            __builtin_amdgcn_wave_barrier();
+        }
+    };
+    if (LPR == 16 && N < IT) rest(std::integral_constant<Fit, kShort>{});
+    else rest(std::integral_constant<Fit, kTail>{});
+    if (x_out && live)
+        for (int n = l; n < k.S; n += LPR)
+            if (SH == kOwnRows || wave == (SH == kTime ? 0 : n % 4)) x_out[(int64_t)rr * k.S + n] = st[n];
 }
 
 // ------------------------------------------------------------------ backward
@@ -870,19 +946,33 @@ size_t bwd_layout(int64_t B, int64_t H, int64_t N, int64_t S, int64_t G, char *b
 
 int64_t chunks(int64_t N) { return (N + kSelChunk - 1) / kSelChunk; }
 
-template <int IO, int LPR, int WPR>
+// Which lanes and waves take a row (scan_io says when).
+template <int IO, int LPR, Share SH>
 hipError_t scan_lanes(const SelArgs &a, void *y, float *x_out, float *saved, hipStream_t s) {
     using T = typename io_elem<IO>::T;
-    constexpr int rows = 4 / WPR * 64 / LPR;
-    return launch(k_sel_scan<IO, LPR, WPR>, dim3((unsigned)((a.B * a.H + rows - 1) / rows)), dim3(256), 0, s,
+    constexpr int rows = (SH == kOwnRows ? 4 : 1) * 64 / LPR;
+    return launch(k_sel_scan<IO, LPR, SH>, dim3((unsigned)((a.B * a.H + rows - 1) / rows)), dim3(256), 0, s,
                   pack_args<IO>(a), (T *)y, x_out, saved, chunks(a.N));
 }
 
 template <int IO>
 hipError_t scan_io(const SelArgs &a, void *y, float *x_out, float *saved, hipStream_t s) {
-    if (a.N <= 16 * kIT) return scan_lanes<IO, 16, 1>(a, y, x_out, saved, s);
-    if (a.N > 64 * kIT && a.B * a.H < 4096) return scan_lanes<IO, 64, 4>(a, y, x_out, saved, s);
-    return scan_lanes<IO, 64, 1>(a, y, x_out, saved, s);
+    // Measured in fp16 with 16 modes and a gate, us, at (rows x steps):
+    //                    288x301  288x4096  1024x2048  1024x4096  2048x250  4096x250  4096x4096
+    //   own rows            12.5      36.8       20.4       39.4      11.7      12.3       99.1
+    //   time                           18.9       32.1       32.1                          105.0
+    //   modes                8.9      22.5       20.6       40.2       8.8      15.3      131.6
+    // A quarter of the time is won where four pieces at once leave no wave idle
+    // and the rows alone are too few to fill the chip; a quarter of the modes
+    // where there is but one wave or two per compute unit.
+    const int64_t rows = a.B * a.H, pieces = (a.N + 64 * kIT - 1) / (64 * kIT);
+    const bool rows16 = a.N <= 16 * kIT;  // lanes per row: 16, else 64
+    if (rows <= 2048 && pieces > 3 * ((pieces + 3) / 4)) return scan_lanes<IO, 64, kTime>(a, y, x_out, saved, s);
+    if (rows <= (rows16 ? 2048 : 512) && a.S >= 4)
+        return rows16 ? scan_lanes<IO, 16, kModeMod4>(a, y, x_out, saved, s)
+                      : scan_lanes<IO, 64, kModeMod4>(a, y, x_out, saved, s);
+    return rows16 ? scan_lanes<IO, 16, kOwnRows>(a, y, x_out, saved, s)
+                  : scan_lanes<IO, 64, kOwnRows>(a, y, x_out, saved, s);
 }
 
 template <int IO>
