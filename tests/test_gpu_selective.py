@@ -297,3 +297,27 @@ def test_selective_refusals():
     with pytest.raises(pkg.H3ConvError):  # pool below the batch
         pkg.selective_step(u[..., 0].contiguous(), dt[..., 0].contiguous(), A, Bm[..., 0].contiguous(),
                            C[..., 0].contiguous(), torch.zeros(1, 4, 3, device=u.device))
+
+
+# Many rows and long rows: the waves of a block have rows of their own, share a
+# row's steps, or share its modes; pieces end inside, before and after a lane.
+WIDE = [
+    (3, 700, 9, 5, 1, True, True, True, True, True, [0, 9, 4]),        # fewer steps than a lane takes
+    (4, 520, 201, 4, 2, True, True, True, True, True, [201, 1, 17, 200]),
+    (2, 300, 301, 3, 3, True, True, True, True, True, None),
+    (2, 300, 1040, 6, 1, True, False, True, True, True, [1024, 1033]),
+    (2, 3, 3090, 5, 1, True, True, True, True, True, [3090, 3079]),
+    (1, 2, 7171, 4, 1, True, True, True, True, True, [4097]),
+]
+
+
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("case", WIDE, ids=ids)
+def test_selective_scan_wide(io, case):
+    test_selective_scan(io, case)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("case", WIDE[1:5], ids=ids)
+def test_selective_scan_bwd_wide(io, case):
+    test_selective_scan_bwd(io, case)
