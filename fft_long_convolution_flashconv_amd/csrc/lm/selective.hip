@@ -456,20 +456,21 @@ __global__ __launch_bounds__(256, IO == IO_F32 || LPR == 16 ? 2 : 3) void k_sel_
 // the row's pieces of kSelChunk steps from the end, with the states at each
 // piece's start as the forward pass saved them.  A wave takes the set's
 // channels w, w + 8, ... alone: its four DPP rows of 16 lanes hold four modes
-// at a time (row r: modes 4r .. 4r+3 of a block of 16, in four rounds), lane l
+// at a time (row r: modes 4r .. 4r+3 of a block of 16, in four rounds; of fewer
+// modes, fewer rounds), lane l
 // of a row kJT steps.  So dB and dC of every mode and step stay in one lane's
 // registers over all the wave's channels (no atomics), the scans over time
 // stay within a DPP row, and the sums over modes are two exchanges between
 // rows.  A lane prepares and finishes a quarter of its steps (softplus, gate)
 // and the rows share them through LDS.
 constexpr int kModes = 16, kJT = kSelChunk / 16, kQ = kJT / 4, kWaves = 8, kPerWave = 16;
-static_assert(kJT == 8 && 2 * kModes * kSelChunk == kWaves * 64 * 8, "one 8-step load of B or C per thread and piece");
+static_assert(kJT == 8 && kQ == 2 && 2 * kModes * kSelChunk == kWaves * 64 * 8, "one 8-step load of B or C per thread and piece");
 
 struct SelBwdWs {
     float *dB, *dC;        // [sets][B][G][S][N]
     float *dA;             // [B][H][S]
     float *dDb;            // [B][H][2]
-    float *acc;            // [3][B*H*N], more than kModes modes only
+    float *acc;            // [B*H][N, in pairs][3][kQ], more than kModes modes only
     int sets, per;         // sets per group, channels per set
 };
 
@@ -542,20 +543,22 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
     const int64_t left = Hg - (int64_t)set * ws.per, h0 = g * Hg + (int64_t)set * ws.per;
     const int nset = (int)(left < ws.per ? left : ws.per);
     const int nch = nset > wave ? (nset - wave + kWaves - 1) / kWaves : 0;  // this wave's channels
-    const int S = WHOLE ? kModes : k.S, m0 = WHOLE ? 4 * row : n0 + 4 * row;  // this row's modes
+    const int S = WHOLE ? kModes : k.S;
+    const int rounds = WHOLE || S - n0 >= kModes ? 4 : (S - n0 + 3) / 4, m0 = n0 + rounds * row;  // this row's modes
     // channel c of this wave: row r0 + kWaves c of the batch, channel hw + kWaves c
     const int64_t hw = h0 + wave, r0 = b * k.H + hw;
     for (int c = 0; c < nch; ++c)
         if (l < 4) {
-            (&carry[wave][c][row].x)[l] = (dx_out && m0 + l < S) ? dx_out[(r0 + kWaves * c) * S + m0 + l] : 0.f;
+            (&carry[wave][c][row].x)[l] = (dx_out && l < rounds && m0 + l < S) ? dx_out[(r0 + kWaves * c) * S + m0 + l] : 0.f;
             (&sumA[wave][c][row].x)[l] = 0.f;
             if (row == 0 && l < 2) sumDb[wave][c][l] = 0.f;
         }
     // this thread's eight steps of B or C in LDS: matrix, mode, steps
     const int cm = tid >> 8, cn = (tid >> 4) & 15, ct = tid & 15;
     const typename io_elem<IO>::T *const bc = cm ? k.C : k.Bm;
-    const bool mode = WHOLE || n0 + cn < S;
-    const int64_t bc0 = (bg * S + (mode ? (WHOLE ? 0 : n0) + cn : 0)) * N + ct * 8;
+    const int n = WHOLE ? cn : n0 + rounds * (cn >> 2) + (cn & 3);
+    const bool mode = WHOLE || ((cn & 3) < rounds && n < S);
+    const int64_t bc0 = (bg * S + (mode ? n : 0)) * N + ct * 8;
     // valid steps of a piece, and those from step `from` of it on
     const auto steps = [&](int64_t ch, int64_t end) {
         const int64_t n = end - ch * kSelChunk;
@@ -588,7 +591,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
         } else {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const bool in = m0 + q < S;
+                const bool in = q < rounds && m0 + q < S;
                 f.A[q] = in ? An[m0 + q] : 0.f;
                 f.x[q] = in ? xh[m0 + q] : 0.f;
             }
@@ -670,9 +673,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
             }
             const float4 cy4 = carry[wave][c][row];
             const float cy[4] = {cy4.x, cy4.y, cy4.z, cy4.w};
-            float out[4], sA[4];
+            float out[4] = {0.f, 0.f, 0.f, 0.f}, sA[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
+                if (!WHOLE && q >= rounds) break;
                 const float A2 = A[q] * kLog2e, P = exp2_(sum * A2);
                 float Bv[kJT], Cv[kJT], a[kJT], ax[kJT];
                 get8(BC[0][4 * row + q] + l, 16, Bv);
@@ -706,7 +710,6 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
                 scan_back(P, Q);
                 out[q] = Q;  // what lane 0 hands to the piece before
                 gx = Cv[kJT - 1] + (dpp0<0x101>(Q) + back);
-                sA[q] = 0.f;
 #pragma unroll
                 for (int i = kJT - 1; i >= 0; --i) {
                     const float w = gx * ax[i];
@@ -736,17 +739,15 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
             sum_rows(sr, s3[0]);
             sum_rows(sb, s3[1]);
             sum_rows(sk, s3[2]);
-            if constexpr (!WHOLE) if (ws.acc) {
-                const int64_t plane = k.B * k.H * N;
+            if constexpr (!WHOLE) {
+                if (ws.acc && keep > 0) {
+                    auto *const acc = (Pack<float, 3 * kQ> *)ws.acc + ((b * k.H + h) * ((N + 1) / kQ) + (ch * kSelChunk + tq) / kQ);
+                    Pack<float, 3 * kQ> t{};
+                    if (n0 > 0) t = *acc;
 #pragma unroll
-                for (int j = 0; j < 3; ++j)
-#pragma unroll
-                    for (int i = 0; i < kQ; ++i)
-                        if (i < keep) {
-                            float *q = ws.acc + j * plane + o0 + tq + i;
-                            if (n0 > 0) s3[j][i] += *q;
-                            if (!last_block) *q = s3[j][i];
-                        }
+                    for (int i = 0; i < 3 * kQ; ++i) t.v[i] = s3[i / kQ][i % kQ] += t.v[i];
+                    if (!last_block) *acc = t;
+                }
             }
             if (WHOLE || last_block) {
 #pragma unroll
@@ -780,6 +781,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
         __syncthreads();
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+            if (!WHOLE && q >= rounds) break;
             float4(*const buf)[4][64] = (float4(*)[4][64])lds;  // [wave][quarter of the 16 values][lane]
             buf[wave][0][lane] = make_float4(aB[q][0], aB[q][1], aB[q][2], aB[q][3]);
             buf[wave][1][lane] = make_float4(aB[q][4], aB[q][5], aB[q][6], aB[q][7]);
@@ -795,7 +797,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
                 s.x += x[0];
                 s.y += x[1];
             }
-            const int n = (WHOLE ? 0 : n0) + 4 * (ll >> 4) + q;
+            const int n = (WHOLE ? 0 : n0) + (WHOLE ? 4 : rounds) * (ll >> 4) + q;
             const int t = (ll & 15) * kJT + (v & 1) * 4 + half * 2;
             if (WHOLE || n < S) {
                 float *o = (v < 2 ? ws.dB : ws.dC) + ((((int64_t)set * k.B + b) * k.G + g) * S + n) * N + ch * kSelChunk + t;
@@ -807,7 +809,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
     }
     for (int c = 0; c < nch; ++c) {
         const int64_t r = r0 + kWaves * c, o = r * S + m0;
-        if (l < 4 && (WHOLE || m0 + l < S)) {
+        if (l < rounds && (WHOLE || m0 + l < S)) {
             ws.dA[o + l] = (&sumA[wave][c][row].x)[l];
             if (dx_in) dx_in[o + l] = (&carry[wave][c][row].x)[l];
         }
@@ -940,7 +942,7 @@ size_t bwd_layout(int64_t B, int64_t H, int64_t N, int64_t S, int64_t G, char *b
     w->dC = take(m);
     w->dA = take((size_t)(B * H * S) * 4);
     w->dDb = take((size_t)(B * H) * 8);
-    w->acc = take(S > kModes ? (size_t)(B * H * N) * 12 : 0);
+    w->acc = take(S > kModes ? (size_t)(B * H * ((N + 1) / kQ)) * (12 * kQ) : 0);
     return at;
 }
 

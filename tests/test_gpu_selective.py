@@ -321,3 +321,10 @@ def test_selective_scan_wide(io, case):
 @pytest.mark.parametrize("case", WIDE[1:5], ids=ids)
 def test_selective_scan_bwd_wide(io, case):
     test_selective_scan_bwd(io, case)
+
+
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("S", [2, 4, 7, 9, 15, 19, 33, 48])
+def test_selective_scan_bwd_modes(io, S):
+    """Blocks of modes of every size, an odd number of steps."""
+    test_selective_scan_bwd(io, (2, 10, 131, S, 2, True, True, True, True, True, [131, 40]))
