@@ -223,33 +223,53 @@ struct Tile {
 
 // ------------------------------------------------------------ fp32 tile products
 //
-// 64 x 64 tiles on the fp32 matrix cores (a sixteenth of the 16-bit rate, so
+// BT x BT tiles on the fp32 matrix cores (a sixteenth of the 16-bit rate, so
 // LDS and caches keep up with small tiles, and small problems fill the chip).
 // Rows may start at any element and have any length: operands are loaded
-// through registers, what lies past the end is zero.
-constexpr int BM = 64, BN = 64, KS32 = 32;
+// through registers, some slabs of KS32 elements ahead, what lies past the end
+// is zero.
+constexpr int KS32 = 32;
 
 // An operand of a tile: K-contiguous (rows of the tile are memory rows) or
-// K-major (memory rows are k).  ld: elements per memory row.
-template <bool KMAJOR>
+// K-major (memory rows are k).
+template <bool KMAJOR, int BT>
 struct Operand32 {
     const float *mem;
-    int64_t ld, rows, k;  // rows: of the operand, from the tile's first; k: valid k
+    int64_t ld, total;  // elements per memory row, and in all from mem on (its memory has four at least, some before mem)
+    int64_t rows, k;    // of the operand, from the tile's first row on
 
-    // chunk `id` (of 512) of the slab from k0: four k of a row, or four rows at one k
-    __device__ __forceinline__ f4 load(int64_t k0, int id) const {
-        const int64_t r = KMAJOR ? k0 + (id >> 4) : id >> 3, c = KMAJOR ? (id & 15) * 4 : k0 + (id & 7) * 4;
-        const int64_t left = (KMAJOR ? rows : k) - c;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (r < (KMAJOR ? k : rows)) ld_row<IO_F32, 4>(mem + r * ld + c, v, left);
+    // chunk `id` of the slab from k0, four k of a row or four rows at one k: its
+    // memory row and first element there
+    __device__ __forceinline__ static int64_t row(int64_t k0, int id) { return KMAJOR ? k0 + id / (BT / 4) : id >> 3; }
+    __device__ __forceinline__ static int64_t col(int64_t k0, int id) { return KMAJOR ? id % (BT / 4) * 4 : k0 + (id & 7) * 4; }
+    __device__ __forceinline__ int64_t last() const { return total - 4; }
+    __device__ __forceinline__ int64_t offset(int64_t k0, int id) const { return row(k0, id) * ld + col(k0, id); }
+    __device__ __forceinline__ int64_t step() const { return KMAJOR ? KS32 * ld : KS32; }
+    // As loaded: always one vector, the operand's last where the chunk passes its
+    // end, so that no load waits for a choice.
+    __device__ __forceinline__ f4 load(int64_t o) const {
+        float v[4];
+        ld_row<IO_F32, 4>(mem + (o < last() ? o : last()), v);
         return f4{v[0], v[1], v[2], v[3]};
+    }
+    // The chunk from what load() gave: zeros past the k.  (Of slabs that end four
+    // k before the last it is what load() gave: all k are valid, and only vectors
+    // of rows past the last, whose products no one stores, pass the end.)
+    __device__ __forceinline__ f4 chunk(f4 v, int64_t k0, int id) const {
+        const int64_t r = row(k0, id), c = col(k0, id), o = offset(k0, id) - last(), n = KMAJOR ? rows : k;
+        const int down = o > 0 ? (int)(o < 4 ? o : 0) : 0;  // (of 4 and more all are past the end)
+        const int valid = r < (KMAJOR ? k : rows) ? (int)(n - c < 4 ? (n > c ? n - c : 0) : 4) : 0;
+        float a = v[0], b = v[1], d = v[2], e = v[3];
+        a = (down & 1) ? b : a, b = (down & 1) ? d : b, d = (down & 1) ? e : d;
+        a = (down & 2) ? d : a, b = (down & 2) ? e : b;
+        return f4{valid > 0 ? a : 0.f, valid > 1 ? b : 0.f, valid > 2 ? d : 0.f, valid > 3 ? e : 0.f};
     }
     // where element (row, k) of the slab is kept: fragment reads (16 rows, one
     // chunk of four k) and transposed writes both spread over the banks
     __device__ __forceinline__ static int at(int row, int chunk) { return row * 8 + (chunk ^ ((row ^ row >> 2) & 7)); }
     __device__ __forceinline__ static void keep(f4 *s, int id, f4 v) {
         if constexpr (KMAJOR) {
-            const int kr = id >> 4, m = (id & 15) * 4;
+            const int kr = id / (BT / 4), m = id % (BT / 4) * 4;
 #pragma unroll
             for (int j = 0; j < 4; ++j) ((float *)&s[at(m + j, kr >> 2)])[kr & 3] = v[j];
         } else {
@@ -258,50 +278,80 @@ struct Operand32 {
     }
 };
 
-// acc[i][j] of this wave's 32 x 32 part of A B^T over k elements.
-template <bool AK, bool BK>
-__device__ __forceinline__ void product32(const Operand32<AK> &a, const Operand32<BK> &b, int64_t k, f4 *sA, f4 *sB,
-                                          f4 (&acc)[2][2]) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-    f4 ga[2], gb[2];
+// A tile of A B^T; four waves have a quarter each.
+template <int BT>
+struct Tile32 {
+    static constexpr int WT = BT / 2, TM = WT / 16, CH = BT * 8 / 256, AHEAD = 128 / BT;  // (slabs in flight)
+    f4 acc[TM][TM];
+
+    __device__ __forceinline__ static int row0() { return (threadIdx.x >> 7) * WT; }
+    __device__ __forceinline__ static int col0() { return ((threadIdx.x >> 6) & 1) * WT; }
+
+    // lds: two slabs of A and of B
+    template <bool AK, bool BK>
+    __device__ __forceinline__ void run(const Operand32<AK, BT> &a, const Operand32<BK, BT> &b, int64_t k,
+                                        f4 (&lds)[2][2][BT * 8]) {
+        const int tid = threadIdx.x, lane = tid & 63;
+        f4 ga[AHEAD][CH], gb[AHEAD][CH];
+        int64_t oa[CH], ob[CH];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
-        ga[i] = a.load(0, tid + i * 256);
-        gb[i] = b.load(0, tid + i * 256);
-    }
-    for (int64_t k0 = 0; k0 < k; k0 += KS32) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            a.keep(sA, tid + i * 256, ga[i]);
-            b.keep(sB, tid + i * 256, gb[i]);
+        for (int i = 0; i < CH; ++i) {
+            oa[i] = a.offset(0, tid + i * 256);
+            ob[i] = b.offset(0, tid + i * 256);
         }
-        __syncthreads();
-        if (k0 + KS32 < k) {
+        const auto load = [&](int p) {  // the next slab
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                ga[i] = a.load(k0 + KS32, tid + i * 256);
-                gb[i] = b.load(k0 + KS32, tid + i * 256);
+            for (int i = 0; i < CH; ++i) {
+                ga[p][i] = a.load(oa[i]);
+                gb[p][i] = b.load(ob[i]);
+                oa[i] += a.step();
+                ob[i] += b.step();
             }
-        }
+        };
+        // one slab; one barrier: the buffer written here was read two slabs ago
+        const auto slab = [&](int64_t k0, int p) {
+            if (k0 + KS32 + 3 >= k) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            u4 fa[2], fb[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int c = s * 4 + (lane >> 4);
-                fa[i] = __builtin_bit_cast(u4, sA[Operand32<AK>::at(wm + i * 16 + (lane & 15), c)]);
-                fb[i] = __builtin_bit_cast(u4, sB[Operand32<BK>::at(wn + i * 16 + (lane & 15), c)]);
+                for (int i = 0; i < CH; ++i) {
+                    ga[p][i] = a.chunk(ga[p][i], k0, tid + i * 256);
+                    gb[p][i] = b.chunk(gb[p][i], k0, tid + i * 256);
+                }
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < CH; ++i) {
+                a.keep(lds[p & 1][0], tid + i * 256, ga[p][i]);
+                b.keep(lds[p & 1][1], tid + i * 256, gb[p][i]);
+            }
+            load(p);
+            __syncthreads();
 #pragma unroll
-                for (int j = 0; j < 2; ++j) acc[i][j] = mfma16<IO_F32>(fa[i], fb[j], acc[i][j]);
+            for (int s = 0; s < 2; ++s) {
+                u4 fa[TM], fb[TM];
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    const int c = s * 4 + (lane >> 4);
+                    fa[i] = __builtin_bit_cast(u4, lds[p & 1][0][Operand32<AK, BT>::at(row0() + i * 16 + (lane & 15), c)]);
+                    fb[i] = __builtin_bit_cast(u4, lds[p & 1][1][Operand32<BK, BT>::at(col0() + i * 16 + (lane & 15), c)]);
+                }
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TM; ++j) acc[i][j] = mfma16<IO_F32>(fa[i], fb[j], acc[i][j]);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TM; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int p = 0; p < AHEAD; ++p) load(p);
+        for (int64_t k0 = 0; k0 < k; k0 += AHEAD * KS32) {
+#pragma unroll
+            for (int p = 0; p < AHEAD; ++p)
+                if (p == 0 || k0 + p * KS32 < k) slab(k0 + p * KS32, p);
         }
     }
-}
+};
 
 struct Labels {
     const int64_t *label;
@@ -317,26 +367,31 @@ __device__ __forceinline__ float2 join(float2 a, float2 b);
 
 // Per token of the tile (its rows): (maximum, sum of e^{l - maximum}) over the
 // tile's columns to part[tile][t], and the label's logit where it is one of them.
-__global__ __launch_bounds__(256) void k_xent_stats32(const float *x, const float *w, const Labels lab,
+template <int BT>
+__global__ __launch_bounds__(256, 4) void k_xent_stats32(const float *x, const float *w, int64_t ld, const Labels lab,
                                                       float2 *__restrict__ part, float *__restrict__ hit, int64_t T,
                                                       int64_t D, int64_t V) {
-    __shared__ f4 sA[BM * 8], sB[BN * 8];
-    __shared__ float2 half[BM];
-    f4 acc[2][2];
-    const int64_t tiles = (T + BM - 1) / BM, tile = blockIdx.x / tiles;  // of the vocabulary; tokens run first
-    const int64_t m0 = (blockIdx.x - tile * tiles) * BM, n0 = tile * BN;
-    product32(Operand32<false>{x + m0 * D, D, T - m0, D}, Operand32<false>{w + n0 * D, D, V - n0, D}, D, sA, sB, acc);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-    float2 st[2][4];
+    using P = Tile32<BT>;
+    constexpr int TM = P::TM;
+    __shared__ f4 lds[2][2][BT * 8];
+    __shared__ float2 half[BT];
+    const int64_t tiles = (T + BT - 1) / BT, tile = blockIdx.x / tiles;  // of the vocabulary; tokens run first
+    const int64_t m0 = (blockIdx.x - tile * tiles) * BT, n0 = tile * BT;
+    P tile32;
+    tile32.run(Operand32<false, BT>{x + m0 * ld, ld, (T - m0) * ld, T - m0, D},
+               Operand32<false, BT>{w + n0 * ld, ld, (V - n0) * ld, V - n0, D}, D, lds);
+    const auto &acc = tile32.acc;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = P::row0(), wn = P::col0();
+    float2 st[TM][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int64_t t = m0 + wm + i * 16 + (lane >> 4) * 4 + e;
             const int64_t l = t < T ? lab.of(t) : -1;
             float m = -INFINITY, s = 0.f;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < TM; ++j) {
                 const int64_t v = n0 + wn + j * 16 + (lane & 15);
                 if (v < V) m = fmaxf(m, acc[i][j][e]);
                 if (v < V && v == l) hit[t] = acc[i][j][e];
@@ -345,7 +400,7 @@ __global__ __launch_bounds__(256) void k_xent_stats32(const float *x, const floa
             for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
             const float mm = m == -INFINITY ? 0.f : m;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < TM; ++j)
                 if (n0 + wn + j * 16 + (lane & 15) < V) s += __builtin_amdgcn_exp2f((acc[i][j][e] - mm) * kLog2e);
 #pragma unroll
             for (int d = 1; d < 16; d <<= 1) s += __shfl_xor(s, d);
@@ -355,7 +410,7 @@ __global__ __launch_bounds__(256) void k_xent_stats32(const float *x, const floa
     __syncthreads();
     if (!(wave & 1) && (lane & 15) == 0) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int row = wm + i * 16 + (lane >> 4) * 4 + e;
@@ -419,20 +474,24 @@ __device__ __forceinline__ float weight(float dloss, float divisor) {
 }
 
 // G of the vocabulary piece [v0, v0 + nv): g[t][v - v0], rows of nv.
-__global__ __launch_bounds__(256) void k_xent_grad32(const float *x, const float *w, const Labels lab,
+template <int BT>
+__global__ __launch_bounds__(256, 4) void k_xent_grad32(const float *x, const float *w, int64_t ld, const Labels lab,
                                                      const float *__restrict__ lse, const float *__restrict__ dloss,
                                                      const float *__restrict__ scale, float *__restrict__ g, int64_t T,
                                                      int64_t D, int64_t v0, int64_t nv) {
-    __shared__ f4 sA[BM * 8], sB[BN * 8];
-    f4 acc[2][2];
-    const int64_t tiles = (T + BM - 1) / BM, tile = blockIdx.x / tiles;  // of the vocabulary; tokens run first
-    const int64_t m0 = (blockIdx.x - tile * tiles) * BM, n0 = tile * BN;
-    product32(Operand32<false>{x + m0 * D, D, T - m0, D}, Operand32<false>{w + (v0 + n0) * D, D, nv - n0, D}, D, sA, sB,
-              acc);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
+    using P = Tile32<BT>;
+    constexpr int TM = P::TM;
+    __shared__ f4 lds[2][2][BT * 8];
+    const int64_t tiles = (T + BT - 1) / BT, tile = blockIdx.x / tiles;  // of the vocabulary; tokens run first
+    const int64_t m0 = (blockIdx.x - tile * tiles) * BT, n0 = tile * BT;
+    P tile32;
+    tile32.run(Operand32<false, BT>{x + m0 * ld, ld, (T - m0) * ld, T - m0, D},
+               Operand32<false, BT>{w + (v0 + n0) * ld, ld, (nv - n0) * ld, nv - n0, D}, D, lds);
+    const auto &acc = tile32.acc;
+    const int lane = threadIdx.x & 63, wm = P::row0(), wn = P::col0();
     const float top = scale[0];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int64_t t = m0 + wm + i * 16 + (lane >> 4) * 4 + e;
@@ -440,7 +499,7 @@ __global__ __launch_bounds__(256) void k_xent_grad32(const float *x, const float
             const int64_t l = lab.of(t);
             const float ls = lse[t], dl = l >= 0 ? weight<IO_F32>(dloss[t], top) : 0.f;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < TM; ++j) {
                 const int64_t c = n0 + wn + j * 16 + (lane & 15);
                 float q = __builtin_amdgcn_exp2f((acc[i][j][e] - ls) * kLog2e);
                 if (v0 + c == l) q -= 1.f;
@@ -449,29 +508,36 @@ __global__ __launch_bounds__(256) void k_xent_grad32(const float *x, const float
         }
 }
 
-// dx and dw of a piece in one launch, tiles of 64 x 64: first those of
+// dx and dw of a piece in one launch: first the tiles of
 // dx[t][d] += sum_v G[t][v] w[v][d], then those of dw[v][d] = sum_t G[t][v] x[t][d].
-__global__ __launch_bounds__(256) void k_xent_products32(const float *x, const float *w, const float *g,
+template <int BT>
+__global__ __launch_bounds__(256) void k_xent_products32(const float *x, const float *w, int64_t ld, const float *g,
                                                          float *__restrict__ dx, float *__restrict__ dw,
                                                          const float *__restrict__ scale, int64_t T, int64_t D,
                                                          int64_t nv, int64_t ndx, int first) {
-    __shared__ f4 sA[BM * 8], sB[BN * 8];
-    f4 acc[2][2];
-    const int64_t cols = (D + BN - 1) / BN;
+    using P = Tile32<BT>;
+    constexpr int TM = P::TM;
+    __shared__ f4 lds[2][2][BT * 8];
+    const int64_t cols = (D + BT - 1) / BT;
     const bool is_dx = (int64_t)blockIdx.x < ndx;
-    const int64_t id = is_dx ? blockIdx.x : blockIdx.x - ndx, m0 = id / cols * BM, n0 = id % cols * BN;
+    const int64_t id = is_dx ? blockIdx.x : blockIdx.x - ndx, m0 = id / cols * BT, n0 = id % cols * BT;
+    const int64_t ng = T * nv > 4 ? T * nv : 4;  // (there is room for four)
+    P tile32;
     if (is_dx)
-        product32(Operand32<false>{g + m0 * nv, nv, T - m0, nv}, Operand32<true>{w + n0, D, D - n0, nv}, nv, sA, sB, acc);
+        tile32.run(Operand32<false, BT>{g + m0 * nv, nv, ng - m0 * nv, T - m0, nv},
+                   Operand32<true, BT>{w + n0, ld, nv * ld - n0, D - n0, nv}, nv, lds);
     else
-        product32(Operand32<true>{g + m0, nv, nv - m0, T}, Operand32<true>{x + n0, D, D - n0, T}, T, sA, sB, acc);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
+        tile32.run(Operand32<true, BT>{g + m0, nv, ng - m0, nv - m0, T},
+                   Operand32<true, BT>{x + n0, ld, T * ld - n0, D - n0, T}, T, lds);
+    const auto &acc = tile32.acc;
+    const int lane = threadIdx.x & 63, wm = P::row0(), wn = P::col0();
     const float down = scale[1];
     const int64_t M = is_dx ? T : nv;
     float *const out = is_dx ? dx : dw;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < TM; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int64_t m = m0 + wm + i * 16 + (lane >> 4) * 4 + e, n = n0 + wn + j * 16 + (lane & 15);
@@ -751,6 +817,16 @@ __global__ __launch_bounds__(256) void k_xent_zero(E *__restrict__ p, int64_t n)
     if (i < n) p[i] = (E)0;
 }
 
+// Side of the fp32 tiles of a launch that forms n x m outputs, or of two that
+// form n x m and o x m: 64, or 32 where those are too few for the compute
+// units.  Tokens x width x vocabulary, us, sides 64 and 32:
+//   logits:    517 x 201 x 1009  17.0  14.8 (144 tiles of 64)   1024 x 256 x 2048  23.3  26.9 (512)
+//   backward:  517 x 201 x 1009  46.4  30.3 (100)               2048 x 512 x 8192   478   586 (1280)
+int64_t side32(int64_t n, int64_t m, int64_t o = 0) {
+    const auto tiles = [](int64_t r) { return (r + 63) / 64; };
+    return (tiles(n) + tiles(o)) * tiles(m) < 256 ? 32 : 64;
+}
+
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 int64_t ceil_to(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
@@ -789,8 +865,8 @@ int64_t makespan(int64_t n, int64_t a, int64_t m, int64_t b) {
 Plan plan(int64_t T, int64_t D, int64_t V, int io, bool bwd, char *base) {
     Plan p = {};
     const bool wide = io == IO_F32;
-    const int64_t e = wide ? 4 : 2, slab = wide ? 1 : LogitTile<IO_F16>::KS, rows = wide ? BN : LogitTile<IO_F16>::BM;
-    p.kD = ceil_to(D, slab);
+    const int64_t e = wide ? 4 : 2, slab = wide ? 1 : LogitTile<IO_F16>::KS, rows = wide ? (bwd ? 64 : side32(T, V)) : LogitTile<IO_F16>::BM;
+    p.kD = wide ? (D < 4 ? 4 : D) : ceil_to(D, slab);  // (fp32: a row holds one vector at least)
     p.Tp = ceil_to(T, slab);
     size_t at = 0;
     const auto take = [&](int64_t bytes) {
@@ -858,8 +934,9 @@ hipError_t fwd_io(const void *x, const void *w, const Labels &lab, float *loss, 
     if (e == hipSuccess) e = padded<IO>(w, p.wp, V, D, p.kD, &wr, s);
     if (e != hipSuccess) return e;
     if constexpr (IO == IO_F32) {
-        e = launch(k_xent_stats32, dim3(blocks(T, BM) * blocks(V, BN)), dim3(256), 0, s, (const float *)x, (const float *)w,
-                   lab, p.part, p.hit, T, D, V);
+        const int64_t bt = side32(T, V);
+        e = launch(bt == 32 ? k_xent_stats32<32> : k_xent_stats32<64>, dim3(blocks(T, bt) * blocks(V, bt)), dim3(256), 0, s,
+                   (const float *)xr, (const float *)wr, p.kD, lab, p.part, p.hit, T, D, V);
     } else {
         using L = LogitTile<IO>;
         e = launch(k_xent_stats16<IO>, dim3(blocks(V, L::BM) * blocks(T, L::BN)), dim3(L::NT), 0, s, xr, wr, ld,
@@ -885,13 +962,16 @@ hipError_t bwd_io(const void *x, const void *w, const Labels &lab, const float *
         const int64_t v0 = i * p.piece, nv = V - v0 < p.piece ? V - v0 : p.piece;
         const int first = i == 0, last = i + 1 == p.pieces;
         if constexpr (IO == IO_F32) {
-            const float *const wv = (const float *)w + v0 * D;
-            const int64_t ndx = (int64_t)blocks(T, BM) * blocks(D, BN), ndw = (int64_t)blocks(nv, BM) * blocks(D, BN);
-            e = launch(k_xent_grad32, dim3(blocks(T, BM) * blocks(nv, BN)), dim3(256), 0, s, (const float *)x,
-                       (const float *)w, lab, lse, dloss, p.scale, (float *)p.g, T, D, v0, nv);
+            const float *const xf = (const float *)xr, *const wf = (const float *)wr;
+            int64_t bt = side32(T, nv);
+            e = launch(bt == 32 ? k_xent_grad32<32> : k_xent_grad32<64>, dim3(blocks(T, bt) * blocks(nv, bt)), dim3(256), 0, s,
+                       xf, wf, p.kD, lab, lse, dloss, p.scale, (float *)p.g, T, D, v0, nv);
             if (e != hipSuccess) break;
-            e = launch(k_xent_products32, dim3((unsigned)(ndx + ndw)), dim3(256), 0, s, (const float *)x, wv,
-                       (const float *)p.g, (float *)dx, (float *)dw + v0 * D, p.scale, T, D, nv, ndx, first);
+            bt = side32(T, D, nv);
+            const int64_t ndx = (int64_t)blocks(T, bt) * blocks(D, bt), ndw = (int64_t)blocks(nv, bt) * blocks(D, bt);
+            e = launch(bt == 32 ? k_xent_products32<32> : k_xent_products32<64>, dim3((unsigned)(ndx + ndw)), dim3(256), 0, s,
+                       xf, wf + v0 * p.kD, p.kD, (const float *)p.g, (float *)dx, (float *)dw + v0 * D, p.scale, T, D, nv,
+                       ndx, first);
         } else {
             using L = LogitTile<IO>;
             using G = GradTile<IO, false>;

@@ -149,3 +149,11 @@ def test_xent_refusals():
 def test_gradient_ranges(T, D, V):
     """dx of few tokens and few columns over many rows: summed over ranges of the vocabulary."""
     _check("bf16", *_make("bf16", T, D, V, 21))
+
+
+# fp32: tiles of both sizes, with rows, columns and sums that end inside a vector
+@pytest.mark.parametrize("T,D,V", [(1, 1, 1), (2, 3, 3), (5, 2, 700), (33, 67, 3), (67, 35, 36), (64, 4, 65),
+                                   (1025, 130, 1030), (40, 1100, 1050)])
+def test_fp32_tiles(T, D, V):
+    say("linear_xent fp32", T, D, V)
+    _check("f32", *_make("f32", T, D, V, T + D + V))
