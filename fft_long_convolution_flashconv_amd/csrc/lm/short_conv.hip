@@ -57,6 +57,18 @@ __device__ __forceinline__ void before(const typename io_elem<IO>::T *x, const t
     }
 }
 
+// As before(), of a row of four steps at least without saved inputs whose steps
+// up to t0 are valid: one load, whatever t0.
+template <int IO, int W>
+__device__ __forceinline__ void before_plain(const typename io_elem<IO>::T *x, int64_t t0, float *v) {
+    if constexpr (W > 1) {
+        float near[4];
+        ld_row<IO, 4>(x + (t0 > 0 ? t0 - 4 : 0), near);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) v[j] = t0 > 0 ? near[j + 5 - W] : 0.f;
+    }
+}
+
 // A count of steps as a small int: at most V matter.
 __device__ __forceinline__ int few(int64_t n) { return (int)(n < 0 ? 0 : (n > 64 ? 64 : n)); }
 
@@ -84,8 +96,14 @@ __global__ __launch_bounds__(kThreads) void k_short_conv(const typename io_elem<
         for (int j = tl; j < W - 1; j += tpr) x_out[r * (W - 1) + j] = from_f<IO>(at_ext<IO, W>(xr, xi, len - (W - 1) + j));
     for (int64_t t0 = ((int64_t)blockIdx.y * tpr + tl) * V; t0 < N; t0 += (int64_t)gridDim.y * tpr * V) {
         float v[V + W - 1], cur[V], o[V];
-        ld_row<IO, V>(xr + t0, cur, len - t0);
-        before<IO, W>(xr, xi, t0, len, v);
+        const bool plain = __all(t0 + V <= len && (t0 > 0 || !xi));  // (of the wave: its loads need no choice)
+        if (plain) {
+            ld_row<IO, V>(xr + t0, cur);
+            before_plain<IO, W>(xr, t0, v);
+        } else {
+            ld_row<IO, V>(xr + t0, cur, len - t0);
+            before<IO, W>(xr, xi, t0, len, v);
+        }
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i + W - 1] = cur[i];
         const int valid = few(len - t0);
@@ -132,9 +150,11 @@ __global__ __launch_bounds__(kThreads) void k_short_conv_bwd(
         sw[k] = 0.f;
     }
     const float bs = bias ? bias[h] : 0.f;
-    const int64_t tasks = (B + rpb - 1) / rpb * pieces;
-    for (int64_t task = blockIdx.y; task < tasks; task += gridDim.y) {
-        const int64_t bg = task / pieces, b = bg * rpb + sub, t0 = ((task - bg * pieces) * tpr + tl) * V;
+    int64_t bg = 0, piece = blockIdx.y;  // task: rows bg .. bg + rpb - 1, a piece of them
+    for (;; piece += gridDim.y) {
+        for (; piece >= pieces; piece -= pieces) bg += rpb;
+        if (bg >= B) break;
+        const int64_t b = bg + sub, t0 = (piece * tpr + tl) * V;
         if (b >= B || (t0 >= N && t0 > 0)) continue;  // (step 0 of an empty row: dx_in alone)
         const int64_t r = b * H + h, len = row_len(lengths, b, N);
         const T *xr = x + r * N, *xi = x_in ? x_in + r * (W - 1) : nullptr, *gr = dy + r * N;
@@ -143,13 +163,26 @@ __global__ __launch_bounds__(kThreads) void k_short_conv_bwd(
         float v[E + W - 1], g[E], dp[E], o[V];
         {
             float cur[V], gc[V], near[4], gn[4];
-            ld_row<IO, V>(xr + t0, cur, len - t0);
-            ld_row<IO, V>(gr + t0, gc, len - t0);
-            if constexpr (W > 1) {
-                ld_row<IO, 4>(xr + t0 + V, near, len - t0 - V);
-                ld_row<IO, 4>(gr + t0 + V, gn, len - t0 - V);
+            const int64_t end = t0 + V;
+            if (__all((end + 4 <= len || (end == len && len == N)) && (t0 > 0 || !xi))) {
+                // (of the wave: its loads need no choice; past the row's end the
+                // thread's own first steps stand in, whose dp is zero)
+                ld_row<IO, V>(xr + t0, cur);
+                ld_row<IO, V>(gr + t0, gc);
+                if constexpr (W > 1) {
+                    ld_row<IO, 4>(xr + (end < len ? end : t0), near);
+                    ld_row<IO, 4>(gr + (end < len ? end : t0), gn);
+                }
+                before_plain<IO, W>(xr, t0, v);
+            } else {
+                ld_row<IO, V>(xr + t0, cur, len - t0);
+                ld_row<IO, V>(gr + t0, gc, len - t0);
+                if constexpr (W > 1) {
+                    ld_row<IO, 4>(xr + end, near, len - end);
+                    ld_row<IO, 4>(gr + end, gn, len - end);
+                }
+                before<IO, W>(xr, xi, t0, len, v);
             }
-            before<IO, W>(xr, xi, t0, len, v);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 v[j + W - 1] = cur[j];
