@@ -157,3 +157,12 @@ def test_gradient_ranges(T, D, V):
 def test_fp32_tiles(T, D, V):
     say("linear_xent fp32", T, D, V)
     _check("f32", *_make("f32", T, D, V, T + D + V))
+
+
+# 16-bit: tiles of every side, sums over the vocabulary and over the tokens in ranges of their own
+@pytest.mark.parametrize("io", ["f16", "bf16"])
+@pytest.mark.parametrize("T,D,V", [(1, 1, 1), (40, 64, 20000), (2500, 70, 130), (1100, 130, 513), (700, 320, 5000),
+                                   (2100, 96, 4200), (300, 65, 33000)])
+def test_16bit_tiles(io, T, D, V):
+    say("linear_xent 16-bit", io, T, D, V)
+    _check(io, *_make(io, T, D, V, T + D + V))
