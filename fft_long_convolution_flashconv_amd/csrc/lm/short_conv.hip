@@ -265,6 +265,7 @@ __global__ void k_short_conv_sums(const float *__restrict__ part, float *__restr
     const int k = (int)(i - h * (kTaps + 1));
     if (h >= H || k > W) return;
     float s = 0.f;
+#pragma unroll 8
     for (int j = 0; j < K; ++j) s += part[((int64_t)j * H + h) * (kTaps + 1) + k];
     if (k < W) dw[h * W + k] = s;
     else if (dbias) dbias[h] = s;

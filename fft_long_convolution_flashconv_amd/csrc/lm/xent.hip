@@ -11,6 +11,8 @@
 // of dx.  Four products of 2 T D V operations each in all: matrix-core bound.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "lm_device.h"
 #include "lm_internal.h"
 
@@ -67,7 +69,7 @@ struct Operand {
     int64_t ld, k;
     int32_t off[kLoads];  // (the shim keeps 256 rows within 31 bits)
 
-    __device__ __forceinline__ static int slot(int krow) { return (krow & 3) | ((krow >> 3) & 1) << 2; }
+    __device__ __forceinline__ static int slot(int krow) { return ((krow & 3) | ((krow >> 3) & 1) << 2) & (ROWS / 16 - 1); }
     __device__ __forceinline__ static int turn(int row) { return (row >> (KS == 32 ? 1 : 0)) & (KS / 8 - 1); }
 
     __device__ __forceinline__ void init(const char *m, int64_t ld_, int64_t rows, int64_t k_) {
@@ -454,6 +456,7 @@ __global__ __launch_bounds__(1024) void k_xent_scale(const float *__restrict__ d
                                                      float *__restrict__ scale, int64_t T) {
     __shared__ float red[16];
     float m = 0.f;
+#pragma unroll 8
     for (int64_t t = threadIdx.x; t < T; t += 1024)
         if (lab.of(t) >= 0) m = fmaxf(m, fabsf(dloss[t]));
 #pragma unroll
@@ -562,20 +565,26 @@ __device__ __forceinline__ void tile_of(int64_t id, int64_t rows, int64_t cols, 
     r = 4 * g + k - c * h;
 }
 
-template <int IO>
-using LogitTile = Tile<IO, 256, 256, 2, 4, 64, 2, false, false>;
-template <int IO, bool G_KMAJOR>
-using GradTile = Tile<IO, 256, 256, 2, 4, 64, 2, true, G_KMAJOR>;
-template <int IO>
-constexpr int kGradThreads = GradTile<IO, false>::NT;
+// Tiles of side BT: large ones need the least traffic per product (eight waves
+// with 128 x 64 parts each), small ones fill the chip when there are few.
+template <int IO, int BT, bool AK, bool BK>
+using Side = std::conditional_t<
+    BT == 256, Tile<IO, 256, 256, 2, 4, 64, 2, AK, BK>,
+    std::conditional_t<BT == 128, Tile<IO, 128, 128, 2, 2, 64, 2, AK, BK>, Tile<IO, 64, 64, 2, 2, 64, 3, AK, BK>>>;
+template <int IO, int BT>
+using LogitTile = Side<IO, BT, false, false>;
+template <int IO, int BT, bool G_KMAJOR>
+using GradTile = Side<IO, BT, true, G_KMAJOR>;
+template <int BT>
+constexpr int kThreads16 = BT == 256 ? 512 : 256;
 
 // As k_xent_stats with w's rows as the tile's rows and tokens as its columns:
 // a lane holds four consecutive rows of w for a token.
-template <int IO>
-__global__ __launch_bounds__(LogitTile<IO>::NT, 1) void k_xent_stats16(const char *x, const char *w, int64_t ld,
+template <int IO, int BT>
+__global__ __launch_bounds__(kThreads16<BT>, BT == 256 ? 1 : 2) void k_xent_stats16(const char *x, const char *w, int64_t ld,
                                                                        const Labels lab, float2 *__restrict__ part,
                                                                        float *__restrict__ hit, int64_t T, int64_t V) {
-    using L = LogitTile<IO>;
+    using L = LogitTile<IO, BT>;
     __shared__ __align__(16) char lds[L::kLds];
     const int64_t rows = (V + L::BM - 1) / L::BM, cols = (T + L::BN - 1) / L::BN;
     int64_t rt, ct;
@@ -641,15 +650,15 @@ __global__ __launch_bounds__(LogitTile<IO>::NT, 1) void k_xent_stats16(const cha
 
 // G of the vocabulary piece [v0, v0 + nv): g[t][v - v0], rows of ldg elements;
 // zero for nv <= v - v0 < ldg and for T <= t < Tp.
-template <int IO>
-__global__ __launch_bounds__(LogitTile<IO>::NT, 1) void k_xent_grad16(const char *x, const char *w, int64_t ld,
+template <int IO, int BT>
+__global__ __launch_bounds__(kThreads16<BT>, BT == 256 ? 1 : 2) void k_xent_grad16(const char *x, const char *w, int64_t ld,
                                                                       const Labels lab, const float *__restrict__ lse,
                                                                       const float *__restrict__ dloss,
                                                                       const float *__restrict__ scale,
                                                                       typename io_elem<IO>::T *__restrict__ gout,
                                                                       int64_t ldg, int64_t T, int64_t Tp, int64_t v0,
                                                                       int64_t nv) {
-    using L = LogitTile<IO>;
+    using L = LogitTile<IO, BT>;
     using E = typename io_elem<IO>::T;
     __shared__ __align__(16) char lds[L::kLds];
     const int64_t rows = (nv + L::BM - 1) / L::BM, cols = (T + L::BN - 1) / L::BN;
@@ -711,14 +720,17 @@ __global__ __launch_bounds__(LogitTile<IO>::NT, 1) void k_xent_grad16(const char
 // tile's rows are d (so that a lane stores four consecutive values), its
 // columns t or v.  dx has few tiles where D is small: the piece's v are cut
 // into `splits` ranges of kx, each with a sum of its own in accum over all
-// pieces; without a cut and with one piece dx is stored at once.
-template <int IO>
-__global__ __launch_bounds__(kGradThreads<IO>, 1) void k_xent_products16(
+// pieces; without a cut and with one piece dx is stored at once.  dw has few
+// tiles where V and D are small: the tokens are cut into `wsplits` ranges of
+// kw, each with a sum of its own in waccum.
+template <int IO, int BT>
+__global__ __launch_bounds__(kThreads16<BT>, BT == 256 ? 1 : 2) void k_xent_products16(
     const char *x, const char *w, int64_t ld, const char *g, int64_t ldg, typename io_elem<IO>::T *__restrict__ dx,
-    typename io_elem<IO>::T *__restrict__ dw, float *__restrict__ accum, const float *__restrict__ scale, int64_t T,
-    int64_t Tp, int64_t D, int64_t nv, int64_t kv, int64_t kx, int splits, int64_t ndx, int first, int whole) {
-    using PX = GradTile<IO, false>;
-    using PW = GradTile<IO, true>;
+    typename io_elem<IO>::T *__restrict__ dw, float *__restrict__ accum, float *__restrict__ waccum,
+    const float *__restrict__ scale, int64_t T, int64_t Tp, int64_t D, int64_t nv, int64_t kv, int64_t kx, int splits,
+    int64_t kw, int wsplits, int64_t ndx, int first, int whole) {
+    using PX = GradTile<IO, BT, false>;
+    using PW = GradTile<IO, BT, true>;
     __shared__ __align__(16) char lds[PX::kLds];
     const int64_t rows = (D + PX::BM - 1) / PX::BM;
     const int lane = threadIdx.x & 63;
@@ -760,15 +772,17 @@ __global__ __launch_bounds__(kGradThreads<IO>, 1) void k_xent_products16(
                 st_row<IO_F32, 4>(sum + t * D + d, q, D - d);
             }
     } else {
-        const int64_t n = (int64_t)gridDim.x - ndx, cols = n / rows;
-        tile_of(xcd_order(blockIdx.x - ndx, n), rows, cols, rt, ct);
-        const int64_t d0 = rt * PW::BM, c0 = ct * PW::BN;
+        const int64_t n = (int64_t)gridDim.x - ndx, cols = n / rows / wsplits;
+        const int64_t id = xcd_order(blockIdx.x - ndx, n), part = id / (rows * cols);
+        tile_of(id - part * rows * cols, rows, cols, rt, ct);
+        const int64_t d0 = rt * PW::BM, c0 = ct * PW::BN, k0 = part * kw, kn = Tp - k0 < kw ? Tp - k0 : kw;
         typename PW::OA a;
         typename PW::OB b;
-        a.init(x + d0 * 2, ld, ld - d0 * 2, T);
-        b.init(g + c0 * 2, ldg * 2, (ldg - c0) * 2, Tp);
+        a.init(x + k0 * ld + d0 * 2, ld, ld - d0 * 2, T - k0);
+        b.init(g + k0 * ldg * 2 + c0 * 2, ldg * 2, (ldg - c0) * 2, Tp - k0);
         PW tile;
-        tile.run(a, b, Tp / PW::KS, lds);
+        tile.run(a, b, kn / PW::KS, lds);
+        float *const sum = waccum + part * nv * D;
 #pragma unroll
         for (int i = 0; i < PW::TM; ++i)
 #pragma unroll
@@ -778,13 +792,14 @@ __global__ __launch_bounds__(kGradThreads<IO>, 1) void k_xent_products16(
                 if (v >= nv || d >= D) continue;
                 float q[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) q[e] = tile.acc[i][j][e] * down;
-                st_row<IO, 4>(dw + v * D + d, q, D - d);
+                for (int e = 0; e < 4; ++e) q[e] = wsplits > 1 ? tile.acc[i][j][e] : tile.acc[i][j][e] * down;
+                if (wsplits > 1) st_row<IO_F32, 4>(sum + v * D + d, q, D - d);
+                else st_row<IO, 4>(dw + v * D + d, q, D - d);
             }
     }
 }
 
-// dx from the sums of its ranges, in order; n values each.
+// dx (or dw) from the sums of its ranges, in order; n values each.
 template <int IO>
 __global__ __launch_bounds__(256) void k_xent_dx(const float *__restrict__ accum, const float *__restrict__ scale,
                                                  typename io_elem<IO>::T *__restrict__ dx, int64_t n, int splits) {
@@ -792,6 +807,7 @@ __global__ __launch_bounds__(256) void k_xent_dx(const float *__restrict__ accum
     if (i >= n) return;
     float s[4];
     ld_row<IO_F32, 4>(accum + i, s, n - i);
+#pragma unroll 4
     for (int k = 1; k < splits; ++k) {
         float o[4];
         ld_row<IO_F32, 4>(accum + k * n + i, o, n - i);
@@ -803,12 +819,21 @@ __global__ __launch_bounds__(256) void k_xent_dx(const float *__restrict__ accum
     st_row<IO, 4>(dx + i, s, n - i);
 }
 
-// dst[r][c] = src[r][c] for c < C, zero up to ldd.
+// dst[r][c] = src[r][c] for c < C, zero up to ldd (whole vectors).
 template <class E>
 __global__ __launch_bounds__(256) void k_xent_pad(const E *__restrict__ src, E *__restrict__ dst, int64_t R,
                                                   int64_t C, int64_t ldd) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / ldd, c = i - r * ldd;
-    if (r < R) dst[i] = c < C ? src[r * C + c] : (E)0;
+    constexpr int n = 16 / (int)sizeof(E);
+    const int64_t v = ldd / n, i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / v, c = (i - r * v) * n;
+    if (r >= R) return;
+    Pack<E, n> q;
+    if (c + n <= C) {
+        q = *reinterpret_cast<const Pack<E, n> *>(src + r * C + c);
+    } else {
+#pragma unroll
+        for (int e = 0; e < n; ++e) q.v[e] = c + e < C ? src[r * C + c + e] : (E)0;
+    }
+    *reinterpret_cast<Pack<E, n> *>(dst + r * ldd + c) = q;
 }
 
 template <class E>
@@ -827,6 +852,18 @@ int64_t side32(int64_t n, int64_t m, int64_t o = 0) {
     return (tiles(n) + tiles(o)) * tiles(m) < 256 ? 32 : 64;
 }
 
+// Side of the 16-bit tiles of n x m logits.  bf16, tokens x width x vocabulary,
+// us of the forward pass, sides 256, 128 and 64:
+//   300 x 256 x 1000    22.0  14.0   9.4  (24 tiles of 128)
+//   300 x 777 x 8000    44.5  33.9  31.5  (189)
+//   1000 x 777 x 8000   46.3  39.4  48.5  (504)
+//   300 x 256 x 50021   38.8  36.5  46.8  (1173; 392 of 256)
+//   1000 x 256 x 50021  64.8  70.4  94.1  (3128; 784 of 256)
+int64_t side16(int64_t n, int64_t m) {
+    const auto tiles = [&](int64_t bt) { return ((n + bt - 1) / bt) * ((m + bt - 1) / bt); };
+    return tiles(256) >= 512 ? 256 : (tiles(128) >= 256 ? 128 : 64);
+}
+
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 int64_t ceil_to(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
@@ -835,19 +872,20 @@ struct Plan {
     int64_t Tp;            // tokens, padded (16-bit): rows of G
     int64_t piece, pieces; // vocabulary rows per piece
     int64_t tiles;         // pairs per token of the forward pass
+    int64_t side;          // of the tiles of dx and dw (16-bit)
     int64_t range, ranges; // vocabulary rows whose part of dx is summed apart, such parts of a piece (16-bit)
+    int64_t wrange, wranges; // tokens whose part of dw is summed apart, such parts (16-bit)
     char *xp, *wp, *g;
-    float *accum, *scale, *hit;
+    float *accum, *waccum, *scale, *hit;
     float2 *part;
     size_t bytes;
 };
 
-// The time of a first-come schedule on the chip's 256 compute units of n tiles
-// of length a, then m of length b.
-int64_t makespan(int64_t n, int64_t a, int64_t m, int64_t b) {
-    constexpr int kUnits = 256;
-    const int64_t full = n / kUnits, more = n % kUnits;  // `more` units finish one a later
-    int64_t early = full * a, late = more ? early + a : early, ne = kUnits - more, nl = more;
+// The time of a first-come schedule on `units` units of n tiles of length a, then
+// m of length b.
+int64_t makespan(int64_t units, int64_t n, int64_t a, int64_t m, int64_t b) {
+    const int64_t full = n / units, more = n % units;  // `more` units finish one a later
+    int64_t early = full * a, late = more ? early + a : early, ne = units - more, nl = more;
     while (m > 0) {  // whole rows of equal units at a time
         if (ne > 0 && (nl == 0 || early <= late)) {
             if (m < ne) return early + b > late ? early + b : late;
@@ -865,7 +903,7 @@ int64_t makespan(int64_t n, int64_t a, int64_t m, int64_t b) {
 Plan plan(int64_t T, int64_t D, int64_t V, int io, bool bwd, char *base) {
     Plan p = {};
     const bool wide = io == IO_F32;
-    const int64_t e = wide ? 4 : 2, slab = wide ? 1 : LogitTile<IO_F16>::KS, rows = wide ? (bwd ? 64 : side32(T, V)) : LogitTile<IO_F16>::BM;
+    const int64_t e = wide ? 4 : 2, slab = wide ? 1 : LogitTile<IO_F16, 256>::KS, rows = bwd ? (wide ? 64 : 256) : (wide ? side32(T, V) : side16(T, V));
     p.kD = wide ? (D < 4 ? 4 : D) : ceil_to(D, slab);  // (fp32: a row holds one vector at least)
     p.Tp = ceil_to(T, slab);
     size_t at = 0;
@@ -889,23 +927,37 @@ Plan plan(int64_t T, int64_t D, int64_t V, int io, bool bwd, char *base) {
         p.piece = ceil_to((V + n - 1) / n, rows);
         p.pieces = (V + p.piece - 1) / p.piece;
         p.g = take(p.Tp * p.piece * e);
-        // the number of ranges that fills the chip best with a piece's tiles
-        // (one more range: one more sum to write and read)
-        int64_t splits = 1;
+        p.side = 256;
+        int64_t splits = 1, wsplits = 1;
         if (!wide) {
-            using G = GradTile<IO_F16, false>;
-            const int64_t rows_d = (D + G::BM - 1) / G::BM, ndx = rows_d * ((T + G::BN - 1) / G::BN);
-            const int64_t ndw = rows_d * ((p.piece + G::BN - 1) / G::BN), kv = ceil_to(p.piece, 64) / 64;
-            int64_t best = makespan(ndx, kv, ndw, p.Tp / 64);
-            for (int64_t k = 2; k <= 8 && k * 8 <= kv; ++k) {
-                const int64_t m = makespan(ndx * k, (kv + k - 1) / k, ndw, p.Tp / 64);
-                if (m * 20 < best * 19) best = m, splits = k;
-            }
+            const int64_t kv = ceil_to(p.piece, 64) / 64, kt = p.Tp / 64;  // slabs of dx's and of dw's sums
+            const auto tiles = [&](int64_t rows) { return (D + p.side - 1) / p.side * ((rows + p.side - 1) / p.side); };
+            const auto work = [&](int64_t side) { return p.side = side, tiles(T) * kv + tiles(p.piece) * kt; };
+            // bf16, us of the backward pass, sides 256, 128 and 64 (slabs per unit):
+            //   1000 x 2048 x 8000   148  153  213  (32)    300 x 777 x 8000   80  66  60  (9, of 128)
+            //   1000 x 256 x 50021   196  166  237  (24)    1000 x 777 x 1000  77  51  38  (3, of 128)
+            // and where D leaves half of the larger tile empty, 256 and 128:
+            //   3000 x 100 x 50021   381  321
+            const int64_t w256 = work(256), w128 = work(128), w64 = work(64);
+            p.side = w256 >= 30 * 256 && 10 * w128 >= 33 * w256 ? 256 : (w128 >= 8 * 512 && 2 * w64 >= 5 * w128 ? 128 : 64);
+            const int64_t units = p.side == 256 ? 256 : 512;  // blocks on the chip at once
+            // the numbers of ranges that fill the chip best (a range more is a sum
+            // more to write and to read, so it has to save a twentieth)
+            const int64_t ndx = tiles(T), ndw = tiles(p.piece);
+            int64_t best = makespan(units, ndx, kv, ndw, kt);
+            for (int64_t j = 1; j <= 32 && (j == 1 || (ndw < units && j * p.piece * D <= 1 << 22 && j * 4 <= kt)); j *= 2)
+                for (int64_t k = 1; k <= 64 && (k <= 8 || k * T * D <= 1 << 22) && (k == 1 || k * 4 <= kv); k += k < 8 ? 1 : k / 4) {
+                    const int64_t m = makespan(units, ndx * k, (kv + k - 1) / k, ndw * j, (kt + j - 1) / j);
+                    if (m * 20 < best * 19) best = m, splits = k, wsplits = j;
+                }
         }
         const int64_t k0 = ceil_to(V < p.piece ? V : p.piece, 64);  // the longest piece's
         p.range = ceil_to((k0 + splits - 1) / splits, 64);
         p.ranges = (k0 + p.range - 1) / p.range;
+        p.wrange = ceil_to((p.Tp + wsplits - 1) / wsplits, 64);
+        p.wranges = (p.Tp + p.wrange - 1) / p.wrange;
         p.accum = (float *)take(!wide && (p.pieces > 1 || p.ranges > 1) ? p.ranges * T * D * 4 : 0);
+        p.waccum = (float *)take(!wide && p.wranges > 1 ? p.wranges * p.piece * D * 4 : 0);
         p.scale = (float *)take(8);
     }
     p.bytes = at;
@@ -921,7 +973,7 @@ hipError_t padded(const void *src, char *dst, int64_t R, int64_t D, int64_t kD, 
     *out = (const char *)src;
     if (kD == D) return hipSuccess;
     *out = dst;
-    return launch(k_xent_pad<E>, dim3(blocks(R * kD, 256)), dim3(256), 0, s, (const E *)src, (E *)dst, R, D, kD);
+    return launch(k_xent_pad<E>, dim3(blocks(R * kD, 256 * 16 / (int64_t)sizeof(E))), dim3(256), 0, s, (const E *)src, (E *)dst, R, D, kD);
 }
 
 template <int IO>
@@ -938,9 +990,9 @@ hipError_t fwd_io(const void *x, const void *w, const Labels &lab, float *loss, 
         e = launch(bt == 32 ? k_xent_stats32<32> : k_xent_stats32<64>, dim3(blocks(T, bt) * blocks(V, bt)), dim3(256), 0, s,
                    (const float *)xr, (const float *)wr, p.kD, lab, p.part, p.hit, T, D, V);
     } else {
-        using L = LogitTile<IO>;
-        e = launch(k_xent_stats16<IO>, dim3(blocks(V, L::BM) * blocks(T, L::BN)), dim3(L::NT), 0, s, xr, wr, ld,
-                   lab, p.part, p.hit, T, V);
+        const int64_t bt = side16(T, V);
+        e = launch(bt == 256 ? k_xent_stats16<IO, 256> : (bt == 128 ? k_xent_stats16<IO, 128> : k_xent_stats16<IO, 64>),
+                   dim3(blocks(V, bt) * blocks(T, bt)), dim3(bt == 256 ? 512 : 256), 0, s, xr, wr, ld, lab, p.part, p.hit, T, V);
     }
     if (e != hipSuccess) return e;
     return launch(k_xent_join, dim3(blocks(T, 64)), dim3(1024), 0, s, p.part, p.hit, lab, loss, lse, T, p.tiles);
@@ -973,21 +1025,27 @@ hipError_t bwd_io(const void *x, const void *w, const Labels &lab, const float *
                        xf, wf + v0 * p.kD, p.kD, (const float *)p.g, (float *)dx, (float *)dw + v0 * D, p.scale, T, D, nv,
                        ndx, first);
         } else {
-            using L = LogitTile<IO>;
-            using G = GradTile<IO, false>;
             const int64_t kv = ceil_to(nv, 64);
-            e = launch(k_xent_grad16<IO>, dim3(blocks(nv, L::BM) * blocks(T, L::BN)), dim3(L::NT), 0, s, xr, wr,
+            int64_t bt = side16(T, nv);
+            e = launch(bt == 256 ? k_xent_grad16<IO, 256> : (bt == 128 ? k_xent_grad16<IO, 128> : k_xent_grad16<IO, 64>),
+                       dim3(blocks(nv, bt) * blocks(T, bt)), dim3(bt == 256 ? 512 : 256), 0, s, xr, wr,
                        ld, lab, lse, dloss, p.scale, (E *)p.g, kv, T, p.Tp, v0, nv);
             if (e != hipSuccess) break;
             // ranges of whole slabs, as long as the first piece's (a shorter last piece has fewer)
             const int64_t kx = p.range, parts = (kv + kx - 1) / kx;
-            const int64_t rows = blocks(D, G::BM), ndx = rows * blocks(T, G::BN) * parts, ndw = rows * blocks(nv, G::BN);
-            e = launch(k_xent_products16<IO>, dim3((unsigned)(ndx + ndw)), dim3(G::NT), 0, s, xr, wr + v0 * ld, ld, p.g,
-                       kv, (E *)dx, (E *)dw + v0 * D, p.accum, p.scale, T, p.Tp, D, nv, kv, kx, (int)parts, ndx, first,
-                       p.accum ? 0 : 1);
+            bt = p.side;
+            const int64_t rows = blocks(D, bt), ndx = rows * blocks(T, bt) * parts, ndw = rows * blocks(nv, bt) * p.wranges;
+            e = launch(bt == 256 ? k_xent_products16<IO, 256>
+                                 : (bt == 128 ? k_xent_products16<IO, 128> : k_xent_products16<IO, 64>),
+                       dim3((unsigned)(ndx + ndw)), dim3(bt == 256 ? 512 : 256), 0, s, xr, wr + v0 * ld, ld, p.g,
+                       kv, (E *)dx, (E *)dw + v0 * D, p.accum, p.waccum, p.scale, T, p.Tp, D, nv, kv, kx, (int)parts, p.wrange, (int)p.wranges, ndx,
+                       first, p.accum ? 0 : 1);
             if (e == hipSuccess && last && p.accum)
                 e = launch(k_xent_dx<IO>, dim3(blocks(T * D, 1024)), dim3(256), 0, s, p.accum, p.scale, (E *)dx, T * D,
                            (int)p.ranges);
+            if (e == hipSuccess && p.waccum)
+                e = launch(k_xent_dx<IO>, dim3(blocks(nv * D, 1024)), dim3(256), 0, s, p.waccum, p.scale, (E *)dw + v0 * D,
+                           nv * D, (int)p.wranges);
         }
     }
     return e;
