@@ -817,40 +817,36 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
     }
 }
 
-// dB, dC: the sets' sums, in order; M = B*G*S*N values each, dB's in the blocks
-// y = 0 and dC's in y = 1.  Bound by reading the partial sums, eight loads of
-// a thread at a time (one at a time: 33 us where this takes 11.5, 4 x 2560 x
-// 2048 with 16 modes and 64 sets: 67 MB).
+// What the blocks of k_sel_bwd left apart, joined in order.  Blocks y = 0 and 1:
+// dB and dC, the sets' sums, M = B*G*S*N values each; bound by reading the
+// partial sums, eight loads of a thread at a time (11.5 us for 67 MB at 4 x 2560
+// x 2048 with 16 modes and 64 sets; one load at a time took 33).  y = 2: dA, dD,
+// ddt_bias, sums over the batch.
 template <int IO>
-__global__ __launch_bounds__(256) void k_sel_join(const float *__restrict__ pB, const float *__restrict__ pC,
-                                                  typename io_elem<IO>::T *__restrict__ dB,
-                                                  typename io_elem<IO>::T *__restrict__ dC, int64_t M, int sets) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= M) return;
-    const float *const p = (blockIdx.y ? pC : pB) + i;
-    float sum = 0.f;
-#pragma unroll 8
-    for (int s = 0; s < sets; ++s) sum += p[s * M];
-    (blockIdx.y ? dC : dB)[i] = from_f<IO>(sum);
-}
-
-// dA, dD, ddt_bias: sums over the batch, in order.
-__global__ __launch_bounds__(256) void k_sel_params(const float *__restrict__ pA, const float *__restrict__ pDb,
-                                                    float *__restrict__ dA, float *__restrict__ dD,
-                                                    float *__restrict__ ddt_bias, int64_t B, int64_t H, int S) {
+__global__ __launch_bounds__(256) void k_sel_join(const SelBwdWs ws, typename io_elem<IO>::T *__restrict__ dB,
+                                                  typename io_elem<IO>::T *__restrict__ dC, float *__restrict__ dA,
+                                                  float *__restrict__ dD, float *__restrict__ ddt_bias, int64_t M,
+                                                  int64_t B, int64_t H, int S) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, HS = H * S;
-    if (i < HS) {
+    if (blockIdx.y < 2) {
+        if (i >= M) return;
+        const float *const p = (blockIdx.y ? ws.dC : ws.dB) + i;
+        float sum = 0.f;
+#pragma unroll 8
+        for (int s = 0; s < ws.sets; ++s) sum += p[s * M];
+        (blockIdx.y ? dC : dB)[i] = from_f<IO>(sum);
+    } else if (i < HS) {
         float s = 0.f;
 #pragma unroll 4
-        for (int64_t b = 0; b < B; ++b) s += pA[b * HS + i];
+        for (int64_t b = 0; b < B; ++b) s += ws.dA[b * HS + i];
         dA[i] = s;
     } else if (i < HS + H) {
         const int64_t h = i - HS;
         float s = 0.f, t = 0.f;
 #pragma unroll 4
         for (int64_t b = 0; b < B; ++b) {
-            s += pDb[(b * H + h) * 2];
-            t += pDb[(b * H + h) * 2 + 1];
+            s += ws.dDb[(b * H + h) * 2];
+            t += ws.dDb[(b * H + h) * 2 + 1];
         }
         if (dD) dD[h] = s;
         if (ddt_bias) ddt_bias[h] = t;
@@ -996,14 +992,9 @@ hipError_t bwd_io(const SelArgs &a, const float *saved, const void *dy, const fl
                    n0 + kModes >= a.S ? 1 : 0);
         if (e != hipSuccess) return e;
     }
-    const int64_t M = a.B * a.G * a.S * a.N;
-    if (M > 0) {
-        const hipError_t e = launch(k_sel_join<IO>, dim3((unsigned)((M + 255) / 256), 2), dim3(256), 0, s, w.dB, w.dC,
-                                    (T *)g.dB, (T *)g.dC, M, w.sets);
-        if (e != hipSuccess) return e;
-    }
-    return launch(k_sel_params, dim3((unsigned)((a.H * (a.S + 1) + 255) / 256)), dim3(256), 0, s, w.dA, w.dDb, g.dA,
-                  g.dD, g.ddt_bias, a.B, a.H, a.S);
+    const int64_t M = a.B * a.G * a.S * a.N, P = a.H * (a.S + 1);
+    return launch(k_sel_join<IO>, dim3((unsigned)(((M > P ? M : P) + 255) / 256), 3), dim3(256), 0, s, w, (T *)g.dB,
+                  (T *)g.dC, g.dA, g.dD, g.ddt_bias, M, a.B, a.H, a.S);
 }
 
 }  // namespace
