@@ -9,6 +9,15 @@
 // the vocabulary, the tiles of x w^T are formed again, G of the piece goes to
 // the workspace, and two products give dw of the piece and the piece's part
 // of dx.  Four products of 2 T D V operations each in all: matrix-core bound.
+// Logits, maxima, sums and the products' sums are fp32.  With 16-bit inputs G is
+// rounded to them, as the operand of two 16-bit products; its error averages out
+// over the sums, and dx and dw are rounded once more.
+//
+// Measured in bf16 at 8192 x 768 x 50021: logits and statistics 655 us (960
+// TFLOP/s; a library product of that size 986), G 2 x 400 us, dx and dw 2 x 750 us
+// (840 TFLOP/s; the library's 1066 and 1254); fp16 at 4096 x 2560 x 32768 forward
+// 605 us (1140 TFLOP/s; 1433); fp32 at 4096 x 768 x 8192 109 TFLOP/s forward, 115
+// backward (154 at 8192^3).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -578,8 +587,11 @@ using GradTile = Side<IO, BT, true, G_KMAJOR>;
 template <int BT>
 constexpr int kThreads16 = BT == 256 ? 512 : 256;
 
-// As k_xent_stats with w's rows as the tile's rows and tokens as its columns:
-// a lane holds four consecutive rows of w for a token.
+// As k_xent_stats32, with w's rows as the tile's rows and tokens as its columns:
+// a lane holds four consecutive rows of w for a token, so it reduces most of the
+// tile's rows by itself and two shuffles finish a wave's.  The reduction (one
+// exponential per logit) takes about 150 of 655 us at 8192 x 768 x 50021, which
+// one block per compute unit does not hide.
 template <int IO, int BT>
 __global__ __launch_bounds__(kThreads16<BT>, BT == 256 ? 1 : 2) void k_xent_stats16(const char *x, const char *w, int64_t ld,
                                                                        const Labels lab, float2 *__restrict__ part,
@@ -649,7 +661,8 @@ __global__ __launch_bounds__(kThreads16<BT>, BT == 256 ? 1 : 2) void k_xent_stat
 }
 
 // G of the vocabulary piece [v0, v0 + nv): g[t][v - v0], rows of ldg elements;
-// zero for nv <= v - v0 < ldg and for T <= t < Tp.
+// zero for nv <= v - v0 < ldg and for T <= t < Tp.  400 us for 8192 x 25088 of
+// width 768, about 70 more than the statistics' half: writing 411 MB.
 template <int IO, int BT>
 __global__ __launch_bounds__(kThreads16<BT>, BT == 256 ? 1 : 2) void k_xent_grad16(const char *x, const char *w, int64_t ld,
                                                                       const Labels lab, const float *__restrict__ lse,
@@ -836,6 +849,7 @@ __global__ __launch_bounds__(256) void k_xent_pad(const E *__restrict__ src, E *
     *reinterpret_cast<Pack<E, n> *>(dst + r * ldd + c) = q;
 }
 
+// dw of no tokens.
 template <class E>
 __global__ __launch_bounds__(256) void k_xent_zero(E *__restrict__ p, int64_t n) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
