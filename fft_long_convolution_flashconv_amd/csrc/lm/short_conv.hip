@@ -20,11 +20,19 @@ constexpr int kThreads = 256;
 constexpr int kTaps = 4;  // the largest W
 
 // Threads of a block along one row (a power of two that covers it, up to the
-// block), the others take rows: short rows leave no thread idle.
-__host__ __device__ inline int threads_per_row(int64_t nvec) {
-    int t = 1;
-    while (t < kThreads && t < nvec) t <<= 1;
+// block), the others take rows: short rows leave few threads idle.
+__host__ __device__ inline int threads_per_row_log2(int64_t nvec) {
+    int t = 0;
+    while (1 << t < kThreads && 1 << t < nvec) ++t;
     return t;
+}
+
+// This thread's row among the block's.  WAVE: a wave has threads of one row, whose
+// addresses, length and taps are then the wave's own (scalar).
+template <bool WAVE>
+__device__ __forceinline__ int row_of(int tpr_log2) {
+    const int sub = (int)threadIdx.x >> tpr_log2;
+    return WAVE ? __builtin_amdgcn_readfirstlane(sub) : sub;
 }
 
 __device__ __forceinline__ int64_t row_len(const int32_t *lengths, int64_t b, int64_t N) {
@@ -76,25 +84,26 @@ __device__ __forceinline__ void before_plain(const typename io_elem<IO>::T *x, i
 __device__ __forceinline__ int few(int64_t n) { return (int)(n < 0 ? 0 : (n > 64 ? 64 : n)); }
 
 // A thread takes one 16-byte vector of a row, and the W - 1 elements before it
-// from the caches (one more load; two vectors per thread: 22.8 us where this
-// takes 19.4).  4 x 2560 x 2048, bf16, 4 taps: 19.4 us, 4.3 TB/s (a copy reaches
-// 5.1); 8 x 768 x 1024 fp16: 10.2 us.
-template <int IO, int W>
+// from the caches (one more load; two vectors per thread were a sixth slower).
+// 4 x 2560 x 2048, bf16, 4 taps: 17.1 us, 4.9 TB/s (a copy reaches 5.1); with a
+// wave's addresses and masks on the vector ALUs, 29 instructions per element,
+// these bounded it: 21.6 us.  8 x 768 x 1024 fp16: 9.2 us.
+template <int IO, int W, bool WAVE>
 __global__ __launch_bounds__(kThreads) void k_short_conv(const typename io_elem<IO>::T *__restrict__ x,
                                                          const typename io_elem<IO>::T *__restrict__ x_in,
                                                          const float *__restrict__ w, const float *__restrict__ bias,
                                                          const int32_t *__restrict__ lengths,
                                                          typename io_elem<IO>::T *__restrict__ y,
                                                          typename io_elem<IO>::T *__restrict__ x_out, int64_t B,
-                                                         int64_t H, int64_t N, int silu, int tpr) {
+                                                         int64_t H, int64_t N, int silu, int tpr_log2) {
     using T = typename io_elem<IO>::T;
     constexpr int V = 16 / (int)sizeof(T);
-    const uint32_t row = blockIdx.x * (uint32_t)(kThreads / tpr) + threadIdx.x / (uint32_t)tpr;
+    const int tpr = 1 << tpr_log2, tl = (int)threadIdx.x & (tpr - 1);
+    const uint32_t row = blockIdx.x * (uint32_t)(kThreads >> tpr_log2) + row_of<WAVE>(tpr_log2);
     if (row >= (uint32_t)(B * H)) return;
     const uint32_t b = row / (uint32_t)H, h = row - b * (uint32_t)H;
     const int64_t r = row, len = row_len(lengths, b, N);
     const T *xr = x + r * N, *xi = x_in ? x_in + r * (W - 1) : nullptr;
-    const int tl = (int)threadIdx.x % tpr;
     float tap[W];
 #pragma unroll
     for (int k = 0; k < W; ++k) tap[k] = w[(int64_t)h * W + k];
@@ -103,26 +112,32 @@ __global__ __launch_bounds__(kThreads) void k_short_conv(const typename io_elem<
         for (int j = tl; j < W - 1; j += tpr) x_out[r * (W - 1) + j] = from_f<IO>(at_ext<IO, W>(xr, xi, len - (W - 1) + j));
     for (int64_t t0 = ((int64_t)blockIdx.y * tpr + tl) * V; t0 < N; t0 += (int64_t)gridDim.y * tpr * V) {
         float v[V + W - 1], cur[V], o[V];
-        const bool plain = __all(t0 + V <= len && (t0 > 0 || !xi));  // (of the wave: its loads need no choice)
-        if (plain) {
+        const auto sums = [&] {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i + W - 1] = cur[i];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float p = bs;
+#pragma unroll
+                for (int k = 0; k < W; ++k) p = fmaf(tap[k], v[i + W - 1 - k], p);
+                o[i] = silu ? p * sigmoid(p) : p;
+            }
+        };
+        if (__all(t0 + V <= len && (t0 > 0 || !xi))) {  // (of the wave: its loads and stores need no choice)
             ld_row<IO, V>(xr + t0, cur);
             before_plain<IO, W>(xr, t0, v);
+            sums();
+            st_row<IO, V>(y + r * N + t0, o, V);
         } else {
             ld_row<IO, V>(xr + t0, cur, len - t0);
             before<IO, W>(xr, xi, t0, len, v);
+            sums();
+            const int valid = few(len - t0);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i >= valid) o[i] = 0.f;
+            st_row<IO, V>(y + r * N + t0, o, N - t0);
         }
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i + W - 1] = cur[i];
-        const int valid = few(len - t0);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float p = bs;
-#pragma unroll
-            for (int k = 0; k < W; ++k) p = fmaf(tap[k], v[i + W - 1 - k], p);
-            if (silu) p *= sigmoid(p);
-            o[i] = i < valid ? p : 0.f;
-        }
-        st_row<IO, V>(y + r * N + t0, o, N - t0);
     }
 }
 
@@ -139,20 +154,21 @@ __device__ __forceinline__ float act_bwd(float p, float dy, int silu) {
 //   dx_s = sum_i w_i dp_{s+i},  dw_i = sum_{b,t} dp_t x_{t-i},  dbias = sum dp.
 // A thread forms dp of its own steps and of the W - 1 after them, which costs
 // 3 of 11 activations at 4 taps and saves an exchange between threads.
-// 4 x 2560 x 2048, bf16, 4 taps: 32.7 us, 3.9 TB/s; the activations and the sums
-// of the taps' gradients keep the vector ALUs busy for two thirds of it.
-template <int IO, int W>
+// 4 x 2560 x 2048, bf16, 4 taps: 29.2 us, 4.3 TB/s, vector ALUs and memory both
+// nearly full.
+template <int IO, int W, bool WAVE>
 __global__ __launch_bounds__(kThreads) void k_short_conv_bwd(
     const typename io_elem<IO>::T *__restrict__ x, const typename io_elem<IO>::T *__restrict__ x_in,
     const float *__restrict__ w, const float *__restrict__ bias, const int32_t *__restrict__ lengths,
     const typename io_elem<IO>::T *__restrict__ dy, const typename io_elem<IO>::T *__restrict__ dx_out,
     typename io_elem<IO>::T *__restrict__ dx, typename io_elem<IO>::T *__restrict__ dx_in, float *__restrict__ part,
-    float *__restrict__ dw, float *__restrict__ dbias, int64_t B, int64_t H, int64_t N, int silu, int tpr,
+    float *__restrict__ dw, float *__restrict__ dbias, int64_t B, int64_t H, int64_t N, int silu, int tpr_log2,
     int64_t pieces) {
     using T = typename io_elem<IO>::T;
     constexpr int V = 16 / (int)sizeof(T), E = V + W - 1;
     const int64_t h = blockIdx.x;
-    const int rpb = kThreads / tpr, tl = (int)threadIdx.x % tpr, sub = (int)threadIdx.x / tpr;
+    const int tpr = 1 << tpr_log2, rpb = kThreads >> tpr_log2, tl = (int)threadIdx.x & (tpr - 1);
+    const int sub = row_of<WAVE>(tpr_log2);
     float tap[W], sw[W], sb = 0.f;
 #pragma unroll
     for (int k = 0; k < W; ++k) {
@@ -170,29 +186,9 @@ __global__ __launch_bounds__(kThreads) void k_short_conv_bwd(
         const T *xr = x + r * N, *xi = x_in ? x_in + r * (W - 1) : nullptr, *gr = dy + r * N;
         // v[j]: x at t0 - (W-1) + j, g[j]: dy at t0 + j; the neighbours'
         // elements come from the caches
-        float v[E + W - 1], g[E], dp[E], o[V];
-        {
-            float cur[V], gc[V], near[4], gn[4];
-            const int64_t end = t0 + V;
-            if (__all((end + 4 <= len || (end == len && len == N)) && (t0 > 0 || !xi))) {
-                // (of the wave: its loads need no choice; past the row's end the
-                // thread's own first steps stand in, whose dp is zero)
-                ld_row<IO, V>(xr + t0, cur);
-                ld_row<IO, V>(gr + t0, gc);
-                if constexpr (W > 1) {
-                    ld_row<IO, 4>(xr + (end < len ? end : t0), near);
-                    ld_row<IO, 4>(gr + (end < len ? end : t0), gn);
-                }
-                before_plain<IO, W>(xr, t0, v);
-            } else {
-                ld_row<IO, V>(xr + t0, cur, len - t0);
-                ld_row<IO, V>(gr + t0, gc, len - t0);
-                if constexpr (W > 1) {
-                    ld_row<IO, 4>(xr + end, near, len - end);
-                    ld_row<IO, 4>(gr + end, gn, len - end);
-                }
-                before<IO, W>(xr, xi, t0, len, v);
-            }
+        float v[E + W - 1], g[E], dp[E], o[V], cur[V], gc[V], near[4], gn[4];
+        const int64_t end = t0 + V;
+        const auto grads = [&](auto mask) {  // mask(j): whether step t0 + j counts
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 v[j + W - 1] = cur[j];
@@ -203,37 +199,63 @@ __global__ __launch_bounds__(kThreads) void k_short_conv_bwd(
                 v[j + V + W - 1] = near[j];
                 g[j + V] = gn[j];
             }
-        }
-        const int valid = few(len - t0);
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            float p = bs;
+            for (int j = 0; j < E; ++j) {
+                float p = bs;
 #pragma unroll
-            for (int k = 0; k < W; ++k) p = fmaf(tap[k], v[j + W - 1 - k], p);
-            dp[j] = j < valid ? act_bwd(p, g[j], silu) : 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float a = 0.f;
-#pragma unroll
-            for (int k = 0; k < W; ++k) a = fmaf(tap[k], dp[j + k], a);
-            o[j] = a;
-            sb += dp[j];
-#pragma unroll
-            for (int k = 0; k < W; ++k) sw[k] = fmaf(dp[j], v[j + W - 1 - k], sw[k]);
-        }
-        // the saved last inputs are inputs len-(W-1) .. len-1
-        if (dx_out && valid < V + W) {
+                for (int k = 0; k < W; ++k) p = fmaf(tap[k], v[j + W - 1 - k], p);
+                dp[j] = mask(j) ? act_bwd(p, g[j], silu) : 0.f;
+            }
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const int q = j - (valid - (W - 1));
-                if (q >= 0 && q < W - 1) o[j] += to_f<IO>(dx_out[r * (W - 1) + q]);
-            }
-        }
+                float a = 0.f;
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (j >= valid) o[j] = 0.f;
-        st_row<IO, V>(dx + r * N + t0, o, N - t0);
+                for (int k = 0; k < W; ++k) a = fmaf(tap[k], dp[j + k], a);
+                o[j] = a;
+                sb += dp[j];
+#pragma unroll
+                for (int k = 0; k < W; ++k) sw[k] = fmaf(dp[j], v[j + W - 1 - k], sw[k]);
+            }
+        };
+        // the saved last inputs are inputs len-(W-1) .. len-1
+        const auto last_inputs = [&](int valid) {
+            if (dx_out && valid < V + W) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const int q = j - (valid - (W - 1));
+                    if (q >= 0 && q < W - 1) o[j] += to_f<IO>(dx_out[r * (W - 1) + q]);
+                }
+            }
+        };
+        if (__all((end + 4 <= len || (end == len && len == N)) && (t0 > 0 || !xi))) {
+            // (of the wave: its loads and stores need no choice; past the row's end
+            // the thread's own first steps stand in, which do not count)
+            ld_row<IO, V>(xr + t0, cur);
+            ld_row<IO, V>(gr + t0, gc);
+            if constexpr (W > 1) {
+                ld_row<IO, 4>(xr + (end < len ? end : t0), near);
+                ld_row<IO, 4>(gr + (end < len ? end : t0), gn);
+            }
+            before_plain<IO, W>(xr, t0, v);
+            grads([&](int j) { return j < V || end < len; });
+            last_inputs(few(len - t0));
+            st_row<IO, V>(dx + r * N + t0, o, V);
+        } else {
+            ld_row<IO, V>(xr + t0, cur, len - t0);
+            ld_row<IO, V>(gr + t0, gc, len - t0);
+            if constexpr (W > 1) {
+                ld_row<IO, 4>(xr + end, near, len - end);
+                ld_row<IO, 4>(gr + end, gn, len - end);
+            }
+            before<IO, W>(xr, xi, t0, len, v);
+            const int valid = few(len - t0);
+            grads([&](int j) { return j < valid; });
+            last_inputs(valid);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (j >= valid) o[j] = 0.f;
+            st_row<IO, V>(dx + r * N + t0, o, N - t0);
+        }
         if (dx_in && t0 == 0) {
             // saved input j stands at position j - (W-1): it meets the steps
             // 0 .. j through the taps W-1-j .. W-1; with len < W-1 it is also
@@ -316,15 +338,15 @@ __global__ __launch_bounds__(kThreads) void k_short_conv_step(
     y[b * H + h] = from_f<IO>(p);
 }
 
-int bwd_splits(int64_t B, int64_t H, int64_t N, int64_t *pieces, int *tpr, int V) {
+int bwd_splits(int64_t B, int64_t H, int64_t N, int64_t *pieces, int *tpr_log2, int V) {
     const int64_t nvec = (N + V - 1) / V;
-    *tpr = threads_per_row(nvec);
-    *pieces = nvec > 0 ? (nvec + *tpr - 1) / *tpr : 1;
-    const int rpb = kThreads / *tpr;
+    *tpr_log2 = threads_per_row_log2(nvec);
+    const int tpr = 1 << *tpr_log2, rpb = kThreads / tpr;
+    *pieces = nvec > 0 ? (nvec + tpr - 1) / tpr : 1;
     const int64_t tasks = (B + rpb - 1) / rpb * *pieces;
     // about 2048 blocks fill the chip; each join costs one more partial sum, and
-    // one more launch (4 x 2560 x 2048: one block per channel 37.4 us, two 39.5
-    // and 4.6 for the sums, four 43.7 and 4.6)
+    // one more launch (4 x 2560 x 2048, before the scalar addresses: one block per
+    // channel 38.0 us, two 39.5 and 4.6 for the sums, four 43.7 and 4.6)
     int64_t k = (2048 + H - 1) / H;
     if (k > tasks) k = tasks;
     if (k > 256) k = 256;
@@ -345,12 +367,12 @@ static hipError_t short_conv_taps(const ShortConvArgs &a, void *y, void *x_out, 
     using T = typename io_elem<IO>::T;
     constexpr int V = 16 / (int)sizeof(T);
     const int64_t nvec = (a.N + V - 1) / V, R = a.B * a.H;
-    const int tpr = threads_per_row(nvec);
+    const int lg = threads_per_row_log2(nvec), tpr = 1 << lg;
     const int64_t rows = (R + kThreads / tpr - 1) / (kThreads / tpr);
     int64_t gy = (nvec + tpr - 1) / tpr;
     gy = gy < 1 ? 1 : (gy > 4096 ? 4096 : gy);
-    return launch(k_short_conv<IO, W>, dim3((unsigned)rows, (unsigned)gy), dim3(kThreads), 0, s, (const T *)a.x,
-                  (const T *)a.x_in, a.w, a.bias, a.lengths, (T *)y, (T *)x_out, a.B, a.H, a.N, a.silu, tpr);
+    return launch(tpr >= 64 ? k_short_conv<IO, W, true> : k_short_conv<IO, W, false>, dim3((unsigned)rows, (unsigned)gy), dim3(kThreads), 0, s, (const T *)a.x,
+                  (const T *)a.x_in, a.w, a.bias, a.lengths, (T *)y, (T *)x_out, a.B, a.H, a.N, a.silu, lg);
 }
 
 template <int IO>
@@ -378,11 +400,11 @@ static hipError_t short_conv_bwd_taps(const ShortConvArgs &a, const void *dy, co
                                       float *dbias, void *dx_in, float *part, hipStream_t s) {
     using T = typename io_elem<IO>::T;
     int64_t pieces;
-    int tpr;
-    const int K = bwd_splits(a.B, a.H, a.N, &pieces, &tpr, 16 / (int)sizeof(T));
-    const hipError_t e = launch(k_short_conv_bwd<IO, W>, dim3((unsigned)a.H, (unsigned)K), dim3(kThreads), 0, s,
+    int tpr_log2;
+    const int K = bwd_splits(a.B, a.H, a.N, &pieces, &tpr_log2, 16 / (int)sizeof(T));
+    const hipError_t e = launch(tpr_log2 >= 6 ? k_short_conv_bwd<IO, W, true> : k_short_conv_bwd<IO, W, false>, dim3((unsigned)a.H, (unsigned)K), dim3(kThreads), 0, s,
                                 (const T *)a.x, (const T *)a.x_in, a.w, a.bias, a.lengths, (const T *)dy,
-                                (const T *)dx_out, (T *)dx, (T *)dx_in, part, dw, dbias, a.B, a.H, a.N, a.silu, tpr,
+                                (const T *)dx_out, (T *)dx, (T *)dx_in, part, dw, dbias, a.B, a.H, a.N, a.silu, tpr_log2,
                                 pieces);
     if (e != hipSuccess || K == 1) return e;
     return launch(k_short_conv_sums, dim3((unsigned)((a.H * (kTaps + 1) + 255) / 256)), dim3(256), 0, s, part, dw,
