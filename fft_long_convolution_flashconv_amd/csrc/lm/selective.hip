@@ -141,6 +141,25 @@ __device__ __forceinline__ void unpack(const Raw<IO, n> &r, float (&o)[n]) {
     }
 }
 
+// o = r times u, element by element.  fp16: one instruction converts and
+// multiplies (the compiler converts first).
+template <int IO, int n>
+__device__ __forceinline__ void times(const Raw<IO, n> &r, const float (&u)[n], float (&o)[n]) {
+    if constexpr (IO == IO_F16) {
+#pragma unroll
+        for (int i = 0; i < n; i += 2) {
+            asm("v_fma_mix_f32 %0, %1, %2, 0 op_sel_hi:[1,0,0]" : "=v"(o[i]) : "v"(r.w[i / 2]), "v"(u[i]));
+            asm("v_fma_mix_f32 %0, %1, %2, 0 op_sel:[1,0,0] op_sel_hi:[1,0,0]"
+                : "=v"(o[i + 1])
+                : "v"(r.w[i / 2]), "v"(u[i + 1]));
+        }
+    } else {
+        unpack<IO, n>(r, o);
+#pragma unroll
+        for (int i = 0; i < n; ++i) o[i] *= u[i];
+    }
+}
+
 // Keeps the values' computation here: the compiler otherwise moves it past
 // later work, and its operands stay in registers for all that time.
 template <int n>
@@ -232,13 +251,12 @@ __device__ __forceinline__ void scan_mode(Raw<IO, kIT> &rB, Raw<IO, kIT> &rC, fl
 #pragma unroll
         for (int i = 0; i < Raw<IO, IT>::kWords; ++i) rB.w[i] &= own.w[i];  // (what is passed over may be NaN)
     }
-    unpack<IO, IT>(rB, w);
+    times<IO, IT>(rB, u, w);
     hold(w);
     nextB();
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         a[i] = exp2_(d[i] * A2);
-        w[i] *= u[i];
         Q = fmaf(a[i], Q, w[i]);
     }
     scan_states<LPR>(P, Q);
@@ -387,8 +405,8 @@ __device__ __forceinline__ void scan_piece(const SelK<typename io_elem<IO>::T> &
 // mode's B and C are in flight while one is worked on; three and more modes ahead
 // spilled registers, and B and C staged in LDS for the block's rows gained
 // nothing.
-// Measured, 16 modes with a gate: 8 x 768 x 1024 fp16 38.8 us, 1 x 1024 x 65536
-// bf16 486 us, 4 x 2560 x 2048 bf16 with saved states 150 us: 2.2 to 2.6 million
+// Measured, 16 modes with a gate: 8 x 768 x 1024 fp16 36.9 us, 1 x 1024 x 65536
+// bf16 486 us, 4 x 2560 x 2048 bf16 with saved states 150 us: 2.2 to 2.7 million
 // million mode-steps a second, the vector ALUs issuing about two cycles of three.
 template <int IO, int LPR, Share SH>
 __global__ __launch_bounds__(256, IO == IO_F32 || LPR == 16 ? 2 : 3) void k_sel_scan(const SelK<typename io_elem<IO>::T> k,
