@@ -443,6 +443,9 @@ def _scratch(workspace, need: int, like) -> torch.Tensor:
     return torch.empty(max(need, 1), device=like.device, dtype=torch.uint8)
 
 
+_Tensor = torch.Tensor
+
+
 def _tensors(dev: int, *specs) -> None:
     """Checks (name, tensor, dtype, shape) of every argument; None passes where an
     argument is optional, its name then ends in "?".  One pass over plain
@@ -452,8 +455,8 @@ def _tensors(dev: int, *specs) -> None:
         if t is None:
             if name[-1] != "?":
                 raise TypeError("%s is required" % name)
-        elif not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-                  and t.get_device() == dev and t.is_cuda):
+        elif not (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                  and t.get_device() == dev):  # (the index of a GPU: -1 elsewhere)
             name = name.rstrip("?")
             _need(t, name, dtype, shape)
             _same_device(**{name: t})
@@ -483,14 +486,15 @@ def _raw_stream(dev: int) -> int:
 
 def _conv_args(x, w, dims: int):
     io = _io(x, "x")
-    if x.dim() != dims:
-        raise ValueError("x must be %s, got %s" % ("[B,H,N]" if dims == 3 else "[B,H]", tuple(x.shape)))
-    H = x.shape[1]
-    if not isinstance(w, torch.Tensor):
+    xs = x.shape
+    if len(xs) != dims:
+        raise ValueError("x must be %s, got %s" % ("[B,H,N]" if dims == 3 else "[B,H]", tuple(xs)))
+    if not isinstance(w, _Tensor):
         raise TypeError("w must be a torch.Tensor")
-    if w.dim() != 2 or w.shape[0] != H or w.shape[1] < 1:
-        raise ValueError("w must be [H,W] with H = %d, got %s" % (H, tuple(w.shape)))
-    return io, H, w.shape[1]
+    H, ws = xs[1], w.shape
+    if len(ws) != 2 or ws[0] != H or ws[1] < 1:
+        raise ValueError("w must be [H,W] with H = %d, got %s" % (H, tuple(ws)))
+    return io, H, ws[1]
 
 
 def short_conv(x, w, bias=None, silu: bool = True, x_in=None, lengths=None, return_state: bool = False, out=None):
@@ -561,18 +565,19 @@ def short_conv_step(x, w, state, bias=None, silu: bool = True, slots=None, state
 
 def _scan_args(u, A, Bm, dims: int):
     io = _io(u, "u")
-    if u.dim() != dims:
-        raise ValueError("u must be %s, got %s" % ("[B,H,N]" if dims == 3 else "[B,H]", tuple(u.shape)))
-    B, H = u.shape[:2]
+    us = u.shape
+    if len(us) != dims:
+        raise ValueError("u must be %s, got %s" % ("[B,H,N]" if dims == 3 else "[B,H]", tuple(us)))
     for t, name in ((A, "A"), (Bm, "Bm")):
-        if not isinstance(t, torch.Tensor):
+        if not isinstance(t, _Tensor):
             raise TypeError("%s must be a torch.Tensor" % name)
-    if A.dim() != 2 or A.shape[0] != H or A.shape[1] < 1:
-        raise ValueError("A must be [H,S] with H = %d, got %s" % (H, tuple(A.shape)))
-    if Bm.dim() != dims + 1 or Bm.shape[1] < 1 or H % Bm.shape[1] != 0:
+    H, As, bs = us[1], A.shape, Bm.shape
+    if len(As) != 2 or As[0] != H or As[1] < 1:
+        raise ValueError("A must be [H,S] with H = %d, got %s" % (H, tuple(As)))
+    if len(bs) != dims + 1 or bs[1] < 1 or H % bs[1] != 0:
         raise ValueError("Bm must be %s with G dividing H = %d, got %s"
-                         % ("[B,G,S,N]" if dims == 3 else "[B,G,S]", H, tuple(Bm.shape)))
-    return io, B, H, A.shape[1], Bm.shape[1]
+                         % ("[B,G,S,N]" if dims == 3 else "[B,G,S]", H, tuple(bs)))
+    return io, us[0], H, As[1], bs[1]
 
 
 def selective_scan(u, dt, A, Bm, C, D=None, z=None, dt_bias=None, softplus: bool = True, x_in=None, lengths=None,
