@@ -455,7 +455,7 @@ __global__ __launch_bounds__(1024) void k_xent_join(const float2 *__restrict__ p
     }
 }
 
-// G is held as a share of the largest |dloss| of a token that counts: with the
+// 16-bit G is held as a share of the largest |dloss| of a token that counts: with the
 // usual equal weights the entry of a label, -(1 - p), is then held almost
 // exactly, and it dominates its row.  fp16 multiplies by 2^15 more, so that
 // probabilities down to 2^-29 stay normal numbers.  scale[0]: the divisor,
@@ -489,7 +489,7 @@ __device__ __forceinline__ float weight(float dloss, float divisor) {
 template <int BT>
 __global__ __launch_bounds__(256, 4) void k_xent_grad32(const float *x, const float *w, int64_t ld, const Labels lab,
                                                      const float *__restrict__ lse, const float *__restrict__ dloss,
-                                                     const float *__restrict__ scale, float *__restrict__ g, int64_t T,
+                                                     float *__restrict__ g, int64_t T,
                                                      int64_t D, int64_t v0, int64_t nv) {
     using P = Tile32<BT>;
     constexpr int TM = P::TM;
@@ -501,7 +501,6 @@ __global__ __launch_bounds__(256, 4) void k_xent_grad32(const float *x, const fl
                Operand32<false, BT>{w + (v0 + n0) * ld, ld, (nv - n0) * ld, nv - n0, D}, D, lds);
     const auto &acc = tile32.acc;
     const int lane = threadIdx.x & 63, wm = P::row0(), wn = P::col0();
-    const float top = scale[0];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -509,7 +508,7 @@ __global__ __launch_bounds__(256, 4) void k_xent_grad32(const float *x, const fl
             const int64_t t = m0 + wm + i * 16 + (lane >> 4) * 4 + e;
             if (t >= T) continue;
             const int64_t l = lab.of(t);
-            const float ls = lse[t], dl = l >= 0 ? weight<IO_F32>(dloss[t], top) : 0.f;
+            const float ls = lse[t], dl = l >= 0 ? dloss[t] : 0.f;
 #pragma unroll
             for (int j = 0; j < TM; ++j) {
                 const int64_t c = n0 + wn + j * 16 + (lane & 15);
@@ -525,7 +524,7 @@ __global__ __launch_bounds__(256, 4) void k_xent_grad32(const float *x, const fl
 template <int BT>
 __global__ __launch_bounds__(256) void k_xent_products32(const float *x, const float *w, int64_t ld, const float *g,
                                                          float *__restrict__ dx, float *__restrict__ dw,
-                                                         const float *__restrict__ scale, int64_t T, int64_t D,
+                                                         int64_t T, int64_t D,
                                                          int64_t nv, int64_t ndx, int first) {
     using P = Tile32<BT>;
     constexpr int TM = P::TM;
@@ -543,7 +542,6 @@ __global__ __launch_bounds__(256) void k_xent_products32(const float *x, const f
                    Operand32<true, BT>{x + n0, ld, T * ld - n0, D - n0, T}, T, lds);
     const auto &acc = tile32.acc;
     const int lane = threadIdx.x & 63, wm = P::row0(), wn = P::col0();
-    const float down = scale[1];
     const int64_t M = is_dx ? T : nv;
     float *const out = is_dx ? dx : dw;
 #pragma unroll
@@ -554,7 +552,7 @@ __global__ __launch_bounds__(256) void k_xent_products32(const float *x, const f
             for (int e = 0; e < 4; ++e) {
                 const int64_t m = m0 + wm + i * 16 + (lane >> 4) * 4 + e, n = n0 + wn + j * 16 + (lane & 15);
                 if (m >= M || n >= D) continue;
-                const float q = acc[i][j][e] * down;
+                const float q = acc[i][j][e];
                 out[m * D + n] = is_dx && !first ? out[m * D + n] + q : q;
             }
 }
@@ -972,7 +970,7 @@ Plan plan(int64_t T, int64_t D, int64_t V, int io, bool bwd, char *base) {
         p.wranges = (p.Tp + p.wrange - 1) / p.wrange;
         p.accum = (float *)take(!wide && (p.pieces > 1 || p.ranges > 1) ? p.ranges * T * D * 4 : 0);
         p.waccum = (float *)take(!wide && p.wranges > 1 ? p.wranges * p.piece * D * 4 : 0);
-        p.scale = (float *)take(8);
+        p.scale = (float *)take(wide ? 0 : 8);
     }
     p.bytes = at;
     return p;
@@ -1023,7 +1021,8 @@ hipError_t bwd_io(const void *x, const void *w, const Labels &lab, const float *
     const char *xr, *wr;
     hipError_t e = padded<IO>(x, p.xp, T, D, p.kD, &xr, s);
     if (e == hipSuccess) e = padded<IO>(w, p.wp, V, D, p.kD, &wr, s);
-    if (e == hipSuccess) e = launch(k_xent_scale<IO>, dim3(1), dim3(1024), 0, s, dloss, lab, p.scale, T);
+    if constexpr (IO != IO_F32)
+        if (e == hipSuccess) e = launch(k_xent_scale<IO>, dim3(1), dim3(1024), 0, s, dloss, lab, p.scale, T);
     for (int64_t i = 0; i < p.pieces && e == hipSuccess; ++i) {
         const int64_t v0 = i * p.piece, nv = V - v0 < p.piece ? V - v0 : p.piece;
         const int first = i == 0, last = i + 1 == p.pieces;
@@ -1031,12 +1030,12 @@ hipError_t bwd_io(const void *x, const void *w, const Labels &lab, const float *
             const float *const xf = (const float *)xr, *const wf = (const float *)wr;
             int64_t bt = side32(T, nv);
             e = launch(bt == 32 ? k_xent_grad32<32> : k_xent_grad32<64>, dim3(blocks(T, bt) * blocks(nv, bt)), dim3(256), 0, s,
-                       xf, wf, p.kD, lab, lse, dloss, p.scale, (float *)p.g, T, D, v0, nv);
+                       xf, wf, p.kD, lab, lse, dloss, (float *)p.g, T, D, v0, nv);
             if (e != hipSuccess) break;
             bt = side32(T, D, nv);
             const int64_t ndx = (int64_t)blocks(T, bt) * blocks(D, bt), ndw = (int64_t)blocks(nv, bt) * blocks(D, bt);
             e = launch(bt == 32 ? k_xent_products32<32> : k_xent_products32<64>, dim3((unsigned)(ndx + ndw)), dim3(256), 0, s,
-                       xf, wf + v0 * p.kD, p.kD, (const float *)p.g, (float *)dx, (float *)dw + v0 * D, p.scale, T, D, nv,
+                       xf, wf + v0 * p.kD, p.kD, (const float *)p.g, (float *)dx, (float *)dw + v0 * D, T, D, nv,
                        ndx, first);
         } else {
             const int64_t kv = ceil_to(nv, 64);
