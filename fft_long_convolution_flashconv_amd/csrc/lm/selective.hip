@@ -407,7 +407,7 @@ __device__ __forceinline__ void scan_piece(const SelK<typename io_elem<IO>::T> &
 // nothing.
 // Measured, 16 modes with a gate: 8 x 768 x 1024 fp16 36.9 us, 1 x 1024 x 65536
 // bf16 486 us, 4 x 2560 x 2048 bf16 with saved states 150 us: 2.2 to 2.7 million
-// million mode-steps a second, the vector ALUs busy 93 % of the compute units' time.
+// million mode-steps a second, the vector ALUs busy 92 % of the compute units' time.
 template <int IO, int LPR, Share SH>
 __global__ __launch_bounds__(256, IO == IO_F32 || LPR == 16 ? 2 : 3) void k_sel_scan(const SelK<typename io_elem<IO>::T> k,
                                                      typename io_elem<IO>::T *__restrict__ y,
