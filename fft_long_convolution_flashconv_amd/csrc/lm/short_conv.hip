@@ -152,11 +152,11 @@ __device__ __forceinline__ float act_bwd(float p, float dy, int silu) {
 // the channel's B rows cut into pieces, so the sums over batch and time stay
 // in one block's registers and are joined in a fixed order:
 //   dx_s = sum_i w_i dp_{s+i},  dw_i = sum_{b,t} dp_t x_{t-i},  dbias = sum dp.
-// A thread forms dp of its own steps and of the W - 1 after them, which costs
-// 3 of 11 activations at 4 taps and saves an exchange between threads.
-// 4 x 2560 x 2048, bf16, 4 taps: 29.2 us, 4.3 TB/s, vector ALUs and memory both
-// nearly full.
-template <int IO, int W, bool WAVE>
+// A thread forms dp of its own V steps and of the W - 1 after them, which costs
+// 3 of 11 (V = 8) or of 19 (16) activations at 4 taps and saves an exchange
+// between threads.  4 x 2560 x 2048, bf16, 4 taps: 25.9 us, 4.9 TB/s,
+// from inputs that the caches hold in part.
+template <int IO, int W, bool WAVE, int V>
 __global__ __launch_bounds__(kThreads) void k_short_conv_bwd(
     const typename io_elem<IO>::T *__restrict__ x, const typename io_elem<IO>::T *__restrict__ x_in,
     const float *__restrict__ w, const float *__restrict__ bias, const int32_t *__restrict__ lengths,
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(kThreads) void k_short_conv_bwd(
     float *__restrict__ dw, float *__restrict__ dbias, int64_t B, int64_t H, int64_t N, int silu, int tpr_log2,
     int64_t pieces) {
     using T = typename io_elem<IO>::T;
-    constexpr int V = 16 / (int)sizeof(T), E = V + W - 1;
+    constexpr int E = V + W - 1;
     const int64_t h = blockIdx.x;
     const int tpr = 1 << tpr_log2, rpb = kThreads >> tpr_log2, tl = (int)threadIdx.x & (tpr - 1);
     const int sub = row_of<WAVE>(tpr_log2);
@@ -357,9 +357,12 @@ int bwd_splits(int64_t B, int64_t H, int64_t N, int64_t *pieces, int *tpr_log2, 
 
 size_t short_conv_bwd_workspace(int64_t B, int64_t H, int64_t N, int W) {
     int64_t pieces;
-    int tpr;
-    const int k16 = bwd_splits(B, H, N, &pieces, &tpr, 8), k32 = bwd_splits(B, H, N, &pieces, &tpr, 4);
-    return (size_t)(k16 > k32 ? k16 : k32) * (size_t)H * (kTaps + 1) * 4;
+    int tpr_log2, most = 0;
+    for (int V = 4; V <= 16; V *= 2) {  // whatever the type
+        const int k = bwd_splits(B, H, N, &pieces, &tpr_log2, V);
+        if (k > most) most = k;
+    }
+    return (size_t)most * (size_t)H * (kTaps + 1) * 4;
 }
 
 template <int IO, int W>
@@ -395,14 +398,22 @@ hipError_t launch_short_conv(const ShortConvArgs &a, void *y, void *x_out, int i
     }
 }
 
-template <int IO, int W>
+// Steps per thread of the backward pass: one vector of 16 bytes, or two where
+// there are enough steps for every compute unit (bf16, us, one and two: 4 x 2560
+// x 2048 28.2 25.9, 8 x 768 x 1024 15.2 14.1, 3 x 96 x 5000 7.9 11.2, 2 x 768 x
+// 100 6.3 7.5).
+static int bwd_steps(int64_t B, int64_t H, int64_t N, int bytes) {
+    return (B * H * N >= (int64_t)3 << 19 ? 32 : 16) / bytes;
+}
+
+template <int IO, int W, int V>
 static hipError_t short_conv_bwd_taps(const ShortConvArgs &a, const void *dy, const void *dx_out, void *dx, float *dw,
                                       float *dbias, void *dx_in, float *part, hipStream_t s) {
     using T = typename io_elem<IO>::T;
     int64_t pieces;
     int tpr_log2;
-    const int K = bwd_splits(a.B, a.H, a.N, &pieces, &tpr_log2, 16 / (int)sizeof(T));
-    const hipError_t e = launch(tpr_log2 >= 6 ? k_short_conv_bwd<IO, W, true> : k_short_conv_bwd<IO, W, false>, dim3((unsigned)a.H, (unsigned)K), dim3(kThreads), 0, s,
+    const int K = bwd_splits(a.B, a.H, a.N, &pieces, &tpr_log2, V);
+    const hipError_t e = launch(tpr_log2 >= 6 ? k_short_conv_bwd<IO, W, true, V> : k_short_conv_bwd<IO, W, false, V>, dim3((unsigned)a.H, (unsigned)K), dim3(kThreads), 0, s,
                                 (const T *)a.x, (const T *)a.x_in, a.w, a.bias, a.lengths, (const T *)dy,
                                 (const T *)dx_out, (T *)dx, (T *)dx_in, part, dw, dbias, a.B, a.H, a.N, a.silu, tpr_log2,
                                 pieces);
@@ -411,14 +422,23 @@ static hipError_t short_conv_bwd_taps(const ShortConvArgs &a, const void *dy, co
                   dbias, a.H, W, K);
 }
 
+template <int IO, int W>
+static hipError_t short_conv_bwd_vec(const ShortConvArgs &a, const void *dy, const void *dx_out, void *dx, float *dw,
+                                     float *dbias, void *dx_in, float *part, hipStream_t s) {
+    constexpr int bytes = (int)sizeof(typename io_elem<IO>::T), V = 16 / bytes;
+    return bwd_steps(a.B, a.H, a.N, bytes) == V
+               ? short_conv_bwd_taps<IO, W, V>(a, dy, dx_out, dx, dw, dbias, dx_in, part, s)
+               : short_conv_bwd_taps<IO, W, 2 * V>(a, dy, dx_out, dx, dw, dbias, dx_in, part, s);
+}
+
 template <int IO>
 static hipError_t short_conv_bwd_io(const ShortConvArgs &a, const void *dy, const void *dx_out, void *dx, float *dw,
                                     float *dbias, void *dx_in, float *part, hipStream_t s) {
     switch (a.W) {
-        case 1: return short_conv_bwd_taps<IO, 1>(a, dy, dx_out, dx, dw, dbias, dx_in, part, s);
-        case 2: return short_conv_bwd_taps<IO, 2>(a, dy, dx_out, dx, dw, dbias, dx_in, part, s);
-        case 3: return short_conv_bwd_taps<IO, 3>(a, dy, dx_out, dx, dw, dbias, dx_in, part, s);
-        case 4: return short_conv_bwd_taps<IO, 4>(a, dy, dx_out, dx, dw, dbias, dx_in, part, s);
+        case 1: return short_conv_bwd_vec<IO, 1>(a, dy, dx_out, dx, dw, dbias, dx_in, part, s);
+        case 2: return short_conv_bwd_vec<IO, 2>(a, dy, dx_out, dx, dw, dbias, dx_in, part, s);
+        case 3: return short_conv_bwd_vec<IO, 3>(a, dy, dx_out, dx, dw, dbias, dx_in, part, s);
+        case 4: return short_conv_bwd_vec<IO, 4>(a, dy, dx_out, dx, dw, dbias, dx_in, part, s);
         default: return hipErrorInvalidValue;
     }
 }

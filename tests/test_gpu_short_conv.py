@@ -206,3 +206,24 @@ def test_short_conv_refusals():
         pkg.short_conv(x, w, out=x)                                 # output over input
     with pytest.raises(pkg.H3ConvError):
         pkg.short_conv_step(x[:, :, 0].contiguous(), w, torch.zeros(1, 3, 3).to(dev))  # pool below the batch
+
+
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+def test_short_conv_bwd_many_steps(io):
+    """Enough steps for two vectors per thread; rows that end inside one, between the two, and before their taps."""
+    B, H, N = 4, 160, 2501
+    say("short_conv_bwd many steps", io)
+    g = torch.Generator().manual_seed(5)
+    t, dev = ref.DT[io], device()
+    x, dy = torch.randn(B, H, N, generator=g).to(t), torch.randn(B, H, N, generator=g).to(t)
+    w, bias = torch.randn(H, 4, generator=g) * 0.5, torch.randn(H, generator=g)
+    x_in, dx_out = torch.randn(B, H, 3, generator=g).to(t), torch.randn(B, H, 3, generator=g).to(t)
+    lengths = [2501, 2488, 2, 1000]
+    got = pkg.short_conv_bwd(x.to(dev), w.to(dev), dy.to(dev), bias.to(dev), x_in=x_in.to(dev),
+                             lengths=torch.tensor(lengths, dtype=torch.int32, device=dev), dx_out=dx_out.to(dev))
+    torch.cuda.synchronize()
+    leaves = [ref.leaf(v) for v in (x, w, bias, x_in)]
+    y, xo = ref.short_conv(leaves[0], leaves[1], leaves[2], True, leaves[3], lengths)
+    ((y * dy.double()).sum() + (xo * dx_out.double()).sum()).backward()
+    for name, a, b, kind in zip(("dx", "dw", "dbias", "dx_in"), got, leaves, (io, "f32", "f32", io)):
+        ref.close(a, b.grad, kind, what=name)
