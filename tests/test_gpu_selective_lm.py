@@ -69,3 +69,43 @@ def test_gradients_against_plain_operators():
         # fp32 throughout, a few hundred operations deep
         err, norm = (a.grad.double().cpu() - b.grad).norm(), b.grad.norm()
         assert err <= 1e-4 * norm + 1e-7, (name, float(err), float(norm))
+
+
+def test_token_steps_in_a_graph():
+    """short_conv_step and selective_step captured once and replayed token by token, against eager calls."""
+    say("token steps in a graph")
+    ex = _example()
+    h3, dev = ex.h3, device()
+    g = torch.Generator().manual_seed(4)
+
+    def r(*s):
+        return torch.randn(*s, generator=g).to(dev)
+
+    B, H, S, P = 6, 40, 16, 9
+    w, bias, A, D = r(H, 4), r(H), -r(H, S).abs(), r(H)
+    x, z, dt, Bm, C = r(B, H), r(B, H), r(B, H), r(B, 1, S), r(B, 1, S)
+    slots = torch.tensor([8, 2, -1, 0, 5, 3], dtype=torch.int32, device=dev)
+    pools = [(torch.zeros(P, H, 3, device=dev), torch.zeros(P, H, S, device=dev)) for _ in range(2)]
+
+    def token(pool):
+        u = h3.short_conv_step(x, w, pool[0], bias, slots=slots)
+        return h3.selective_step(u, dt, A, Bm, C, pool[1], D, z, slots=slots)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        token(tuple(t.clone() for t in pools[0]))
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = token(pools[0])
+    for t in pools[0]:
+        t.zero_()
+    for i in range(5):
+        for t in (x, z, dt, Bm, C):
+            t.copy_(r(*t.shape))
+        graph.replay()
+        want = token(pools[1])
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), i
+        assert torch.equal(pools[0][0], pools[1][0]) and torch.equal(pools[0][1], pools[1][1]), i
