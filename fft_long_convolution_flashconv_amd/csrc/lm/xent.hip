@@ -521,29 +521,33 @@ __global__ __launch_bounds__(256, 4) void k_xent_grad32(const float *x, const fl
 
 // dx and dw of a piece in one launch: first the tiles of
 // dx[t][d] += sum_v G[t][v] w[v][d], then those of dw[v][d] = sum_t G[t][v] x[t][d].
+// As in 16 bits, the v may be cut into `splits` ranges of kx with sums of their
+// own in accum.
 template <int BT>
 __global__ __launch_bounds__(256) void k_xent_products32(const float *x, const float *w, int64_t ld, const float *g,
                                                          float *__restrict__ dx, float *__restrict__ dw,
-                                                         int64_t T, int64_t D,
-                                                         int64_t nv, int64_t ndx, int first) {
+                                                         float *__restrict__ accum, int64_t T, int64_t D, int64_t nv,
+                                                         int64_t kx, int splits, int64_t ndx, int first) {
     using P = Tile32<BT>;
     constexpr int TM = P::TM;
     __shared__ f4 lds[2][2][BT * 8];
     const int64_t cols = (D + BT - 1) / BT;
     const bool is_dx = (int64_t)blockIdx.x < ndx;
-    const int64_t id = is_dx ? blockIdx.x : blockIdx.x - ndx, m0 = id / cols * BT, n0 = id % cols * BT;
+    const int64_t tiles = ndx / splits, part = is_dx ? blockIdx.x / tiles : 0, k0 = part * kx;
+    const int64_t id = is_dx ? blockIdx.x - part * tiles : blockIdx.x - ndx, m0 = id / cols * BT, n0 = id % cols * BT;
+    const int64_t kn = nv - k0 < kx ? nv - k0 : kx;
     const int64_t ng = T * nv > 4 ? T * nv : 4;  // (there is room for four)
     P tile32;
     if (is_dx)
-        tile32.run(Operand32<false, BT>{g + m0 * nv, nv, ng - m0 * nv, T - m0, nv},
-                   Operand32<true, BT>{w + n0, ld, nv * ld - n0, D - n0, nv}, nv, lds);
+        tile32.run(Operand32<false, BT>{g + m0 * nv + k0, nv, ng - m0 * nv - k0, T - m0, kn},
+                   Operand32<true, BT>{w + k0 * ld + n0, ld, (nv - k0) * ld - n0, D - n0, kn}, kn, lds);
     else
         tile32.run(Operand32<true, BT>{g + m0, nv, ng - m0, nv - m0, T},
                    Operand32<true, BT>{x + n0, ld, T * ld - n0, D - n0, T}, T, lds);
     const auto &acc = tile32.acc;
     const int lane = threadIdx.x & 63, wm = P::row0(), wn = P::col0();
     const int64_t M = is_dx ? T : nv;
-    float *const out = is_dx ? dx : dw;
+    float *const out = is_dx ? (accum ? accum + part * T * D : dx) : dw;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -826,7 +830,8 @@ __global__ __launch_bounds__(256) void k_xent_dx(const float *__restrict__ accum
         for (int e = 0; e < 4; ++e) s[e] += o[e];
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] *= scale[1];
+    for (int e = 0; e < 4; ++e)
+        if (scale) s[e] *= scale[1];
     st_row<IO, 4>(dx + i, s, n - i);
 }
 
@@ -884,8 +889,8 @@ struct Plan {
     int64_t Tp;            // tokens, padded (16-bit): rows of G
     int64_t piece, pieces; // vocabulary rows per piece
     int64_t tiles;         // pairs per token of the forward pass
-    int64_t side;          // of the tiles of dx and dw (16-bit)
-    int64_t range, ranges; // vocabulary rows whose part of dx is summed apart, such parts of a piece (16-bit)
+    int64_t side;          // of the tiles of dx and dw
+    int64_t range, ranges; // vocabulary rows whose part of dx is summed apart, such parts of a piece
     int64_t wrange, wranges; // tokens whose part of dw is summed apart, such parts (16-bit)
     char *xp, *wp, *g;
     float *accum, *waccum, *scale, *hit;
@@ -939,9 +944,19 @@ Plan plan(int64_t T, int64_t D, int64_t V, int io, bool bwd, char *base) {
         p.piece = ceil_to((V + n - 1) / n, rows);
         p.pieces = (V + p.piece - 1) / p.piece;
         p.g = take(p.Tp * p.piece * e);
-        p.side = 256;
+        p.side = wide ? side32(T, D, p.piece) : 256;
         int64_t splits = 1, wsplits = 1;
-        if (!wide) {
+        if (wide) {
+            // as below; 512 blocks at once (backward pass at 320 x 972 x 27650: about 950 us
+            // without ranges, 559 with)
+            const int64_t cols = (D + p.side - 1) / p.side, kv = (p.piece + 31) / 32, kt = (T + 31) / 32;
+            const int64_t ndx = (T + p.side - 1) / p.side * cols, ndw = (p.piece + p.side - 1) / p.side * cols;
+            int64_t best = makespan(512, ndx, kv, ndw, kt);
+            for (int64_t k = 2; k <= 64 && (k <= 8 || k * T * D <= 1 << 22) && k * 8 <= kv; k += k < 8 ? 1 : k / 4) {
+                const int64_t m = makespan(512, ndx * k, (kv + k - 1) / k, ndw, kt);
+                if (m * 20 < best * 19) best = m, splits = k;
+            }
+        } else {
             const int64_t kv = ceil_to(p.piece, 64) / 64, kt = p.Tp / 64;  // slabs of dx's and of dw's sums
             const auto tiles = [&](int64_t rows) { return (D + p.side - 1) / p.side * ((rows + p.side - 1) / p.side); };
             const auto work = [&](int64_t side) { return p.side = side, tiles(T) * kv + tiles(p.piece) * kt; };
@@ -968,7 +983,7 @@ Plan plan(int64_t T, int64_t D, int64_t V, int io, bool bwd, char *base) {
         p.ranges = (k0 + p.range - 1) / p.range;
         p.wrange = ceil_to((p.Tp + wsplits - 1) / wsplits, 64);
         p.wranges = (p.Tp + p.wrange - 1) / p.wrange;
-        p.accum = (float *)take(!wide && (p.pieces > 1 || p.ranges > 1) ? p.ranges * T * D * 4 : 0);
+        p.accum = (float *)take((!wide && p.pieces > 1) || p.ranges > 1 ? p.ranges * T * D * 4 : 0);
         p.waccum = (float *)take(!wide && p.wranges > 1 ? p.wranges * p.piece * D * 4 : 0);
         p.scale = (float *)take(wide ? 0 : 8);
     }
@@ -1032,11 +1047,15 @@ hipError_t bwd_io(const void *x, const void *w, const Labels &lab, const float *
             e = launch(bt == 32 ? k_xent_grad32<32> : k_xent_grad32<64>, dim3(blocks(T, bt) * blocks(nv, bt)), dim3(256), 0, s,
                        xf, wf, p.kD, lab, lse, dloss, (float *)p.g, T, D, v0, nv);
             if (e != hipSuccess) break;
-            bt = side32(T, D, nv);
-            const int64_t ndx = (int64_t)blocks(T, bt) * blocks(D, bt), ndw = (int64_t)blocks(nv, bt) * blocks(D, bt);
+            bt = p.side;
+            const int64_t parts = (nv + p.range - 1) / p.range;  // (a shorter last piece has fewer)
+            const int64_t ndx = (int64_t)blocks(T, bt) * blocks(D, bt) * parts, ndw = (int64_t)blocks(nv, bt) * blocks(D, bt);
             e = launch(bt == 32 ? k_xent_products32<32> : k_xent_products32<64>, dim3((unsigned)(ndx + ndw)), dim3(256), 0, s,
-                       xf, wf + v0 * p.kD, p.kD, (const float *)p.g, (float *)dx, (float *)dw + v0 * D, T, D, nv,
-                       ndx, first);
+                       xf, wf + v0 * p.kD, p.kD, (const float *)p.g, (float *)dx, (float *)dw + v0 * D, p.accum, T, D, nv,
+                       p.range, (int)parts, ndx, first);
+            if (e == hipSuccess && last && p.accum)
+                e = launch(k_xent_dx<IO>, dim3(blocks(T * D, 1024)), dim3(256), 0, s, p.accum, p.scale, (E *)dx, T * D,
+                           (int)p.ranges);
         } else {
             const int64_t kv = ceil_to(nv, 64);
             int64_t bt = side16(T, nv);

@@ -166,3 +166,10 @@ def test_fp32_tiles(T, D, V):
 def test_16bit_tiles(io, T, D, V):
     say("linear_xent 16-bit", io, T, D, V)
     _check(io, *_make(io, T, D, V, T + D + V))
+
+
+@pytest.mark.parametrize("T,D,V", [(40, 70, 20000), (33, 3, 9001), (130, 257, 12345)])
+def test_fp32_ranges(T, D, V):
+    """fp32: sums of dx over the vocabulary in ranges of their own."""
+    say("linear_xent fp32 ranges", T, D, V)
+    _check("f32", *_make("f32", T, D, V, T + D + V))
