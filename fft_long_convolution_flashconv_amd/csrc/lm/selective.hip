@@ -299,11 +299,14 @@ struct Lane {
 };
 
 // One piece of LPR*IT steps of each of the wave's rows, from its u and dt as
-// loaded; reload() loads the next piece's into the same registers.
+// loaded; reload() loads the next piece's into the same registers.  turn: which
+// of the two buffers of maps mode 0 takes.  The modes take them in turn, across
+// pieces too: with one barrier per mode, a wave may write a mode's map while
+// another still reads those of the mode before, never of the one before that.
 template <int IO, int LPR, Share SH, Fit F, class Reload>
 __device__ __forceinline__ void scan_piece(const SelK<typename io_elem<IO>::T> &k, const Lane &p, Raw<IO, kIT> &ru,
                                            Raw<IO, kIT> &rd, const float *Ap, float Dh, float bias, float *st, int l,
-                                           bool live, float2 (*maps)[4], float (*part)[kIT][64],
+                                           bool live, int turn, float2 (*maps)[4], float (*part)[kIT][64],
                                            typename io_elem<IO>::T *y, float *saved, const Reload &reload) {
     constexpr int IT = kIT, AH = kAhead, MS = SH == kModeMod4 ? 4 : 1;
     const int last = k.S - 1, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), first = MS > 1 ? wave : 0;
@@ -357,7 +360,7 @@ __device__ __forceinline__ void scan_piece(const SelK<typename io_elem<IO>::T> &
             const float A2 = A * kLog2e, in0 = l == 0 ? in : 0.f;
             A = Ap[next];
             in = st[next];
-            scan_mode<IO, LPR, SH, F>(rB[j], rC[j], A2, in0, d, u, sum, o, st + n, l, maps + (n & 1), sv ? sv + n : nullptr,
+            scan_mode<IO, LPR, SH, F>(rB[j], rC[j], A2, in0, d, u, sum, o, st + n, l, maps + ((n + turn) & 1), sv ? sv + n : nullptr,
                                own, [&] { rB[j] = loadB(n + MS * AH); }, [&] { rC[j] = loadC(n + MS * AH); });
         }
     }
@@ -440,6 +443,7 @@ __global__ __launch_bounds__(256, IO == IO_F32 || LPR == 16 ? 2 : 3) void k_sel_
     };
     Raw<IO, IT> ru, rd;
     int64_t base = 0;
+    int turn = 0;
     if (__all(len >= PIECE)) {  // the pieces that are full in every row of the wave
         Lane p = piece(0);
         ru = ld_steps<IO, IT, kFull>(k.u, p.row, 0, N);
@@ -447,13 +451,14 @@ __global__ __launch_bounds__(256, IO == IO_F32 || LPR == 16 ? 2 : 3) void k_sel_
         bool more;
         do {
             more = __all(len >= base + 2 * PIECE);
-            scan_piece<IO, LPR, SH, kFull>(k, p, ru, rd, Ap, Dh, bias, st, l, live, maps, part, y, sv, [&] {
+            scan_piece<IO, LPR, SH, kFull>(k, p, ru, rd, Ap, Dh, bias, st, l, live, turn, maps, part, y, sv, [&] {
                 const int64_t o = more ? p.row + PIECE : p.row;
                 ru = ld_steps<IO, IT, kFull>(k.u, o, 0, N);
                 rd = ld_steps<IO, IT, kFull>(k.dt, o, 0, N);
             });
             __builtin_amdgcn_wave_barrier();
             base += PIECE;
+            turn ^= k.S & 1;
             p = piece(base);
         } while (more);
     }
@@ -463,8 +468,9 @@ __global__ __launch_bounds__(256, IO == IO_F32 || LPR == 16 ? 2 : 3) void k_sel_
             const Lane p = piece(base);
             ru = ld_steps<IO, IT, F>(k.u, p.row, 0, N);
             rd = ld_steps<IO, IT, F>(k.dt, p.row, 0, N);
-            scan_piece<IO, LPR, SH, F>(k, p, ru, rd, Ap, Dh, bias, st, l, live, maps, part, y, sv, [] {});
+            scan_piece<IO, LPR, SH, F>(k, p, ru, rd, Ap, Dh, bias, st, l, live, turn, maps, part, y, sv, [] {});
             __builtin_amdgcn_wave_barrier();
+            turn ^= k.S & 1;
         }
     };
     if (LPR == 16 && N < IT) rest(std::integral_constant<Fit, kShort>{});
