@@ -4,8 +4,12 @@
 #pragma once
 
 #include "../h3conv_device.h"
+#include "lm_internal.h"
 
 namespace h3c {
+
+// This block's number in a grid that grid_of() made.
+__device__ __forceinline__ int64_t block_id() { return blockIdx.x + (int64_t)blockIdx.z * kGridX; }
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;

@@ -8,6 +8,14 @@
 
 namespace h3c {
 
+// A dispatch takes fewer than 2^32 threads along x.  A grid of n blocks (of up
+// to 1024 threads): along x, and past kGridX of them along z.  The last of
+// several z may hold blocks numbered n and up, which have nothing to do.
+constexpr int64_t kGridX = (int64_t)1 << 21;
+inline dim3 grid_of(int64_t n, unsigned y = 1) {
+    return n <= kGridX ? dim3((unsigned)n, y, 1) : dim3((unsigned)kGridX, y, (unsigned)((n + kGridX - 1) / kGridX));
+}
+
 // ------------------------------------------------------------ short_conv
 struct ShortConvArgs {
     const void *x, *x_in;        // [B,H,N], [B,H,W-1] or null

@@ -424,7 +424,7 @@ __global__ __launch_bounds__(256, IO == IO_F32 || LPR == 16 ? 2 : 3) void k_sel_
     __shared__ float part[SH == kModeMod4 ? 4 : 1][kIT][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane / LPR, l = lane % LPR;
     const uint32_t R = (uint32_t)(k.B * k.H), H = (uint32_t)k.H;
-    const uint32_t r = (SH == kOwnRows ? blockIdx.x * 4 + wave : blockIdx.x) * RPW + sub;
+    const uint32_t block = (uint32_t)block_id(), r = (SH == kOwnRows ? block * 4 + wave : block) * RPW + sub;
     if (r - sub >= R) return;  // (the whole wave)
     const bool live = r < R;
     const uint32_t rr = live ? r : R - 1, b = rr / H, h = rr - b * H, g = h / (H / (uint32_t)k.G);
@@ -576,8 +576,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // (scalar: so are the rows' base addresses)
     float4(*const mine)[F4] = (float4(*)[F4])(lds + 2 * kModes * F4) + 3 * wave;
     const int64_t N = k.N, Hg = k.H / k.G;
-    const int set = (int)(blockIdx.x % ws.sets);
-    const int64_t bg = blockIdx.x / ws.sets, g = bg % k.G, b = bg / k.G;
+    const uint32_t block = (uint32_t)block_id();
+    const int set = (int)(block % (uint32_t)ws.sets);
+    const int64_t bg = block / (uint32_t)ws.sets, g = bg % k.G, b = bg / k.G;
+    if (b >= k.B) return;
     const int64_t len = row_len(k.lengths, b, N);
     const int64_t left = Hg - (int64_t)set * ws.per, h0 = g * Hg + (int64_t)set * ws.per;
     const int nset = (int)(left < ws.per ? left : ws.per);
@@ -866,7 +868,7 @@ __global__ __launch_bounds__(256) void k_sel_join(const SelBwdWs ws, typename io
                                                   typename io_elem<IO>::T *__restrict__ dC, float *__restrict__ dA,
                                                   float *__restrict__ dD, float *__restrict__ ddt_bias, int64_t M,
                                                   int64_t B, int64_t H, int S) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, HS = H * S;
+    const int64_t i = block_id() * 256 + threadIdx.x, HS = H * S;
     if (blockIdx.y < 2) {
         if (i >= M) return;
         const float *const p = (blockIdx.y ? ws.dC : ws.dB) + i;
@@ -911,7 +913,7 @@ __global__ __launch_bounds__(256) void k_sel_step(const typename io_elem<IO>::T 
                                                   typename io_elem<IO>::T *__restrict__ y, int64_t H, int64_t P,
                                                   int S, int G, int softplus_, int lpc) {
     const int sub = (int)threadIdx.x % lpc;
-    const int64_t h = (int64_t)blockIdx.x * (256 / lpc) + threadIdx.x / lpc, b = blockIdx.y;
+    const int64_t h = block_id() * (256 / lpc) + threadIdx.x / lpc, b = blockIdx.y;
     const int64_t slot = slots ? (int64_t)slots[b] : b;
     const bool in = h < H, ok = in && slot >= 0 && slot < P;
     float s = 0.f, uv = 0.f;
@@ -992,7 +994,7 @@ template <int IO, int LPR, Share SH>
 hipError_t scan_lanes(const SelArgs &a, void *y, float *x_out, float *saved, hipStream_t s) {
     using T = typename io_elem<IO>::T;
     constexpr int rows = (SH == kOwnRows ? 4 : 1) * 64 / LPR;
-    return launch(k_sel_scan<IO, LPR, SH>, dim3((unsigned)((a.B * a.H + rows - 1) / rows)), dim3(256), 0, s,
+    return launch(k_sel_scan<IO, LPR, SH>, grid_of((a.B * a.H + rows - 1) / rows), dim3(256), 0, s,
                   pack_args<IO>(a), (T *)y, x_out, saved, chunks(a.N));
 }
 
@@ -1022,7 +1024,7 @@ hipError_t bwd_io(const SelArgs &a, const float *saved, const void *dy, const fl
     using T = typename io_elem<IO>::T;
     SelBwdWs w;
     bwd_layout(a.B, a.H, a.N, a.S, a.G, ws, &w);
-    const dim3 grid((unsigned)(a.B * a.G * w.sets));
+    const dim3 grid = grid_of(a.B * a.G * w.sets);
     // (float4 loads of decay rates: A may start at any element)
     const bool whole = a.S == kModes && ((uintptr_t)a.A & 15) == 0;
     for (int n0 = 0; n0 < a.S && a.B > 0; n0 += kModes) {
@@ -1033,7 +1035,7 @@ hipError_t bwd_io(const SelArgs &a, const float *saved, const void *dy, const fl
         if (e != hipSuccess) return e;
     }
     const int64_t M = a.B * a.G * a.S * a.N, P = a.H * (a.S + 1);
-    return launch(k_sel_join<IO>, dim3((unsigned)(((M > P ? M : P) + 255) / 256), 3), dim3(256), 0, s, w, (T *)g.dB,
+    return launch(k_sel_join<IO>, grid_of(((M > P ? M : P) + 255) / 256, 3), dim3(256), 0, s, w, (T *)g.dB,
                   (T *)g.dC, g.dA, g.dD, g.ddt_bias, M, a.B, a.H, a.S);
 }
 
@@ -1075,7 +1077,7 @@ static hipError_t step_io(const void *u, const void *dt, const float *A, const v
     using T = typename io_elem<IO>::T;
     int lpc = 1;
     while (lpc * 4 < S) lpc <<= 1;
-    return launch(k_sel_step<IO>, dim3((unsigned)((H * lpc + 255) / 256), (unsigned)B), dim3(256), 0, s, (const T *)u,
+    return launch(k_sel_step<IO>, grid_of((H * lpc + 255) / 256, (unsigned)B), dim3(256), 0, s, (const T *)u,
                   (const T *)dt, A, (const T *)Bm, (const T *)C, D, (const T *)z, dt_bias, slots, x_in, x_out, (T *)y,
                   H, P, S, G, softplus, lpc);
 }

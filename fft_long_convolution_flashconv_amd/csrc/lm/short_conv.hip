@@ -99,7 +99,7 @@ __global__ __launch_bounds__(kThreads) void k_short_conv(const typename io_elem<
     using T = typename io_elem<IO>::T;
     constexpr int V = 16 / (int)sizeof(T);
     const int tpr = 1 << tpr_log2, tl = (int)threadIdx.x & (tpr - 1);
-    const uint32_t row = blockIdx.x * (uint32_t)(kThreads >> tpr_log2) + row_of<WAVE>(tpr_log2);
+    const uint32_t row = (uint32_t)block_id() * (uint32_t)(kThreads >> tpr_log2) + row_of<WAVE>(tpr_log2);
     if (row >= (uint32_t)(B * H)) return;
     const uint32_t b = row / (uint32_t)H, h = row - b * (uint32_t)H;
     const int64_t r = row, len = row_len(lengths, b, N);
@@ -166,7 +166,8 @@ __global__ __launch_bounds__(kThreads) void k_short_conv_bwd(
     int64_t pieces) {
     using T = typename io_elem<IO>::T;
     constexpr int E = V + W - 1;
-    const int64_t h = blockIdx.x;
+    const int64_t h = block_id();
+    if (h >= H) return;
     const int tpr = 1 << tpr_log2, rpb = kThreads >> tpr_log2, tl = (int)threadIdx.x & (tpr - 1);
     const int sub = row_of<WAVE>(tpr_log2);
     float tap[W], sw[W], sb = 0.f;
@@ -374,7 +375,7 @@ static hipError_t short_conv_taps(const ShortConvArgs &a, void *y, void *x_out, 
     const int64_t rows = (R + kThreads / tpr - 1) / (kThreads / tpr);
     int64_t gy = (nvec + tpr - 1) / tpr;
     gy = gy < 1 ? 1 : (gy > 4096 ? 4096 : gy);
-    return launch(tpr >= 64 ? k_short_conv<IO, W, true> : k_short_conv<IO, W, false>, dim3((unsigned)rows, (unsigned)gy), dim3(kThreads), 0, s, (const T *)a.x,
+    return launch(tpr >= 64 ? k_short_conv<IO, W, true> : k_short_conv<IO, W, false>, grid_of(rows, (unsigned)gy), dim3(kThreads), 0, s, (const T *)a.x,
                   (const T *)a.x_in, a.w, a.bias, a.lengths, (T *)y, (T *)x_out, a.B, a.H, a.N, a.silu, lg);
 }
 
@@ -413,7 +414,7 @@ static hipError_t short_conv_bwd_taps(const ShortConvArgs &a, const void *dy, co
     int64_t pieces;
     int tpr_log2;
     const int K = bwd_splits(a.B, a.H, a.N, &pieces, &tpr_log2, V);
-    const hipError_t e = launch(tpr_log2 >= 6 ? k_short_conv_bwd<IO, W, true, V> : k_short_conv_bwd<IO, W, false, V>, dim3((unsigned)a.H, (unsigned)K), dim3(kThreads), 0, s,
+    const hipError_t e = launch(tpr_log2 >= 6 ? k_short_conv_bwd<IO, W, true, V> : k_short_conv_bwd<IO, W, false, V>, grid_of(a.H, (unsigned)K), dim3(kThreads), 0, s,
                                 (const T *)a.x, (const T *)a.x_in, a.w, a.bias, a.lengths, (const T *)dy,
                                 (const T *)dx_out, (T *)dx, (T *)dx_in, part, dw, dbias, a.B, a.H, a.N, a.silu, tpr_log2,
                                 pieces);

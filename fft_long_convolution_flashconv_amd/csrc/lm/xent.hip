@@ -386,8 +386,9 @@ __global__ __launch_bounds__(256, 4) void k_xent_stats32(const float *x, const f
     constexpr int TM = P::TM;
     __shared__ f4 lds[2][2][BT * 8];
     __shared__ float2 half[BT];
-    const int64_t tiles = (T + BT - 1) / BT, tile = blockIdx.x / tiles;  // of the vocabulary; tokens run first
-    const int64_t m0 = (blockIdx.x - tile * tiles) * BT, n0 = tile * BT;
+    const int64_t id = block_id(), tiles = (T + BT - 1) / BT, tile = id / tiles;  // of the vocabulary; tokens run first
+    const int64_t m0 = (id - tile * tiles) * BT, n0 = tile * BT;
+    if (n0 >= V) return;
     P tile32;
     tile32.run(Operand32<false, BT>{x + m0 * ld, ld, (T - m0) * ld, T - m0, D},
                Operand32<false, BT>{w + n0 * ld, ld, (V - n0) * ld, V - n0, D}, D, lds);
@@ -440,7 +441,7 @@ __global__ __launch_bounds__(1024) void k_xent_join(const float2 *__restrict__ p
                                                     const Labels lab, float *__restrict__ loss,
                                                     float *__restrict__ lse, int64_t T, int64_t tiles) {
     __shared__ float2 red[16][64];
-    const int64_t t = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+    const int64_t t = block_id() * 64 + (threadIdx.x & 63);
     const int g = threadIdx.x >> 6;
     float2 a = make_float2(-INFINITY, 0.f);
     if (t < T)
@@ -494,8 +495,9 @@ __global__ __launch_bounds__(256, 4) void k_xent_grad32(const float *x, const fl
     using P = Tile32<BT>;
     constexpr int TM = P::TM;
     __shared__ f4 lds[2][2][BT * 8];
-    const int64_t tiles = (T + BT - 1) / BT, tile = blockIdx.x / tiles;  // of the vocabulary; tokens run first
-    const int64_t m0 = (blockIdx.x - tile * tiles) * BT, n0 = tile * BT;
+    const int64_t id = block_id(), tiles = (T + BT - 1) / BT, tile = id / tiles;  // of the vocabulary; tokens run first
+    const int64_t m0 = (id - tile * tiles) * BT, n0 = tile * BT;
+    if (n0 >= nv) return;
     P tile32;
     tile32.run(Operand32<false, BT>{x + m0 * ld, ld, (T - m0) * ld, T - m0, D},
                Operand32<false, BT>{w + (v0 + n0) * ld, ld, (nv - n0) * ld, nv - n0, D}, D, lds);
@@ -531,10 +533,11 @@ __global__ __launch_bounds__(256) void k_xent_products32(const float *x, const f
     using P = Tile32<BT>;
     constexpr int TM = P::TM;
     __shared__ f4 lds[2][2][BT * 8];
-    const int64_t cols = (D + BT - 1) / BT;
-    const bool is_dx = (int64_t)blockIdx.x < ndx;
-    const int64_t tiles = ndx / splits, part = is_dx ? blockIdx.x / tiles : 0, k0 = part * kx;
-    const int64_t id = is_dx ? blockIdx.x - part * tiles : blockIdx.x - ndx, m0 = id / cols * BT, n0 = id % cols * BT;
+    const int64_t cols = (D + BT - 1) / BT, block = block_id();
+    const bool is_dx = block < ndx;
+    const int64_t tiles = ndx / splits, part = is_dx ? block / tiles : 0, k0 = part * kx;
+    const int64_t id = is_dx ? block - part * tiles : block - ndx, m0 = id / cols * BT, n0 = id % cols * BT;
+    if (!is_dx && m0 >= nv) return;
     const int64_t kn = nv - k0 < kx ? nv - k0 : kx;
     const int64_t ng = T * nv > 4 ? T * nv : 4;  // (there is room for four)
     P tile32;
@@ -602,7 +605,8 @@ __global__ __launch_bounds__(kThreads16<BT>, BT == 256 ? 1 : 2) void k_xent_stat
     __shared__ __align__(16) char lds[L::kLds];
     const int64_t rows = (V + L::BM - 1) / L::BM, cols = (T + L::BN - 1) / L::BN;
     int64_t rt, ct;
-    tile_of(xcd_order(blockIdx.x, rows * cols), rows, cols, rt, ct);
+    if (block_id() >= rows * cols) return;
+    tile_of(xcd_order(block_id(), rows * cols), rows, cols, rt, ct);
     const int64_t v0 = rt * L::BM, t0 = ct * L::BN;
     typename L::OA a;
     typename L::OB b;
@@ -678,7 +682,8 @@ __global__ __launch_bounds__(kThreads16<BT>, BT == 256 ? 1 : 2) void k_xent_grad
     __shared__ __align__(16) char lds[L::kLds];
     const int64_t rows = (nv + L::BM - 1) / L::BM, cols = (T + L::BN - 1) / L::BN;
     int64_t rt, ct;
-    tile_of(xcd_order(blockIdx.x, rows * cols), rows, cols, rt, ct);
+    if (block_id() >= rows * cols) return;
+    tile_of(xcd_order(block_id(), rows * cols), rows, cols, rt, ct);
     const int64_t r0 = rt * L::BM, t0 = ct * L::BN;
     typename L::OA a;
     typename L::OB b;
@@ -751,8 +756,9 @@ __global__ __launch_bounds__(kThreads16<BT>, BT == 256 ? 1 : 2) void k_xent_prod
     const int lane = threadIdx.x & 63;
     const float down = scale[1];
     int64_t rt, ct;
-    if ((int64_t)blockIdx.x < ndx) {
-        const int64_t cols = ndx / rows / splits, id = xcd_order(blockIdx.x, ndx), part = id / (rows * cols);
+    const int64_t block = block_id();
+    if (block < ndx) {
+        const int64_t cols = ndx / rows / splits, id = xcd_order(block, ndx), part = id / (rows * cols);
         tile_of(id - part * rows * cols, rows, cols, rt, ct);
         const int64_t d0 = rt * PX::BM, t0 = ct * PX::BN, k0 = part * kx, kn = kv - k0 < kx ? kv - k0 : kx;
         typename PX::OA a;
@@ -787,8 +793,9 @@ __global__ __launch_bounds__(kThreads16<BT>, BT == 256 ? 1 : 2) void k_xent_prod
                 st_row<IO_F32, 4>(sum + t * D + d, q, D - d);
             }
     } else {
-        const int64_t n = (int64_t)gridDim.x - ndx, cols = n / rows / wsplits;
-        const int64_t id = xcd_order(blockIdx.x - ndx, n), part = id / (rows * cols);
+        const int64_t cols = (nv + PW::BN - 1) / PW::BN, n = rows * cols * wsplits;
+        if (block - ndx >= n) return;
+        const int64_t id = xcd_order(block - ndx, n), part = id / (rows * cols);
         tile_of(id - part * rows * cols, rows, cols, rt, ct);
         const int64_t d0 = rt * PW::BM, c0 = ct * PW::BN, k0 = part * kw, kn = Tp - k0 < kw ? Tp - k0 : kw;
         typename PW::OA a;
@@ -818,7 +825,7 @@ __global__ __launch_bounds__(kThreads16<BT>, BT == 256 ? 1 : 2) void k_xent_prod
 template <int IO>
 __global__ __launch_bounds__(256) void k_xent_dx(const float *__restrict__ accum, const float *__restrict__ scale,
                                                  typename io_elem<IO>::T *__restrict__ dx, int64_t n, int splits) {
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    const int64_t i = (block_id() * 256 + threadIdx.x) * 4;
     if (i >= n) return;
     float s[4];
     ld_row<IO_F32, 4>(accum + i, s, n - i);
@@ -840,7 +847,7 @@ template <class E>
 __global__ __launch_bounds__(256) void k_xent_pad(const E *__restrict__ src, E *__restrict__ dst, int64_t R,
                                                   int64_t C, int64_t ldd) {
     constexpr int n = 16 / (int)sizeof(E);
-    const int64_t v = ldd / n, i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / v, c = (i - r * v) * n;
+    const int64_t v = ldd / n, i = block_id() * 256 + threadIdx.x, r = i / v, c = (i - r * v) * n;
     if (r >= R) return;
     Pack<E, n> q;
     if (c + n <= C) {
@@ -855,7 +862,7 @@ __global__ __launch_bounds__(256) void k_xent_pad(const E *__restrict__ src, E *
 // dw of no tokens.
 template <class E>
 __global__ __launch_bounds__(256) void k_xent_zero(E *__restrict__ p, int64_t n) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = block_id() * 256 + threadIdx.x;
     if (i < n) p[i] = (E)0;
 }
 
@@ -991,7 +998,7 @@ Plan plan(int64_t T, int64_t D, int64_t V, int io, bool bwd, char *base) {
     return p;
 }
 
-unsigned blocks(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per); }
+int64_t blocks(int64_t n, int64_t per) { return (n + per - 1) / per; }
 
 // x and w with rows of whole slabs: as they are, or copied.
 template <int IO>
@@ -1000,7 +1007,7 @@ hipError_t padded(const void *src, char *dst, int64_t R, int64_t D, int64_t kD, 
     *out = (const char *)src;
     if (kD == D) return hipSuccess;
     *out = dst;
-    return launch(k_xent_pad<E>, dim3(blocks(R * kD, 256 * 16 / (int64_t)sizeof(E))), dim3(256), 0, s, (const E *)src, (E *)dst, R, D, kD);
+    return launch(k_xent_pad<E>, grid_of(blocks(R * kD, 256 * 16 / (int64_t)sizeof(E))), dim3(256), 0, s, (const E *)src, (E *)dst, R, D, kD);
 }
 
 template <int IO>
@@ -1014,15 +1021,15 @@ hipError_t fwd_io(const void *x, const void *w, const Labels &lab, float *loss, 
     if (e != hipSuccess) return e;
     if constexpr (IO == IO_F32) {
         const int64_t bt = side32(T, V);
-        e = launch(bt == 32 ? k_xent_stats32<32> : k_xent_stats32<64>, dim3(blocks(T, bt) * blocks(V, bt)), dim3(256), 0, s,
+        e = launch(bt == 32 ? k_xent_stats32<32> : k_xent_stats32<64>, grid_of(blocks(T, bt) * blocks(V, bt)), dim3(256), 0, s,
                    (const float *)xr, (const float *)wr, p.kD, lab, p.part, p.hit, T, D, V);
     } else {
         const int64_t bt = side16(T, V);
         e = launch(bt == 256 ? k_xent_stats16<IO, 256> : (bt == 128 ? k_xent_stats16<IO, 128> : k_xent_stats16<IO, 64>),
-                   dim3(blocks(V, bt) * blocks(T, bt)), dim3(bt == 256 ? 512 : 256), 0, s, xr, wr, ld, lab, p.part, p.hit, T, V);
+                   grid_of(blocks(V, bt) * blocks(T, bt)), dim3(bt == 256 ? 512 : 256), 0, s, xr, wr, ld, lab, p.part, p.hit, T, V);
     }
     if (e != hipSuccess) return e;
-    return launch(k_xent_join, dim3(blocks(T, 64)), dim3(1024), 0, s, p.part, p.hit, lab, loss, lse, T, p.tiles);
+    return launch(k_xent_join, grid_of(blocks(T, 64)), dim3(1024), 0, s, p.part, p.hit, lab, loss, lse, T, p.tiles);
 }
 
 template <int IO>
@@ -1030,7 +1037,7 @@ hipError_t bwd_io(const void *x, const void *w, const Labels &lab, const float *
                   void *dw, int64_t T, int64_t D, int64_t V, char *ws, hipStream_t s) {
     using E = typename io_elem<IO>::T;
     const int64_t es = sizeof(E);
-    if (T == 0) return launch(k_xent_zero<E>, dim3(blocks(V * D, 256)), dim3(256), 0, s, (E *)dw, V * D);
+    if (T == 0) return launch(k_xent_zero<E>, grid_of(blocks(V * D, 256)), dim3(256), 0, s, (E *)dw, V * D);
     const Plan p = plan(T, D, V, IO, true, ws);
     const int64_t ld = p.kD * es;
     const char *xr, *wr;
@@ -1044,23 +1051,23 @@ hipError_t bwd_io(const void *x, const void *w, const Labels &lab, const float *
         if constexpr (IO == IO_F32) {
             const float *const xf = (const float *)xr, *const wf = (const float *)wr;
             int64_t bt = side32(T, nv);
-            e = launch(bt == 32 ? k_xent_grad32<32> : k_xent_grad32<64>, dim3(blocks(T, bt) * blocks(nv, bt)), dim3(256), 0, s,
+            e = launch(bt == 32 ? k_xent_grad32<32> : k_xent_grad32<64>, grid_of(blocks(T, bt) * blocks(nv, bt)), dim3(256), 0, s,
                        xf, wf, p.kD, lab, lse, dloss, (float *)p.g, T, D, v0, nv);
             if (e != hipSuccess) break;
             bt = p.side;
             const int64_t parts = (nv + p.range - 1) / p.range;  // (a shorter last piece has fewer)
-            const int64_t ndx = (int64_t)blocks(T, bt) * blocks(D, bt) * parts, ndw = (int64_t)blocks(nv, bt) * blocks(D, bt);
-            e = launch(bt == 32 ? k_xent_products32<32> : k_xent_products32<64>, dim3((unsigned)(ndx + ndw)), dim3(256), 0, s,
+            const int64_t ndx = blocks(T, bt) * blocks(D, bt) * parts, ndw = blocks(nv, bt) * blocks(D, bt);
+            e = launch(bt == 32 ? k_xent_products32<32> : k_xent_products32<64>, grid_of(ndx + ndw), dim3(256), 0, s,
                        xf, wf + v0 * p.kD, p.kD, (const float *)p.g, (float *)dx, (float *)dw + v0 * D, p.accum, T, D, nv,
                        p.range, (int)parts, ndx, first);
             if (e == hipSuccess && last && p.accum)
-                e = launch(k_xent_dx<IO>, dim3(blocks(T * D, 1024)), dim3(256), 0, s, p.accum, p.scale, (E *)dx, T * D,
+                e = launch(k_xent_dx<IO>, grid_of(blocks(T * D, 1024)), dim3(256), 0, s, p.accum, p.scale, (E *)dx, T * D,
                            (int)p.ranges);
         } else {
             const int64_t kv = ceil_to(nv, 64);
             int64_t bt = side16(T, nv);
             e = launch(bt == 256 ? k_xent_grad16<IO, 256> : (bt == 128 ? k_xent_grad16<IO, 128> : k_xent_grad16<IO, 64>),
-                       dim3(blocks(nv, bt) * blocks(T, bt)), dim3(bt == 256 ? 512 : 256), 0, s, xr, wr,
+                       grid_of(blocks(nv, bt) * blocks(T, bt)), dim3(bt == 256 ? 512 : 256), 0, s, xr, wr,
                        ld, lab, lse, dloss, p.scale, (E *)p.g, kv, T, p.Tp, v0, nv);
             if (e != hipSuccess) break;
             // ranges of whole slabs, as long as the first piece's (a shorter last piece has fewer)
@@ -1069,14 +1076,14 @@ hipError_t bwd_io(const void *x, const void *w, const Labels &lab, const float *
             const int64_t rows = blocks(D, bt), ndx = rows * blocks(T, bt) * parts, ndw = rows * blocks(nv, bt) * p.wranges;
             e = launch(bt == 256 ? k_xent_products16<IO, 256>
                                  : (bt == 128 ? k_xent_products16<IO, 128> : k_xent_products16<IO, 64>),
-                       dim3((unsigned)(ndx + ndw)), dim3(bt == 256 ? 512 : 256), 0, s, xr, wr + v0 * ld, ld, p.g,
+                       grid_of(ndx + ndw), dim3(bt == 256 ? 512 : 256), 0, s, xr, wr + v0 * ld, ld, p.g,
                        kv, (E *)dx, (E *)dw + v0 * D, p.accum, p.waccum, p.scale, T, p.Tp, D, nv, kv, kx, (int)parts, p.wrange, (int)p.wranges, ndx,
                        first, p.accum ? 0 : 1);
             if (e == hipSuccess && last && p.accum)
-                e = launch(k_xent_dx<IO>, dim3(blocks(T * D, 1024)), dim3(256), 0, s, p.accum, p.scale, (E *)dx, T * D,
+                e = launch(k_xent_dx<IO>, grid_of(blocks(T * D, 1024)), dim3(256), 0, s, p.accum, p.scale, (E *)dx, T * D,
                            (int)p.ranges);
             if (e == hipSuccess && p.waccum)
-                e = launch(k_xent_dx<IO>, dim3(blocks(nv * D, 1024)), dim3(256), 0, s, p.waccum, p.scale, (E *)dw + v0 * D,
+                e = launch(k_xent_dx<IO>, grid_of(blocks(nv * D, 1024)), dim3(256), 0, s, p.waccum, p.scale, (E *)dw + v0 * D,
                            nv * D, (int)p.wranges);
         }
     }
