@@ -168,35 +168,55 @@ __device__ __forceinline__ void hold(float (&v)[n]) {
     for (int i = 0; i < n; ++i) asm volatile("" : "+v"(v[i]));
 }
 
-// P times the P of the lane CTRL names.  In a group of one DPP row (16 lanes)
-// the lanes without such a source have reached the group's start, whose
-// entering state is folded into Q: their P is not needed any more, and reading
-// zero is as good as one (and is one instruction).  Otherwise it reads one.
-template <int LPR, int CTRL>
-__device__ __forceinline__ float shorten(float P) {
-    return P * (LPR == 16 ? dpp0<CTRL>(P) : dpp_rows<CTRL, 0xf>(1.f, P));
+// A map x -> 2^E x + Q by its factor.  Where no mode has A > 0 and no step is
+// negative, E <= 0, and the factor is 2^E itself.  Else (GROWS) the factor of
+// many steps may pass the largest float where the state, zero or small, does
+// not: it is held as 2^(E/2), at most 2^127, and applied twice.  (At that bound
+// a state that is not zero passes the largest float itself.)
+constexpr float kMostGrowth = 0x1p127f;
+template <bool GROWS>
+__device__ __forceinline__ float factor(float E) {
+    return GROWS ? fminf(exp2_(0.5f * E), kMostGrowth) : exp2_(E);
+}
+template <bool GROWS>
+__device__ __forceinline__ float apply(float P, float x, float Q) {
+    return GROWS ? fmaf(P * x, P, Q) : fmaf(P, x, Q);
+}
+template <bool GROWS>
+__device__ __forceinline__ float compose(float P, float R) {
+    return GROWS ? fminf(P * R, kMostGrowth) : P * R;
 }
 
-// Inclusive composition over groups of LPR lanes of maps x -> P x + Q, whose
+// P composed with the P of the lane CTRL names.  In a group of one DPP row (16
+// lanes) the lanes without such a source have reached the group's start, whose
+// entering state is folded into Q: their P is not needed any more, and reading
+// zero is as good as one (and is one instruction; P is finite).  Otherwise it
+// reads one.
+template <int LPR, bool GROWS, int CTRL>
+__device__ __forceinline__ float shorten(float P) {
+    return compose<GROWS>(P, LPR == 16 ? dpp0<CTRL>(P) : dpp_rows<CTRL, 0xf>(1.f, P));
+}
+
+// Inclusive composition over groups of LPR lanes of maps with factors P, whose
 // first lane has its entering state folded into Q: on return Q is the state
 // that leaves each lane.
-template <int LPR>
+template <int LPR, bool GROWS>
 __device__ __forceinline__ void scan_states(float P, float &Q) {
-    Q = fmaf(P, dpp0<0x111>(Q), Q);  // row_shr:1
-    P = shorten<LPR, 0x111>(P);
-    Q = fmaf(P, dpp0<0x112>(Q), Q);
-    P = shorten<LPR, 0x112>(P);
-    Q = fmaf(P, dpp0<0x114>(Q), Q);
-    P = shorten<LPR, 0x114>(P);
-    Q = fmaf(P, dpp0<0x118>(Q), Q);
+    Q = apply<GROWS>(P, dpp0<0x111>(Q), Q);  // row_shr:1
+    P = shorten<LPR, GROWS, 0x111>(P);
+    Q = apply<GROWS>(P, dpp0<0x112>(Q), Q);
+    P = shorten<LPR, GROWS, 0x112>(P);
+    Q = apply<GROWS>(P, dpp0<0x114>(Q), Q);
+    P = shorten<LPR, GROWS, 0x114>(P);
+    Q = apply<GROWS>(P, dpp0<0x118>(Q), Q);
     if constexpr (LPR == 64) {
-        P = shorten<LPR, 0x118>(P);
+        P = shorten<LPR, GROWS, 0x118>(P);
         // the rows of 16 lanes: row 1 after row 0 and row 3 after row 2, then
         // rows 2 and 3 after row 1
         const float q = dpp_rows<0x142, 0xa>(0.f, Q), p = dpp_rows<0x142, 0xa>(1.f, P);  // row_bcast:15
-        Q = fmaf(P, q, Q);
-        P *= p;
-        Q = fmaf(P, dpp_rows<0x143, 0xc>(0.f, Q), Q);  // row_bcast:31
+        Q = apply<GROWS>(P, q, Q);
+        P = compose<GROWS>(P, p);
+        Q = apply<GROWS>(P, dpp_rows<0x143, 0xc>(0.f, Q), Q);  // row_bcast:31
     }
 }
 
@@ -240,13 +260,13 @@ enum Share {
 // wave keeps in its own *st the state before the first and then after the
 // last.  B and C arrive as loaded; nextB() and nextC() load a later mode's
 // into the same registers once they are unpacked.
-template <int IO, int LPR, Share SH, Fit F, class NextB, class NextC>
+template <int IO, int LPR, Share SH, Fit F, bool GROWS, class NextB, class NextC>
 __device__ __forceinline__ void scan_mode(Raw<IO, kIT> &rB, Raw<IO, kIT> &rC, float A2, float in,
                                           const float (&d)[kIT], const float (&u)[kIT], const Sums &sum,
                                           float (&o)[kIT], float *st, int l, float2 (*maps)[4], float *saved,
                                           const Raw<IO, kIT> &own, const NextB &nextB, const NextC &nextC) {
     constexpr int IT = kIT;
-    float a[IT], w[IT], c[IT], P = exp2_(sum.lane * A2), Q = SH != kTime ? in : 0.f;
+    float a[IT], w[IT], c[IT], P = factor<GROWS>(sum.lane * A2), Q = SH != kTime ? in : 0.f;
     if (F != kFull) {
 #pragma unroll
         for (int i = 0; i < Raw<IO, IT>::kWords; ++i) rB.w[i] &= own.w[i];  // (what is passed over may be NaN)
@@ -259,23 +279,23 @@ __device__ __forceinline__ void scan_mode(Raw<IO, kIT> &rB, Raw<IO, kIT> &rC, fl
         a[i] = exp2_(d[i] * A2);
         Q = fmaf(a[i], Q, w[i]);
     }
-    scan_states<LPR>(P, Q);
+    scan_states<LPR, GROWS>(P, Q);
     float x0 = dpp0<LPR == 64 ? 0x138 : 0x111>(Q);  // from the lane before
     if constexpr (SH != kTime) {
         x0 += in;
     } else {
         const int wave = threadIdx.x >> 6;
-        if (l == LPR - 1) (*maps)[wave] = make_float2(exp2_(sum.wave * A2), Q);
+        if (l == LPR - 1) (*maps)[wave] = make_float2(factor<GROWS>(sum.wave * A2), Q);
         __syncthreads();
         float x = *st, enter = x;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 m = (*maps)[i];
-            x = fmaf(m.x, x, m.y);
+            x = apply<GROWS>(m.x, x, m.y);
             if (i + 1 == wave) enter = x;
         }
         Q = x;
-        x0 = fmaf(exp2_(sum.before * A2), enter, x0);
+        x0 = apply<GROWS>(factor<GROWS>(sum.before * A2), enter, x0);
     }
     float x = x0;
     unpack<IO, IT>(rC, c);
@@ -303,7 +323,7 @@ struct Lane {
 // of the two buffers of maps mode 0 takes.  The modes take them in turn, across
 // pieces too: with one barrier per mode, a wave may write a mode's map while
 // another still reads those of the mode before, never of the one before that.
-template <int IO, int LPR, Share SH, Fit F, class Reload>
+template <int IO, int LPR, Share SH, Fit F, bool GROWS, class Reload>
 __device__ __forceinline__ void scan_piece(const SelK<typename io_elem<IO>::T> &k, const Lane &p, Raw<IO, kIT> &ru,
                                            Raw<IO, kIT> &rd, const float *Ap, float Dh, float bias, float *st, int l,
                                            bool live, int turn, float2 (*maps)[4], float (*part)[kIT][64],
@@ -344,7 +364,7 @@ __device__ __forceinline__ void scan_piece(const SelK<typename io_elem<IO>::T> &
     }
     if (SH == kTime) {
         float s = sum.lane;
-        scan_states<64>(1.f, s);
+        scan_states<64, false>(1.f, s);
         sum.before = dpp0<0x138>(s);
         sum.wave = lane_of(s, 63);
     }
@@ -360,7 +380,7 @@ __device__ __forceinline__ void scan_piece(const SelK<typename io_elem<IO>::T> &
             const float A2 = A * kLog2e, in0 = l == 0 ? in : 0.f;
             A = Ap[next];
             in = st[next];
-            scan_mode<IO, LPR, SH, F>(rB[j], rC[j], A2, in0, d, u, sum, o, st + n, l, maps + ((n + turn) & 1), sv ? sv + n : nullptr,
+            scan_mode<IO, LPR, SH, F, GROWS>(rB[j], rC[j], A2, in0, d, u, sum, o, st + n, l, maps + ((n + turn) & 1), sv ? sv + n : nullptr,
                                own, [&] { rB[j] = loadB(n + MS * AH); }, [&] { rC[j] = loadC(n + MS * AH); });
         }
     }
@@ -432,7 +452,11 @@ __global__ __launch_bounds__(256, IO == IO_F32 || LPR == 16 ? 2 : 3) void k_sel_
     const float Dh = k.D ? k.D[h] : 0.f, bias = k.dt_bias ? k.dt_bias[h] : 0.f;
     const float *Ap = k.A + (int64_t)h * k.S;
     float *st = state[wave][sub];
-    for (int n = l; n < k.S; n += LPR) st[n] = k.x_in ? k.x_in[(int64_t)rr * k.S + n] : 0.f;
+    bool grows = !k.softplus;  // (or might: the same for the waves of a shared row)
+    for (int n = l; n < k.S; n += LPR) {
+        st[n] = k.x_in ? k.x_in[(int64_t)rr * k.S + n] : 0.f;
+        grows |= Ap[n] > 0.f;
+    }
     __builtin_amdgcn_wave_barrier();
     float *sv = saved ? saved + (int64_t)rr * nchunk * k.S : nullptr;
     const auto piece = [&](int64_t base) {
@@ -441,40 +465,56 @@ __global__ __launch_bounds__(256, IO == IO_F32 || LPR == 16 ? 2 : 3) void k_sel_
         const int lo = (int)(t0 - w0 < IT ? t0 - w0 : IT), hi = (int)(len - w0 < IT ? (len > w0 ? len - w0 : 0) : IT);
         return Lane{t0, rr * N + w0, (int64_t)(b * (uint32_t)k.G + g) * k.S * N + w0, lo, hi > lo ? hi : lo};
     };
-    Raw<IO, IT> ru, rd;
-    int64_t base = 0;
-    int turn = 0;
-    if (__all(len >= PIECE)) {  // the pieces that are full in every row of the wave
-        Lane p = piece(0);
-        ru = ld_steps<IO, IT, kFull>(k.u, p.row, 0, N);
-        rd = ld_steps<IO, IT, kFull>(k.dt, p.row, 0, N);
-        bool more;
-        do {
-            more = __all(len >= base + 2 * PIECE);
-            scan_piece<IO, LPR, SH, kFull>(k, p, ru, rd, Ap, Dh, bias, st, l, live, turn, maps, part, y, sv, [&] {
-                const int64_t o = more ? p.row + PIECE : p.row;
-                ru = ld_steps<IO, IT, kFull>(k.u, o, 0, N);
-                rd = ld_steps<IO, IT, kFull>(k.dt, o, 0, N);
-            });
-            __builtin_amdgcn_wave_barrier();
-            base += PIECE;
-            turn ^= k.S & 1;
-            p = piece(base);
-        } while (more);
-    }
-    const auto rest = [&](auto fit) {
-        constexpr Fit F = decltype(fit)::value;
-        for (; base < N; base += PIECE) {
-            const Lane p = piece(base);
-            ru = ld_steps<IO, IT, F>(k.u, p.row, 0, N);
-            rd = ld_steps<IO, IT, F>(k.dt, p.row, 0, N);
-            scan_piece<IO, LPR, SH, F>(k, p, ru, rd, Ap, Dh, bias, st, l, live, turn, maps, part, y, sv, [] {});
-            __builtin_amdgcn_wave_barrier();
-            turn ^= k.S & 1;
+    const auto scan = [&](auto growing) {
+        constexpr bool GROWS = decltype(growing)::value;
+        Raw<IO, IT> ru, rd;
+        int64_t base = 0;
+        int turn = 0;
+        if (__all(len >= PIECE)) {  // the pieces that are full in every row of the wave
+            Lane p = piece(0);
+            ru = ld_steps<IO, IT, kFull>(k.u, p.row, 0, N);
+            rd = ld_steps<IO, IT, kFull>(k.dt, p.row, 0, N);
+            bool more;
+            do {
+                more = __all(len >= base + 2 * PIECE);
+                scan_piece<IO, LPR, SH, kFull, GROWS>(k, p, ru, rd, Ap, Dh, bias, st, l, live, turn, maps, part, y, sv, [&] {
+                    const int64_t o = more ? p.row + PIECE : p.row;
+                    ru = ld_steps<IO, IT, kFull>(k.u, o, 0, N);
+                    rd = ld_steps<IO, IT, kFull>(k.dt, o, 0, N);
+                });
+                __builtin_amdgcn_wave_barrier();
+                base += PIECE;
+                turn ^= k.S & 1;
+                p = piece(base);
+            } while (more);
         }
+        const auto rest = [&](auto fit) {
+            constexpr Fit F = decltype(fit)::value;
+            for (; base < N; base += PIECE) {
+                const Lane p = piece(base);
+                ru = ld_steps<IO, IT, F>(k.u, p.row, 0, N);
+                rd = ld_steps<IO, IT, F>(k.dt, p.row, 0, N);
+                scan_piece<IO, LPR, SH, F, GROWS>(k, p, ru, rd, Ap, Dh, bias, st, l, live, turn, maps, part, y, sv, [] {});
+                __builtin_amdgcn_wave_barrier();
+                turn ^= k.S & 1;
+            }
+        };
+        if (LPR == 16 && N < IT) rest(std::integral_constant<Fit, kShort>{});
+        else rest(std::integral_constant<Fit, kTail>{});
     };
-    if (LPR == 16 && N < IT) rest(std::integral_constant<Fit, kShort>{});
-    else rest(std::integral_constant<Fit, kTail>{});
+    // The form that bears growth has a body of its own: without softplus, where
+    // it is always taken, 1 x 1024 x 65536 bf16 takes 460 us with it and 439
+    // without, 8 x 768 x 1024 fp16 36.5 and 35.8.  (The marks keep the compiler
+    // from merging the two, with the registers of both.)
+    if (__any(grows)) {
+        asm volatile("; growing" ::: "memory");
+        scan(std::true_type{});
+        asm volatile("; growing" ::: "memory");
+    } else {
+        asm volatile("; steady" ::: "memory");
+        scan(std::false_type{});
+        asm volatile("; steady" ::: "memory");
+    }
     if (x_out && live)
         for (int n = l; n < k.S; n += LPR)
             if (SH == kOwnRows || wave == (SH == kTime ? 0 : n % 4)) x_out[(int64_t)rr * k.S + n] = st[n];
@@ -497,7 +537,9 @@ __global__ __launch_bounds__(256, IO == IO_F32 || LPR == 16 ? 2 : 3) void k_sel_
 // registers over all the wave's channels (no atomics), the scans over time
 // stay within a DPP row, and the sums over modes are two exchanges between
 // rows.  A lane prepares and finishes a quarter of its steps (softplus, gate)
-// and the rows share them through LDS.
+// and the rows share them through LDS.  Factors always take their GROWS form,
+// which costs 2 % (4 x 2560 x 2048 bf16, both passes, 506 to 517 us; a second
+// body, as the forward pass has, cost 3 to 10: the registers of both).
 // Measured: 4 x 2560 x 2048 bf16 with 16 modes 390 us, 0.86 million million
 // mode-steps a second; vector ALUs busy 74 % of the time at two waves per SIMD
 // (about 250 registers, which dB and dC of 4 modes x 8 steps need).  Two launches
@@ -513,15 +555,15 @@ struct SelBwdWs {
     int sets, per;         // sets per group, channels per set
 };
 
-// As scan_states<16>, from the last lane of a DPP row down.
+// As scan_states<16, true>, from the last lane of a DPP row down.
 __device__ __forceinline__ void scan_back(float P, float &Q) {
-    Q = fmaf(P, dpp0<0x101>(Q), Q);  // row_shl:1
-    P *= dpp0<0x101>(P);
-    Q = fmaf(P, dpp0<0x102>(Q), Q);
-    P *= dpp0<0x102>(P);
-    Q = fmaf(P, dpp0<0x104>(Q), Q);
-    P *= dpp0<0x104>(P);
-    Q = fmaf(P, dpp0<0x108>(Q), Q);
+    Q = apply<true>(P, dpp0<0x101>(Q), Q);  // row_shl:1
+    P = compose<true>(P, dpp0<0x101>(P));
+    Q = apply<true>(P, dpp0<0x102>(Q), Q);
+    P = compose<true>(P, dpp0<0x102>(P));
+    Q = apply<true>(P, dpp0<0x104>(Q), Q);
+    P = compose<true>(P, dpp0<0x104>(P));
+    Q = apply<true>(P, dpp0<0x108>(Q), Q);
 }
 
 // Sums over the wave's four DPP rows of v[0 .. 7]; row r gets those of
@@ -718,7 +760,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 if (!WHOLE && q >= rounds) break;
-                const float A2 = A[q] * kLog2e, P = exp2_(sum * A2);
+                const float A2 = A[q] * kLog2e, P = factor<true>(sum * A2);
                 float Bv[kJT], Cv[kJT], a[kJT], ax[kJT];
                 get8(BC[0][4 * row + q] + l, 16, Bv);
                 const float in = l == 0 ? xs[q] : 0.f;
@@ -729,7 +771,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_sel_bwd(
                     ax[i] = bu[i] * Bv[i];
                     Q = fmaf(a[i], Q, ax[i]);
                 }
-                scan_states<16>(P, Q);
+                scan_states<16, true>(P, Q);
                 float x = dpp0<0x111>(Q) + in;
                 get8(BC[1][4 * row + q] + l, 16, Cv);
 #pragma unroll
