@@ -456,14 +456,43 @@ __global__ __launch_bounds__(1024) void k_xent_join(const float2 *__restrict__ p
     }
 }
 
-// 16-bit G is held as a share of the largest |dloss| of a token that counts: with the
-// usual equal weights the entry of a label, -(1 - p), is then held almost
-// exactly, and it dominates its row.  fp16 multiplies by 2^15 more, so that
-// probabilities down to 2^-29 stay normal numbers.  scale[0]: the divisor,
-// scale[1]: what undoes both in the fp32 sums.
+// Vector i (16 bytes) of dst[r][c] = src[r][c] for c < C, zero up to ldd (whole
+// vectors) and in rows that keep(r) does not.
+template <class E, class Keep>
+__device__ __forceinline__ void pad_vector(const E *src, E *dst, int64_t R, int64_t C, int64_t ldd, int64_t i,
+                                           const Keep &keep) {
+    constexpr int n = 16 / (int)sizeof(E);
+    const int64_t v = ldd / n, r = i / v, c = (i - r * v) * n;
+    if (r >= R) return;
+    Pack<E, n> q{};
+    if (keep(r)) {
+        if (c + n <= C) {
+            q = *reinterpret_cast<const Pack<E, n> *>(src + r * C + c);
+        } else {
+#pragma unroll
+            for (int e = 0; e < n; ++e) q.v[e] = c + e < C ? src[r * C + c + e] : (E)0;
+        }
+    }
+    *reinterpret_cast<Pack<E, n> *>(dst + r * ldd + c) = q;
+}
+
+// What the 16-bit gradients need of the tokens, in one launch.  Blocks from 1 on
+// copy x to rows of whole slabs, and to zeros where a token carries no loss: dw
+// multiplies those by a G of zero, but they may hold anything.  Block 0, which
+// takes longer, finds the scale of G: it is held as a share of the largest
+// |dloss| of a token that counts.  With the usual equal weights the entry of a
+// label, -(1 - p), is then held almost exactly, and it dominates its row.  fp16
+// multiplies by 2^15 more, so that probabilities down to 2^-29 stay normal
+// numbers.  scale[0]: the divisor, scale[1]: what undoes both in the fp32 sums.
 template <int IO>
-__global__ __launch_bounds__(1024) void k_xent_scale(const float *__restrict__ dloss, const Labels lab,
-                                                     float *__restrict__ scale, int64_t T) {
+__global__ __launch_bounds__(1024) void k_xent_tokens16(const typename io_elem<IO>::T *__restrict__ x,
+                                                        typename io_elem<IO>::T *__restrict__ xc, int64_t D, int64_t kD,
+                                                        const float *__restrict__ dloss, const Labels lab,
+                                                        float *__restrict__ scale, int64_t T) {
+    if (block_id() > 0) {
+        pad_vector(x, xc, T, D, kD, (block_id() - 1) * 1024 + threadIdx.x, [&](int64_t t) { return lab.of(t) >= 0; });
+        return;
+    }
     __shared__ float red[16];
     float m = 0.f;
 #pragma unroll 8
@@ -486,11 +515,13 @@ __device__ __forceinline__ float weight(float dloss, float divisor) {
     return dloss / divisor * (IO == IO_F16 ? 0x1p15f : 1.f);
 }
 
-// G of the vocabulary piece [v0, v0 + nv): g[t][v - v0], rows of nv.
+// G of the vocabulary piece [v0, v0 + nv): g[t][v - v0], rows of nv.  xc, unless
+// null: x for dw's product, with zero rows as in k_xent_tokens16, each block a
+// share of its tokens' (so that small problems need no launch more).
 template <int BT>
 __global__ __launch_bounds__(256, 4) void k_xent_grad32(const float *x, const float *w, int64_t ld, const Labels lab,
                                                      const float *__restrict__ lse, const float *__restrict__ dloss,
-                                                     float *__restrict__ g, int64_t T,
+                                                     float *__restrict__ g, float *__restrict__ xc, int64_t T,
                                                      int64_t D, int64_t v0, int64_t nv) {
     using P = Tile32<BT>;
     constexpr int TM = P::TM;
@@ -519,6 +550,11 @@ __global__ __launch_bounds__(256, 4) void k_xent_grad32(const float *x, const fl
                 if (c < nv) g[t * nv + c] = l >= 0 ? q * dl : 0.f;
             }
         }
+    if (xc) {
+        const int n = (int)((T - m0 < BT ? T - m0 : BT) * ld), shares = (int)((nv + BT - 1) / BT);
+        for (int i = (int)tile * 256 + (int)threadIdx.x; i < n; i += shares * 256)
+            xc[m0 * ld + i] = lab.of(m0 + i / (int)ld) >= 0 ? x[m0 * ld + i] : 0.f;
+    }
 }
 
 // dx and dw of a piece in one launch: first the tiles of
@@ -842,21 +878,10 @@ __global__ __launch_bounds__(256) void k_xent_dx(const float *__restrict__ accum
     st_row<IO, 4>(dx + i, s, n - i);
 }
 
-// dst[r][c] = src[r][c] for c < C, zero up to ldd (whole vectors).
 template <class E>
 __global__ __launch_bounds__(256) void k_xent_pad(const E *__restrict__ src, E *__restrict__ dst, int64_t R,
                                                   int64_t C, int64_t ldd) {
-    constexpr int n = 16 / (int)sizeof(E);
-    const int64_t v = ldd / n, i = block_id() * 256 + threadIdx.x, r = i / v, c = (i - r * v) * n;
-    if (r >= R) return;
-    Pack<E, n> q;
-    if (c + n <= C) {
-        q = *reinterpret_cast<const Pack<E, n> *>(src + r * C + c);
-    } else {
-#pragma unroll
-        for (int e = 0; e < n; ++e) q.v[e] = c + e < C ? src[r * C + c + e] : (E)0;
-    }
-    *reinterpret_cast<Pack<E, n> *>(dst + r * ldd + c) = q;
+    pad_vector(src, dst, R, C, ldd, block_id() * 256 + threadIdx.x, [](int64_t) { return true; });
 }
 
 // dw of no tokens.
@@ -899,7 +924,7 @@ struct Plan {
     int64_t side;          // of the tiles of dx and dw
     int64_t range, ranges; // vocabulary rows whose part of dx is summed apart, such parts of a piece
     int64_t wrange, wranges; // tokens whose part of dw is summed apart, such parts (16-bit)
-    char *xp, *wp, *g;
+    char *xp, *wp, *xc, *g;
     float *accum, *waccum, *scale, *hit;
     float2 *part;
     size_t bytes;
@@ -936,7 +961,8 @@ Plan plan(int64_t T, int64_t D, int64_t V, int io, bool bwd, char *base) {
         at += align256((size_t)bytes);
         return q;
     };
-    p.xp = take(p.kD != D ? T * p.kD * e : 0);
+    p.xp = take(p.kD != D && (wide || !bwd) ? T * p.kD * e : 0);
+    p.xc = take(bwd ? T * p.kD * e : 0);  // x with zero rows for tokens without a loss
     p.wp = take(p.kD != D ? V * p.kD * e : 0);
     p.tiles = (V + rows - 1) / rows;
     if (!bwd) {
@@ -1000,7 +1026,7 @@ Plan plan(int64_t T, int64_t D, int64_t V, int io, bool bwd, char *base) {
 
 int64_t blocks(int64_t n, int64_t per) { return (n + per - 1) / per; }
 
-// x and w with rows of whole slabs: as they are, or copied.
+// x or w with rows of whole slabs: as it is, or copied.
 template <int IO>
 hipError_t padded(const void *src, char *dst, int64_t R, int64_t D, int64_t kD, const char **out, hipStream_t s) {
     using E = typename io_elem<IO>::T;
@@ -1040,11 +1066,14 @@ hipError_t bwd_io(const void *x, const void *w, const Labels &lab, const float *
     if (T == 0) return launch(k_xent_zero<E>, grid_of(blocks(V * D, 256)), dim3(256), 0, s, (E *)dw, V * D);
     const Plan p = plan(T, D, V, IO, true, ws);
     const int64_t ld = p.kD * es;
-    const char *xr, *wr;
-    hipError_t e = padded<IO>(x, p.xp, T, D, p.kD, &xr, s);
-    if (e == hipSuccess) e = padded<IO>(w, p.wp, V, D, p.kD, &wr, s);
-    if constexpr (IO != IO_F32)
-        if (e == hipSuccess) e = launch(k_xent_scale<IO>, dim3(1), dim3(1024), 0, s, dloss, lab, p.scale, T);
+    const char *xr = p.xc, *wr;
+    hipError_t e = padded<IO>(w, p.wp, V, D, p.kD, &wr, s);
+    if (e == hipSuccess) {
+        if constexpr (IO == IO_F32) e = padded<IO>(x, p.xp, T, D, p.kD, &xr, s);
+        else
+            e = launch(k_xent_tokens16<IO>, grid_of(1 + blocks(T * p.kD, 1024 * 8)), dim3(1024), 0, s, (const E *)x, (E *)p.xc,
+                       D, p.kD, dloss, lab, p.scale, T);
+    }
     for (int64_t i = 0; i < p.pieces && e == hipSuccess; ++i) {
         const int64_t v0 = i * p.piece, nv = V - v0 < p.piece ? V - v0 : p.piece;
         const int first = i == 0, last = i + 1 == p.pieces;
@@ -1052,13 +1081,13 @@ hipError_t bwd_io(const void *x, const void *w, const Labels &lab, const float *
             const float *const xf = (const float *)xr, *const wf = (const float *)wr;
             int64_t bt = side32(T, nv);
             e = launch(bt == 32 ? k_xent_grad32<32> : k_xent_grad32<64>, grid_of(blocks(T, bt) * blocks(nv, bt)), dim3(256), 0, s,
-                       xf, wf, p.kD, lab, lse, dloss, (float *)p.g, T, D, v0, nv);
+                       xf, wf, p.kD, lab, lse, dloss, (float *)p.g, first ? (float *)p.xc : nullptr, T, D, v0, nv);
             if (e != hipSuccess) break;
             bt = p.side;
             const int64_t parts = (nv + p.range - 1) / p.range;  // (a shorter last piece has fewer)
             const int64_t ndx = blocks(T, bt) * blocks(D, bt) * parts, ndw = blocks(nv, bt) * blocks(D, bt);
             e = launch(bt == 32 ? k_xent_products32<32> : k_xent_products32<64>, grid_of(ndx + ndw), dim3(256), 0, s,
-                       xf, wf + v0 * p.kD, p.kD, (const float *)p.g, (float *)dx, (float *)dw + v0 * D, p.accum, T, D, nv,
+                       (const float *)p.xc, wf + v0 * p.kD, p.kD, (const float *)p.g, (float *)dx, (float *)dw + v0 * D, p.accum, T, D, nv,
                        p.range, (int)parts, ndx, first);
             if (e == hipSuccess && last && p.accum)
                 e = launch(k_xent_dx<IO>, grid_of(blocks(T * D, 1024)), dim3(256), 0, s, p.accum, p.scale, (E *)dx, T * D,

@@ -449,6 +449,7 @@ h3conv_status h3conv_linear_xent(const void *x, const void *w, const int64_t *la
  * loss (lse as that call wrote it):
  *     G[t,v] = (exp(l[t,v] - lse[t]) - [v == labels[t]]) dloss[t]   (0 on ignored tokens)
  *     dx = G w  [T,D],   dw = G^T x  [V,D]     io dtype, written
+ * Ignored tokens add nothing to dw, whatever their x, lse and dloss hold.
  * The vocabulary is taken in pieces; G of one piece is held in the workspace
  * in the io dtype (fp16: scaled by a power of two from the largest |dloss|),
  * ws: at least h3conv_linear_xent_workspace_size(T, D, V, io, 1) bytes.
