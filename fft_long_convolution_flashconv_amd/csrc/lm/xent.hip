@@ -480,7 +480,7 @@ __device__ __forceinline__ void pad_vector(const E *src, E *dst, int64_t R, int6
 // copy x to rows of whole slabs, and to zeros where a token carries no loss: dw
 // multiplies those by a G of zero, but they may hold anything.  Block 0, which
 // takes longer, finds the scale of G: it is held as a share of the largest
-// |dloss| of a token that counts.  With the usual equal weights the entry of a
+// finite |dloss| of a token that counts.  With the usual equal weights the entry of a
 // label, -(1 - p), is then held almost exactly, and it dominates its row.  fp16
 // multiplies by 2^15 more, so that probabilities down to 2^-29 stay normal
 // numbers.  scale[0]: the divisor, scale[1]: what undoes both in the fp32 sums.
@@ -497,14 +497,14 @@ __global__ __launch_bounds__(1024) void k_xent_tokens16(const typename io_elem<I
     float m = 0.f;
 #pragma unroll 8
     for (int64_t t = threadIdx.x; t < T; t += 1024)
-        if (lab.of(t) >= 0) m = fmaxf(m, fabsf(dloss[t]));
+        if (lab.of(t) >= 0 && fabsf(dloss[t]) < INFINITY) m = fmaxf(m, fabsf(dloss[t]));
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int i = 1; i < 16; ++i) m = fmaxf(m, red[i]);
-        if (!(m > 0.f && m < INFINITY)) m = 1.f;
+        if (!(m > 0.f)) m = 1.f;
         scale[0] = m;
         scale[1] = IO == IO_F16 ? m * 0x1p-15f : m;
     }

@@ -451,7 +451,8 @@ h3conv_status h3conv_linear_xent(const void *x, const void *w, const int64_t *la
  *     dx = G w  [T,D],   dw = G^T x  [V,D]     io dtype, written
  * Ignored tokens add nothing to dw, whatever their x, lse and dloss hold.
  * The vocabulary is taken in pieces; G of one piece is held in the workspace
- * in the io dtype (fp16: scaled by a power of two from the largest |dloss|),
+ * in the io dtype, in 16 bits as a share of the largest finite |dloss| (fp16:
+ * times 2^15, so that its entries are held to 2^-40 of that one at least).
  * ws: at least h3conv_linear_xent_workspace_size(T, D, V, io, 1) bytes.
  */
 h3conv_status h3conv_linear_xent_bwd(const void *x, const void *w, const int64_t *labels, int64_t ignore_index,
