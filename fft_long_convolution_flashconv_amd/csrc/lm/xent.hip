@@ -79,7 +79,7 @@ struct Operand {
     int32_t off[kLoads];  // (the shim keeps 256 rows within 31 bits)
 
     __device__ __forceinline__ static int slot(int krow) { return ((krow & 3) | ((krow >> 3) & 1) << 2) & (ROWS / 16 - 1); }
-    __device__ __forceinline__ static int turn(int row) { return (row >> (KS == 32 ? 1 : 0)) & (KS / 8 - 1); }
+    __device__ __forceinline__ static int turn(int row) { return row & (KS / 8 - 1); }
 
     __device__ __forceinline__ void init(const char *m, int64_t ld_, int64_t rows, int64_t k_) {
         mem = m;
@@ -140,8 +140,9 @@ struct Tile {
     static constexpr int BM = BM_, BN = BN_, KS = KS_, NT = WM * WN * 64, TM = BM / WM / 16, TN = BN / WN / 16;
     using OA = Operand<BM, KS, NT, AK>;
     using OB = Operand<BN, KS, NT, BK>;
-    static constexpr int kStage = OA::kBytes + OB::kBytes, kLds = NS * kStage, NK = KS / 32;
+    static constexpr int kStage = OA::kBytes + OB::kBytes, kLds = NS * kStage;
     static constexpr int kLoads = OA::kLoads + OB::kLoads;
+    static_assert(KS == 64, "two k steps per slab");
     f4 acc[TM][TN];
 
     __device__ __forceinline__ static int wave() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6); }
@@ -195,40 +196,20 @@ struct Tile {
         read(lds, 0, fa[0], fb[0]);
         int64_t s = 0;
         int st = 0;  // s % NS
-        if constexpr (NK == 2) {
-            for (; s + 1 < slabs; ++s) {
-                const int nx = st + 1 == NS ? 0 : st + 1;
-                read(lds + st * kStage, 1, fa[1], fb[1]);
-                __builtin_amdgcn_sched_barrier(0);
-                mul(fa[0], fb[0]);
-                turn(a, b, lds, s, slabs);
-                read(lds + nx * kStage, 0, fa[0], fb[0]);
-                __builtin_amdgcn_sched_barrier(0);
-                mul(fa[1], fb[1]);
-                st = nx;
-            }
+        for (; s + 1 < slabs; ++s) {
+            const int nx = st + 1 == NS ? 0 : st + 1;
             read(lds + st * kStage, 1, fa[1], fb[1]);
+            __builtin_amdgcn_sched_barrier(0);
             mul(fa[0], fb[0]);
-            mul(fa[1], fb[1]);
-        } else {
-            static_assert(NK == 1, "one or two k steps per slab");
-            // two slabs per turn of the loop (slabs is even: k is padded to 64)
-            for (; s + 2 < slabs; s += 2) {
-                const int n1 = st + 1 == NS ? 0 : st + 1, n2 = n1 + 1 == NS ? 0 : n1 + 1;
-                turn(a, b, lds, s, slabs);
-                read(lds + n1 * kStage, 0, fa[1], fb[1]);
-                mul(fa[0], fb[0]);
-                turn(a, b, lds, s + 1, slabs);
-                read(lds + n2 * kStage, 0, fa[0], fb[0]);
-                mul(fa[1], fb[1]);
-                st = n2;
-            }
-            const int n1 = st + 1 == NS ? 0 : st + 1;
             turn(a, b, lds, s, slabs);
-            read(lds + n1 * kStage, 0, fa[1], fb[1]);
-            mul(fa[0], fb[0]);
+            read(lds + nx * kStage, 0, fa[0], fb[0]);
+            __builtin_amdgcn_sched_barrier(0);
             mul(fa[1], fb[1]);
+            st = nx;
         }
+        read(lds + st * kStage, 1, fa[1], fb[1]);
+        mul(fa[0], fb[0]);
+        mul(fa[1], fb[1]);
     }
 };
 
