@@ -1,48 +1,20 @@
 // h3conv_api.hip -- the C ABI: argument validation (host only, before any HIP
 // call), device check, dispatch to the kernel launchers.  See include/h3conv.h
 // for the contract of every entry point.
-#include <atomic>
-#include <cstring>
 #include <mutex>
 
-#include "../../include/h3conv.h"
+#include "api_checks.h"
 #include "h3conv_internal.h"
 
 namespace {
 
-constexpr int kMaxDevices = 64;
-std::atomic<int> g_dev_ok[kMaxDevices];  // 0 unknown, 1 usable gfx950, -1 not usable
+using namespace h3c;  // the host-side checks
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 size_t esize(int io) { return io == H3CONV_F32 ? 4 : 2; }
 
-bool valid_io(int io) { return io == H3CONV_F32 || io == H3CONV_F16 || io == H3CONV_BF16; }
-
-// [p, p + n) and [q, q + m) overlap?
-bool overlap(const void *p, size_t n, const void *q, size_t m) {
-    if (!p || !q || n == 0 || m == 0) return false;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return a < b + m && b < a + n;
-}
-
 bool mul_ok(int64_t a, int64_t b, int64_t lim) { return a >= 0 && b >= 0 && (a == 0 || b <= lim / a); }
-
-h3conv_status device_check() {
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return H3CONV_ERR_NO_DEVICE;
-    if (dev >= kMaxDevices) return H3CONV_ERR_NO_DEVICE;
-    int st = g_dev_ok[dev].load(std::memory_order_acquire);
-    if (st == 0) {
-        hipDeviceProp_t p;
-        if (hipGetDeviceProperties(&p, dev) != hipSuccess) return H3CONV_ERR_NO_DEVICE;
-        st = (std::strncmp(p.gcnArchName, "gfx950", 6) == 0) ? 1 : -1;
-        g_dev_ok[dev].store(st, std::memory_order_release);
-    }
-    return st == 1 ? H3CONV_OK : H3CONV_ERR_NO_DEVICE;
-}
-
-h3conv_status from_hip(hipError_t e) { return e == hipSuccess ? H3CONV_OK : H3CONV_ERR_HIP; }
 
 // Scratch memory of h3conv_state_pass_noalloc: one array per device, part of
 // the library's device code (allocated when the code is loaded on a device,

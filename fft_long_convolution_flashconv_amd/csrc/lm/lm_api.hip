@@ -2,35 +2,16 @@
 // linear cross entropy: argument validation (host only, before any HIP call)
 // and dispatch to the kernel launchers.  See include/h3conv.h for the
 // contract of every entry point.
-#include <atomic>
-#include <cstring>
 #include <initializer_list>
 
-#include "../../../include/h3conv.h"
+#include "../api_checks.h"
 #include "lm_internal.h"
 
 namespace {
 
-constexpr int kMaxDevices = 64;
-std::atomic<int> g_dev_ok[kMaxDevices];  // 0 unknown, 1 usable gfx950, -1 not usable
+using namespace h3c;  // the host-side checks
 
-bool valid_io(int io) { return io == H3CONV_F32 || io == H3CONV_F16 || io == H3CONV_BF16; }
 int64_t esize(int io) { return io == H3CONV_F32 ? 4 : 2; }
-
-h3conv_status device_check() {
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return H3CONV_ERR_NO_DEVICE;
-    int st = g_dev_ok[dev].load(std::memory_order_acquire);
-    if (st == 0) {
-        hipDeviceProp_t p;
-        if (hipGetDeviceProperties(&p, dev) != hipSuccess) return H3CONV_ERR_NO_DEVICE;
-        st = (std::strncmp(p.gcnArchName, "gfx950", 6) == 0) ? 1 : -1;
-        g_dev_ok[dev].store(st, std::memory_order_release);
-    }
-    return st == 1 ? H3CONV_OK : H3CONV_ERR_NO_DEVICE;
-}
-
-h3conv_status from_hip(hipError_t e) { return e == hipSuccess ? H3CONV_OK : H3CONV_ERR_HIP; }
 
 // One buffer argument of a call.
 struct Buf {
@@ -41,9 +22,7 @@ struct Buf {
 };
 
 bool overlap(const Buf &a, const Buf &b) {
-    if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+    return a.bytes > 0 && b.bytes > 0 && h3c::overlap(a.p, (size_t)a.bytes, b.p, (size_t)b.bytes);
 }
 
 // Pointers present and aligned; no output overlaps an input or another output.

@@ -11,6 +11,13 @@ namespace h3c {
 // This block's number in a grid that grid_of() made.
 __device__ __forceinline__ int64_t block_id() { return blockIdx.x + (int64_t)blockIdx.z * kGridX; }
 
+// Valid steps of batch row b.
+__device__ __forceinline__ int64_t row_len(const int32_t *lengths, int64_t b, int64_t N) {
+    if (!lengths) return N;
+    const int64_t n = lengths[b];
+    return n < 0 ? 0 : (n > N ? N : n);
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

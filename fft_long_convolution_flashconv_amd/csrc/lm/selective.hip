@@ -14,19 +14,12 @@
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
-#include <cstdlib>
 
 #include "lm_device.h"
 #include "lm_internal.h"
 
 namespace h3c {
 namespace {
-
-__device__ __forceinline__ int64_t row_len(const int32_t *lengths, int64_t b, int64_t N) {
-    if (!lengths) return N;
-    const int64_t n = lengths[b];
-    return n < 0 ? 0 : (n > N ? N : n);
-}
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 

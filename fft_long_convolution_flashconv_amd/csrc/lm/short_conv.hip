@@ -35,12 +35,6 @@ __device__ __forceinline__ int row_of(int tpr_log2) {
     return WAVE ? __builtin_amdgcn_readfirstlane(sub) : sub;
 }
 
-__device__ __forceinline__ int64_t row_len(const int32_t *lengths, int64_t b, int64_t N) {
-    if (!lengths) return N;
-    const int64_t n = lengths[b];
-    return n < 0 ? 0 : (n > N ? N : n);
-}
-
 // x at position p of a row that starts at p = -(W-1), the first W-1 from the
 // saved inputs
 template <int IO, int W>
