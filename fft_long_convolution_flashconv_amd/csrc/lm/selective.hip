@@ -422,8 +422,10 @@ __device__ __forceinline__ void scan_piece(const SelK<typename io_elem<IO>::T> &
 // spilled registers, and B and C staged in LDS for the block's rows gained
 // nothing.
 // Measured, 16 modes with a gate: 8 x 768 x 1024 fp16 36.9 us, 1 x 1024 x 65536
-// bf16 486 us, 4 x 2560 x 2048 bf16 with saved states 150 us: 2.2 to 2.7 million
-// million mode-steps a second, the vector ALUs busy 92 % of the compute units' time.
+// bf16 483 us, 4 x 2560 x 2048 bf16 with saved states 124 us (146 in a
+// training pass): 2.2 to 2.7 million million mode-steps a second, the vector ALUs
+// busy 90 to 95 % of the compute units' time.  (In bf16, rows of their own spill 11
+// registers at three waves per SIMD.)
 template <int IO, int LPR, Share SH>
 __global__ __launch_bounds__(256, IO == IO_F32 || LPR == 16 ? 2 : 3) void k_sel_scan(const SelK<typename io_elem<IO>::T> k,
                                                      typename io_elem<IO>::T *__restrict__ y,
@@ -533,10 +535,11 @@ __global__ __launch_bounds__(256, IO == IO_F32 || LPR == 16 ? 2 : 3) void k_sel_
 // and the rows share them through LDS.  Factors always take their GROWS form,
 // which costs 2 % (4 x 2560 x 2048 bf16, both passes, 506 to 517 us; a second
 // body, as the forward pass has, cost 3 to 10: the registers of both).
-// Measured: 4 x 2560 x 2048 bf16 with 16 modes 390 us, 0.86 million million
-// mode-steps a second; vector ALUs busy 74 % of the time at two waves per SIMD
-// (about 250 registers, which dB and dC of 4 modes x 8 steps need).  Two launches
-// of 16 and 8 modes take 207 and 174 us at 4 x 2560 x 1024, 8 modes alone 146.
+// Measured: 4 x 2560 x 2048 bf16 with 16 modes 400 us, 0.84 million million
+// mode-steps a second; vector ALUs busy 75 % of the time at two waves per SIMD
+// (about 250 registers, which dB and dC of 4 modes x 8 steps need; numbers of
+// modes other than 16 spill 8 to 17).  Two launches of 16 and 8 modes take 210
+// and 174 us at 4 x 2560 x 1024, 8 modes alone 149.
 constexpr int kModes = 16, kJT = kSelChunk / 16, kQ = kJT / 4, kWaves = 8, kPerWave = 16;
 static_assert(kJT == 8 && kQ == 2 && 2 * kModes * kSelChunk == kWaves * 64 * 8, "one 8-step load of B or C per thread and piece");
 
@@ -931,10 +934,12 @@ __global__ __launch_bounds__(256) void k_sel_join(const SelBwdWs ws, typename io
 
 // -------------------------------------------------------------- single token
 
-// LPC lanes per channel, four modes each (a channel's states are read as
-// whole lines).  Bound by the launch and one chain of loads (slot, state): 6.8 us
-// for 64 x 768 with 16 modes (6.7 MB, 1.3 us at a copy's rate).  A slot outside the pool leaves its row's output zero and no
-// state changed.
+// LPC lanes per channel, four modes each (a channel's states are read as whole
+// lines).  Bound by the launch and a chain of about eight trips to memory: the
+// slot; u, dt and bias; a lane's four modes one after another (the pools may be
+// one, so the load of a state stands behind the store of the one before it); D;
+// z.  6.5 us for 64 x 768 with 16 modes (6.7 MB, 1.3 us at a copy's rate).  A
+// slot outside the pool leaves its row's output zero and no state changed.
 template <int IO>
 __global__ __launch_bounds__(256) void k_sel_step(const typename io_elem<IO>::T *__restrict__ u,
                                                   const typename io_elem<IO>::T *__restrict__ dt,
@@ -1037,9 +1042,9 @@ template <int IO>
 hipError_t scan_io(const SelArgs &a, void *y, float *x_out, float *saved, hipStream_t s) {
     // Measured in fp16 with 16 modes and a gate, us, at (rows x steps):
     //                    288x301  288x4096  1024x2048  1024x4096  2048x250  4096x250  4096x4096
-    //   own rows            12.5      36.8       20.4       39.4      11.7      12.3       99.1
-    //   time                           18.9       32.1       32.1                          105.0
-    //   modes                8.9      22.5       20.6       40.2       8.8      15.3      131.6
+    //   own rows            12.1      35.4       19.3       36.7      11.3      11.5       95.4
+    //   time                           17.7       31.3       30.3                          102.1
+    //   modes                8.4      21.1       19.8       37.8       8.2      14.2      128.5
     // A quarter of the time is won where four pieces at once leave no wave idle
     // and the rows alone are too few to fill the chip; a quarter of the modes
     // where there is but one wave or two per compute unit.

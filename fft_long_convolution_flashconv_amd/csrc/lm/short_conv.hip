@@ -79,9 +79,10 @@ __device__ __forceinline__ int few(int64_t n) { return (int)(n < 0 ? 0 : (n > 64
 
 // A thread takes one 16-byte vector of a row, and the W - 1 elements before it
 // from the caches (one more load; two vectors per thread were a sixth slower).
-// 4 x 2560 x 2048, bf16, 4 taps: 17.1 us, 4.9 TB/s (a copy reaches 5.1); with a
-// wave's addresses and masks on the vector ALUs, 29 instructions per element,
-// these bounded it: 21.6 us.  8 x 768 x 1024 fp16: 9.2 us.
+// 4 x 2560 x 2048, 4 taps: bf16 16.7 us, 5.0 TB/s (a copy reaches 5.1), fp32 25.4
+// (168 MB, which the caches hold in part); with a wave's addresses and masks on
+// the vector ALUs, 29 instructions per element, these bounded it: 21.6 us in bf16.
+// 8 x 768 x 1024 fp16: 8.5 us.
 template <int IO, int W, bool WAVE>
 __global__ __launch_bounds__(kThreads) void k_short_conv(const typename io_elem<IO>::T *__restrict__ x,
                                                          const typename io_elem<IO>::T *__restrict__ x_in,
@@ -148,8 +149,9 @@ __device__ __forceinline__ float act_bwd(float p, float dy, int silu) {
 //   dx_s = sum_i w_i dp_{s+i},  dw_i = sum_{b,t} dp_t x_{t-i},  dbias = sum dp.
 // A thread forms dp of its own V steps and of the W - 1 after them, which costs
 // 3 of 11 (V = 8) or of 19 (16) activations at 4 taps and saves an exchange
-// between threads.  4 x 2560 x 2048, bf16, 4 taps: 25.9 us, 4.9 TB/s,
-// from inputs that the caches hold in part.
+// between threads.  4 x 2560 x 2048, 4 taps: bf16 24.8 us, 5.1 TB/s, fp32 41.1 us
+// (252 MB), from inputs that the caches hold in part; 27.3 in bf16 after a forward
+// pass.
 template <int IO, int W, bool WAVE, int V>
 __global__ __launch_bounds__(kThreads) void k_short_conv_bwd(
     const typename io_elem<IO>::T *__restrict__ x, const typename io_elem<IO>::T *__restrict__ x_in,

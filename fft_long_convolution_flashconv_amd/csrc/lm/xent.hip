@@ -10,14 +10,18 @@
 // the workspace, and two products give dw of the piece and the piece's part
 // of dx.  Four products of 2 T D V operations each in all: matrix-core bound.
 // Logits, maxima, sums and the products' sums are fp32.  With 16-bit inputs G is
-// rounded to them, as the operand of two 16-bit products; its error averages out
-// over the sums, and dx and dw are rounded once more.
+// rounded to them, as the operand of two 16-bit products (in 32 bits they would
+// run at a sixteenth of the rate).  Its error averages out over the sums: at 8192
+// x 768 x 50021 bf16, dx and dw are off by 1.660e-3 and 1.663e-3 of their norms
+// with it and by 1.658e-3 and 1.661e-3 with G in 32 bits, which is what rounding
+// dx and dw themselves to bf16 makes.
 //
-// Measured in bf16 at 8192 x 768 x 50021: logits and statistics 655 us (960
+// Measured in bf16 at 8192 x 768 x 50021: logits and statistics 640 us (980
 // TFLOP/s; a library product of that size 986), G 2 x 400 us, dx and dw 2 x 750 us
 // (840 TFLOP/s; the library's 1066 and 1254); fp16 at 4096 x 2560 x 32768 forward
-// 605 us (1140 TFLOP/s; 1433); fp32 at 4096 x 768 x 8192 109 TFLOP/s forward, 115
-// backward (154 at 8192^3).
+// 580 to 605 us (1140 to 1180 TFLOP/s; 1433); fp32 at 4096 x 768 x 8192 109 TFLOP/s
+// forward, 114 backward (154 at 8192^3).  The 256-sided tiles of G and of the
+// products spill two and three registers, outside their loops.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
