@@ -372,7 +372,7 @@ h3conv_status h3conv_short_conv_step(const void *x, const float *w, const float 
  *   u, dt, y  [B,H,N]    io dtype
  *   z         [B,H,N]    io dtype  gate, or NULL (none)
  *   A         [H,S]      fp32      decay rates (negative for stable modes; a state that grows
- *                                  is right while it is itself within fp32)
+ *                                  is right while it and every step's exp(d_t A) are within fp32)
  *   Bm, C     [B,G,S,N]  io dtype
  *   D, dt_bias [H]       fp32      NULL = zeros
  *   x_in      [B,H,S]    fp32      initial state, or NULL for zero

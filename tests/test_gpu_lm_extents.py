@@ -192,3 +192,38 @@ def test_xent_no_tokens(room):
                                 torch.zeros(V, D, device=dev, dtype=torch.bfloat16),
                                 torch.empty(0, device=dev, dtype=torch.int64), none, none)
     assert not any(bool(part.any()) for part in dw.split(1 << 18))
+
+
+def test_selective_step_channels(room):
+    """2^28 + 3 channels of 33 modes, sixteen threads each."""
+    room(90)
+    H, S = (1 << 28) + 3, 33
+    say("selective_step", H, S)
+    dev = device()
+    g = torch.Generator(device=dev).manual_seed(8)
+    u, dt = (torch.randn(1, H, generator=g, device=dev, dtype=torch.float16) for _ in range(2))
+    A, x = torch.full((H, S), -1.0, device=dev), torch.ones(1, H, S, device=dev)
+    Bm, C = (torch.full((1, 1, S), v, device=dev, dtype=torch.float16) for v in (0.5, 0.25))
+    y = pkg.selective_step(u, dt, A, Bm, C, x)
+    del A
+    d = torch.nn.functional.softplus(dt.float())
+    state = torch.exp(-d) + 0.5 * d * u.float()
+    _close(y, S * 0.25 * state, "f16", "y")
+    for j in (0, S - 1):
+        _close(x[0, :, j].contiguous(), state[0], "f32", "state %d" % j)
+
+
+def test_xent_padding(room):
+    """A padded copy of w of 2^36 bytes: 2^22 rows of 8129 elements."""
+    room(160)
+    V, D = 1 << 22, 8129
+    say("linear_xent padding", V, D)
+    dev = device()
+    x = torch.ones(1, D, device=dev, dtype=torch.bfloat16)
+    w = torch.zeros(V, D, device=dev, dtype=torch.bfloat16)
+    w[0, 0], w[V // 2, D - 1], w[V - 1, D - 1] = 10.0, 11.0, 12.0  # logits 10, 11, 12 and zeros
+    for label, logit in ((V - 1, 12.0), (V // 2, 11.0), (0, 10.0), (5, 0.0)):
+        loss, lse = pkg.linear_xent(x, w, torch.tensor([label], device=dev), return_lse=True)
+        want = float(torch.tensor([V - 3.0]).double().add(torch.tensor([10.0, 11.0, 12.0]).double().exp().sum()).log())
+        # fp32 sums of 2^22 equal terms in pairs, a logarithm of about 15
+        assert abs(float(lse) - want) <= 1e-4 and abs(float(loss) - (want - logit)) <= 1e-4, label
