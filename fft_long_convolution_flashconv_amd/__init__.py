@@ -21,6 +21,11 @@ and the layers and loss of a language model with input-dependent state spaces:
                   for one token per sequence, short_conv_step
   selective_scan  x_t = exp(d_t A) x_{t-1} + d_t B_t u_t, y = (C_t x_t + D u) silu(z),
                   with selective_scan_bwd and selective_step
+  linear_attn     S_t = e^{g_t} S_{t-1} + k_t v_t^T, y_t = scale S_t^T q_t per head, with
+                  linear_attn_bwd and linear_attn_step
+  block_norm      the norm of a block's output, its gate, the scaled residual sum and
+                  the norm before the next block, with block_norm_bwd
+  embed           rows of a table by token, scaled, with embed_bwd
   linear_xent     cross entropy of x w^T without the logits in memory, with
                   linear_xent_bwd
 """
@@ -44,6 +49,8 @@ MAX_FUSED_N = 8192
 MAX_FUSED_N_16BIT = 16384
 MAX_STATE = 64
 MAX_TAPS = 4
+MAX_HEAD = 256
+MAX_NORM = 16384
 
 _IO = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _lib = None
@@ -53,7 +60,11 @@ EXPORTS = ("h3conv_fft_conv", "h3conv_fft_conv_bidir", "h3conv_fft_conv_bwd", "h
            "h3conv_short_conv", "h3conv_short_conv_bwd", "h3conv_short_conv_bwd_workspace_size", "h3conv_short_conv_step",
            "h3conv_selective_scan", "h3conv_selective_saved_size", "h3conv_selective_scan_bwd",
            "h3conv_selective_scan_bwd_workspace_size", "h3conv_selective_step",
-           "h3conv_linear_xent", "h3conv_linear_xent_bwd", "h3conv_linear_xent_workspace_size")
+           "h3conv_linear_xent", "h3conv_linear_xent_bwd", "h3conv_linear_xent_workspace_size",
+           "h3conv_linear_attn", "h3conv_linear_attn_workspace_size", "h3conv_linear_attn_bwd",
+           "h3conv_linear_attn_bwd_workspace_size", "h3conv_linear_attn_step",
+           "h3conv_block_norm", "h3conv_block_norm_bwd", "h3conv_block_norm_bwd_workspace_size",
+           "h3conv_embed", "h3conv_embed_bwd", "h3conv_embed_bwd_workspace_size")
 NOALLOC_WORKSPACE_BYTES = 128 * 1024 * 1024
 
 
@@ -98,14 +109,30 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.h3conv_selective_step.argtypes = [P] * 12 + [I64] * 5 + [I, I, P]
     lib.h3conv_linear_xent.argtypes = [P, P, P, I64, P, P, I64, I64, I64, I, P, SZ, P]
     lib.h3conv_linear_xent_bwd.argtypes = [P, P, P, I64, P, P, P, P, I64, I64, I64, I, P, SZ, P]
+    F = ctypes.c_float
+    lib.h3conv_linear_attn.argtypes = [P] * 8 + [I64] * 9 + [F, I, I, P, SZ, P]
+    lib.h3conv_linear_attn_bwd.argtypes = [P] * 13 + [I64] * 9 + [F, I, I, P, SZ, P]
+    lib.h3conv_linear_attn_step.argtypes = [P] * 8 + [I64] * 9 + [F, I, I, P]
+    lib.h3conv_block_norm.argtypes = [P] * 8 + [I64] * 3 + [F, I, P]
+    lib.h3conv_block_norm_bwd.argtypes = [P] * 14 + [I64] * 3 + [F, I, P, SZ, P]
+    lib.h3conv_embed.argtypes = [P] * 3 + [I64] * 3 + [F, I, P]
+    lib.h3conv_embed_bwd.argtypes = [P] * 3 + [I64] * 3 + [F, I, P, SZ, P]
     for name in ("h3conv_short_conv", "h3conv_short_conv_bwd", "h3conv_short_conv_step", "h3conv_selective_scan",
-                 "h3conv_selective_scan_bwd", "h3conv_selective_step", "h3conv_linear_xent", "h3conv_linear_xent_bwd"):
+                 "h3conv_selective_scan_bwd", "h3conv_selective_step", "h3conv_linear_xent", "h3conv_linear_xent_bwd",
+                 "h3conv_linear_attn", "h3conv_linear_attn_bwd", "h3conv_linear_attn_step", "h3conv_block_norm",
+                 "h3conv_block_norm_bwd", "h3conv_embed", "h3conv_embed_bwd"):
         getattr(lib, name).restype = I
     lib.h3conv_short_conv_bwd_workspace_size.argtypes = [I64] * 4
     lib.h3conv_selective_saved_size.argtypes = [I64] * 4
     lib.h3conv_selective_scan_bwd_workspace_size.argtypes = [I64] * 5
     lib.h3conv_linear_xent_workspace_size.argtypes = [I64, I64, I64, I, I]
-    for name in ("h3conv_short_conv_bwd_workspace_size", "h3conv_selective_saved_size",
+    lib.h3conv_linear_attn_workspace_size.argtypes = [I64] * 5
+    lib.h3conv_linear_attn_bwd_workspace_size.argtypes = [I64] * 6
+    lib.h3conv_block_norm_bwd_workspace_size.argtypes = [I64] * 2
+    lib.h3conv_embed_bwd_workspace_size.argtypes = [I64] * 3
+    for name in ("h3conv_linear_attn_workspace_size", "h3conv_linear_attn_bwd_workspace_size",
+                 "h3conv_block_norm_bwd_workspace_size", "h3conv_embed_bwd_workspace_size",
+                 "h3conv_short_conv_bwd_workspace_size", "h3conv_selective_saved_size",
                  "h3conv_selective_scan_bwd_workspace_size", "h3conv_linear_xent_workspace_size"):
         getattr(lib, name).restype = SZ
     _lib = lib
@@ -669,6 +696,231 @@ def selective_step(u, dt, A, Bm, C, x, D=None, z=None, dt_bias=None, softplus: b
                                         1 if softplus else 0, io, _raw_stream(dev)),
            "h3conv_selective_step")
     return y
+
+
+def _heads(t, name: str, dev: int, dtype, lead, heads: int, dim: int) -> int:
+    """Checks a tensor of tokens and heads, [*lead, heads, dim]; the elements from one token to the next.
+    Its heads lie side by side and its tokens at equal distances: it may be a slice of a wider projection."""
+    shape = (*lead, heads, dim)
+    if not isinstance(t, _Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype is not dtype or tuple(t.shape) != shape or t.get_device() != dev:
+        if t.dtype is not dtype:
+            raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        if tuple(t.shape) != shape:
+            raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+        _same_device(**{name: t})
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, dev))
+    if t.is_contiguous():
+        return heads * dim
+    st = t.stride()
+    if (dim > 1 and st[-1] != 1) or (heads > 1 and st[-2] != dim):
+        raise ValueError("%s must have its heads side by side, got strides %s" % (name, st))
+    at = [(n, s) for n, s in zip(lead, st) if n > 1]  # (a dimension of one token has no distance)
+    if not at:
+        return heads * dim
+    ld = at[-1][1]
+    if ld < heads * dim or (len(at) > 1 and at[0][1] != at[1][0] * ld):
+        raise ValueError("%s must have its tokens at equal distances, got strides %s" % (name, st))
+    return ld
+
+
+def _attn_args(q, k, v, g, dims: int):
+    if not (isinstance(q, _Tensor) and isinstance(v, _Tensor) and isinstance(g, _Tensor)):
+        raise TypeError("q, k, v and g must be torch.Tensors")
+    dev = v.get_device()
+    if not v.is_cuda or dev != torch.cuda.current_device():
+        _same_device(v=v)
+    io, form = _io(v, "v"), ("B,N" if dims == 4 else "B")
+    if v.dim() != dims or v.shape[-1] < 1:
+        raise ValueError("v must be [%s,H,dv], got %s" % (form, tuple(v.shape)))
+    lead, H, dv = v.shape[:-2], v.shape[-2], v.shape[-1]
+    if q.dim() != dims or q.shape[-1] < 1 or q.shape[-2] < 1 or H % q.shape[-2] != 0:
+        raise ValueError("q must be [%s,G,dk] with G dividing H = %d, got %s" % (form, H, tuple(q.shape)))
+    G, dk, t = q.shape[-2], q.shape[-1], v.dtype
+    lds = (_heads(q, "q", dev, t, lead, G, dk), _heads(k, "k", dev, t, lead, G, dk), _heads(v, "v", dev, t, lead, H, dv))
+    per_token = g.dim() > 1
+    _tensors(dev, ("g", g, torch.float32, (*lead, H) if per_token else (H,)))
+    return dev, io, lead, H, G, dk, dv, lds, int(per_token)
+
+
+def linear_attn(q, k, v, g, scale: float = 1.0, x_in=None, lengths=None, return_state: bool = False, out=None,
+                workspace=None):
+    """Linear attention with a decay for each head: S_t = e^{g_t} S_{t-1} + k_t v_t^T, y_t = scale S_t^T q_t.
+
+    q, k [B,N,G,dk] and v [B,N,H,dv] f32/f16/bf16, dk, dv <= MAX_HEAD, q and k
+    shared by the H/G heads of a group; each may be a slice of a wider
+    projection.  g f32, the log of the decay factor: [H], or [B,N,H] for one of
+    each token.  x_in [B,H,dk,dv] f32; lengths [B] int32, valid steps of every
+    row.  Returns y [B,N,H,dv], or (y, x_out) with the final state if
+    ``return_state``."""
+    dev, io, (B, N), H, G, dk, dv, lds, per_token = _attn_args(q, k, v, g, 4)
+    _tensors(dev, ("x_in?", x_in, torch.float32, (B, H, dk, dv)), ("lengths?", lengths, torch.int32, (B,)),
+             ("out?", out, v.dtype, (B, N, H, dv)))
+    ws = _scratch(workspace, _size("h3conv_linear_attn_workspace_size", B, N, H, dk, dv), v)
+    y = torch.empty((B, N, H, dv), device=v.device, dtype=v.dtype) if out is None else out
+    x_out = torch.empty((B, H, dk, dv), device=v.device, dtype=torch.float32) if return_state else None
+    _check(load().h3conv_linear_attn(_at(q), _at(k), _at(v), _at(g), _at(x_in), _at(lengths), _at(y), _at(x_out), B, N, H,
+                                     G, dk, dv, *lds, float(scale), per_token, io, _at(ws), ws.numel() * ws.element_size(),
+                                     _raw_stream(dev)),
+           "h3conv_linear_attn")
+    return (y, x_out) if return_state else y
+
+
+class LinearAttnGrads(NamedTuple):
+    """Gradients of linear_attn."""
+    dq: torch.Tensor
+    dk: torch.Tensor
+    dv: torch.Tensor
+    dg: torch.Tensor
+    dx_in: torch.Tensor
+
+
+def linear_attn_bwd(q, k, v, g, dy, scale: float = 1.0, x_in=None, lengths=None, dx_out=None,
+                    workspace=None) -> LinearAttnGrads:
+    """Gradients of linear_attn (same arguments) for dy [B,N,H,dv] and dx_out [B,H,dk,dv] f32 (upstream of the
+    final state, or None)."""
+    dev, io, (B, N), H, G, dk, dv, lds, per_token = _attn_args(q, k, v, g, 4)
+    f32 = torch.float32
+    _tensors(dev, ("dy", dy, v.dtype, (B, N, H, dv)), ("x_in?", x_in, f32, (B, H, dk, dv)),
+             ("lengths?", lengths, torch.int32, (B,)), ("dx_out?", dx_out, f32, (B, H, dk, dv)))
+    ws = _scratch(workspace, _size("h3conv_linear_attn_bwd_workspace_size", B, N, H, G, dk, dv), v)
+
+    def new(*shape, dtype=v.dtype):
+        return torch.empty(shape, device=v.device, dtype=dtype)
+
+    o = LinearAttnGrads(new(B, N, G, dk), new(B, N, G, dk), new(B, N, H, dv), torch.empty_like(g),
+                        new(B, H, dk, dv, dtype=f32))
+    _check(load().h3conv_linear_attn_bwd(_at(q), _at(k), _at(v), _at(g), _at(x_in), _at(lengths), _at(dy), _at(dx_out),
+                                         _at(o.dq), _at(o.dk), _at(o.dv), _at(o.dg), _at(o.dx_in), B, N, H, G, dk, dv,
+                                         *lds, float(scale), per_token, io, _at(ws), ws.numel() * ws.element_size(),
+                                         _raw_stream(dev)),
+           "h3conv_linear_attn_bwd")
+    return o
+
+
+def linear_attn_step(q, k, v, g, x, scale: float = 1.0, slots=None, x_out=None, out=None):
+    """linear_attn for one token of each sequence.
+
+    q, k [B,G,dk]; v [B,H,dv]; g [H] or [B,H]; x [P,H,dk,dv] f32, a pool of
+    states, updated in place (or into ``x_out``, of which only the slots in use
+    are written); slots [B] int32, the slot of each sequence (sequence b in slot
+    b if None).  A slot outside the pool marks an idle row: its output is zero.
+    Returns y [B,H,dv]."""
+    dev, io, (B,), H, G, dk, dv, lds, per_token = _attn_args(q, k, v, g, 3)
+    P = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 4 else 0
+    f32 = torch.float32
+    _tensors(dev, ("x", x, f32, (P, H, dk, dv)), ("slots?", slots, torch.int32, (B,)),
+             ("x_out?", x_out, f32, (P, H, dk, dv)), ("out?", out, v.dtype, (B, H, dv)))
+    y = torch.empty((B, H, dv), device=v.device, dtype=v.dtype) if out is None else out
+    _check(load().h3conv_linear_attn_step(_at(q), _at(k), _at(v), _at(g), _at(slots), _at(x),
+                                          _at(x if x_out is None else x_out), _at(y), B, H, G, P, dk, dv, *lds,
+                                          float(scale), per_token, io, _raw_stream(dev)),
+           "h3conv_linear_attn_step")
+    return y
+
+
+def _norm_args(f, res, gate, w_out, scale, w_in, groups):
+    dev = _device_of(f, "f")
+    io = _io(f, "f")
+    if f.dim() != 2 or f.shape[1] < 1:
+        raise ValueError("f must be [T,D], got %s" % (tuple(f.shape),))
+    T, D = f.shape
+    if groups < 1 or D % groups != 0:
+        raise ValueError("groups must divide D = %d, got %s" % (D, groups))
+    t, f32 = f.dtype, torch.float32
+    _tensors(dev, ("res?", res, t, (T, D)), ("gate?", gate, t, (T, D)), ("w_out?", w_out, f32, (D,)),
+             ("scale?", scale, f32, (D,)), ("w_in?", w_in, f32, (D,)))
+    return dev, io, T, D
+
+
+def block_norm(f, res=None, gate=None, w_out=None, scale=None, w_in=None, groups: int = 1, eps: float = 1e-5, out=None):
+    """Between two blocks: m = norm(f) w_out silu(gate), r = res + scale m, y = norm(r) w_in.
+
+    f (a block's output), res (the residual stream) and gate [T,D]
+    f32/f16/bf16, D <= MAX_NORM; w_out, scale and w_in [D] f32; what is None is
+    left out.  norm(x) = x / sqrt(mean x^2 + eps), of f over each of ``groups``
+    equal parts of a row (heads).  Returns (r, y), or r alone without a w_in;
+    ``out`` takes them likewise."""
+    dev, io, T, D = _norm_args(f, res, gate, w_out, scale, w_in, groups)
+    two = w_in is not None
+    r, y = (out if two else (out, None)) if out is not None else (None, None)
+    _tensors(dev, ("out?", r, f.dtype, (T, D)), ("out?", y, f.dtype, (T, D)))
+    r = torch.empty_like(f) if r is None else r
+    y = torch.empty_like(f) if y is None and two else y
+    _check(load().h3conv_block_norm(_at(f), _at(res), _at(gate), _at(w_out), _at(scale), _at(w_in), _at(r), _at(y), T, D,
+                                    int(groups), float(eps), io, _raw_stream(dev)),
+           "h3conv_block_norm")
+    return (r, y) if two else r
+
+
+class BlockNormGrads(NamedTuple):
+    """Gradients of block_norm; None for an input that was not given."""
+    df: torch.Tensor
+    dres: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    dw_out: Optional[torch.Tensor]
+    dscale: Optional[torch.Tensor]
+    dw_in: Optional[torch.Tensor]
+
+
+def block_norm_bwd(f, dr=None, dy=None, res=None, gate=None, w_out=None, scale=None, w_in=None, groups: int = 1,
+                   eps: float = 1e-5, workspace=None) -> BlockNormGrads:
+    """Gradients of block_norm (same arguments) for dr and dy [T,D], the upstream gradients of r and y (or None)."""
+    dev, io, T, D = _norm_args(f, res, gate, w_out, scale, w_in, groups)
+    if dy is not None and w_in is None:
+        raise ValueError("dy needs w_in: there is no y without it")
+    _tensors(dev, ("dr?", dr, f.dtype, (T, D)), ("dy?", dy, f.dtype, (T, D)))
+    ws = _scratch(workspace, _size("h3conv_block_norm_bwd_workspace_size", T, D), f)
+    o = BlockNormGrads(torch.empty_like(f), *(None if t is None else torch.empty_like(t)
+                                              for t in (res, gate, w_out, scale, w_in)))
+    _check(load().h3conv_block_norm_bwd(_at(f), _at(res), _at(gate), _at(w_out), _at(scale), _at(w_in), _at(dr), _at(dy),
+                                        *(_at(t) for t in o), T, D, int(groups), float(eps), io, _at(ws),
+                                        ws.numel() * ws.element_size(), _raw_stream(dev)),
+           "h3conv_block_norm_bwd")
+    return o
+
+
+def embed(tokens, w, scale: float = 1.0, out=None):
+    """Rows of a table by token: y = scale w[tokens].
+
+    tokens int64 of any shape; w [V,D] f32/f16/bf16.  Returns y [*tokens.shape,
+    D]; zeros where a token is outside 0 .. V-1."""
+    dev = _device_of(tokens, "tokens")
+    if not isinstance(w, torch.Tensor):
+        raise TypeError("w must be a torch.Tensor")
+    io = _io(w, "w")
+    if w.dim() != 2 or w.shape[1] < 1:
+        raise ValueError("w must be [V,D], got %s" % (tuple(w.shape),))
+    V, D = w.shape
+    shape = (*tokens.shape, D)
+    _tensors(dev, ("tokens", tokens, torch.int64, tokens.shape), ("w", w, w.dtype, (V, D)), ("out?", out, w.dtype, shape))
+    y = torch.empty(shape, device=w.device, dtype=w.dtype) if out is None else out
+    _check(load().h3conv_embed(_at(tokens), _at(w), _at(y), tokens.numel(), D, V, float(scale), io, _raw_stream(dev)),
+           "h3conv_embed")
+    return y
+
+
+def embed_bwd(tokens, dy, V: int, scale: float = 1.0, out=None, workspace=None):
+    """The table's gradient dw [V,D] (like dy) of embed(tokens, w, scale) for dy [*tokens.shape, D].  Sums run in
+    fp32 and in the same order every time; rows of absent tokens are zero."""
+    dev = _device_of(tokens, "tokens")
+    if not isinstance(dy, torch.Tensor):
+        raise TypeError("dy must be a torch.Tensor")
+    io = _io(dy, "dy")
+    if dy.dim() < 1 or dy.shape[-1] < 1:
+        raise ValueError("dy must be [*tokens.shape, D], got %s" % (tuple(dy.shape),))
+    V, T, D = int(V), tokens.numel(), dy.shape[-1]
+    if V < 0:
+        raise ValueError("V must not be negative, got %d" % V)
+    _tensors(dev, ("tokens", tokens, torch.int64, tokens.shape), ("dy", dy, dy.dtype, (*tokens.shape, D)),
+             ("out?", out, dy.dtype, (V, D)))
+    ws = _scratch(workspace, _size("h3conv_embed_bwd_workspace_size", T, D, V), dy)
+    dw = torch.empty((V, D), device=dy.device, dtype=dy.dtype) if out is None else out
+    _check(load().h3conv_embed_bwd(_at(tokens), _at(dy), _at(dw), T, D, V, float(scale), io, _at(ws),
+                                   ws.numel() * ws.element_size(), _raw_stream(dev)),
+           "h3conv_embed_bwd")
+    return dw
 
 
 def _xent_args(x, w, labels):

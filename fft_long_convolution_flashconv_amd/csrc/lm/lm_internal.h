@@ -66,4 +66,61 @@ hipError_t launch_linear_xent_bwd(const void *x, const void *w, const int64_t *l
                                   const float *lse, const float *dloss, void *dx, void *dw, int64_t T, int64_t D,
                                   int64_t V, int io, void *ws, hipStream_t s);
 
+// ----------------------------------------------------------- linear_attn
+struct LinAttnArgs {
+    const void *q, *k, *v;                           // [B,N,G,dk] twice, [B,N,H,dv]; ld elements between tokens
+    const float *g, *x_in;                           // [H] or [B,N,H], [B,H,dk,dv] or null
+    const int32_t *lengths;                          // [B] or null
+    int64_t B, N, H, G;
+    int dk, dv;
+    int64_t ldq, ldk, ldv;
+    float scale;
+    int per_token;
+};
+struct LinAttnGrads {
+    void *dq, *dk, *dv;
+    float *dg, *dx_in;                               // may be null
+};
+struct LinStepArgs {
+    const void *q, *k, *v;                           // [B,G,dk] twice, [B,H,dv]; ld elements between sequences
+    const float *g, *x_in;                           // [H] or [B,H], [P,H,dk,dv]
+    const int32_t *slots;
+    float *x_out;
+    void *y;
+    int64_t B, H, G, P;
+    int dk, dv;
+    int64_t ldq, ldk, ldv;
+    float scale;
+    int per_token;
+};
+size_t linear_attn_workspace(int64_t B, int64_t N, int64_t H, int64_t dk, int64_t dv);
+size_t linear_attn_bwd_workspace(int64_t B, int64_t N, int64_t H, int64_t G, int64_t dk, int64_t dv);
+hipError_t launch_linear_attn(const LinAttnArgs &a, void *y, float *x_out, int io, void *ws, hipStream_t s);
+hipError_t launch_linear_attn_bwd(const LinAttnArgs &a, const void *dy, const float *dx_out, const LinAttnGrads &o, int io,
+                                  void *ws, hipStream_t s);
+hipError_t launch_linear_attn_step(const LinStepArgs &a, int io, hipStream_t s);
+
+// ------------------------------------------------------------ block_norm
+struct BlockNormArgs {
+    const void *f, *res, *gate;                      // [T,D]; res, gate may be null
+    const float *w_out, *scale, *w_in;               // [D] or null
+    int64_t T, D, groups;
+    float eps;
+};
+struct BlockNormGrads {
+    void *df, *dres, *dgate;                         // dres, dgate null without a res, a gate
+    float *dw_out, *dscale, *dw_in;                  // null without their parameters
+};
+hipError_t launch_block_norm(const BlockNormArgs &a, void *r, void *y, int io, hipStream_t s);
+size_t block_norm_bwd_workspace(int64_t T, int64_t D);
+hipError_t launch_block_norm_bwd(const BlockNormArgs &a, const void *dr, const void *dy, const BlockNormGrads &o, int io,
+                                 void *ws, hipStream_t s);
+
+// ----------------------------------------------------------------- embed
+hipError_t launch_embed(const int64_t *tok, const void *w, void *y, int64_t T, int64_t D, int64_t vocab, float scale, int io,
+                        hipStream_t s);
+size_t embed_bwd_workspace(int64_t T, int64_t D, int64_t vocab);
+hipError_t launch_embed_bwd(const int64_t *tok, const void *dy, void *dw, int64_t T, int64_t D, int64_t vocab, float scale,
+                            int io, void *ws, hipStream_t s);
+
 }  // namespace h3c

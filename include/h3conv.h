@@ -426,6 +426,134 @@ h3conv_status h3conv_selective_step(const void *u, const void *dt, const float *
                                     const float *x_in, float *x_out, void *y, int64_t B, int64_t H, int64_t P,
                                     int64_t S, int64_t G, int softplus, int io, void *stream);
 
+/* Largest dimension of a head of linear attention. */
+#define H3CONV_MAX_HEAD 256
+
+/*
+ * Linear attention with a decay for each head: a state of dk x dv per sequence
+ * and head,
+ *     S_t = e^{g_t} S_{t-1} + k_t v_t^T,   y_t = scale S_t^T q_t
+ * q_t and k_t are shared by the H/G consecutive heads of a group.
+ *
+ *   q, k      [B,N,G,dk]   io dtype   ldq, ldk elements from one token to the next (>= G dk),
+ *                                     N ldq from one sequence to the next: a slice of a wider
+ *                                     projection need not be copied
+ *   v, y      [B,N,H,dv]   io dtype   v likewise with ldv (>= H dv); y is contiguous
+ *   g         [H]          fp32       log of the decay factor of each head, or, if per_token,
+ *             [B,N,H]                 of each token and head.  Usually <= 0; -infinity starts the
+ *                                     state anew.  A state that grows is right while it and the
+ *                                     factors over any 64 steps are within fp32.
+ *   x_in      [B,H,dk,dv]  fp32       initial state, or NULL for zero
+ *   lengths   [B]          int32      valid steps of every row (clamped to 0 .. N), or NULL = N:
+ *                                     later steps leave the state alone, their y is zero and
+ *                                     their inputs are not read into any result
+ *   x_out     [B,H,dk,dv]  fp32       state after the last valid step, or NULL
+ *   ws        at least h3conv_linear_attn_workspace_size bytes
+ * All tensors but ws need only the alignment of their elements.  Values at valid
+ * steps are taken to be finite: steps are taken 64 at a time, and a NaN or an
+ * infinity in v or k reaches the others of its 64, also those before it.
+ * Products run on the matrix cores, fp32 elements on the fp32 ones; sums and
+ * states are fp32, and what multiplies an input again (weights, states) keeps 22
+ * bits or more where inputs have 16.
+ * Supported: dk, dv <= H3CONV_MAX_HEAD, G divides H, B*H <= 2^28, and
+ * B*N*H*max(dk,dv), B*H*dk*dv and B*N*ld <= 2^40; any N.
+ */
+h3conv_status h3conv_linear_attn(const void *q, const void *k, const void *v, const float *g, const float *x_in,
+                                 const int32_t *lengths, void *y, float *x_out, int64_t B, int64_t N, int64_t H,
+                                 int64_t G, int64_t dk, int64_t dv, int64_t ldq, int64_t ldk, int64_t ldv, float scale,
+                                 int per_token, int io, void *ws, size_t ws_bytes, void *stream);
+size_t h3conv_linear_attn_workspace_size(int64_t B, int64_t N, int64_t H, int64_t dk, int64_t dv);
+
+/*
+ * Backward pass of h3conv_linear_attn (same inputs) for upstream gradients dy
+ * [B,N,H,dv] of y and dx_out [B,H,dk,dv] fp32 of x_out (NULL = none).  With D_t
+ * the gradient of S_t, D_t = scale q_t dy_t^T + e^{g_{t+1}} D_{t+1}:
+ *     dq_t = scale S_t dy_t,  dk_t = D_t v_t,  dv_t = D_t^T k_t,  dg_t = e^{g_t} <S_{t-1}, D_t>
+ *   dq, dk    [B,N,G,dk]   io dtype   summed over the heads of the group
+ *   dv        [B,N,H,dv]   io dtype
+ *   dg        like g       fp32       summed over batch and time if not per_token; may be NULL
+ *   dx_in     [B,H,dk,dv]  fp32       may be NULL
+ *   ws        at least h3conv_linear_attn_bwd_workspace_size bytes
+ * Gradients are contiguous, written, and zero past a row's length; all sums run in a
+ * fixed order.  Nothing is kept from the forward pass: the states are formed again.
+ */
+h3conv_status h3conv_linear_attn_bwd(const void *q, const void *k, const void *v, const float *g, const float *x_in,
+                                     const int32_t *lengths, const void *dy, const float *dx_out, void *dq, void *dk_,
+                                     void *dv_, float *dg, float *dx_in, int64_t B, int64_t N, int64_t H, int64_t G,
+                                     int64_t dk, int64_t dv, int64_t ldq, int64_t ldk, int64_t ldv, float scale,
+                                     int per_token, int io, void *ws, size_t ws_bytes, void *stream);
+size_t h3conv_linear_attn_bwd_workspace_size(int64_t B, int64_t N, int64_t H, int64_t G, int64_t dk, int64_t dv);
+
+/*
+ * h3conv_linear_attn for one token of each of B sequences, whose states are kept
+ * in a pool of P slots (slots and the pool as in h3conv_short_conv_step).
+ *
+ *   q, k [B,G,dk], v, y [B,H,dv]  io dtype   ldq, ldk, ldv elements between sequences
+ *   g    [H], or [B,H] if per_token  fp32
+ *   x_in, x_out [P,H,dk,dv]  fp32            the same pool (updated in place) or separate ones
+ * Supported: as h3conv_linear_attn, B <= 65535.
+ */
+h3conv_status h3conv_linear_attn_step(const void *q, const void *k, const void *v, const float *g, const int32_t *slots,
+                                      const float *x_in, float *x_out, void *y, int64_t B, int64_t H, int64_t G,
+                                      int64_t P, int64_t dk, int64_t dv, int64_t ldq, int64_t ldk, int64_t ldv,
+                                      float scale, int per_token, int io, void *stream);
+
+/* Largest number of channels of h3conv_block_norm. */
+#define H3CONV_MAX_NORM 16384
+
+/*
+ * What stands between two blocks of a network, per row of D channels: the norm of a
+ * block's output f over each of `groups` equal parts (heads), its gate, the residual
+ * sum with a scale per channel, and the norm before the next block:
+ *     fh = f / sqrt(mean_part f^2 + eps),  m = fh w_out silu(gate),
+ *     r = res + scale m,                   y = r / sqrt(mean r^2 + eps) w_in
+ *
+ *   f, res, gate, r, y  [T,D]  io dtype   res, gate NULL = without; y given exactly if w_in is
+ *   w_out, scale, w_in  [D]    fp32       NULL = without that norm (m = f silu(gate), no y), scale 1
+ * Rows need only the alignment of their elements; squares and sums are fp32, and y
+ * is the norm of r before r is rounded.
+ * Supported: D <= H3CONV_MAX_NORM, groups divides D, with groups > 1 also
+ * D + groups <= H3CONV_MAX_NORM; T <= 2^30; eps >= 0.
+ */
+h3conv_status h3conv_block_norm(const void *f, const void *res, const void *gate, const float *w_out, const float *scale,
+                                const float *w_in, void *r, void *y, int64_t T, int64_t D, int64_t groups, float eps,
+                                int io, void *stream);
+
+/*
+ * Gradients of h3conv_block_norm (same inputs) for upstream gradients dr and dy
+ * [T,D] (NULL = none; dy only with a w_in).
+ *
+ *   df, dres, dgate [T,D]  io dtype  dgate given exactly if gate is; dres may be NULL
+ *   dw_out, dscale, dw_in [D]  fp32  each given exactly if its parameter is; summed over the
+ *                                    rows in a fixed order, written
+ *   ws   at least h3conv_block_norm_bwd_workspace_size bytes
+ */
+h3conv_status h3conv_block_norm_bwd(const void *f, const void *res, const void *gate, const float *w_out,
+                                    const float *scale, const float *w_in, const void *dr, const void *dy, void *df,
+                                    void *dres, void *dgate, float *dw_out, float *dscale, float *dw_in, int64_t T,
+                                    int64_t D, int64_t groups, float eps, int io, void *ws, size_t ws_bytes, void *stream);
+size_t h3conv_block_norm_bwd_workspace_size(int64_t T, int64_t D);
+
+/*
+ * Embedding: rows of a table by token, scaled,
+ *     y[t] = scale w[tokens[t]]
+ *   tokens [T] int64     w [V,D], y [T,D]  io dtype
+ * A token outside 0 .. V-1 gives a row of zeros.
+ * Supported: T, V <= 2^30, D <= 2^20, T*D, V*D <= 2^40.
+ */
+h3conv_status h3conv_embed(const int64_t *tokens, const void *w, void *y, int64_t T, int64_t D, int64_t V, float scale,
+                           int io, void *stream);
+
+/*
+ * The table's gradient: dw[v] = scale * the sum of dy[t] over the t with
+ * tokens[t] = v, in fp32, always in the same order; dw [V,D] (io dtype) is written, rows of absent
+ * tokens with zeros.  Tokens outside the table add nothing, whatever their dy holds.
+ *   ws   at least h3conv_embed_bwd_workspace_size bytes
+ */
+h3conv_status h3conv_embed_bwd(const int64_t *tokens, const void *dy, void *dw, int64_t T, int64_t D, int64_t V,
+                               float scale, int io, void *ws, size_t ws_bytes, void *stream);
+size_t h3conv_embed_bwd_workspace_size(int64_t T, int64_t D, int64_t V);
+
 /*
  * Softmax cross entropy of a linear output layer, without the logits in
  * memory:
