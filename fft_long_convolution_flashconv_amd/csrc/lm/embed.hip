@@ -6,6 +6,8 @@
 // order, in fp32, and is rounded once: equal calls give equal bits.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "lm_device.h"
 #include "lm_internal.h"
 
@@ -34,35 +36,301 @@ __global__ __launch_bounds__(256) void k_embed(const int64_t *__restrict__ tok, 
     }
 }
 
-// One wave per row of the table; it looks through all tokens.
-template <int IO>
-__global__ __launch_bounds__(256) void k_embed_bwd(const int64_t *__restrict__ tok,
-                                                   const typename io_elem<IO>::T *__restrict__ dy,
-                                                   typename io_elem<IO>::T *__restrict__ dw, int64_t T, int64_t D,
-                                                   int64_t vocab, float scale) {
-    const int64_t id = block_id() * 4 + (threadIdx.x >> 6);
-    if (id >= vocab) return;
-    const int lane = threadIdx.x & 63;
-    for (int64_t c0 = 0; c0 < D; c0 += 64 * V) {
-        const int64_t c = c0 + lane * V;
-        float s[V];
+// The gradient goes by the tokens in sorted order:
+//   k_embed_cut   pieces of kPiece tokens, each sorted by the upper bits of its ids into
+//                 at most 256 ranges of ids
+//   k_embed_sort  a range's entries of all pieces, sorted by the other bits; for every id
+//                 that occurs, where its entries stand
+//   k_embed_hot   ids of more than kUnit entries: sums of the entries in each kUnit places
+//   k_embed_rows  the table's rows, from their entries or from such sums
+// Every sort is stable, so an id's entries are in the order of time.
+constexpr int kPiece = 1024, kUnit = 64, kSort = 1024, kCols = 64 * V;
+
+struct Sorted {
+    int2 *buf[3];    // (id, time) of every entry: by pieces, then [1] and [2] in turn, by ranges
+    int *off;        // [ranges + 1][pieces]: where a range begins in a piece
+    int2 *span;      // [vocabulary]: where an id's entries begin and end (0, 0: none)
+    int64_t *total;  // entries
+    float *part;     // [units][2][D]: sums of a unit's first id, and of its last if it is another
+    int64_t pieces, ranges, units;
+    int shift, passes;
+    __device__ __forceinline__ const int2 *done() const { return buf[1 + (passes & 1)]; }
+};
+
+// Lanes of the wave whose 8-bit digit is this one's, among those that are `on`.
+__device__ __forceinline__ uint64_t same_digit(int d, bool on) {
+    uint64_t m = __ballot(on);
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[i] = 0.f;
-        for (int64_t t0 = 0; t0 < T; t0 += 64) {
-            uint64_t hit = __ballot(t0 + lane < T && tok[t0 + lane < T ? t0 + lane : 0] == id);
-            while (hit) {
-                const int64_t t = t0 + __builtin_ctzll(hit);
-                hit &= hit - 1;
-                float v[V];
-                ld_row<IO, V>(dy + t * D + c, v, D - c);
+    for (int i = 0; i < 8; ++i) {
+        const uint64_t bit = __ballot((d >> i) & 1);
+        m &= (d >> i) & 1 ? bit : ~bit;
+    }
+    return m;
+}
+__device__ __forceinline__ int lanes_before(uint64_t m) { return __popcll(m & ((1ull << (threadIdx.x & 63)) - 1)); }
+
+// The counts of every wave and digit become the entries of the digit in earlier waves;
+// first[d] is where digit d begins.
+template <int NT>
+__device__ __forceinline__ void places(int (*cnt)[256], int *first) {
+    const int d = threadIdx.x;
+    if (d < 256) {
+        int total = 0;
+        for (int w = 0; w < NT / 64; ++w) {
+            const int n = cnt[w][d];
+            cnt[w][d] = total;
+            total += n;
+        }
+        first[d] = total;
+    }
+    __syncthreads();
+    if (d < 64) {  // 256 counts, four per lane
+        int v[4], sum = 0;
 #pragma unroll
-                for (int i = 0; i < V; ++i) s[i] += v[i];
-            }
+        for (int i = 0; i < 4; ++i) {
+            v[i] = sum;
+            sum += first[4 * d + i];
+        }
+        int run = sum;
+#pragma unroll
+        for (int k = 1; k < 64; k <<= 1) {
+            const int u = __shfl_up(run, k);
+            if (d >= k) run += u;
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[i] *= scale;
-        st_row<IO, V>(dw + id * D + c, s, D - c);
+        for (int i = 0; i < 4; ++i) first[4 * d + i] = v[i] + run - sum;
+        if (d == 63) first[256] = run;
     }
+    __syncthreads();
+}
+
+__global__ __launch_bounds__(256) void k_embed_cut(const int64_t *__restrict__ tok, int64_t T, int64_t vocab, Sorted s) {
+    __shared__ int cnt[4][256], first[257];
+    const int64_t piece = block_id(), blocks = (int64_t)gridDim.x * gridDim.z;
+    for (int64_t v = piece * 256 + threadIdx.x; v < vocab; v += blocks * 256) s.span[v] = int2{0, 0};
+    if (piece >= s.pieces) return;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    for (int i = threadIdx.x; i < 4 * 256; i += 256) cnt[i >> 8][i & 255] = 0;
+    __syncthreads();
+    constexpr int R = kPiece / 256;
+    const int64_t t0 = piece * kPiece + wave * (kPiece / 4) + lane;
+    int id[R], rank[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t t = t0 + i * 64, v = t < T ? tok[t] : -1;
+        id[i] = v >= 0 && v < vocab ? (int)v : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const bool on = id[i] >= 0;
+        const int d = on ? id[i] >> s.shift : 0;
+        const uint64_t same = same_digit(d, on);
+        rank[i] = cnt[wave][d] + lanes_before(same);
+        __builtin_amdgcn_wave_barrier();
+        if (on && lanes_before(same) == 0) cnt[wave][d] += __popcll(same);
+        __builtin_amdgcn_wave_barrier();
+    }
+    __syncthreads();
+    places<256>(cnt, first);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (id[i] < 0) continue;
+        const int d = id[i] >> s.shift;
+        s.buf[0][piece * kPiece + first[d] + cnt[wave][d] + rank[i]] = int2{id[i], (int)(t0 + i * 64)};
+    }
+    for (int64_t r = threadIdx.x; r <= s.ranges; r += 256) s.off[r * s.pieces + piece] = first[r];
+}
+
+// One stable pass over n entries by the digit from `bit` on; a wave has consecutive ones.
+__device__ __forceinline__ void sort_pass(const int2 *from, int2 *to, int64_t n, int bit, int (*cnt)[256], int *first) {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t per = (n + kSort - 1) / kSort * 64, lo = wave * per, hi = lo + per < n ? lo + per : n;
+    for (int i = threadIdx.x; i < kSort / 64 * 256; i += kSort) cnt[i >> 8][i & 255] = 0;
+    __syncthreads();
+    for (int place = 0; place < 2; ++place) {
+        for (int64_t i0 = lo; i0 < hi; i0 += 64) {
+            const bool on = i0 + lane < hi;
+            const int2 e = from[on ? i0 + lane : lo];
+            const int d = (e.x >> bit) & 255;
+            const uint64_t same = same_digit(d, on);
+            const int before = lanes_before(same), have = cnt[wave][d];
+            __builtin_amdgcn_wave_barrier();
+            if (on && place) to[first[d] + have + before] = e;
+            if (on && before == 0) cnt[wave][d] = have + __popcll(same);
+            __builtin_amdgcn_wave_barrier();
+        }
+        __syncthreads();
+        if (!place) places<kSort>(cnt, first);
+    }
+}
+
+__global__ __launch_bounds__(kSort) void k_embed_sort(Sorted s) {
+    __shared__ int cnt[kSort / 64][256], first[257];
+    __shared__ int64_t sums[kSort / 64];
+    const int64_t r = blockIdx.x;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    // where the range begins among all entries
+    int64_t base = 0, n = 0;
+    for (int64_t p = threadIdx.x; p < s.pieces; p += kSort) base += s.off[r * s.pieces + p];
+    for (int d = 32; d > 0; d >>= 1) base += __shfl_xor(base, d);
+    if (lane == 0) sums[wave] = base;
+    __syncthreads();
+    base = 0;
+    for (int w = 0; w < kSort / 64; ++w) base += sums[w];
+    // its entries from the pieces, in order: a thread has a piece's place, a wave copies its 64 pieces
+    for (int64_t p0 = 0; p0 < s.pieces; p0 += kSort) {
+        const int64_t p = p0 + threadIdx.x;
+        const int lo = p < s.pieces ? s.off[r * s.pieces + p] : 0, hi = p < s.pieces ? s.off[(r + 1) * s.pieces + p] : 0;
+        int64_t run = hi - lo;
+        for (int k = 1; k < 64; k <<= 1) {
+            const int64_t u = __shfl_up(run, k);
+            if (lane >= k) run += u;
+        }
+        __syncthreads();
+        if (lane == 63) sums[wave] = run;
+        __syncthreads();
+        int64_t at = base + n + run - (hi - lo), all = 0;
+        for (int w = 0; w < kSort / 64; ++w) {
+            if (w < wave) at += sums[w];
+            all += sums[w];
+        }
+        for (int i = 0; i < 64 && p0 + wave * 64 + i < s.pieces; ++i) {
+            const int from = __shfl(lo, i), m = __shfl(hi, i) - from;
+            const int64_t to = __shfl(at, i), src = (p0 + wave * 64 + i) * kPiece + from;
+            for (int j = lane; j < m; j += 64) s.buf[1][to + j] = s.buf[0][src + j];
+        }
+        n += all;
+    }
+    __syncthreads();
+    for (int i = 0; i < s.passes; ++i) sort_pass(s.buf[1 + (i & 1)] + base, s.buf[2 - (i & 1)] + base, n, 8 * i, cnt, first);
+    const int2 *e = s.done() + base;
+    for (int64_t i = threadIdx.x; i < n; i += kSort) {
+        const int id = e[i].x;
+        if (i == 0 || e[i - 1].x != id) s.span[id].x = (int)(base + i);
+        if (i == n - 1 || e[i + 1].x != id) s.span[id].y = (int)(base + i + 1);
+    }
+    if (r == s.ranges - 1 && threadIdx.x == 0) *s.total = base + n;
+}
+
+// The sum of the rows of dy that n entries name, n at most 64: this lane's columns.
+template <int IO>
+__device__ __forceinline__ void sum_rows(const int2 *e, int n, const typename io_elem<IO>::T *dy, int64_t D, int64_t c,
+                                         float (&sum)[V]) {
+    const int lane = threadIdx.x & 63;
+    const int t = lane < n ? e[lane].y : 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum[i] = 0.f;
+    for (int j = 0; j < n; j += 4) {
+        float v[4][V];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // (past the last: its row once more, not added)
+            ld_row<IO, V>(dy + (int64_t)__builtin_amdgcn_readlane(t, j + k < n ? j + k : n - 1) * D + c, v[k], D - c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (j + k < n) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum[i] += v[k][i];
+            }
+    }
+}
+
+// A wave per unit of places and kCols columns.
+template <int IO>
+__global__ __launch_bounds__(256) void k_embed_hot(const typename io_elem<IO>::T *__restrict__ dy, int64_t D, Sorted s) {
+    const int64_t u = block_id() * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), p0 = u * kUnit;
+    const int64_t total = *s.total, c = (int64_t)blockIdx.y * kCols + (threadIdx.x & 63) * V;
+    if (p0 >= total) return;
+    const int64_t p1 = p0 + kUnit < total ? p0 + kUnit : total;
+    const int2 *e = s.done();
+    const int ida = __builtin_amdgcn_readfirstlane(e[p0].x), idb = __builtin_amdgcn_readfirstlane(e[p1 - 1].x);
+    for (int w = 0; w < (ida == idb ? 1 : 2); ++w) {
+        const int2 sp = s.span[w ? idb : ida];
+        if (sp.y - sp.x <= kUnit) continue;
+        const int64_t lo = sp.x > p0 ? sp.x : p0, hi = sp.y < p1 ? sp.y : p1;
+        float sum[V];
+        sum_rows<IO>(e + lo, __builtin_amdgcn_readfirstlane((int)(hi - lo)), dy, D, c, sum);
+        st_row<IO_F32, V>(s.part + (2 * u + w) * D + c, sum, D - c);
+    }
+}
+
+// A wave per id; the block's four join the sums of one of many entries.
+template <int IO>
+__global__ __launch_bounds__(256) void k_embed_rows(const typename io_elem<IO>::T *__restrict__ dy,
+                                                    typename io_elem<IO>::T *__restrict__ dw, int64_t D, int64_t vocab,
+                                                    float scale, Sorted s) {
+    __shared__ float lds[4][kCols];
+    __shared__ int2 spans[4];
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int64_t id0 = block_id() * 4;
+    if (id0 >= vocab) return;
+    const int64_t id = id0 + wave;
+    const int2 sp = id < vocab ? s.span[id] : int2{0, 0};
+    const int n = __builtin_amdgcn_readfirstlane(sp.y - sp.x);
+    if (lane == 0) spans[wave] = sp;
+    if (id < vocab && n <= kUnit) {
+        for (int64_t c0 = 0; c0 < D; c0 += kCols) {  // (every lane: each holds an entry)
+            const int64_t c = c0 + lane * V;
+            float sum[V];
+            sum_rows<IO>(s.done() + sp.x, n, dy, D, c, sum);
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum[i] *= scale;
+            st_row<IO, V>(dw + id * D + c, sum, D - c);
+        }
+    }
+    if (!__syncthreads_or(n > kUnit)) return;
+    for (int w = 0; w < 4; ++w) {
+        const int2 x = spans[w];
+        if (x.y - x.x <= kUnit) continue;
+        // units first .. last; the first is the id's own only where it begins with it
+        const int64_t u0 = x.x / kUnit, u1 = (x.y - 1) / kUnit + 1, per = (u1 - u0 + 3) / 4;
+        const int64_t lo = u0 + wave * per, hi = lo + per < u1 ? lo + per : u1;
+        for (int64_t c0 = 0; c0 < D; c0 += kCols) {
+            const int64_t c = c0 + lane * V;
+            float sum[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum[i] = 0.f;
+#pragma unroll 4
+            for (int64_t u = lo; u < hi; ++u) {
+                float v[V];
+                ld_row<IO_F32, V>(s.part + (2 * u + (u == u0 && x.x % kUnit != 0 ? 1 : 0)) * D + c, v, D - c);
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum[i] += v[i];
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) lds[wave][lane * V + i] = sum[i];
+            __syncthreads();
+            if (wave == 0) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int k = lane * V + i;
+                    sum[i] = (((lds[0][k] + lds[1][k]) + lds[2][k]) + lds[3][k]) * scale;
+                }
+                st_row<IO, V>(dw + (id0 + w) * D + c, sum, D - c);
+            }
+            __syncthreads();
+        }
+    }
+}
+
+int64_t up(int64_t n) { return (n + 255) & ~(int64_t)255; }
+
+// The workspace's parts from `base` on; its size.
+int64_t plan(int64_t T, int64_t D, int64_t vocab, char *base, Sorted &s) {
+    s.pieces = (T + kPiece - 1) / kPiece;
+    s.units = (T + kUnit - 1) / kUnit;
+    int bits = 0;
+    while (bits < 31 && ((vocab - 1) >> bits) > 0) ++bits;
+    s.shift = bits > 8 ? bits - 8 : 0;
+    s.passes = (s.shift + 7) / 8;
+    s.ranges = vocab > 0 ? ((vocab - 1) >> s.shift) + 1 : 0;
+    int64_t at = 0;
+    const auto take = [&](int64_t n) { char *p = base + at; at += up(n); return p; };
+    for (int2 *&b : s.buf) b = (int2 *)take(s.pieces * kPiece * 8);
+    s.off = (int *)take((s.ranges + 1) * s.pieces * 4);
+    s.span = (int2 *)take(vocab * 8);
+    s.total = (int64_t *)take(8);
+    s.part = (float *)take(s.units * 2 * D * 4);
+    return at;
 }
 
 template <int IO>
@@ -71,14 +339,27 @@ hipError_t fwd_io(const int64_t *tok, const void *w, void *y, int64_t T, int64_t
     return launch(k_embed<IO>, grid_of((T + 3) / 4), dim3(256), 0, s, tok, (const E *)w, (E *)y, T, D, vocab, scale);
 }
 template <int IO>
-hipError_t bwd_io(const int64_t *tok, const void *dy, void *dw, int64_t T, int64_t D, int64_t vocab, float scale, hipStream_t s) {
+hipError_t bwd_io(const int64_t *tok, const void *dy_, void *dw, int64_t T, int64_t D, int64_t vocab, float scale, void *ws,
+                  hipStream_t st) {
     using E = typename io_elem<IO>::T;
-    return launch(k_embed_bwd<IO>, grid_of((vocab + 3) / 4), dim3(256), 0, s, tok, (const E *)dy, (E *)dw, T, D, vocab, scale);
+    const E *dy = (const E *)dy_;
+    Sorted s;
+    plan(T, D, vocab, (char *)ws, s);
+    const int64_t clear = std::min<int64_t>(1024, vocab / 2048 + 1);
+    hipError_t e = launch(k_embed_cut, grid_of(std::max(s.pieces, clear)), dim3(256), 0, st, tok, T, vocab, s);
+    if (e == hipSuccess) e = launch(k_embed_sort, dim3((unsigned)s.ranges), dim3(kSort), 0, st, s);
+    if (e == hipSuccess && T > kUnit)
+        e = launch(k_embed_hot<IO>, grid_of((s.units + 3) / 4, (unsigned)((D + kCols - 1) / kCols)), dim3(256), 0, st, dy, D, s);
+    if (e == hipSuccess) e = launch(k_embed_rows<IO>, grid_of((vocab + 3) / 4), dim3(256), 0, st, dy, (E *)dw, D, vocab, scale, s);
+    return e;
 }
 
 }  // namespace
 
-size_t embed_bwd_workspace(int64_t T, int64_t D, int64_t vocab) { return 0; }
+size_t embed_bwd_workspace(int64_t T, int64_t D, int64_t vocab) {
+    Sorted s;
+    return (size_t)plan(T, D, vocab, nullptr, s);
+}
 
 hipError_t launch_embed(const int64_t *tok, const void *w, void *y, int64_t T, int64_t D, int64_t vocab, float scale, int io,
                         hipStream_t s) {
@@ -92,9 +373,9 @@ hipError_t launch_embed(const int64_t *tok, const void *w, void *y, int64_t T, i
 hipError_t launch_embed_bwd(const int64_t *tok, const void *dy, void *dw, int64_t T, int64_t D, int64_t vocab, float scale,
                             int io, void *ws, hipStream_t s) {
     switch (io) {
-        case IO_F32: return bwd_io<IO_F32>(tok, dy, dw, T, D, vocab, scale, s);
-        case IO_F16: return bwd_io<IO_F16>(tok, dy, dw, T, D, vocab, scale, s);
-        default: return bwd_io<IO_BF16>(tok, dy, dw, T, D, vocab, scale, s);
+        case IO_F32: return bwd_io<IO_F32>(tok, dy, dw, T, D, vocab, scale, ws, s);
+        case IO_F16: return bwd_io<IO_F16>(tok, dy, dw, T, D, vocab, scale, ws, s);
+        default: return bwd_io<IO_BF16>(tok, dy, dw, T, D, vocab, scale, ws, s);
     }
 }
 

@@ -115,7 +115,9 @@ def test_embed_bwd_validation(lib):
     def f(tok=A[0], dy=A[1], dw=A[2], T=5, D=8, V=10, ws=A[3], n=BIG):
         return lib.h3conv_embed_bwd(tok, dy, dw, T, D, V, 1.0, 1, ws, n, None)
 
-    for bad in (dict(tok=None), dict(dy=None), dict(dw=None), dict(T=-1), dict(D=0), dict(dw=A[0]), dict(dw=A[1] + 2)):
+    for bad in (dict(tok=None), dict(dy=None), dict(dw=None), dict(T=-1), dict(D=0), dict(dw=A[0]), dict(dw=A[1] + 2), dict(ws=A[2])):
         assert f(**bad) == pkg.ERR_INVALID_ARG, bad
+    assert f(ws=None) == pkg.ERR_WORKSPACE
+    assert f(n=pkg._size("h3conv_embed_bwd_workspace_size", 5, 8, 10) - 1) == pkg.ERR_WORKSPACE
     assert f(V=(1 << 30) + 1) == pkg.ERR_UNSUPPORTED
     assert f(V=0) == pkg.OK
