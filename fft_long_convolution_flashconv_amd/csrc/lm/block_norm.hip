@@ -28,23 +28,59 @@ namespace {
 constexpr int V = 8;  // channels of one vector
 constexpr int block_waves(int W) { return W < 4 ? 4 : W; }
 
-// A vector as loaded (packed, so that a row of several tensors fits the registers).
-template <int IO>
+// A vector as loaded, in whole words: elements one by one would take a register each.  Rows are whole vectors, and a
+// vector past the row's end is zeros (loaded from its start, by choice and not by a branch), or ODD, and every element
+// is loaded by itself.
+template <int IO, bool ODD>
 struct Vec {
     using T = typename io_elem<IO>::T;
-    Pack<T, V> r;
-    __device__ __forceinline__ void load(const T *p, int valid) {
-        if (valid >= V) {
-            r = *reinterpret_cast<const Pack<T, V> *>(p);
+    static constexpr int WORDS = V * (int)sizeof(T) / 4;
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const T *p, uint32_t c, int D) {
+        if constexpr (!ODD) {
+            struct __attribute__((packed, aligned(sizeof(T)))) Words { uint32_t w[WORDS]; };
+            const bool in = (int)c < D;
+            const Words r = *reinterpret_cast<const Words *>(p + (in ? c : 0u));
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) w[i] = in ? r.w[i] : 0;
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) r.v[i] = i < valid ? p[i] : T(0);
+            for (int i = 0; i < WORDS; ++i) w[i] = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const bool in = (int)c + i < D;
+                const T v = p[in ? c + i : 0u];
+                if constexpr (IO == IO_F32) w[i] = in ? __float_as_uint(v) : 0;
+                else w[i >> 1] |= (in ? (uint32_t)__builtin_bit_cast(uint16_t, v) : 0u) << (16 * (i & 1));
+            }
         }
     }
-    __device__ __forceinline__ float operator[](int i) const { return to_f<IO>(r.v[i]); }
+    // From here on the words are not known to be the same: what was made of them is made again, not kept.
+    __device__ __forceinline__ void forget() {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) asm volatile("" : "+v"(w[i]));
+    }
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (IO == IO_F32) return __uint_as_float(w[i]);
+        else if constexpr (IO == IO_BF16) return __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+        else return (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i >> 1] >> (16 * (i & 1))));
+    }
 };
-
-__device__ __forceinline__ void ld_par(const float *p, float (&o)[V], int valid) { ld_row<IO_F32, V>(p, o, valid); }
+template <bool ODD>
+__device__ __forceinline__ void ld_par(const float *p, uint32_t c, int D, float (&o)[V]) {
+    Vec<IO_F32, ODD> v;
+    v.load(p, c, D);
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = v[i];
+}
+template <int IO, bool ODD>
+__device__ __forceinline__ void st_vec(typename io_elem<IO>::T *p, uint32_t c, int left, const float (&o)[V]) {
+    if constexpr (!ODD) {
+        if (left > 0) st_row<IO, V>(p + c, o, V);
+    } else {
+        st_row<IO, V>(p + c, o, left);
+    }
+}
 
 // Sum over segments of `n` consecutive lanes, n a power of two up to 64; every lane gets its segment's.
 __device__ __forceinline__ float seg_sum(float v, int n) {
@@ -57,7 +93,8 @@ template <int W>
 struct Row {
     static constexpr int kRows = block_waves(W) / W, kLanes = 64 * W, kThreads = block_waves(W) * 64;
     int sub, lane;  // the row among the block's, the thread among the row's
-    __device__ __forceinline__ Row() : sub((int)threadIdx.x / kLanes), lane((int)threadIdx.x % kLanes) {}
+    // (the same in a wave: its rows' addresses are scalar)
+    __device__ __forceinline__ Row() : sub(__builtin_amdgcn_readfirstlane((int)threadIdx.x / kLanes)), lane((int)threadIdx.x % kLanes) {}
     // The sum of v over the row's threads.  lds: a float per wave, free since the last barrier but one.
     __device__ __forceinline__ float sum(float v, float *lds) const {
         v = seg_sum(v, 64);
@@ -79,32 +116,36 @@ struct Groups {
     float inv;           // 1 / size
 };
 
-// Per vector the sums of its elements' products a b over their group.  A group of
-// a power of two of vectors lies in the lanes of one wave; any other goes through
-// LDS, element by element.  GEN: the latter.
-template <int W, int NV, bool GEN, class F>
-__device__ __forceinline__ void group_sums(const Row<W> &row, const Groups &g, int D, F value, float (&out)[NV][GEN ? V : 1],
+// Per vector the sums of its elements' values over their group.  A group of a
+// power of two of vectors lies in the lanes of one wave; any other (ODD) goes
+// through LDS, element by element.
+template <int W, int NV, bool ODD, class F>
+__device__ __forceinline__ void group_sums(const Row<W> &row, const Groups &g, int D, F value, float (&out)[NV][ODD ? V : 1],
                                            float *small, float *wide) {
-    if constexpr (!GEN) {
-        float s[NV];
+    if (!ODD || g.n == 1) {
+        float v[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            s[j] = 0.f;
+            v[j] = 0.f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) s[j] += value(j, i);
+            for (int i = 0; i < V; ++i) v[j] += value(j, i);
         }
         if (g.n == 1) {
             float all = 0.f;
 #pragma unroll
-            for (int j = 0; j < NV; ++j) all += s[j];
+            for (int j = 0; j < NV; ++j) all += v[j];
             all = row.sum(all, small);
 #pragma unroll
-            for (int j = 0; j < NV; ++j) out[j][0] = all;
+            for (int j = 0; j < NV; ++j) v[j] = all;
         } else {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) out[j][0] = seg_sum(s[j], g.lanes);
+            for (int j = 0; j < NV; ++j) v[j] = seg_sum(v[j], g.lanes);
         }
-    } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < (ODD ? V : 1); ++i) out[j][i] = v[j];
+    } else if constexpr (ODD) {
         float *mine = wide + (int64_t)row.sub * (D + g.n), *tot = mine + D;
         __syncthreads();  // (what the last sums read of it has been read)
 #pragma unroll
@@ -140,10 +181,9 @@ struct Ptr {
     float *part;  // [blocks][3][D]: sums of dw_out, dscale, dw_in
 };
 
-template <int IO, int W, int NV, bool GEN, bool BWD>
-__global__ __launch_bounds__(Row<W>::kThreads) void k_block_norm(Ptr<IO> p, int64_t T_, int D, Groups g, float eps) {
+template <int IO, int W, int NV, bool ODD, bool BWD>
+__global__ __launch_bounds__(Row<W>::kThreads, ODD || W == 8 ? 2 : BWD ? 5 - NV : 4) void k_block_norm(Ptr<IO> p, int64_t T_, int D, Groups g, float eps) {
     using R = Row<W>;
-    using E = typename io_elem<IO>::T;
     extern __shared__ float wide[];
     __shared__ float small[4][block_waves(W)];
     const R row;
@@ -157,37 +197,40 @@ __global__ __launch_bounds__(Row<W>::kThreads) void k_block_norm(Ptr<IO> p, int6
             for (int i = 0; i < V; ++i) aw[j][i] = as[j][i] = ai[j][i] = 0.f;
     }
     for (int64_t t0 = block_id() * R::kRows; t0 < T_; t0 += (int64_t)gridDim.x * gridDim.z * R::kRows) {
+        // (the parameters are loaded again for every row, from the caches: kept, they would take the registers of a
+        // second wave)
+        if constexpr (BWD) asm volatile("" ::: "memory");
         const bool on = t0 + row.sub < T_;
         const int64_t at = (on ? t0 + row.sub : T_ - 1) * D;
-        Vec<IO> f[NV], res[NV], z[NV], dr[BWD ? NV : 1], dy[BWD ? NV : 1];
+        Vec<IO, ODD> f[NV], res[NV], z[NV], dr[BWD ? NV : 1], dy[BWD ? NV : 1];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * R::kLanes + row.lane) * V, n = D - c;
-            f[j].load(p.f + at + c, n);
-            if (p.res) res[j].load(p.res + at + c, n);
-            if (p.z) z[j].load(p.z + at + c, n);
+            const uint32_t c = (j * R::kLanes + row.lane) * V;
+            f[j].load(p.f + at, c, D);
+            if (p.res) res[j].load(p.res + at, c, D);
+            if (p.z) z[j].load(p.z + at, c, D);
             if constexpr (BWD) {
-                if (p.dr) dr[j].load(p.dr + at + c, n);
-                if (p.dy) dy[j].load(p.dy + at + c, n);
+                if (p.dr) dr[j].load(p.dr + at, c, D);
+                if (p.dy) dy[j].load(p.dy + at, c, D);
             }
         }
-        float ra[NV][GEN ? V : 1];
-        const auto ra_of = [&](int j, int i) { return ra[j][GEN ? i : 0]; };
+        float ra[NV][ODD ? V : 1];
+        const auto ra_of = [&](int j, int i) { return ra[j][ODD ? i : 0]; };
         if (out_norm) {
-            group_sums<W, NV, GEN>(row, g, D, [&](int j, int i) { return f[j][i] * f[j][i]; }, ra, small[0], wide);
+            group_sums<W, NV, ODD>(row, g, D, [&](int j, int i) { return f[j][i] * f[j][i]; }, ra, small[0], wide);
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int i = 0; i < (GEN ? V : 1); ++i) ra[j][i] = __builtin_amdgcn_rsqf(fmaf(ra[j][i], g.inv, eps));
+                for (int i = 0; i < (ODD ? V : 1); ++i) ra[j][i] = __builtin_amdgcn_rsqf(fmaf(ra[j][i], g.inv, eps));
         }
         // m and r of one vector
         const auto middle = [&](int j, float (&m)[V], float (&r)[V], float (&n)[V], float (&sg)[V]) {
-            const int c = (j * R::kLanes + row.lane) * V, left = D - c;
+            const uint32_t c = (j * R::kLanes + row.lane) * V;
 #pragma unroll
             for (int i = 0; i < V; ++i) n[i] = f[j][i];
             if (out_norm) {
                 float w[V];
-                ld_par(p.w_out + c, w, left);
+                ld_par<ODD>(p.w_out, c, D, w);
 #pragma unroll
                 for (int i = 0; i < V; ++i) n[i] *= ra_of(j, i) * w[i];
             }
@@ -199,7 +242,7 @@ __global__ __launch_bounds__(Row<W>::kThreads) void k_block_norm(Ptr<IO> p, int6
             }
             if (p.scale) {
                 float s[V];
-                ld_par(p.scale + c, s, left);
+                ld_par<ODD>(p.scale, c, D, s);
 #pragma unroll
                 for (int i = 0; i < V; ++i) r[i] *= s[i];
             }
@@ -216,7 +259,7 @@ __global__ __launch_bounds__(Row<W>::kThreads) void k_block_norm(Ptr<IO> p, int6
             if (in_norm) {
                 float w[V];
                 if constexpr (BWD)
-                    if (p.dy) ld_par(p.w_in + (j * R::kLanes + row.lane) * V, w, D - (j * R::kLanes + row.lane) * V);
+                    if (p.dy) ld_par<ODD>(p.w_in, (j * R::kLanes + row.lane) * V, D, w);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     ss = fmaf(r[j][i], r[j][i], ss);
@@ -233,28 +276,35 @@ __global__ __launch_bounds__(Row<W>::kThreads) void k_block_norm(Ptr<IO> p, int6
         if constexpr (!BWD) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int c = (j * R::kLanes + row.lane) * V, left = on ? D - c : 0;
-                st_row<IO, V>(p.r + at + c, r[j], left);
+                const uint32_t c = (j * R::kLanes + row.lane) * V;
+                const int left = on ? D - (int)c : 0;
+                st_vec<IO, ODD>(p.r + at, c, left, r[j]);
                 if (in_norm) {
                     float w[V], o[V];
-                    ld_par(p.w_in + c, w, D - c);
+                    ld_par<ODD>(p.w_in, c, D, w);
 #pragma unroll
                     for (int i = 0; i < V; ++i) o[i] = r[j][i] * rb * w[i];
-                    st_row<IO, V>(p.y + at + c, o, left);
+                    st_vec<IO, ODD>(p.y + at, c, left, o);
                 }
             }
         } else {
             float dn[NV][V];
+            asm volatile("" ::: "memory");
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int c = (j * R::kLanes + row.lane) * V, left = on ? D - c : 0;
+                f[j].forget();
+                if (p.res) res[j].forget();
+                if (p.z) z[j].forget();
+                if (p.dy) dy[j].forget();
+                const uint32_t c = (j * R::kLanes + row.lane) * V;
+                const int left = on ? D - (int)c : 0;
                 float t[V];
                 middle(j, m, r[j], n, sg);
 #pragma unroll
                 for (int i = 0; i < V; ++i) t[i] = p.dr ? dr[j][i] : 0.f;
                 if (in_norm && p.dy) {
                     float w[V];
-                    ld_par(p.w_in + c, w, D - c);
+                    ld_par<ODD>(p.w_in, c, D, w);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         const float rh = r[j][i] * rb;
@@ -262,10 +312,10 @@ __global__ __launch_bounds__(Row<W>::kThreads) void k_block_norm(Ptr<IO> p, int6
                         if (on) ai[j][i] = fmaf(dy[j][i], rh, ai[j][i]);
                     }
                 }
-                if (p.dres) st_row<IO, V>(p.dres + at + c, t, left);
+                if (p.dres) st_vec<IO, ODD>(p.dres + at, c, left, t);
                 if (p.scale) {
                     float s[V];
-                    ld_par(p.scale + c, s, D - c);
+                    ld_par<ODD>(p.scale, c, D, s);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         if (on) as[j][i] = fmaf(t[i], m[i], as[j][i]);
@@ -280,31 +330,32 @@ __global__ __launch_bounds__(Row<W>::kThreads) void k_block_norm(Ptr<IO> p, int6
                         dz[i] = t[i] * n[i] * sg[i] * fmaf(zz, 1.f - sg[i], 1.f);
                         t[i] *= zz * sg[i];
                     }
-                    st_row<IO, V>(p.dz + at + c, dz, left);
+                    st_vec<IO, ODD>(p.dz + at, c, left, dz);
                 }
                 if (out_norm) {
                     float w[V];
-                    ld_par(p.w_out + c, w, D - c);
+                    ld_par<ODD>(p.w_out, c, D, w);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         if (on) aw[j][i] = fmaf(t[i], f[j][i] * ra_of(j, i), aw[j][i]);
                         dn[j][i] = t[i] * w[i];
                     }
                 } else {
-                    st_row<IO, V>(p.df + at + c, t, left);
+                    st_vec<IO, ODD>(p.df + at, c, left, t);
                 }
             }
             if (out_norm) {
-                float c2[NV][GEN ? V : 1];
-                group_sums<W, NV, GEN>(row, g, D, [&](int j, int i) { return dn[j][i] * f[j][i] * ra_of(j, i); }, c2, small[3], wide);
+                float c2[NV][ODD ? V : 1];
+                group_sums<W, NV, ODD>(row, g, D, [&](int j, int i) { return dn[j][i] * f[j][i] * ra_of(j, i); }, c2, small[3], wide);
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    const int c = (j * R::kLanes + row.lane) * V, left = on ? D - c : 0;
+                    const uint32_t c = (j * R::kLanes + row.lane) * V;
+                const int left = on ? D - (int)c : 0;
                     float o[V];
 #pragma unroll
                     for (int i = 0; i < V; ++i)
-                        o[i] = ra_of(j, i) * fmaf(-f[j][i] * ra_of(j, i), c2[j][GEN ? i : 0] * g.inv, dn[j][i]);
-                    st_row<IO, V>(p.df + at + c, o, left);
+                        o[i] = ra_of(j, i) * fmaf(-f[j][i] * ra_of(j, i), c2[j][ODD ? i : 0] * g.inv, dn[j][i]);
+                    st_vec<IO, ODD>(p.df + at, c, left, o);
                 }
             }
         }
@@ -336,39 +387,43 @@ __global__ __launch_bounds__(Row<W>::kThreads) void k_block_norm(Ptr<IO> p, int6
     }
 }
 
-// Column sums of the blocks' parts, in order: 64 columns per block, its four
-// waves a quarter of the parts each.
-__global__ __launch_bounds__(256) void k_join_parts(const float *__restrict__ part, int parts, int D, float *dw_out,
-                                                    float *dscale, float *dw_in) {
-    __shared__ float lds[4][64];
+// Column sums of the blocks' parts, in order: 64 columns per block, its sixteen
+// waves a share of the parts each, eight loads on their way.
+constexpr int kJoin = 1024;
+__global__ __launch_bounds__(kJoin) void k_join_parts(const float *__restrict__ part, int parts, int D, float *dw_out,
+                                                      float *dscale, float *dw_in) {
+    __shared__ float lds[kJoin / 64][64];
     const int lane = threadIdx.x & 63, q = threadIdx.x >> 6, c = (int)blockIdx.x * 64 + lane, which = blockIdx.y;
     float *to = which == 0 ? dw_out : which == 1 ? dscale : dw_in;
     if (!to) return;
-    const int per = (parts + 3) / 4, lo = q * per, hi = min(parts, lo + per);
+    const int per = (parts + kJoin / 64 - 1) / (kJoin / 64), lo = q * per, hi = min(parts, lo + per);
     float s = 0.f;
-    if (c < D)
+    if (c < D) {
+#pragma unroll 8
         for (int i = lo; i < hi; ++i) s += part[((int64_t)i * 3 + which) * D + c];
+    }
     lds[q][lane] = s;
     __syncthreads();
-    if (q == 0 && c < D) to[c] = ((lds[0][lane] + lds[1][lane]) + lds[2][lane]) + lds[3][lane];
+    if (q == 0 && c < D) {
+        for (int w = 1; w < kJoin / 64; ++w) s += lds[w][lane];
+        to[c] = s;
+    }
 }
-
 
 // Blocks whose sums of weights' gradients are joined by k_join_parts.
 constexpr int64_t kParts = 512;
 
 // Waves of a row and vectors per thread: as few waves as hold the row in three
-// vectors per thread (eight of them four).  Groups that go through LDS are for odd
-// sizes: they have three shapes only.
+// vectors per thread (eight of them four).  Odd rows and groups have three shapes only.
 struct Shape {
     int W, NV;
 };
-Shape shape_of(int64_t D, bool gen) {
+Shape shape_of(int64_t D, bool odd) {
     const int64_t vecs = (D + V - 1) / V;
     int W = 1;
-    while (W < 8 && vecs > 64 * W * 3) W *= gen && W == 1 ? 4 : 2;
+    while (W < 8 && vecs > 64 * W * 3) W *= odd && W == 1 ? 4 : 2;
     const int nv = (int)((vecs + 64 * W - 1) / (64 * W));
-    return {W, W == 8 ? 4 : gen ? 3 : nv};
+    return {W, W == 8 ? 4 : odd ? 3 : nv};
 }
 
 Groups groups_of(int64_t D, int64_t n) {
@@ -381,6 +436,8 @@ Groups groups_of(int64_t D, int64_t n) {
     return g;
 }
 
+bool is_odd(const BlockNormArgs &a, const Groups &g) { return a.D % V != 0 || (a.w_out && g.n > 1 && !g.lanes); }
+
 int64_t blocks_of(int64_t T, int rows, bool bwd) {
     const int64_t n = (T + rows - 1) / rows;
     return bwd ? std::min(n, kParts) : n;
@@ -389,14 +446,14 @@ int64_t blocks_of(int64_t T, int rows, bool bwd) {
 template <int IO, bool BWD>
 hipError_t run(const Ptr<IO> &p, const BlockNormArgs &a, hipStream_t s) {
     const Groups g = groups_of(a.D, a.groups);
-    const bool gen = a.w_out && g.n > 1 && !g.lanes;
-    const Shape sh = shape_of(a.D, gen);
+    const bool odd = is_odd(a, g);
+    const Shape sh = shape_of(a.D, odd);
     const int rows = block_waves(sh.W) / sh.W;
     const int64_t n = blocks_of(a.T, rows, BWD);
-    const size_t lds = std::max(gen ? (size_t)rows * (a.D + g.n) * 4 : 0, BWD ? (size_t)a.D * 4 : 0);
-    const auto go = [&](auto w, auto nv, auto ge) {
+    const size_t lds = std::max(odd && g.n > 1 ? (size_t)rows * (a.D + g.n) * 4 : 0, BWD ? (size_t)a.D * 4 : 0);
+    const auto go = [&](auto w, auto nv, auto odds) {
         constexpr int W = decltype(w)::value, NV = decltype(nv)::value;
-        return launch(k_block_norm<IO, W, NV, decltype(ge)::value, BWD>, grid_of(n), dim3(Row<W>::kThreads), lds, s, p, a.T,
+        return launch(k_block_norm<IO, W, NV, decltype(odds)::value, BWD>, grid_of(n), dim3(Row<W>::kThreads), lds, s, p, a.T,
                       (int)a.D, g, a.eps);
     };
     using std::integral_constant;
@@ -405,14 +462,14 @@ hipError_t run(const Ptr<IO> &p, const BlockNormArgs &a, hipStream_t s) {
     constexpr integral_constant<int, 3> three{};
     constexpr integral_constant<int, 4> four{};
     constexpr integral_constant<int, 8> eight{};
-    constexpr std::true_type wide{};
-    constexpr std::false_type lanes{};
-    if (gen) return sh.W == 1 ? go(one, three, wide) : sh.W == 4 ? go(four, three, wide) : go(eight, four, wide);
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    if (odd) return sh.W == 1 ? go(one, three, yes) : sh.W == 4 ? go(four, three, yes) : go(eight, four, yes);
     switch (sh.W) {
-        case 1: return sh.NV == 1 ? go(one, one, lanes) : sh.NV == 2 ? go(one, two, lanes) : go(one, three, lanes);
-        case 2: return sh.NV == 2 ? go(two, two, lanes) : go(two, three, lanes);
-        case 4: return sh.NV == 2 ? go(four, two, lanes) : go(four, three, lanes);
-        default: return go(eight, four, lanes);
+        case 1: return sh.NV == 1 ? go(one, one, no) : sh.NV == 2 ? go(one, two, no) : go(one, three, no);
+        case 2: return sh.NV == 2 ? go(two, two, no) : go(two, three, no);
+        case 4: return sh.NV == 2 ? go(four, two, no) : go(four, three, no);
+        default: return go(eight, four, no);
     }
 }
 
@@ -463,9 +520,9 @@ hipError_t launch_block_norm_bwd(const BlockNormArgs &a, const void *dr, const v
     }
     if (!o.dw_out && !o.dscale && !o.dw_in) return hipSuccess;
     const Groups g = groups_of(a.D, a.groups);
-    const int W = shape_of(a.D, a.w_out && g.n > 1 && !g.lanes).W;
+    const int W = shape_of(a.D, is_odd(a, g)).W;
     const int parts = (int)blocks_of(a.T, block_waves(W) / W, true);
-    return launch(k_join_parts, dim3((unsigned)((a.D + 63) / 64), 3), dim3(256), 0, s, (const float *)ws, parts, (int)a.D,
+    return launch(k_join_parts, dim3((unsigned)((a.D + 63) / 64), 3), dim3(kJoin), 0, s, (const float *)ws, parts, (int)a.D,
                   o.dw_out, o.dscale, o.dw_in);
 }
 

@@ -44,7 +44,7 @@ __global__ __launch_bounds__(256) void k_embed(const int64_t *__restrict__ tok, 
 //   k_embed_hot   ids of more than kUnit entries: sums of the entries in each kUnit places
 //   k_embed_rows  the table's rows, from their entries or from such sums
 // Every sort is stable, so an id's entries are in the order of time.
-constexpr int kPiece = 1024, kUnit = 64, kSort = 1024, kCols = 64 * V;
+constexpr int kPiece = 1024, kUnit = 32, kSort = 1024, kCols = 64 * V;
 
 struct Sorted {
     int2 *buf[3];    // (id, time) of every entry: by pieces, then [1] and [2] in turn, by ranges
@@ -141,23 +141,31 @@ __global__ __launch_bounds__(256) void k_embed_cut(const int64_t *__restrict__ t
     for (int64_t r = threadIdx.x; r <= s.ranges; r += 256) s.off[r * s.pieces + piece] = first[r];
 }
 
-// One stable pass over n entries by the digit from `bit` on; a wave has consecutive ones.
+// One stable pass over n entries by the digit from `bit` on; a wave has consecutive ones, whose loads go out
+// kBatch at a time.
+constexpr int kBatch = 8;
 __device__ __forceinline__ void sort_pass(const int2 *from, int2 *to, int64_t n, int bit, int (*cnt)[256], int *first) {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int64_t per = (n + kSort - 1) / kSort * 64, lo = wave * per, hi = lo + per < n ? lo + per : n;
     for (int i = threadIdx.x; i < kSort / 64 * 256; i += kSort) cnt[i >> 8][i & 255] = 0;
     __syncthreads();
     for (int place = 0; place < 2; ++place) {
-        for (int64_t i0 = lo; i0 < hi; i0 += 64) {
-            const bool on = i0 + lane < hi;
-            const int2 e = from[on ? i0 + lane : lo];
-            const int d = (e.x >> bit) & 255;
-            const uint64_t same = same_digit(d, on);
-            const int before = lanes_before(same), have = cnt[wave][d];
-            __builtin_amdgcn_wave_barrier();
-            if (on && place) to[first[d] + have + before] = e;
-            if (on && before == 0) cnt[wave][d] = have + __popcll(same);
-            __builtin_amdgcn_wave_barrier();
+        for (int64_t i0 = lo; i0 < hi; i0 += 64 * kBatch) {
+            int2 e[kBatch];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) e[q] = from[i0 + q * 64 + lane < hi ? i0 + q * 64 + lane : lo];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                if (i0 + q * 64 >= hi) break;
+                const bool on = i0 + q * 64 + lane < hi;
+                const int d = (e[q].x >> bit) & 255;
+                const uint64_t same = same_digit(d, on);
+                const int before = lanes_before(same), have = cnt[wave][d];
+                __builtin_amdgcn_wave_barrier();
+                if (on && place) to[first[d] + have + before] = e[q];
+                if (on && before == 0) cnt[wave][d] = have + __popcll(same);
+                __builtin_amdgcn_wave_barrier();
+            }
         }
         __syncthreads();
         if (!place) places<kSort>(cnt, first);
@@ -166,7 +174,8 @@ __device__ __forceinline__ void sort_pass(const int2 *from, int2 *to, int64_t n,
 
 __global__ __launch_bounds__(kSort) void k_embed_sort(Sorted s) {
     __shared__ int cnt[kSort / 64][256], first[257];
-    __shared__ int64_t sums[kSort / 64];
+    __shared__ int64_t sums[kSort / 64], to[kSort];
+    __shared__ int from[kSort], many[kSort];
     const int64_t r = blockIdx.x;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     // where the range begins among all entries
@@ -177,7 +186,8 @@ __global__ __launch_bounds__(kSort) void k_embed_sort(Sorted s) {
     __syncthreads();
     base = 0;
     for (int w = 0; w < kSort / 64; ++w) base += sums[w];
-    // its entries from the pieces, in order: a thread has a piece's place, a wave copies its 64 pieces
+    __syncthreads();
+    // its entries from the pieces, in order: a thread has a piece's place, the waves copy pieces in turn
     for (int64_t p0 = 0; p0 < s.pieces; p0 += kSort) {
         const int64_t p = p0 + threadIdx.x;
         const int lo = p < s.pieces ? s.off[r * s.pieces + p] : 0, hi = p < s.pieces ? s.off[(r + 1) * s.pieces + p] : 0;
@@ -186,7 +196,6 @@ __global__ __launch_bounds__(kSort) void k_embed_sort(Sorted s) {
             const int64_t u = __shfl_up(run, k);
             if (lane >= k) run += u;
         }
-        __syncthreads();
         if (lane == 63) sums[wave] = run;
         __syncthreads();
         int64_t at = base + n + run - (hi - lo), all = 0;
@@ -194,11 +203,19 @@ __global__ __launch_bounds__(kSort) void k_embed_sort(Sorted s) {
             if (w < wave) at += sums[w];
             all += sums[w];
         }
-        for (int i = 0; i < 64 && p0 + wave * 64 + i < s.pieces; ++i) {
-            const int from = __shfl(lo, i), m = __shfl(hi, i) - from;
-            const int64_t to = __shfl(at, i), src = (p0 + wave * 64 + i) * kPiece + from;
-            for (int j = lane; j < m; j += 64) s.buf[1][to + j] = s.buf[0][src + j];
+        from[threadIdx.x] = lo;
+        many[threadIdx.x] = hi - lo;
+        to[threadIdx.x] = at;
+        __syncthreads();
+        const int last = (int)std::min<int64_t>(kSort, s.pieces - p0);
+        for (int q = wave; q < last; q += kSort / 64) {
+            const int2 *src = s.buf[0] + (p0 + q) * kPiece + from[q];
+            int2 *dst = s.buf[1] + to[q];
+            const int m = many[q];
+#pragma unroll 4
+            for (int j = lane; j < m; j += 64) dst[j] = src[j];
         }
+        __syncthreads();
         n += all;
     }
     __syncthreads();
@@ -212,25 +229,37 @@ __global__ __launch_bounds__(kSort) void k_embed_sort(Sorted s) {
     if (r == s.ranges - 1 && threadIdx.x == 0) *s.total = base + n;
 }
 
-// The sum of the rows of dy that n entries name, n at most 64: this lane's columns.
+// One vector as loaded; zeros past the row.
 template <int IO>
-__device__ __forceinline__ void sum_rows(const int2 *e, int n, const typename io_elem<IO>::T *dy, int64_t D, int64_t c,
+struct Raw {
+    Pack<typename io_elem<IO>::T, V> r;
+    __device__ __forceinline__ void load(const typename io_elem<IO>::T *p, int64_t valid) {
+        if (valid >= V) {
+            r = *reinterpret_cast<const Pack<typename io_elem<IO>::T, V> *>(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) r.v[i] = i < valid ? p[i] : typename io_elem<IO>::T(0);
+        }
+    }
+    __device__ __forceinline__ void add_to(float (&s)[V]) const {
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] += to_f<IO>(r.v[i]);
+    }
+};
+
+// The sum of n rows of dy, n at most 64, in order: this lane's columns.  t: the rows, lane by lane from `first` on.
+// DEEP rows are on their way at a time.
+template <int IO, int DEEP>
+__device__ __forceinline__ void sum_rows(int t, int first, int n, const typename io_elem<IO>::T *dy, int64_t D, int64_t c,
                                          float (&sum)[V]) {
-    const int lane = threadIdx.x & 63;
-    const int t = lane < n ? e[lane].y : 0;
+    for (int j = 0; j < n; j += DEEP) {
+        Raw<IO> v[DEEP];
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum[i] = 0.f;
-    for (int j = 0; j < n; j += 4) {
-        float v[4][V];
+        for (int k = 0; k < DEEP; ++k)
+            if (j + k < n) v[k].load(dy + (int64_t)__builtin_amdgcn_readlane(t, first + j + k) * D + c, D - c);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)  // (past the last: its row once more, not added)
-            ld_row<IO, V>(dy + (int64_t)__builtin_amdgcn_readlane(t, j + k < n ? j + k : n - 1) * D + c, v[k], D - c);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (j + k < n) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) sum[i] += v[k][i];
-            }
+        for (int k = 0; k < DEEP; ++k)
+            if (j + k < n) v[k].add_to(sum);
     }
 }
 
@@ -247,38 +276,53 @@ __global__ __launch_bounds__(256) void k_embed_hot(const typename io_elem<IO>::T
         const int2 sp = s.span[w ? idb : ida];
         if (sp.y - sp.x <= kUnit) continue;
         const int64_t lo = sp.x > p0 ? sp.x : p0, hi = sp.y < p1 ? sp.y : p1;
-        float sum[V];
-        sum_rows<IO>(e + lo, __builtin_amdgcn_readfirstlane((int)(hi - lo)), dy, D, c, sum);
+        const int lane = threadIdx.x & 63, n = __builtin_amdgcn_readfirstlane((int)(hi - lo));
+        const int t = lane < n ? e[lo + lane].y : 0;
+        float sum[V] = {};
+        sum_rows<IO, 16>(t, 0, n, dy, D, c, sum);
         st_row<IO_F32, V>(s.part + (2 * u + w) * D + c, sum, D - c);
     }
 }
 
-// A wave per id; the block's four join the sums of one of many entries.
+// A wave has kIds ids.  Their places and the first 64 of their entries are loaded together; rows of absent ids are
+// zeros at once.  The block's four waves join the sums of an id of many entries.
+constexpr int kIds = 16;
 template <int IO>
 __global__ __launch_bounds__(256) void k_embed_rows(const typename io_elem<IO>::T *__restrict__ dy,
                                                     typename io_elem<IO>::T *__restrict__ dw, int64_t D, int64_t vocab,
                                                     float scale, Sorted s) {
     __shared__ float lds[4][kCols];
-    __shared__ int2 spans[4];
+    __shared__ int2 spans[4 * kIds];
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int64_t id0 = block_id() * 4;
-    if (id0 >= vocab) return;
-    const int64_t id = id0 + wave;
-    const int2 sp = id < vocab ? s.span[id] : int2{0, 0};
-    const int n = __builtin_amdgcn_readfirstlane(sp.y - sp.x);
-    if (lane == 0) spans[wave] = sp;
-    if (id < vocab && n <= kUnit) {
+    const int64_t block0 = block_id() * 4 * kIds, id0 = block0 + wave * kIds;
+    if (block0 >= vocab) return;
+    const int ids = (int)(vocab - id0 < kIds ? (vocab > id0 ? vocab - id0 : 0) : kIds);
+    const int2 sp = lane < ids ? s.span[id0 + lane] : int2{0, 0};
+    const int n = sp.y - sp.x;
+    if (lane < kIds) spans[wave * kIds + lane] = sp;
+    // the entries of the ids of few, which stand one after another: lane l has the l-th from the first id's first
+    uint64_t some = __ballot(n > 0);
+    const int e0 = some ? __builtin_amdgcn_readlane(sp.x, __builtin_ctzll(some)) : 0, total = (int)*s.total;
+    const int t = s.done()[e0 + lane < total ? e0 + lane : 0].y;
+    for (int q = 0; q < ids; ++q) {
+        const int nq = __builtin_amdgcn_readlane(n, q), at = __builtin_amdgcn_readlane(sp.x, q) - e0;
+        if (nq > kUnit) continue;
+        int tq = t, first = at;
+        if (nq > 0 && at + nq > 64) {  // (past the 64)
+            tq = lane < nq ? s.done()[e0 + at + lane].y : 0;
+            first = 0;
+        }
         for (int64_t c0 = 0; c0 < D; c0 += kCols) {  // (every lane: each holds an entry)
             const int64_t c = c0 + lane * V;
-            float sum[V];
-            sum_rows<IO>(s.done() + sp.x, n, dy, D, c, sum);
+            float sum[V] = {};
+            sum_rows<IO, 4>(tq, first, nq, dy, D, c, sum);
 #pragma unroll
             for (int i = 0; i < V; ++i) sum[i] *= scale;
-            st_row<IO, V>(dw + id * D + c, sum, D - c);
+            st_row<IO, V>(dw + (id0 + q) * D + c, sum, D - c);
         }
     }
     if (!__syncthreads_or(n > kUnit)) return;
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < 4 * kIds; ++w) {
         const int2 x = spans[w];
         if (x.y - x.x <= kUnit) continue;
         // units first .. last; the first is the id's own only where it begins with it
@@ -286,10 +330,8 @@ __global__ __launch_bounds__(256) void k_embed_rows(const typename io_elem<IO>::
         const int64_t lo = u0 + wave * per, hi = lo + per < u1 ? lo + per : u1;
         for (int64_t c0 = 0; c0 < D; c0 += kCols) {
             const int64_t c = c0 + lane * V;
-            float sum[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) sum[i] = 0.f;
-#pragma unroll 4
+            float sum[V] = {};
+#pragma unroll 8
             for (int64_t u = lo; u < hi; ++u) {
                 float v[V];
                 ld_row<IO_F32, V>(s.part + (2 * u + (u == u0 && x.x % kUnit != 0 ? 1 : 0)) * D + c, v, D - c);
@@ -305,7 +347,7 @@ __global__ __launch_bounds__(256) void k_embed_rows(const typename io_elem<IO>::
                     const int k = lane * V + i;
                     sum[i] = (((lds[0][k] + lds[1][k]) + lds[2][k]) + lds[3][k]) * scale;
                 }
-                st_row<IO, V>(dw + (id0 + w) * D + c, sum, D - c);
+                st_row<IO, V>(dw + (block0 + w) * D + c, sum, D - c);
             }
             __syncthreads();
         }
@@ -350,7 +392,7 @@ hipError_t bwd_io(const int64_t *tok, const void *dy_, void *dw, int64_t T, int6
     if (e == hipSuccess) e = launch(k_embed_sort, dim3((unsigned)s.ranges), dim3(kSort), 0, st, s);
     if (e == hipSuccess && T > kUnit)
         e = launch(k_embed_hot<IO>, grid_of((s.units + 3) / 4, (unsigned)((D + kCols - 1) / kCols)), dim3(256), 0, st, dy, D, s);
-    if (e == hipSuccess) e = launch(k_embed_rows<IO>, grid_of((vocab + 3) / 4), dim3(256), 0, st, dy, (E *)dw, D, vocab, scale, s);
+    if (e == hipSuccess) e = launch(k_embed_rows<IO>, grid_of((vocab + 4 * kIds - 1) / (4 * kIds)), dim3(256), 0, st, dy, (E *)dw, D, vocab, scale, s);
     return e;
 }
 

@@ -15,6 +15,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "lm_device.h"
 #include "lm_internal.h"
@@ -62,6 +63,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f2 __attribute__((ext_vector_type(2)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 typedef int i2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) s4 lds_s4;
@@ -124,25 +126,23 @@ struct Mx<IO_F32> {
     }
 };
 
-// A tile of steps in LDS: rows of COLS elements in units of 16 bytes, which a row's
-// number permutes so that neither kind of fragment meets a bank more often than it must.
+// A tile of steps in LDS, rows of COLS elements and 16 bytes: 16 lanes that read a unit of 16 consecutive rows
+// each, or the four-row blocks of a transposed read, then meet all banks, and every address is one of the lane plus a
+// constant.
 template <int IO, int COLS>
 struct Lds {
     using T = typename io_elem<IO>::T;
-    static constexpr int E = 16 / (int)sizeof(T), CH = COLS / E, ROWS = Mx<IO>::C, kBytes = ROWS * COLS * (int)sizeof(T);
+    static constexpr int E = 16 / (int)sizeof(T), CH = COLS / E, ROWS = Mx<IO>::C, STRIDE = (CH + 1) * 16, kBytes = ROWS * STRIDE;
     using Frag = typename Mx<IO>::Frag;
-    __device__ __forceinline__ static int at(int row, int chunk) {
-        const int turn = CH >= 16 ? row & 15 : (row / (16 / CH)) & (CH - 1);
-        return (row * CH + (chunk ^ turn)) * 16;
-    }
+    __device__ __forceinline__ static int at(int row, int chunk) { return row * STRIDE + chunk * 16; }
     // the row `row` + lane & 15, its 32 elements from k on, 8 of them per lane
     __device__ __forceinline__ static Frag along(const char *p, int row, int k) {
         const int i = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
         Frag f;
         if constexpr (IO != IO_F32) {
-            f.v = *(const u4 *)(p + at(row + i, k / E + g));
+            f.v = *(const u4 *)(p + at(i, g) + at(row, k / E));
         } else {
-            const f4 a = *(const f4 *)(p + at(row + i, k / E + 2 * g)), b = *(const f4 *)(p + at(row + i, k / E + 2 * g + 1));
+            const f4 a = *(const f4 *)(p + at(i, 2 * g) + at(row, k / E)), b = *(const f4 *)(p + at(i, 2 * g) + at(row, k / E + 1));
 #pragma unroll
             for (int j = 0; j < 4; ++j) f.v[j] = a[j], f.v[4 + j] = b[j];
         }
@@ -155,19 +155,16 @@ struct Lds {
         const int i = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
         Frag f;
         if constexpr (IO != IO_F32) {
-            const int c = SPREAD ? col + 8 * (i & 3) : col + 4 * (i & 3);
+            const char *mine = p + at(4 * g + (i >> 2), 0) + (SPREAD ? 16 : 8) * (i & 3);
             i2 h[2];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int r = row + 16 * q + 4 * g + (i >> 2);
-                h[q] = __builtin_bit_cast(i2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(p + at(r, c / E) + (c & 4) * 2)));
-            }
+            for (int q = 0; q < 2; ++q)
+                h[q] = __builtin_bit_cast(i2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(mine + at(row + 16 * q, 0) + col * 2)));
             f.v = u4{(uint32_t)h[0].x, (uint32_t)h[0].y, (uint32_t)h[1].x, (uint32_t)h[1].y};
         } else {
-            const int c = SPREAD ? col + 8 * (i >> 2) + (i & 3) : col + i;
+            const char *mine = p + at(4 * g, 0) + (SPREAD ? 8 * (i >> 2) + (i & 3) : i) * 4;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                f.v[j] = *(const float *)(p + at(row + 16 * (j >> 2) + 4 * g + (j & 3), c / E) + (c & 3) * 4);
+            for (int j = 0; j < 8; ++j) f.v[j] = *(const float *)(mine + at(row + 16 * (j >> 2) + (j & 3), 0) + col * 4);
         }
         return f;
     }
@@ -189,6 +186,8 @@ __device__ __forceinline__ float exp2_of(double x) {
     return __builtin_amdgcn_exp2f(d) * fmaf((float)(x - (double)d), kLn2, 1.f);
 }
 
+enum { STATES, FORWARD, BACKWARD };  // what a launch of chunks is for
+
 // Where the segments of the rows meet.
 struct Segs {
     int64_t len, n;      // steps of one, number
@@ -197,139 +196,255 @@ struct Segs {
     int64_t plane;       // K*M
 };
 
-template <int IO, int KP, int NV, bool OUT>
-__global__ __launch_bounds__(256) void k_lin_chunk(Roles roles, Shape s, Segs sg, int tiles) {
+// Waves of a SIMD that the registers are to leave room for: as many as the LDS does.
+constexpr int waves_per_simd(int io, int KP, int WV, bool whole_heads) {
+    return io == IO_F32 || KP > 64 || !whole_heads || WV == 8 ? 2 : KP == 32 ? 4 : 3;
+}
+
+// (a lambda left as a call would keep all that it captures in memory)
+#define INLINE __attribute__((always_inline))
+
+template <int IO, int KP, int WV, int DO, bool WHOLE>
+__global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_lin_chunk(Roles roles, Shape s, Segs sg, int tiles) {
     using T = typename io_elem<IO>::T;
     using X = Mx<IO>;
     using Frag = typename X::Frag;
-    constexpr int C = X::C, MB = 4 * NV * 16, KS = KP / 32, NT = C / 16, NU = C / 32;
+    constexpr bool OUT = DO != STATES;
+    constexpr int C = X::C, TH = WV * 64, MB = WV * 16, KS = KP / 32, NT = C / 16, NU = C / 32;
     using LK = Lds<IO, KP>;
     using LM = Lds<IO, MB>;
     constexpr int E = LK::E;
-    constexpr int NA = C * LK::CH / 256, NC = C * LM::CH / 256;  // units of 16 bytes per thread
-    static_assert(C * LK::CH % 256 == 0 && C * LM::CH % 256 == 0, "whole units");
+    constexpr int NA = C * LK::CH / TH, NC = C * LM::CH / TH;  // units of 16 bytes per thread
+    static_assert(C * LK::CH % TH == 0 && C * LM::CH % TH == 0 && NT <= 4, "whole units, a wave per 16 steps");
+    // pieces of weights and states in the output's products (24 bits where the decays' gradients take them); fragments of weights
+    constexpr int NP = IO == IO_F32 ? 1 : IO == IO_F16 || DO == FORWARD ? 2 : 3, WF = NT == 4 ? 6 : 2;
     __shared__ __attribute__((aligned(16))) char la[OUT ? LK::kBytes : 16], lb[LK::kBytes], lc[LM::kBytes];
-    __shared__ __attribute__((aligned(16))) float dec[4 * C + 4];  // [hi, lo, into, upd][C], then the chunk's factor in two parts
-    __shared__ float dots[OUT ? 4 * C : 4];                        // [wave][C]
-    const Role &r = roles.r[blockIdx.y];
-    const int K = r.a.dim, M = r.c.dim;
+    __shared__ __attribute__((aligned(16))) float decays[2][4 * C + 4];  // of a chunk [hi, lo, into, upd][C] and its factor in two parts
+    __shared__ Frag weights[OUT ? WF * NP * 64 : 1];                     // [fragment][piece][lane]
+    __shared__ float owns[OUT ? C : 1], downs[OUT ? C : 1];              // a step's weight of itself, what its weights were scaled by
+    __shared__ float dots[OUT ? WV * C : 1];                             // [wave][C]
+    // (read once: the compiler keeps a struct of a launch's arguments that varies by block in memory)
+    const Role *role = &roles.r[blockIdx.y];
+    const float out = role->out, upd = role->upd;
+    const int rs = role->rs, cs = role->cs, wide = role->wide;
+    float *const dot_to = role->dot, *const s1 = role->s1;
+    const float *const s0 = role->s0;
+    void *const o = role->o;
+    const int K = role->a.dim, M = role->c.dim;
     int64_t id = block_id();
     const int tile = (int)(id % tiles);
     id /= tiles;
     const int64_t BH = s.B * s.H, bh = id % BH, seg = id / BH;
     if (seg >= (OUT ? sg.n : sg.n - 1) || tile * MB >= M) return;
-    const int64_t b = bh / s.H, h = bh - b * s.H, n = row_len(s.lengths, b, s.N);
-    const int64_t i_lo = seg * sg.len, i_hi = std::min(n, i_lo + sg.len);
+    const int64_t b = bh / s.H;
+    const int h = (int)(bh - b * s.H), n = (int)row_len(s.lengths, b, s.N);
+    const int i_lo = (int)(seg * sg.len), i_hi = (int)std::min<int64_t>(n, seg * sg.len + sg.len);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), li = lane & 15, lg = lane >> 4;
-    const int col0 = tile * MB + wave * NV * 16;  // the wave's columns
-    const bool dot = OUT && r.dot;
-    const int np = IO == IO_F32 ? 1 : IO == IO_F16 ? 2 : dot ? 3 : 2;  // pieces of weights and states in the output's products
-    const auto time = [&](int64_t i) { return r.reverse ? n - 1 - i : i; };
-    const auto base = [&](const Seq &q) { return (const T *)q.p + b * s.N * q.ld + h / q.share * q.dim; };
-    const T *pa = OUT ? base(r.a) : nullptr, *pb = base(r.b), *pc = base(r.c);
+    const int col0 = tile * MB + wave * 16;  // the wave's columns
+    constexpr int EW = WV > NT ? WV - 1 : 0;  // the wave of the decays' exponents, one with few weights to form
+    const bool dot = DO == BACKWARD && dot_to, back = role->reverse;
+    // A chunk takes steps i0 .. i0 + cnt - 1 in the order of the recurrence, which lie in memory from `low` on, in
+    // this order or the other: step i0 + j at low + at(j).  What lies past them is taken to be the last.
+    const auto low = [&](int i0, int cnt) INLINE { return b * s.N + (back ? n - i0 - cnt : i0); };
+    const auto at = [&](int j, int cnt) INLINE { return back ? cnt - 1 - std::min(j, cnt - 1) : std::min(j, cnt - 1); };
+    const auto count = [&](int i0) INLINE { return std::min(C, i_hi - i0); };
+    const auto base = [&](const Seq &q) INLINE { return (const T *)q.p + h / q.share * q.dim; };
+    const T *pa = OUT ? base(role->a) : nullptr, *pb = base(role->b), *pc = base(role->c), *pe = dot ? base(role->e) : nullptr;
+    const int lda = (int)role->a.ld, ldb = (int)role->b.ld, ldc = (int)role->c.ld, lde = (int)role->e.ld, ldo = (int)s.H * M;
 
-    f4 st[2 * KS][NV];  // the state: rows 32 p + 8 g + 4 (m & 1) + j of tile m = 2 p, 2 p + 1, column lane & 15
+    f4 st[2 * KS];  // the state: rows 32 p + 8 g + 4 (m & 1) + j of tile m = 2 p, 2 p + 1, column lane & 15
     const int64_t slot = ((int64_t)blockIdx.y * sg.n + seg) * BH + bh;
-    const float *enter = OUT ? (seg == 0 && sg.n == 1 ? (r.s0 ? r.s0 + bh * K * M : nullptr) : sg.state + slot * sg.plane) : nullptr;
+    const float *enter = OUT ? (seg == 0 && sg.n == 1 ? (s0 ? s0 + bh * K * M : nullptr) : sg.state + slot * sg.plane) : nullptr;
 #pragma unroll
     for (int m = 0; m < 2 * KS; ++m)
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = 16 * (m & ~1) + 8 * lg + 4 * (m & 1) + j, c = col0 + 16 * v + li;
-                st[m][v][j] = enter && k < K && c < M ? enter[(int64_t)k * r.rs + (int64_t)c * r.cs] : 0.f;
-            }
+        for (int j = 0; j < 4; ++j) {
+            const int k = 16 * (m & ~1) + 8 * lg + 4 * (m & 1) + j, c = col0 + li;
+            st[m][j] = enter ? enter[std::min(k, K - 1) * rs + std::min(c, M - 1) * cs] : 0.f;
+            if (k >= K || c >= M) st[m][j] = 0.f;
+        }
 
     // the next chunk's units, on their way
-    Pack<T, E> ga[OUT ? NA : 1], gb[NA], gc[NC];
+    u4 ga[OUT ? NA : 1], gb[NA], gc[NC];
     float gg = 0.f;
-    const auto fetch = [&](const T *p, int64_t ld, int64_t i, int c, int dim) {
-        Pack<T, E> u;
-        const int left = i < i_hi ? dim - c : 0;
-        const T *q = p + time(i) * ld + c;
-        if (left >= E) {
-            u = *(const Pack<T, E> *)q;
-        } else {
+    // WHOLE: heads are whole units at whole dwords, and tiles go through buffer resources that end with the chunk's
+    // last row: what is past the rows (or, by its offset, past the head) loads as zero and is not stored.  Else
+    // every element is loaded by itself, from a place in bounds.
+    const auto window = [&](const void *p, int ld, int dim, int cnt, int e) INLINE {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, ((cnt - 1) * ld + dim) * e, 0x00020000);
+    };
+    // a row's offset: a part of the lane, and one of the rows before it
+    const auto lane_at = [&](int row, int ld, int c, int dim, int e) INLINE {
+        return c < dim ? (back ? -row : row) * ld * e + c * e : (int)0x80000000;
+    };
+    const auto rows_at = [&](int row, int ld, int cnt, int e) INLINE { return (back ? cnt - 1 - row : row) * ld * e; };
+    const auto element = [&](const T *p, int ld, int j, int cnt, int c, int dim) INLINE {
+        u4 u = {0, 0, 0, 0};
+        const uint32_t row = (uint32_t)at(j, cnt) * (uint32_t)ld;
 #pragma unroll
-            for (int j = 0; j < E; ++j) u.v[j] = j < left ? q[j] : T(0);
+        for (int k = 0; k < E; ++k) {
+            const T v = p[row + std::min(c + k, dim - 1)];
+            const bool in = j < cnt && c + k < dim;
+            if constexpr (E == 4) u[k] = in ? __float_as_uint(v) : 0;
+            else u[k >> 1] |= (in ? (uint32_t)__builtin_bit_cast(uint16_t, v) : 0u) << (16 * (k & 1));
         }
         return u;
     };
-    const auto load = [&](int64_t i0) {
+    constexpr int RA = TH / LK::CH, RC = TH / LM::CH, EB = (int)sizeof(T);
+    const int ra = tid / LK::CH, ca = tid % LK::CH * E, rc = tid / LM::CH, cc = tile * MB + tid % LM::CH * E;
+    const int va = lane_at(ra, lda, ca, K, EB), vb = lane_at(ra, ldb, ca, K, EB), vc = lane_at(rc, ldc, cc, M, EB);
+    const auto load = [&](int i0) INLINE {
+        const int cnt = count(i0);
+        const int64_t l = low(i0, cnt);
+        const T *qa = OUT ? pa + l * lda : nullptr, *qb = pb + l * ldb, *qc = pc + l * ldc;
+        if constexpr (WHOLE) {
+            const __amdgpu_buffer_rsrc_t wb = window(qb, ldb, K, cnt, EB), wc = window(qc, ldc, M, cnt, EB);
 #pragma unroll
-        for (int q = 0; q < NA; ++q) {
-            const int u = q * 256 + tid, row = u / LK::CH, c = u % LK::CH * E;
-            if constexpr (OUT) ga[q] = fetch(pa, r.a.ld, i0 + row, c, K);
-            gb[q] = fetch(pb, r.b.ld, i0 + row, c, K);
-        }
+            for (int q = 0; q < NA; ++q)
+                gb[q] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(wb, vb + rows_at(q * RA, ldb, cnt, EB), 0, 0));
 #pragma unroll
-        for (int q = 0; q < NC; ++q) {
-            const int u = q * 256 + tid, row = u / LM::CH, c = tile * MB + u % LM::CH * E;
-            gc[q] = fetch(pc, r.c.ld, i0 + row, c, M);
-        }
-        if (wave == 0) {
-            gg = 0.f;
-            if (i0 + lane < i_hi && lane < C) gg = s.per_token ? s.g[(b * s.N + time(i0 + lane)) * s.H + h] : s.g[h];
+            for (int q = 0; q < NC; ++q)
+                gc[q] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(wc, vc + rows_at(q * RC, ldc, cnt, EB), 0, 0));
+            if constexpr (OUT) {
+                const __amdgpu_buffer_rsrc_t wa = window(qa, lda, K, cnt, EB);
+#pragma unroll
+                for (int q = 0; q < NA; ++q)
+                    ga[q] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(wa, va + rows_at(q * RA, lda, cnt, EB), 0, 0));
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < NA; ++q) {
+                if constexpr (OUT) ga[q] = element(qa, lda, ra + q * RA, cnt, ca, K);
+                gb[q] = element(qb, ldb, ra + q * RA, cnt, ca, K);
+            }
+#pragma unroll
+            for (int q = 0; q < NC; ++q) gc[q] = element(qc, ldc, rc + q * RC, cnt, cc, M);
         }
     };
-    double all = 0.0;  // (of wave 0) the segment's decay, as an exponent of two
-    const auto keep = [&] {
+    const auto decay = [&](int i0) INLINE {
+        float g = 0.f;
+        const int cnt = i0 < i_hi ? count(i0) : 0;
+        if (lane < cnt) g = s.per_token ? s.g[(low(i0, cnt) + at(lane, cnt)) * s.H + h] : s.g[h];
+        return g;
+    };
+    double all = 0.0;  // (of wave EW) the segment's decay, as an exponent of two
+    const auto keep = [&]() INLINE {
 #pragma unroll
         for (int q = 0; q < NA; ++q) {
-            const int u = q * 256 + tid;
-            if constexpr (OUT) *(Pack<T, E> *)(la + LK::at(u / LK::CH, u % LK::CH)) = ga[q];
-            *(Pack<T, E> *)(lb + LK::at(u / LK::CH, u % LK::CH)) = gb[q];
+            const int u = q * TH + tid;
+            if constexpr (OUT) *(u4 *)(la + LK::at(u / LK::CH, u % LK::CH)) = ga[q];
+            *(u4 *)(lb + LK::at(u / LK::CH, u % LK::CH)) = gb[q];
         }
 #pragma unroll
         for (int q = 0; q < NC; ++q) {
-            const int u = q * 256 + tid;
-            *(Pack<T, E> *)(lc + LM::at(u / LM::CH, u % LM::CH)) = gc[q];
+            const int u = q * TH + tid;
+            *(u4 *)(lc + LM::at(u / LM::CH, u % LM::CH)) = gc[q];
         }
-        if (wave == 0) {
-            // exponents of two from the chunk's start on, in 64 bits: with the step's own decay where time runs
-            // on, without it where it runs back
-            const double own = (double)fmaxf(gg, kLeast) * 1.4426950408889634;
-            double sum = own;
+    };
+    // (wave EW) Exponents of two from the chunk's start on, in 64 bits: with the step's own decay where time runs
+    // on, without it where it runs back.
+    const auto exponents = [&](float *dec, float g) INLINE {
+        const double own = (double)fmaxf(g, kLeast) * 1.4426950408889634;
+        double sum = own;
 #pragma unroll
-            for (int d = 1; d < C; d <<= 1) {
-                const double u = __shfl_up(sum, d);
-                if (lane >= d) sum += u;
-            }
-            const double total = __shfl(sum, C - 1), e = r.reverse ? sum - own : sum;
-            all += total;
-            if (lane < C) {
-                const float hi = (float)e;
-                dec[lane] = hi;
-                dec[C + lane] = (float)(e - (double)hi);
-                dec[2 * C + lane] = exp2_of(e);
-                dec[3 * C + lane] = exp2_of(total - e) * r.upd;
-            }
-            if (lane == 0) {
-                const double f = exp2(total);
-                dec[4 * C] = (float)f;
-                dec[4 * C + 1] = (float)(f - (double)(float)f);
-            }
+        for (int d = 1; d < C; d <<= 1) {
+            const double u = __shfl_up(sum, d);
+            if (lane >= d) sum += u;
+        }
+        const double total = __shfl(sum, C - 1), e = back ? sum - own : sum;
+        all += total;
+        if (lane < C) {
+            const float hi = (float)e;
+            dec[lane] = hi;
+            dec[C + lane] = (float)(e - (double)hi);
+            dec[2 * C + lane] = exp2_of(e);
+            dec[3 * C + lane] = exp2_of(total - e) * upd;
+        }
+        if (lane == 0) {
+            const double f = exp2(total);
+            dec[4 * C] = (float)f;
+            dec[4 * C + 1] = (float)(f - (double)(float)f);
         }
     };
 
-    if (i_lo < i_hi) load(i_lo);
-    for (int64_t i0 = i_lo; i0 < i_hi; i0 += C) {
+    int turn = 0;
+    if (i_lo < i_hi) {
+        load(i_lo);
+        if (wave == EW) {
+            exponents(decays[0], decay(i_lo));
+            gg = decay(i_lo + C);
+        }
+    }
+    for (int i0 = i_lo; i0 < i_hi; i0 += C, turn ^= 1) {
+        const float *dec = decays[turn];
+        const int cnt = count(i0);
+        const int64_t row0 = low(i0, cnt);
         __syncthreads();  // (the last chunk has been read)
         keep();
         __syncthreads();
-        if (i0 + C < i_hi) load(i0 + C);
-        Frag cf[NV][NU];
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int u = 0; u < NU; ++u) cf[v][u] = LM::template across<false>(lc, 32 * u, wave * NV * 16 + 16 * v);
+        if constexpr (!OUT)
+            if (i0 + C < i_hi) load(i0 + C);
         if constexpr (OUT) {
-            f4 acc[NT][NV];
+            // the chunk's weights, once for all columns: 16 steps t by a wave, transposed, as they are operands
+            if (wave < NT) {
+                const int t = wave;
+                Frag a[KS];
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+                for (int p = 0; p < KS; ++p) a[p] = LK::along(la, 16 * t, 32 * p);
+                const float hi = dec[16 * t + li], lo = dec[C + 16 * t + li];
+                float w[NT][4];  // of steps 16 q + 4 g + j
+                float m = 0.f, own = 0.f;
 #pragma unroll
-                for (int v = 0; v < NV; ++v) acc[t][v] = f4{0.f, 0.f, 0.f, 0.f};
+                for (int q = 0; q < NT; ++q) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[q][j] = 0.f;
+                    if (q > t) continue;
+                    f4 d = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int p = 0; p < KS; ++p) d = X::mul(LK::along(lb, 16 * q, 32 * p), a[p], d);
+                    const f4 h2 = *(const f4 *)(dec + 16 * q + 4 * lg), l2 = *(const f4 *)(dec + C + 16 * q + 4 * lg);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float x = d[j] * (out * upd) * __builtin_amdgcn_exp2f((hi - h2[j]) + (lo - l2[j]));
+                        w[q][j] = q < t || 4 * lg + j <= li ? x : 0.f;
+                        if (dot && q == t && 4 * lg + j == li) {
+                            own = x;
+                            w[q][j] = 0.f;
+                        }
+                        if constexpr (X::SCALE) m = fmaxf(m, fabsf(w[q][j]));
+                    }
+                }
+                if (dot && (li >> 2) == lg) owns[16 * t + li] = own;
+                float up_w = 1.f;
+                if constexpr (X::SCALE) {
+                    const int e = near_2_14(lanes_max(m, 16));
+                    up_w = pow2(e);
+                    if (lg == 0) downs[16 * t + li] = pow2(-e);
+                }
+#pragma unroll
+                for (int u = 0; u < NU; ++u) {
+                    if (2 * u > t) continue;
+                    float x[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = X::SCALE ? w[2 * u + (j >> 2)][j & 3] * up_w : w[2 * u + (j >> 2)][j & 3];
+                    Frag *to = weights + (t < 2 ? t : 2 * t - 2 + u) * NP * 64 + lane;
+#pragma unroll
+                    for (int q = 0; q < NP; ++q)
+                        to[q * 64] = X::piece(x, q == NP - 1);
+                }
+            }
+        }
+        if (wave == EW && i0 + C < i_hi) {
+            exponents(decays[turn ^ 1], gg);
+            gg = decay(i0 + 2 * C);
+        }
+        Frag cf[NU];
+#pragma unroll
+        for (int u = 0; u < NU; ++u) cf[u] = LM::template across<false>(lc, 32 * u, wave * 16);
+        if constexpr (OUT) {
+            f4 acc[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[t] = f4{0.f, 0.f, 0.f, 0.f};
             // the state's part: o^T = X^T a^T, the pieces of X straight from the accumulators
             int se = 0;
             if constexpr (X::SCALE) {
@@ -337,216 +452,156 @@ __global__ __launch_bounds__(256) void k_lin_chunk(Roles roles, Shape s, Segs sg
 #pragma unroll
                 for (int p = 0; p < 2 * KS; ++p)
 #pragma unroll
-                    for (int v = 0; v < NV; ++v)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(st[p][v][j]));
+                    for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(st[p][j]));
                 se = near_2_14(lanes_max(m, 1));
             }
             const float up_s = pow2(se);
 #pragma unroll
             for (int p = 0; p < KS; ++p) {
-                Frag x[NV][3];
+                Frag x[NP];
+                float w[8];
 #pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    float w[8];
+                for (int j = 0; j < 8; ++j) w[j] = X::SCALE ? st[2 * p + (j >> 2)][j & 3] * up_s : st[2 * p + (j >> 2)][j & 3];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) w[j] = X::SCALE ? st[2 * p + (j >> 2)][v][j & 3] * up_s : st[2 * p + (j >> 2)][v][j & 3];
-                    x[v][0] = X::piece(w, IO == IO_F32);
-                    if constexpr (IO != IO_F32) x[v][1] = X::piece(w, IO == IO_F16);
-                    if constexpr (IO == IO_BF16)
-                        if (np == 3) x[v][2] = X::piece(w, true);
-                }
+                for (int q = 0; q < NP; ++q)
+                    x[q] = X::piece(w, q == NP - 1);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     const Frag a = LK::along(la, 16 * t, 32 * p);
 #pragma unroll
-                    for (int v = 0; v < NV; ++v) {
-                        acc[t][v] = X::mul(x[v][0], a, acc[t][v]);
-                        if constexpr (IO != IO_F32) acc[t][v] = X::mul(x[v][1], a, acc[t][v]);
-                        if constexpr (IO == IO_BF16)
-                            if (np == 3) acc[t][v] = X::mul(x[v][2], a, acc[t][v]);
-                    }
+                    for (int q = 0; q < NP; ++q)
+                        acc[t] = X::mul(x[q], a, acc[t]);
                 }
             }
+            if (i0 + C < i_hi) load(i0 + C);  // (here and not before: 24 registers for a part of the chunk only)
+            __syncthreads();  // (the weights are there)
             // the chunk's own part, 16 steps at a time
+            const int eo = wide ? 4 : EB;
+            const __amdgpu_buffer_rsrc_t wo = window((char *)o + (row0 * ldo + h * M) * eo, ldo, M, cnt, eo);
+            const int vo = lane_at(li, ldo, col0 + 4 * lg, M, eo);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                Frag a[KS];
+                const float mid = dec[2 * C + 16 * t + li] * out * (X::SCALE ? pow2(-se) : 1.f);
+                const float down = X::SCALE ? downs[16 * t + li] : 1.f;
+                f4 in = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int p = 0; p < KS; ++p) a[p] = LK::along(la, 16 * t, 32 * p);
-                const float hi = dec[16 * t + li], lo = dec[C + 16 * t + li], into = dec[2 * C + 16 * t + li];
-                float w[NT][4], own[4];  // weights of steps 16 q + 4 g + j, and of the step itself
-                float m = 0.f;
+                for (int u = 0; u <= t / 2; ++u)
 #pragma unroll
-                for (int q = 0; q < NT; ++q) {
-                    if (q > t) {
+                    for (int q = 0; q < NP; ++q)
+                        in = X::mul(cf[u], weights[((t < 2 ? t : 2 * t - 2 + u) * NP + q) * 64 + lane], in);
+                const int j0 = 16 * t + li, c = col0 + 4 * lg;
+                const uint32_t row = (uint32_t)at(j0, cnt);
+                float y[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) w[q][j] = 0.f;
-                        continue;
-                    }
-                    f4 d = f4{0.f, 0.f, 0.f, 0.f};
+                for (int j = 0; j < 4; ++j) y[j] = fmaf(in[j], down, acc[t][j] * mid);
+                if (dot) {  // and then the step's own product
+                    float z[4], e = 0.f;
+                    ld_row<IO, 4>(pe + row0 * lde + (row * (uint32_t)lde + c), z, M - c);
 #pragma unroll
-                    for (int p = 0; p < KS; ++p) d = X::mul(LK::along(lb, 16 * q, 32 * p), a[p], d);
-                    const f4 h2 = *(const f4 *)(dec + 16 * q + 4 * lg), l2 = *(const f4 *)(dec + C + 16 * q + 4 * lg);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float x = d[j] * (r.out * r.upd) * __builtin_amdgcn_exp2f((hi - h2[j]) + (lo - l2[j]));
-                        w[q][j] = q < t || 4 * lg + j <= li ? x : 0.f;
-                        if constexpr (X::SCALE) m = fmaxf(m, fabsf(w[q][j]));
-                        if (q == t) {
-                            own[j] = 4 * lg + j == li ? w[q][j] : 0.f;
-                            if (dot) w[q][j] -= own[j];
-                        }
-                    }
-                }
-                int we = 0;
-                if constexpr (X::SCALE) we = near_2_14(lanes_max(m, 16));
-                const float up_w = pow2(we), down = pow2(-we), mid = into * r.out * (X::SCALE ? pow2(-se) : 1.f);
-                f4 in[NV];
-#pragma unroll
-                for (int v = 0; v < NV; ++v) in[v] = f4{0.f, 0.f, 0.f, 0.f};
-                const auto value = [&](int v, int j) { return fmaf(in[v][j], X::SCALE ? down : 1.f, acc[t][v][j] * mid); };
-                const auto add = [&](float (&x)[8], int u) {
-                    if constexpr (X::SCALE) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) x[j] *= up_w;
-                    }
-                    Frag f = X::piece(x, IO == IO_F32);
-#pragma unroll
-                    for (int v = 0; v < NV; ++v) in[v] = X::mul(cf[v][u], f, in[v]);
-                    if constexpr (IO != IO_F32) {
-                        f = X::piece(x, IO == IO_F16);
-#pragma unroll
-                        for (int v = 0; v < NV; ++v) in[v] = X::mul(cf[v][u], f, in[v]);
-                    }
-                    if constexpr (IO == IO_BF16)
-                        if (np == 3) {
-                            f = X::piece(x, true);
-#pragma unroll
-                            for (int v = 0; v < NV; ++v) in[v] = X::mul(cf[v][u], f, in[v]);
-                        }
-                };
-#pragma unroll
-                for (int u = 0; u <= t / 2; ++u) {
-                    float x[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = w[2 * u + (j >> 2)][j & 3];
-                    add(x, u);
-                }
-                const int64_t i = i0 + 16 * t + li;
-                const bool on = i < i_hi;
-                const int64_t step = b * s.N + time(on ? i : i_hi - 1);
-                if (dot) {
-                    float e = 0.f;
-                    const T *pe = (const T *)r.e.p + step * r.e.ld + h / r.e.share * r.e.dim;
-#pragma unroll
-                    for (int v = 0; v < NV; ++v) {
-                        const int c = col0 + 16 * v + 4 * lg;
-                        float y[4];
-                        ld_row<IO, 4>(pe + c, y, M - c);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) e = fmaf(y[j], value(v, j), e);
-                    }
+                    for (int j = 0; j < 4; ++j) e = fmaf(z[j], y[j], e);
                     e += __shfl_xor(e, 16);
                     e += __shfl_xor(e, 32);
                     if (lg == 0) dots[wave * C + 16 * t + li] = e;
-                    float x[8];
+                    const int cl = wave * 16 + 4 * lg;
+                    const float own = owns[16 * t + li];
+                    ld_row<IO, 4>((const T *)(lc + LM::at(16 * t + li, cl / E)) + cl % E, z);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = (j >> 2) == (t & 1) ? own[j & 3] : 0.f;
-                    add(x, t / 2);
+                    for (int j = 0; j < 4; ++j) y[j] = fmaf(own, z[j], y[j]);
                 }
+                if constexpr (WHOLE) {
+                    if (IO == IO_F32 || wide) {
+                        const f4 v = {y[0], y[1], y[2], y[3]};
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, v), wo, vo + rows_at(16 * t, ldo, cnt, 4), 0, 0);
+                    } else {
+                        uint16_t v[4];
 #pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    const int c = col0 + 16 * v + 4 * lg, left = on ? M - c : 0;
-                    float y[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) y[j] = value(v, j);
-                    const int64_t at = (step * s.H + h) * M + c;
-                    if (r.wide) st_row<IO_F32, 4>((float *)r.o + at, y, left);
-                    else st_row<IO, 4>((T *)r.o + at, y, left);
+                        for (int j = 0; j < 4; ++j) v[j] = __builtin_bit_cast(uint16_t, from_f<IO == IO_F32 ? IO_F16 : IO>(y[j]));
+                        __builtin_amdgcn_raw_buffer_store_b64(u2{v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16}, wo,
+                                                              vo + rows_at(16 * t, ldo, cnt, 2), 0, 0);
+                    }
+                } else {
+                    const int64_t first = row0 * ldo + h * M;
+                    const uint32_t to = row * (uint32_t)ldo + c;
+                    if (wide) st_row<IO_F32, 4>((float *)o + first + to, y, j0 < cnt ? M - c : 0);
+                    else st_row<IO, 4>((T *)o + first + to, y, j0 < cnt ? M - c : 0);
                 }
             }
         }
         // the state: decayed, and the chunk's products added
         const float f1 = dec[4 * C], f2 = dec[4 * C + 1];
-        Frag x[NV][NU][X::UPD];
-        float down[NV];
+        Frag x[NU][X::UPD];
+        float w[NU][8], m = 0.f, down = 1.f;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            float w[NU][8], m = 0.f;
+        for (int u = 0; u < NU; ++u)
 #pragma unroll
-            for (int u = 0; u < NU; ++u)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const f4 d = *(const f4 *)(dec + 3 * C + 32 * u + 16 * q + 4 * lg);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        w[u][4 * q + j] = X::get(cf[v][u], 4 * q + j) * d[j];
-                        if constexpr (X::SCALE) m = fmaxf(m, fabsf(w[u][4 * q + j]));
-                    }
-                }
-            down[v] = 1.f;
-            if constexpr (X::SCALE) {
-                const int e = near_2_14(lanes_max(m, 16));
-                down[v] = pow2(-e);
-                const float up_v = pow2(e);
-#pragma unroll
-                for (int u = 0; u < NU; ++u)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) w[u][j] *= up_v;
-            }
-#pragma unroll
-            for (int u = 0; u < NU; ++u)
-#pragma unroll
-                for (int q = 0; q < X::UPD; ++q) x[v][u][q] = X::piece(w[u], q == X::UPD - 1);
-        }
-#pragma unroll
-        for (int m = 0; m < 2 * KS; ++m) {
-            Frag k[NU];
-#pragma unroll
-            for (int u = 0; u < NU; ++u) k[u] = LK::template across<true>(lb, 32 * u, 16 * (m & ~1) + 4 * (m & 1));
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                f4 add = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int u = 0; u < NU; ++u)
-#pragma unroll
-                    for (int q = 0; q < X::UPD; ++q) add = X::mul(k[u], x[v][u][q], add);
+            for (int q = 0; q < 2; ++q) {
+                const f4 d = *(const f4 *)(dec + 3 * C + 32 * u + 16 * q + 4 * lg);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float old = st[m][v][j];
-                    st[m][v][j] = fmaf(old, f1, fmaf(old, f2, X::SCALE ? add[j] * down[v] : add[j]));
+                    w[u][4 * q + j] = X::get(cf[u], 4 * q + j) * d[j];
+                    if constexpr (X::SCALE) m = fmaxf(m, fabsf(w[u][4 * q + j]));
                 }
+            }
+        if constexpr (X::SCALE) {
+            const int e = near_2_14(lanes_max(m, 16));
+            const float up_v = pow2(e);
+            down = pow2(-e);
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[u][j] *= up_v;
+        }
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+#pragma unroll
+            for (int q = 0; q < X::UPD; ++q) x[u][q] = X::piece(w[u], q == X::UPD - 1);
+#pragma unroll
+        for (int p = 0; p < 2 * KS; ++p) {
+            f4 add = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+                const Frag k = LK::template across<true>(lb, 32 * u, 16 * (p & ~1) + 4 * (p & 1));
+#pragma unroll
+                for (int q = 0; q < X::UPD; ++q) add = X::mul(k, x[u][q], add);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float old = st[p][j];
+                st[p][j] = fmaf(old, f1, fmaf(old, f2, X::SCALE ? add[j] * down : add[j]));
             }
         }
         if (dot) {
             __syncthreads();
-            if (tid < C && i0 + tid < i_hi)
-                r.dot[(tile * BH + bh) * s.N + time(i0 + tid)] = ((dots[tid] + dots[C + tid]) + dots[2 * C + tid]) + dots[3 * C + tid];
+            if (tid < cnt) {
+                float e = dots[tid];
+#pragma unroll
+                for (int q = 1; q < WV; ++q) e += dots[q * C + tid];
+                dot_to[(tile * BH + bh) * s.N + (row0 - b * s.N) + at(tid, cnt)] = e;
+            }
         }
     }
-    const auto put = [&](float *to) {
+    int rows = K;
+    asm volatile("" : "+s"(rows));  // (else the choices made for the state that entered are kept for this one)
+    const auto put = [&](float *to) INLINE {
 #pragma unroll
         for (int m = 0; m < 2 * KS; ++m)
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int k = 16 * (m & ~1) + 8 * lg + 4 * (m & 1) + j, c = col0 + 16 * v + li;
-                    if (k < K && c < M) to[(int64_t)k * r.rs + (int64_t)c * r.cs] = st[m][v][j];
-                }
+            for (int j = 0; j < 4; ++j) {
+                const int k = 16 * (m & ~1) + 8 * lg + 4 * (m & 1) + j, c = col0 + li;
+                if (k < rows && c < M) to[k * rs + c * cs] = st[m][j];
+            }
     };
     if constexpr (OUT) {
-        if (r.s1 && seg == sg.n - 1) put(r.s1 + bh * K * M);
-        for (int64_t t = std::max(n, i_lo) + wave; t < std::min(s.N, i_lo + sg.len); t += 4)  // past the row's end
+        if (s1 && seg == sg.n - 1) put(s1 + bh * K * M);
+        for (int64_t t = std::max<int64_t>(n, seg * sg.len) + wave; t < std::min<int64_t>(s.N, seg * sg.len + sg.len); t += WV)  // past the row's end
             for (int c = tile * MB + lane; c < std::min(M, (tile + 1) * MB); c += 64) {
-                const int64_t at = ((b * s.N + t) * s.H + h) * M + c;
-                if (r.wide) ((float *)r.o)[at] = 0.f;
-                else ((T *)r.o)[at] = T(0);
+                const int64_t to = (b * s.N + t) * ldo + h * M + c;
+                if (wide) ((float *)o)[to] = 0.f;
+                else ((T *)o)[to] = T(0);
             }
     } else {
         put(sg.state + slot * sg.plane);
-        if (tile == 0 && tid == 0) {
+        if (tile == 0 && wave == EW && lane == 0) {
             const double f = exp2(all);
             sg.factor[slot * 2] = (float)f;
             sg.factor[slot * 2 + 1] = (float)(f - (double)(float)f);
@@ -694,15 +749,18 @@ __global__ __launch_bounds__(256) void k_lin_step(LinStepArgs s) {
 
 int64_t up(int64_t n) { return (n + 255) & ~(int64_t)255; }
 
-// Columns of a block, from the most that a launch's states have and their rows.
-int cols_of(int K, int M) { return M > 64 && K <= 128 ? 128 : 64; }
-int tiles_of(int M, int cols) { return (M + cols - 1) / cols; }
+// Columns of a block: 16 for each of its waves.
+int cols_of(int M) { return M > 64 ? 128 : 64; }
+int tiles_of(int M) { return (M + cols_of(M) - 1) / cols_of(M); }
+
+// Blocks that the chip holds at once.
+int64_t at_once(int K, int M) { return cols_of(M) == 64 && K <= 64 ? 768 : cols_of(M) == 64 && K <= 128 ? 512 : 256; }
 
 // Segments of a row of N steps where `blocks` work on each.
 constexpr int kChunk = 64;
-Segs segs_of(int64_t N, int64_t blocks) {
+Segs segs_of(int64_t N, int64_t blocks, int64_t at_once) {
     const int64_t chunks = std::max<int64_t>(1, (N + kChunk - 1) / kChunk);
-    int64_t n = std::min(chunks, std::max<int64_t>(1, 1024 / std::max<int64_t>(1, blocks)));
+    int64_t n = std::min(chunks, std::max<int64_t>(1, at_once / std::max<int64_t>(1, blocks)));
     const int64_t per = (chunks + n - 1) / n;
     Segs g = {};
     g.len = per * kChunk;
@@ -713,41 +771,60 @@ int64_t seg_bytes(const Segs &g, int64_t BH, int roles, int64_t plane) {
     return g.n == 1 ? 0 : up(roles * g.n * BH * plane * 4) + up(roles * g.n * BH * 8);
 }
 
-template <int IO, int KP, int NV>
+template <int IO, int KP, int WV, int DO, bool WHOLE>
 hipError_t run_chunks(const Roles &r, int n, const Shape &s, const Segs &g, int tiles, hipStream_t st) {
     const int64_t BH = s.B * s.H;
     if (g.n > 1) {
-        hipError_t e = launch(k_lin_chunk<IO, KP, NV, false>, grid_of((g.n - 1) * BH * tiles, (unsigned)n), dim3(256), 0, st, r,
+        hipError_t e = launch(k_lin_chunk<IO, KP, WV, STATES, WHOLE>, grid_of((g.n - 1) * BH * tiles, (unsigned)n), dim3(WV * 64), 0, st, r,
                               s, g, tiles);
         if (e != hipSuccess) return e;
         e = launch(k_lin_enter, grid_of((BH * g.plane + 255) / 256, (unsigned)n), dim3(256), 0, st, r, g, BH);
         if (e != hipSuccess) return e;
     }
-    return launch(k_lin_chunk<IO, KP, NV, true>, grid_of(g.n * BH * tiles, (unsigned)n), dim3(256), 0, st, r, s, g, tiles);
+    return launch(k_lin_chunk<IO, KP, WV, DO, WHOLE>, grid_of(g.n * BH * tiles, (unsigned)n), dim3(WV * 64), 0, st, r, s, g, tiles);
+}
+
+// Whether every head is whole units of 16 bytes, and every token begins at a dword.
+template <int IO>
+bool whole(const Roles &r, int n) {
+    constexpr int e = IO == IO_F32 ? 4 : 2;
+    for (int i = 0; i < n; ++i) {
+        for (const Seq *q : {&r.r[i].a, &r.r[i].b, &r.r[i].c, &r.r[i].e})
+            if (q->dim * e % 16 != 0 || q->ld * e % 4 != 0 || reinterpret_cast<uintptr_t>(q->p) % 4 != 0) return false;
+        if (reinterpret_cast<uintptr_t>(r.r[i].o) % 4 != 0) return false;
+    }
+    return true;
 }
 
 // K, M: the most rows and columns of the roles' states; ws: seg_bytes.
-template <int IO>
+template <int IO, int DO>
 hipError_t run_roles(const Roles &r, int n, const Shape &s, int K, int M, Segs g, int64_t plane, void *ws, hipStream_t st) {
-    const int cols = cols_of(K, M), tiles = tiles_of(M, cols);
+    const int tiles = tiles_of(M);
     g.plane = plane;
     g.state = (float *)ws;
     g.factor = (float *)((char *)ws + up(n * g.n * s.B * s.H * plane * 4));
-    if (cols == 64) {
-        if (K <= 32) return run_chunks<IO, 32, 1>(r, n, s, g, tiles, st);
-        if (K <= 64) return run_chunks<IO, 64, 1>(r, n, s, g, tiles, st);
-        if (K <= 128) return run_chunks<IO, 128, 1>(r, n, s, g, tiles, st);
-        return run_chunks<IO, 256, 1>(r, n, s, g, tiles, st);
+    if (!whole<IO>(r, n)) {
+        const bool few = cols_of(M) == 64;
+        if (K <= 64) return few ? run_chunks<IO, 64, 4, DO, false>(r, n, s, g, tiles, st) : run_chunks<IO, 64, 8, DO, false>(r, n, s, g, tiles, st);
+        if (K <= 128) return few ? run_chunks<IO, 128, 4, DO, false>(r, n, s, g, tiles, st) : run_chunks<IO, 128, 8, DO, false>(r, n, s, g, tiles, st);
+        return few ? run_chunks<IO, 256, 4, DO, false>(r, n, s, g, tiles, st) : run_chunks<IO, 256, 8, DO, false>(r, n, s, g, tiles, st);
     }
-    if (K <= 64) return run_chunks<IO, 64, 2>(r, n, s, g, tiles, st);
-    return run_chunks<IO, 128, 2>(r, n, s, g, tiles, st);
+    if (cols_of(M) == 64) {
+        if (K <= 32) return run_chunks<IO, 32, 4, DO, true>(r, n, s, g, tiles, st);
+        if (K <= 64) return run_chunks<IO, 64, 4, DO, true>(r, n, s, g, tiles, st);
+        if (K <= 128) return run_chunks<IO, 128, 4, DO, true>(r, n, s, g, tiles, st);
+        return run_chunks<IO, 256, 4, DO, true>(r, n, s, g, tiles, st);
+    }
+    if (K <= 64) return run_chunks<IO, 64, 8, DO, true>(r, n, s, g, tiles, st);
+    if (K <= 128) return run_chunks<IO, 128, 8, DO, true>(r, n, s, g, tiles, st);
+    return run_chunks<IO, 256, 8, DO, true>(r, n, s, g, tiles, st);
 }
 Segs fwd_segs(int64_t B, int64_t N, int64_t H, int64_t dk, int64_t dv) {
-    return segs_of(N, B * H * tiles_of((int)dv, cols_of((int)dk, (int)dv)));
+    return segs_of(N, B * H * tiles_of((int)dv), at_once((int)dk, (int)dv));
 }
 Segs bwd_segs(int64_t B, int64_t N, int64_t H, int64_t dk, int64_t dv) {
     const int m = (int)std::max(dk, dv);
-    return segs_of(N, 3 * B * H * tiles_of(m, cols_of(m, m)));
+    return segs_of(N, 3 * B * H * tiles_of(m), at_once(m, m));
 }
 
 // The parts of the backward pass's workspace, in bytes from its start.
@@ -755,8 +832,8 @@ struct BwdSpace {
     int64_t row, col, s_end, sums, dq, dk, segs, all;
 };
 int dot_tiles(int64_t dk, int64_t dv) {
-    const int m = (int)std::max(dk, dv);
-    return tiles_of((int)dk, cols_of(m, m));
+    const int cols = cols_of((int)std::max(dk, dv));
+    return (int)((dk + cols - 1) / cols);
 }
 BwdSpace space_of(int64_t B, int64_t N, int64_t H, int64_t G, int64_t dk, int64_t dv) {
     BwdSpace w;
@@ -782,7 +859,7 @@ hipError_t fwd_io(const LinAttnArgs &a, void *y, float *x_out, void *ws, hipStre
     const Seq q = {a.q, a.ldq, share, a.dk}, k = {a.k, a.ldk, share, a.dk}, v = {a.v, a.ldv, 1, a.dv};
     Roles r = {};
     r.r[0] = {q, k, v, v, y, nullptr, a.x_in, x_out, a.dv, 1, a.scale, 1.f, 0, 0};
-    return run_roles<IO>(r, 1, shape_of(a), a.dk, a.dv, fwd_segs(a.B, a.N, a.H, a.dk, a.dv), (int64_t)a.dk * a.dv, ws, s);
+    return run_roles<IO, FORWARD>(r, 1, shape_of(a), a.dk, a.dv, fwd_segs(a.B, a.N, a.H, a.dk, a.dv), (int64_t)a.dk * a.dv, ws, s);
 }
 
 template <int IO>
@@ -801,7 +878,7 @@ hipError_t bwd_io(const LinAttnArgs &a, const void *dy_, const float *dx_out, co
     r.r[1] = {v, dy, q, k, dk, o.dg ? col : nullptr, dx_out, nullptr, 1, a.dv, 1.f, a.scale, 1, wide};
     r.r[2] = {k, q, dy, dy, o.dv, nullptr, dx_out, o.dx_in, a.dv, 1, 1.f, a.scale, 1, 0};
     const int m = std::max(a.dk, a.dv);
-    hipError_t e = a.B > 0 ? run_roles<IO>(r, 3, s, m, m, bwd_segs(a.B, a.N, a.H, a.dk, a.dv), (int64_t)a.dk * a.dv,
+    hipError_t e = a.B > 0 ? run_roles<IO, BACKWARD>(r, 3, s, m, m, bwd_segs(a.B, a.N, a.H, a.dk, a.dv), (int64_t)a.dk * a.dv,
                                            base + w.segs, st)
                            : hipSuccess;
     if (e != hipSuccess) return e;

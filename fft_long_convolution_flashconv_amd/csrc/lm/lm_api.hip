@@ -72,13 +72,13 @@ bool xent_sizes_ok(int64_t T, int64_t D, int64_t V) {
 }
 
 bool attn_sizes_ok(int64_t B, int64_t N, int64_t H, int64_t G, int64_t dk, int64_t dv) {
-    return H <= ((int64_t)1 << 28) && dk <= H3CONV_MAX_HEAD && dv <= H3CONV_MAX_HEAD && product_ok({B, H}, (int64_t)1 << 28) &&
+    return N <= ((int64_t)1 << 30) && dk <= H3CONV_MAX_HEAD && dv <= H3CONV_MAX_HEAD && H <= H3CONV_MAX_LD / (dk > dv ? dk : dv) && product_ok({B, H}, (int64_t)1 << 28) &&
            product_ok({B, N, H * (dk > dv ? dk : dv)}, kElems) && product_ok({B, H, dk, dv}, kElems);
 }
 // Elements from the first to the last of n tokens' rows, ld apart.
 int64_t extent(int64_t n, int64_t ld, int64_t row) { return n == 0 ? 0 : (n - 1) * ld + row; }
-// Rows ld apart stay within the largest tensor.
-bool ld_small(int64_t n, int64_t ld) { return product_ok({n, ld}, kElems); }
+// Rows ld apart stay within the largest tensor, and 64 of them within 32 bits.
+bool ld_small(int64_t n, int64_t ld) { return ld <= H3CONV_MAX_LD && product_ok({n, ld}, kElems); }
 
 bool norm_sizes_ok(int64_t T, int64_t D, int64_t groups) {
     return D <= H3CONV_MAX_NORM && (groups == 1 || D + groups <= H3CONV_MAX_NORM) && T <= ((int64_t)1 << 30);

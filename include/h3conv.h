@@ -428,6 +428,8 @@ h3conv_status h3conv_selective_step(const void *u, const void *dt, const float *
 
 /* Largest dimension of a head of linear attention. */
 #define H3CONV_MAX_HEAD 256
+/* Largest number of elements from one token to the next there. */
+#define H3CONV_MAX_LD (1 << 22)
 
 /*
  * Linear attention with a decay for each head: a state of dk x dv per sequence
@@ -455,8 +457,8 @@ h3conv_status h3conv_selective_step(const void *u, const void *dt, const float *
  * Products run on the matrix cores, fp32 elements on the fp32 ones; sums and
  * states are fp32, and what multiplies an input again (weights, states) keeps 22
  * bits or more where inputs have 16.
- * Supported: dk, dv <= H3CONV_MAX_HEAD, G divides H, B*H <= 2^28, and
- * B*N*H*max(dk,dv), B*H*dk*dv and B*N*ld <= 2^40; any N.
+ * Supported: dk, dv <= H3CONV_MAX_HEAD, G divides H, ld and H*max(dk,dv) <=
+ * H3CONV_MAX_LD, N <= 2^30, B*H <= 2^28, B*N*H*max(dk,dv), B*H*dk*dv and B*N*ld <= 2^40.
  */
 h3conv_status h3conv_linear_attn(const void *q, const void *k, const void *v, const float *g, const float *x_in,
                                  const int32_t *lengths, void *y, float *x_out, int64_t B, int64_t N, int64_t H,
