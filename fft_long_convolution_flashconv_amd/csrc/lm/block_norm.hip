@@ -18,6 +18,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "lm_device.h"
 #include "lm_internal.h"
@@ -26,72 +27,114 @@ namespace h3c {
 namespace {
 
 constexpr int V = 8;  // channels of one vector
-constexpr int block_waves(int W) { return W < 4 ? 4 : W; }
+constexpr int block_rows(int W) { return W == 1 ? 4 : W <= 3 ? 2 : 1; }
 
-// A vector as loaded, in whole words: elements one by one would take a register each.  Rows are whole vectors, and a
-// vector past the row's end is zeros (loaded from its start, by choice and not by a branch), or ODD, and every element
-// is loaded by itself.
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
+// A row of n elements at p.  Where rows are whole vectors at whole dwords they are read and written through a buffer
+// resource that ends with the row: a lane has one offset for all tensors, past the row it loads zeros and stores
+// nothing.  (With an address per tensor and lane the backward kernel waits for spilled addresses before every load: 215
+// us and 99 for 8192 x 2560 in bf16.)  ODD, every element is loaded by itself.
+template <int IO, bool ODD>
+struct Line {
+    using T = typename io_elem<IO>::T;
+    T *p;
+    __amdgpu_buffer_rsrc_t b;
+    int n;
+    __device__ __forceinline__ Line(const T *q, int64_t at, int n_) : p(const_cast<T *>(q) + at), n(n_) {
+        if constexpr (!ODD) b = __builtin_amdgcn_make_buffer_rsrc(p, (short)0, n * (int)sizeof(T), 0x00020000);
+    }
+};
+
+// A vector as loaded, in whole words: elements one by one would take a register each.
 template <int IO, bool ODD>
 struct Vec {
     using T = typename io_elem<IO>::T;
     static constexpr int WORDS = V * (int)sizeof(T) / 4;
     uint32_t w[WORDS];
-    __device__ __forceinline__ void load(const T *p, uint32_t c, int D) {
+    __device__ __forceinline__ void load(const Line<IO, ODD> &l, uint32_t c) {
         if constexpr (!ODD) {
-            struct __attribute__((packed, aligned(sizeof(T)))) Words { uint32_t w[WORDS]; };
-            const bool in = (int)c < D;
-            const Words r = *reinterpret_cast<const Words *>(p + (in ? c : 0u));
 #pragma unroll
-            for (int i = 0; i < WORDS; ++i) w[i] = in ? r.w[i] : 0;
+            for (int q = 0; q < WORDS / 4; ++q) {
+                const u4 r = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(l.b, (int)(c * sizeof(T)) + 16 * q, 0, 0));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[4 * q + i] = r[i];
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < WORDS; ++i) w[i] = 0;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const bool in = (int)c + i < D;
-                const T v = p[in ? c + i : 0u];
-                if constexpr (IO == IO_F32) w[i] = in ? __float_as_uint(v) : 0;
-                else w[i >> 1] |= (in ? (uint32_t)__builtin_bit_cast(uint16_t, v) : 0u) << (16 * (i & 1));
+                if ((int)c + i >= l.n) continue;
+                if constexpr (IO == IO_F32) w[i] = __float_as_uint(l.p[c + i]);
+                else w[i >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, l.p[c + i]) << (16 * (i & 1));
             }
         }
-    }
-    // From here on the words are not known to be the same: what was made of them is made again, not kept.
-    __device__ __forceinline__ void forget() {
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i) asm volatile("" : "+v"(w[i]));
     }
     __device__ __forceinline__ float operator[](int i) const {
         if constexpr (IO == IO_F32) return __uint_as_float(w[i]);
         else if constexpr (IO == IO_BF16) return __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
         else return (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i >> 1] >> (16 * (i & 1))));
     }
+    // From here on the words are not known to be the same: what was made of them is made again, not kept.
+    __device__ __forceinline__ void forget() {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) asm volatile("" : "+v"(w[i]));
+    }
 };
 template <bool ODD>
 __device__ __forceinline__ void ld_par(const float *p, uint32_t c, int D, float (&o)[V]) {
     Vec<IO_F32, ODD> v;
-    v.load(p, c, D);
+    v.load(Line<IO_F32, ODD>(p, 0, D), c);
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = v[i];
 }
 template <int IO, bool ODD>
-__device__ __forceinline__ void st_vec(typename io_elem<IO>::T *p, uint32_t c, int left, const float (&o)[V]) {
+__device__ __forceinline__ void st_vec(const Line<IO, ODD> &l, uint32_t c, const float (&o)[V]) {
     if constexpr (!ODD) {
-        if (left > 0) st_row<IO, V>(p + c, o, V);
+        using T = typename io_elem<IO>::T;
+        T e[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) e[i] = from_f<IO>(o[i]);
+#pragma unroll
+        for (int q = 0; q < V * (int)sizeof(T) / 16; ++q) {
+            u4 r;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (IO == IO_F32) r[i] = __float_as_uint(e[4 * q + i]);
+                else r[i] = __builtin_bit_cast(uint16_t, e[2 * i]) | (uint32_t)__builtin_bit_cast(uint16_t, e[2 * i + 1]) << 16;
+            }
+            __builtin_amdgcn_raw_buffer_store_b128(r, l.b, (int)(c * sizeof(T)) + 16 * q, 0, 0);
+        }
     } else {
-        st_row<IO, V>(p + c, o, left);
+        st_row<IO, V>(l.p + c, o, l.n - (int)c);
     }
 }
 
-// Sum over segments of `n` consecutive lanes, n a power of two up to 64; every lane gets its segment's.
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+// Sum over segments of `n` consecutive lanes, n a power of two up to 64; every lane gets its segment's.  Within 16
+// lanes by DPP (neighbours, pairs, halves, halves of eight), which waits for no LDS.
 __device__ __forceinline__ float seg_sum(float v, int n) {
-    for (int d = 1; d < n; d <<= 1) v += __shfl_xor(v, d);
+    if (n >= 2) v = add_dpp<0xb1>(v);
+    if (n >= 4) v = add_dpp<0x4e>(v);
+    if (n >= 8) v = add_dpp<0x141>(v);
+    if (n >= 16) v = add_dpp<0x140>(v);
+    if (n == 32) v += __shfl_xor(v, 16);
+    if (n == 64) {
+        const int i = __float_as_int(v);
+        v = (__int_as_float(__builtin_amdgcn_readlane(i, 0)) + __int_as_float(__builtin_amdgcn_readlane(i, 16))) +
+            (__int_as_float(__builtin_amdgcn_readlane(i, 32)) + __int_as_float(__builtin_amdgcn_readlane(i, 48)));
+    }
     return v;
 }
 
-// The threads of a row: W waves of a block of four, or of W if they are more.
+// The threads of a row: W waves of a block of one, two or four rows.
 template <int W>
 struct Row {
-    static constexpr int kRows = block_waves(W) / W, kLanes = 64 * W, kThreads = block_waves(W) * 64;
+    static constexpr int kRows = block_rows(W), kLanes = 64 * W, kThreads = kRows * kLanes;
     int sub, lane;  // the row among the block's, the thread among the row's
     // (the same in a wave: its rows' addresses are scalar)
     __device__ __forceinline__ Row() : sub(__builtin_amdgcn_readfirstlane((int)threadIdx.x / kLanes)), lane((int)threadIdx.x % kLanes) {}
@@ -182,10 +225,10 @@ struct Ptr {
 };
 
 template <int IO, int W, int NV, bool ODD, bool BWD>
-__global__ __launch_bounds__(Row<W>::kThreads, ODD || W == 8 ? 2 : BWD ? 5 - NV : 4) void k_block_norm(Ptr<IO> p, int64_t T_, int D, Groups g, float eps) {
+__global__ __launch_bounds__(Row<W>::kThreads, ODD || W * NV >= 16 ? 2 : BWD && IO == IO_F32 ? 3 : 4) void k_block_norm(Ptr<IO> p, int64_t T_, int D, Groups g, float eps) {
     using R = Row<W>;
     extern __shared__ float wide[];
-    __shared__ float small[4][block_waves(W)];
+    __shared__ float small[4][R::kRows * W];
     const R row;
     const float invD = 1.f / (float)D;
     const bool out_norm = p.w_out != nullptr, in_norm = p.w_in != nullptr;
@@ -202,16 +245,17 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W == 8 ? 2 : BWD ? 5 - NV 
         if constexpr (BWD) asm volatile("" ::: "memory");
         const bool on = t0 + row.sub < T_;
         const int64_t at = (on ? t0 + row.sub : T_ - 1) * D;
+        const int n = on ? D : 0;
         Vec<IO, ODD> f[NV], res[NV], z[NV], dr[BWD ? NV : 1], dy[BWD ? NV : 1];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const uint32_t c = (j * R::kLanes + row.lane) * V;
-            f[j].load(p.f + at, c, D);
-            if (p.res) res[j].load(p.res + at, c, D);
-            if (p.z) z[j].load(p.z + at, c, D);
+            f[j].load(Line<IO, ODD>(p.f, at, n), c);
+            if (p.res) res[j].load(Line<IO, ODD>(p.res, at, n), c);
+            if (p.z) z[j].load(Line<IO, ODD>(p.z, at, n), c);
             if constexpr (BWD) {
-                if (p.dr) dr[j].load(p.dr + at, c, D);
-                if (p.dy) dy[j].load(p.dy + at, c, D);
+                if (p.dr) dr[j].load(Line<IO, ODD>(p.dr, at, n), c);
+                if (p.dy) dy[j].load(Line<IO, ODD>(p.dy, at, n), c);
             }
         }
         float ra[NV][ODD ? V : 1];
@@ -224,20 +268,20 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W == 8 ? 2 : BWD ? 5 - NV 
                 for (int i = 0; i < (ODD ? V : 1); ++i) ra[j][i] = __builtin_amdgcn_rsqf(fmaf(ra[j][i], g.inv, eps));
         }
         // m and r of one vector
-        const auto middle = [&](int j, float (&m)[V], float (&r)[V], float (&n)[V], float (&sg)[V]) {
+        const auto middle = [&](int j, float (&m)[V], float (&r)[V], float (&nf)[V], float (&sg)[V]) {
             const uint32_t c = (j * R::kLanes + row.lane) * V;
 #pragma unroll
-            for (int i = 0; i < V; ++i) n[i] = f[j][i];
+            for (int i = 0; i < V; ++i) nf[i] = f[j][i];
             if (out_norm) {
                 float w[V];
                 ld_par<ODD>(p.w_out, c, D, w);
 #pragma unroll
-                for (int i = 0; i < V; ++i) n[i] *= ra_of(j, i) * w[i];
+                for (int i = 0; i < V; ++i) nf[i] *= ra_of(j, i) * w[i];
             }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 sg[i] = p.z ? sigmoid(z[j][i]) : 1.f;
-                m[i] = p.z ? n[i] * z[j][i] * sg[i] : n[i];
+                m[i] = p.z ? nf[i] * z[j][i] * sg[i] : nf[i];
                 r[i] = m[i];
             }
             if (p.scale) {
@@ -251,11 +295,11 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W == 8 ? 2 : BWD ? 5 - NV 
                 for (int i = 0; i < V; ++i) r[i] += res[j][i];
             }
         };
-        float m[V], r[NV][V], n[V], sg[V], rb = 0.f, c1 = 0.f;
+        float m[V], r[NV][V], nf[V], sg[V], rb = 0.f, c1 = 0.f;
         float ss = 0.f, er = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            middle(j, m, r[j], n, sg);
+            middle(j, m, r[j], nf, sg);
             if (in_norm) {
                 float w[V];
                 if constexpr (BWD)
@@ -277,14 +321,13 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W == 8 ? 2 : BWD ? 5 - NV 
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const uint32_t c = (j * R::kLanes + row.lane) * V;
-                const int left = on ? D - (int)c : 0;
-                st_vec<IO, ODD>(p.r + at, c, left, r[j]);
+                st_vec<IO, ODD>(Line<IO, ODD>(p.r, at, n), c, r[j]);
                 if (in_norm) {
                     float w[V], o[V];
                     ld_par<ODD>(p.w_in, c, D, w);
 #pragma unroll
                     for (int i = 0; i < V; ++i) o[i] = r[j][i] * rb * w[i];
-                    st_vec<IO, ODD>(p.y + at, c, left, o);
+                    st_vec<IO, ODD>(Line<IO, ODD>(p.y, at, n), c, o);
                 }
             }
         } else {
@@ -297,9 +340,8 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W == 8 ? 2 : BWD ? 5 - NV 
                 if (p.z) z[j].forget();
                 if (p.dy) dy[j].forget();
                 const uint32_t c = (j * R::kLanes + row.lane) * V;
-                const int left = on ? D - (int)c : 0;
                 float t[V];
-                middle(j, m, r[j], n, sg);
+                middle(j, m, r[j], nf, sg);
 #pragma unroll
                 for (int i = 0; i < V; ++i) t[i] = p.dr ? dr[j][i] : 0.f;
                 if (in_norm && p.dy) {
@@ -312,7 +354,7 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W == 8 ? 2 : BWD ? 5 - NV 
                         if (on) ai[j][i] = fmaf(dy[j][i], rh, ai[j][i]);
                     }
                 }
-                if (p.dres) st_vec<IO, ODD>(p.dres + at, c, left, t);
+                if (p.dres) st_vec<IO, ODD>(Line<IO, ODD>(p.dres, at, n), c, t);
                 if (p.scale) {
                     float s[V];
                     ld_par<ODD>(p.scale, c, D, s);
@@ -327,10 +369,10 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W == 8 ? 2 : BWD ? 5 - NV 
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         const float zz = z[j][i];
-                        dz[i] = t[i] * n[i] * sg[i] * fmaf(zz, 1.f - sg[i], 1.f);
+                        dz[i] = t[i] * nf[i] * sg[i] * fmaf(zz, 1.f - sg[i], 1.f);
                         t[i] *= zz * sg[i];
                     }
-                    st_vec<IO, ODD>(p.dz + at, c, left, dz);
+                    st_vec<IO, ODD>(Line<IO, ODD>(p.dz, at, n), c, dz);
                 }
                 if (out_norm) {
                     float w[V];
@@ -341,7 +383,7 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W == 8 ? 2 : BWD ? 5 - NV 
                         dn[j][i] = t[i] * w[i];
                     }
                 } else {
-                    st_vec<IO, ODD>(p.df + at, c, left, t);
+                    st_vec<IO, ODD>(Line<IO, ODD>(p.df, at, n), c, t);
                 }
             }
             if (out_norm) {
@@ -350,12 +392,11 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W == 8 ? 2 : BWD ? 5 - NV 
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
                     const uint32_t c = (j * R::kLanes + row.lane) * V;
-                const int left = on ? D - (int)c : 0;
                     float o[V];
 #pragma unroll
                     for (int i = 0; i < V; ++i)
                         o[i] = ra_of(j, i) * fmaf(-f[j][i] * ra_of(j, i), c2[j][ODD ? i : 0] * g.inv, dn[j][i]);
-                    st_vec<IO, ODD>(p.df + at, c, left, o);
+                    st_vec<IO, ODD>(Line<IO, ODD>(p.df, at, n), c, o);
                 }
             }
         }
@@ -410,20 +451,23 @@ __global__ __launch_bounds__(kJoin) void k_join_parts(const float *__restrict__ 
     }
 }
 
-// Blocks whose sums of weights' gradients are joined by k_join_parts.
-constexpr int64_t kParts = 512;
+// Blocks whose sums of weights' gradients are joined by k_join_parts: as many as run at once, 16 waves per CU.
+constexpr int64_t kParts = 1024;
+int64_t parts_of(int W) { return 256 * (16 / (block_rows(W) * W)); }
 
-// Waves of a row and vectors per thread: as few waves as hold the row in three
-// vectors per thread (eight of them four).  Odd rows and groups have three shapes only.
+// Waves of a row and vectors per thread.  Forward: as few waves as hold the row in three vectors per thread (eight of
+// them four).  Backward a vector's sums, gradients and inputs take some 120 registers, so one vector per thread and as
+// many waves as that takes, up to eight.  Odd rows and groups have four shapes only.
 struct Shape {
     int W, NV;
 };
-Shape shape_of(int64_t D, bool odd) {
+Shape shape_of(int64_t D, bool odd, bool bwd) {
     const int64_t vecs = (D + V - 1) / V;
+    if (bwd && !odd) return vecs <= 512 ? Shape{(int)((vecs + 63) / 64), 1} : Shape{8, vecs <= 1024 ? 2 : 4};
     int W = 1;
     while (W < 8 && vecs > 64 * W * 3) W *= odd && W == 1 ? 4 : 2;
     const int nv = (int)((vecs + 64 * W - 1) / (64 * W));
-    return {W, W == 8 ? 4 : odd ? 3 : nv};
+    return {W, W == 8 ? 4 : odd && nv > 1 ? 3 : nv};
 }
 
 Groups groups_of(int64_t D, int64_t n) {
@@ -436,40 +480,64 @@ Groups groups_of(int64_t D, int64_t n) {
     return g;
 }
 
-bool is_odd(const BlockNormArgs &a, const Groups &g) { return a.D % V != 0 || (a.w_out && g.n > 1 && !g.lanes); }
+// Whether a call takes the kernels for odd rows: rows that are not whole vectors, groups that are not a power of two of
+// them, or a tensor that does not begin at a dword.
+bool is_odd(const BlockNormArgs &a, const Groups &g, std::initializer_list<const void *> tensors) {
+    if (a.D % V != 0 || (a.w_out && g.n > 1 && !g.lanes)) return true;
+    for (const void *p : tensors)
+        if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return true;
+    return false;
+}
 
-int64_t blocks_of(int64_t T, int rows, bool bwd) {
-    const int64_t n = (T + rows - 1) / rows;
-    return bwd ? std::min(n, kParts) : n;
+int64_t blocks_of(int64_t T, int W, bool bwd) {
+    const int64_t n = (T + block_rows(W) - 1) / block_rows(W);
+    return bwd ? std::min(n, parts_of(W)) : n;
 }
 
 template <int IO, bool BWD>
-hipError_t run(const Ptr<IO> &p, const BlockNormArgs &a, hipStream_t s) {
+hipError_t run(const Ptr<IO> &p, const BlockNormArgs &a, hipStream_t s, int &blocks) {
     const Groups g = groups_of(a.D, a.groups);
-    const bool odd = is_odd(a, g);
-    const Shape sh = shape_of(a.D, odd);
-    const int rows = block_waves(sh.W) / sh.W;
-    const int64_t n = blocks_of(a.T, rows, BWD);
+    const bool odd = is_odd(a, g, {p.f, p.res, p.z, p.dr, p.dy, p.r, p.y, p.df, p.dres, p.dz});
+    const Shape sh = shape_of(a.D, odd, BWD);
+    const int rows = block_rows(sh.W);
+    const int64_t n = blocks_of(a.T, sh.W, BWD);
+    blocks = (int)std::min<int64_t>(n, kParts);
     const size_t lds = std::max(odd && g.n > 1 ? (size_t)rows * (a.D + g.n) * 4 : 0, BWD ? (size_t)a.D * 4 : 0);
+    using std::integral_constant;
     const auto go = [&](auto w, auto nv, auto odds) {
         constexpr int W = decltype(w)::value, NV = decltype(nv)::value;
         return launch(k_block_norm<IO, W, NV, decltype(odds)::value, BWD>, grid_of(n), dim3(Row<W>::kThreads), lds, s, p, a.T,
                       (int)a.D, g, a.eps);
     };
-    using std::integral_constant;
+    const auto whole = [&](auto w, auto nv) { return go(w, nv, std::false_type{}); };
     constexpr integral_constant<int, 1> one{};
     constexpr integral_constant<int, 2> two{};
     constexpr integral_constant<int, 3> three{};
     constexpr integral_constant<int, 4> four{};
     constexpr integral_constant<int, 8> eight{};
-    constexpr std::true_type yes{};
-    constexpr std::false_type no{};
-    if (odd) return sh.W == 1 ? go(one, three, yes) : sh.W == 4 ? go(four, three, yes) : go(eight, four, yes);
-    switch (sh.W) {
-        case 1: return sh.NV == 1 ? go(one, one, no) : sh.NV == 2 ? go(one, two, no) : go(one, three, no);
-        case 2: return sh.NV == 2 ? go(two, two, no) : go(two, three, no);
-        case 4: return sh.NV == 2 ? go(four, two, no) : go(four, three, no);
-        default: return go(eight, four, no);
+    if (odd) {
+        constexpr std::true_type yes{};
+        if (sh.W == 1 && sh.NV == 1) return go(one, one, yes);
+        return sh.W == 1 ? go(one, three, yes) : sh.W == 4 ? go(four, three, yes) : go(eight, four, yes);
+    }
+    if constexpr (BWD) {
+        switch (sh.W) {
+            case 1: return whole(one, one);
+            case 2: return whole(two, one);
+            case 3: return whole(three, one);
+            case 4: return whole(four, one);
+            case 5: return whole(integral_constant<int, 5>{}, one);
+            case 6: return whole(integral_constant<int, 6>{}, one);
+            case 7: return whole(integral_constant<int, 7>{}, one);
+            default: return sh.NV == 1 ? whole(eight, one) : sh.NV == 2 ? whole(eight, two) : whole(eight, four);
+        }
+    } else {
+        switch (sh.W) {
+            case 1: return sh.NV == 1 ? whole(one, one) : sh.NV == 2 ? whole(one, two) : whole(one, three);
+            case 2: return sh.NV == 2 ? whole(two, two) : whole(two, three);
+            case 4: return sh.NV == 2 ? whole(four, two) : whole(four, three);
+            default: return whole(eight, four);
+        }
     }
 }
 
@@ -486,17 +554,19 @@ template <int IO>
 hipError_t fwd_io(const BlockNormArgs &a, void *r, void *y, hipStream_t s) {
     Ptr<IO> p = ptr_of<IO>(a);
     p.r = (typename io_elem<IO>::T *)r, p.y = (typename io_elem<IO>::T *)y;
-    return run<IO, false>(p, a, s);
+    int none;
+    return run<IO, false>(p, a, s, none);
 }
 
 template <int IO>
-hipError_t bwd_io(const BlockNormArgs &a, const void *dr, const void *dy, const BlockNormGrads &o, void *ws, hipStream_t s) {
+hipError_t bwd_io(const BlockNormArgs &a, const void *dr, const void *dy, const BlockNormGrads &o, void *ws, hipStream_t s,
+                  int &parts) {
     using T = typename io_elem<IO>::T;
     Ptr<IO> p = ptr_of<IO>(a);
     p.dr = (const T *)dr, p.dy = (const T *)dy;
     p.df = (T *)o.df, p.dres = (T *)o.dres, p.dz = (T *)o.dgate;
     p.part = (float *)ws;
-    return run<IO, true>(p, a, s);
+    return run<IO, true>(p, a, s, parts);
 }
 
 }  // namespace
@@ -513,15 +583,13 @@ hipError_t launch_block_norm(const BlockNormArgs &a, void *r, void *y, int io, h
 
 hipError_t launch_block_norm_bwd(const BlockNormArgs &a, const void *dr, const void *dy, const BlockNormGrads &o, int io,
                                  void *ws, hipStream_t s) {
+    int parts = 0;
     if (a.T > 0) {
-        hipError_t e = io == IO_F32 ? bwd_io<IO_F32>(a, dr, dy, o, ws, s)
-                     : io == IO_F16 ? bwd_io<IO_F16>(a, dr, dy, o, ws, s) : bwd_io<IO_BF16>(a, dr, dy, o, ws, s);
+        hipError_t e = io == IO_F32 ? bwd_io<IO_F32>(a, dr, dy, o, ws, s, parts)
+                     : io == IO_F16 ? bwd_io<IO_F16>(a, dr, dy, o, ws, s, parts) : bwd_io<IO_BF16>(a, dr, dy, o, ws, s, parts);
         if (e != hipSuccess) return e;
     }
     if (!o.dw_out && !o.dscale && !o.dw_in) return hipSuccess;
-    const Groups g = groups_of(a.D, a.groups);
-    const int W = shape_of(a.D, is_odd(a, g)).W;
-    const int parts = (int)blocks_of(a.T, block_waves(W) / W, true);
     return launch(k_join_parts, dim3((unsigned)((a.D + 63) / 64), 3), dim3(kJoin), 0, s, (const float *)ws, parts, (int)a.D,
                   o.dw_out, o.dscale, o.dw_in);
 }

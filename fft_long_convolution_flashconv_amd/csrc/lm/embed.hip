@@ -158,11 +158,22 @@ __device__ __forceinline__ void sort_pass(const int2 *from, int2 *to, int64_t n,
             for (int q = 0; q < kBatch; ++q) {
                 if (i0 + q * 64 >= hi) break;
                 const bool on = i0 + q * 64 + lane < hi;
-                const int d = (e[q].x >> bit) & 255;
-                const uint64_t same = same_digit(d, on);
+                const int d = (e[q].x >> bit) & 255, d0 = __builtin_amdgcn_readfirstlane(d);
+                // (one id most often where there are many entries)
+                const uint64_t all = __ballot(on);
+                const bool one = __ballot(on && d != d0) == 0;
+                if (!place) {
+                    if (one) {
+                        if (lane == 0) cnt[wave][d0] += __popcll(all);
+                    } else if (on) {
+                        atomicAdd(&cnt[wave][d], 1);
+                    }
+                    continue;
+                }
+                const uint64_t same = one ? all : same_digit(d, on);
                 const int before = lanes_before(same), have = cnt[wave][d];
                 __builtin_amdgcn_wave_barrier();
-                if (on && place) to[first[d] + have + before] = e[q];
+                if (on) to[first[d] + have + before] = e[q];
                 if (on && before == 0) cnt[wave][d] = have + __popcll(same);
                 __builtin_amdgcn_wave_barrier();
             }
@@ -267,26 +278,26 @@ __device__ __forceinline__ void sum_rows(int t, int first, int n, const typename
 template <int IO>
 __global__ __launch_bounds__(256) void k_embed_hot(const typename io_elem<IO>::T *__restrict__ dy, int64_t D, Sorted s) {
     const int64_t u = block_id() * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), p0 = u * kUnit;
-    const int64_t total = *s.total, c = (int64_t)blockIdx.y * kCols + (threadIdx.x & 63) * V;
+    const int lane = threadIdx.x & 63;
+    const int64_t total = *s.total, c = (int64_t)blockIdx.y * kCols + lane * V;
     if (p0 >= total) return;
-    const int64_t p1 = p0 + kUnit < total ? p0 + kUnit : total;
-    const int2 *e = s.done();
-    const int ida = __builtin_amdgcn_readfirstlane(e[p0].x), idb = __builtin_amdgcn_readfirstlane(e[p1 - 1].x);
+    const int many = __builtin_amdgcn_readfirstlane((int)(total - p0 < kUnit ? total - p0 : kUnit));
+    const int2 e = s.done()[p0 + (lane < many ? lane : 0)];
+    const int ida = __builtin_amdgcn_readfirstlane(e.x), idb = __builtin_amdgcn_readlane(e.x, many - 1);
+    const int2 spa = s.span[ida], spb = s.span[idb];
     for (int w = 0; w < (ida == idb ? 1 : 2); ++w) {
-        const int2 sp = s.span[w ? idb : ida];
+        const int2 sp = w ? spb : spa;
         if (sp.y - sp.x <= kUnit) continue;
-        const int64_t lo = sp.x > p0 ? sp.x : p0, hi = sp.y < p1 ? sp.y : p1;
-        const int lane = threadIdx.x & 63, n = __builtin_amdgcn_readfirstlane((int)(hi - lo));
-        const int t = lane < n ? e[lo + lane].y : 0;
+        const int lo = sp.x > p0 ? (int)(sp.x - p0) : 0, hi = sp.y < p0 + many ? (int)(sp.y - p0) : many;
         float sum[V] = {};
-        sum_rows<IO, 16>(t, 0, n, dy, D, c, sum);
+        sum_rows<IO, 16>(e.y, __builtin_amdgcn_readfirstlane(lo), __builtin_amdgcn_readfirstlane(hi - lo), dy, D, c, sum);
         st_row<IO_F32, V>(s.part + (2 * u + w) * D + c, sum, D - c);
     }
 }
 
-// A wave has kIds ids.  Their places and the first 64 of their entries are loaded together; rows of absent ids are
-// zeros at once.  The block's four waves join the sums of an id of many entries.
-constexpr int kIds = 16;
+// A wave has kIds ids and kCols columns.  Their places and the first 64 of their entries are loaded together; rows of
+// absent ids are zeros at once.  The block's four waves join the sums of an id of many entries.
+constexpr int kIds = 8;
 template <int IO>
 __global__ __launch_bounds__(256) void k_embed_rows(const typename io_elem<IO>::T *__restrict__ dy,
                                                     typename io_elem<IO>::T *__restrict__ dw, int64_t D, int64_t vocab,
@@ -294,33 +305,40 @@ __global__ __launch_bounds__(256) void k_embed_rows(const typename io_elem<IO>::
     __shared__ float lds[4][kCols];
     __shared__ int2 spans[4 * kIds];
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int64_t block0 = block_id() * 4 * kIds, id0 = block0 + wave * kIds;
+    const int64_t block0 = block_id() * 4 * kIds, id0 = block0 + wave * kIds, c = (int64_t)blockIdx.y * kCols + lane * V;
     if (block0 >= vocab) return;
     const int ids = (int)(vocab - id0 < kIds ? (vocab > id0 ? vocab - id0 : 0) : kIds);
     const int2 sp = lane < ids ? s.span[id0 + lane] : int2{0, 0};
     const int n = sp.y - sp.x;
     if (lane < kIds) spans[wave * kIds + lane] = sp;
-    // the entries of the ids of few, which stand one after another: lane l has the l-th from the first id's first
-    uint64_t some = __ballot(n > 0);
-    const int e0 = some ? __builtin_amdgcn_readlane(sp.x, __builtin_ctzll(some)) : 0, total = (int)*s.total;
-    const int t = s.done()[e0 + lane < total ? e0 + lane : 0].y;
-    for (int q = 0; q < ids; ++q) {
-        const int nq = __builtin_amdgcn_readlane(n, q), at = __builtin_amdgcn_readlane(sp.x, q) - e0;
-        if (nq > kUnit) continue;
-        int tq = t, first = at;
-        if (nq > 0 && at + nq > 64) {  // (past the 64)
-            tq = lane < nq ? s.done()[e0 + at + lane].y : 0;
-            first = 0;
-        }
-        for (int64_t c0 = 0; c0 < D; c0 += kCols) {  // (every lane: each holds an entry)
-            const int64_t c = c0 + lane * V;
+    const auto put = [&](int q, const float (&sum)[V]) {
+        float o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = sum[i] * scale;
+        st_row<IO, V>(dw + (id0 + q) * D + c, o, D - c);
+    };
+    const uint64_t some = __ballot(n > 0);
+    if (some) {
+        // the entries stand one after another: lane l has the l-th from the first id's first
+        const int e0 = __builtin_amdgcn_readlane(sp.x, __builtin_ctzll(some));
+        const int end = __builtin_amdgcn_readlane(sp.y, 63 - __builtin_clzll(some));
+        const int t = s.done()[e0 + lane < end ? e0 + lane : e0].y;
+        for (uint64_t left = some; left; left &= left - 1) {
+            const int q = __builtin_ctzll(left), nq = __builtin_amdgcn_readlane(n, q), at = __builtin_amdgcn_readlane(sp.x, q) - e0;
+            if (nq > kUnit) continue;
+            int tq = t, first = at;
+            if (at + nq > 64) {
+                tq = lane < nq ? s.done()[e0 + at + lane].y : 0;
+                first = 0;
+            }
             float sum[V] = {};
             sum_rows<IO, 4>(tq, first, nq, dy, D, c, sum);
-#pragma unroll
-            for (int i = 0; i < V; ++i) sum[i] *= scale;
-            st_row<IO, V>(dw + (id0 + q) * D + c, sum, D - c);
+            put(q, sum);
         }
     }
+    const float none[V] = {};
+    for (int q = 0; q < ids; ++q)
+        if (!((some >> q) & 1)) put(q, none);
     if (!__syncthreads_or(n > kUnit)) return;
     for (int w = 0; w < 4 * kIds; ++w) {
         const int2 x = spans[w];
@@ -328,29 +346,26 @@ __global__ __launch_bounds__(256) void k_embed_rows(const typename io_elem<IO>::
         // units first .. last; the first is the id's own only where it begins with it
         const int64_t u0 = x.x / kUnit, u1 = (x.y - 1) / kUnit + 1, per = (u1 - u0 + 3) / 4;
         const int64_t lo = u0 + wave * per, hi = lo + per < u1 ? lo + per : u1;
-        for (int64_t c0 = 0; c0 < D; c0 += kCols) {
-            const int64_t c = c0 + lane * V;
-            float sum[V] = {};
+        float sum[V] = {};
 #pragma unroll 8
-            for (int64_t u = lo; u < hi; ++u) {
-                float v[V];
-                ld_row<IO_F32, V>(s.part + (2 * u + (u == u0 && x.x % kUnit != 0 ? 1 : 0)) * D + c, v, D - c);
+        for (int64_t u = lo; u < hi; ++u) {
+            float v[V];
+            ld_row<IO_F32, V>(s.part + (2 * u + (u == u0 && x.x % kUnit != 0 ? 1 : 0)) * D + c, v, D - c);
 #pragma unroll
-                for (int i = 0; i < V; ++i) sum[i] += v[i];
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) lds[wave][lane * V + i] = sum[i];
-            __syncthreads();
-            if (wave == 0) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int k = lane * V + i;
-                    sum[i] = (((lds[0][k] + lds[1][k]) + lds[2][k]) + lds[3][k]) * scale;
-                }
-                st_row<IO, V>(dw + (block0 + w) * D + c, sum, D - c);
-            }
-            __syncthreads();
+            for (int i = 0; i < V; ++i) sum[i] += v[i];
         }
+#pragma unroll
+        for (int i = 0; i < V; ++i) lds[wave][lane * V + i] = sum[i];
+        __syncthreads();
+        if (wave == 0) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int k = lane * V + i;
+                sum[i] = (((lds[0][k] + lds[1][k]) + lds[2][k]) + lds[3][k]) * scale;
+            }
+            st_row<IO, V>(dw + (block0 + w) * D + c, sum, D - c);
+        }
+        __syncthreads();
     }
 }
 
@@ -392,7 +407,8 @@ hipError_t bwd_io(const int64_t *tok, const void *dy_, void *dw, int64_t T, int6
     if (e == hipSuccess) e = launch(k_embed_sort, dim3((unsigned)s.ranges), dim3(kSort), 0, st, s);
     if (e == hipSuccess && T > kUnit)
         e = launch(k_embed_hot<IO>, grid_of((s.units + 3) / 4, (unsigned)((D + kCols - 1) / kCols)), dim3(256), 0, st, dy, D, s);
-    if (e == hipSuccess) e = launch(k_embed_rows<IO>, grid_of((vocab + 4 * kIds - 1) / (4 * kIds)), dim3(256), 0, st, dy, (E *)dw, D, vocab, scale, s);
+    if (e == hipSuccess) e = launch(k_embed_rows<IO>, grid_of((vocab + 4 * kIds - 1) / (4 * kIds), (unsigned)((D + kCols - 1) / kCols)),
+                   dim3(256), 0, st, dy, (E *)dw, D, vocab, scale, s);
     return e;
 }
 
