@@ -232,45 +232,56 @@ __global__ __launch_bounds__(kSort) void k_embed_sort(Sorted s) {
     __syncthreads();
     for (int i = 0; i < s.passes; ++i) sort_pass(s.buf[1 + (i & 1)] + base, s.buf[2 - (i & 1)] + base, n, 8 * i, cnt, first);
     const int2 *e = s.done() + base;
-    for (int64_t i = threadIdx.x; i < n; i += kSort) {
-        const int id = e[i].x;
-        if (i == 0 || e[i - 1].x != id) s.span[id].x = (int)(base + i);
-        if (i == n - 1 || e[i + 1].x != id) s.span[id].y = (int)(base + i + 1);
+    for (int64_t i0 = threadIdx.x; i0 < n; i0 += kSort * kBatch) {
+        int id[kBatch][3];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q)
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                const int64_t i = i0 + q * kSort + k - 1;
+                id[q][k] = e[i < 0 ? 0 : i < n ? i : n - 1].x;
+            }
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int64_t i = i0 + q * kSort;
+            if (i < n && (i == 0 || id[q][0] != id[q][1])) s.span[id[q][1]].x = (int)(base + i);
+            if (i < n && (i == n - 1 || id[q][2] != id[q][1])) s.span[id[q][1]].y = (int)(base + i + 1);
+        }
     }
     if (r == s.ranges - 1 && threadIdx.x == 0) *s.total = base + n;
 }
 
-// One vector as loaded; zeros past the row.
-template <int IO>
-struct Raw {
-    Pack<typename io_elem<IO>::T, V> r;
-    __device__ __forceinline__ void load(const typename io_elem<IO>::T *p, int64_t valid) {
-        if (valid >= V) {
-            r = *reinterpret_cast<const Pack<typename io_elem<IO>::T, V> *>(p);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) r.v[i] = i < valid ? p[i] : typename io_elem<IO>::T(0);
-        }
-    }
-    __device__ __forceinline__ void add_to(float (&s)[V]) const {
-#pragma unroll
-        for (int i = 0; i < V; ++i) s[i] += to_f<IO>(r.v[i]);
-    }
-};
-
-// The sum of n rows of dy, n at most 64, in order: this lane's columns.  t: the rows, lane by lane from `first` on.
-// DEEP rows are on their way at a time.
+// The sum of n rows of dy, n at most 64, in order: this lane's columns, c to c + V - 1.  t: the rows, lane by lane from
+// `first` on.  DEEP rows are on their way at a time, their loads without branches: a vector that passes the row's end
+// is taken to end with it, and where rows are not whole vectors its lane sums its elements one by one instead.
 template <int IO, int DEEP>
 __device__ __forceinline__ void sum_rows(int t, int first, int n, const typename io_elem<IO>::T *dy, int64_t D, int64_t c,
                                          float (&sum)[V]) {
-    for (int j = 0; j < n; j += DEEP) {
-        Raw<IO> v[DEEP];
+    using T = typename io_elem<IO>::T;
+    if (D >= V) {
+        const int64_t cc = c + V <= D ? c : D - V;
+        for (int j = 0; j < n; j += DEEP) {
+            Pack<T, V> v[DEEP];
 #pragma unroll
-        for (int k = 0; k < DEEP; ++k)
-            if (j + k < n) v[k].load(dy + (int64_t)__builtin_amdgcn_readlane(t, first + j + k) * D + c, D - c);
+            for (int k = 0; k < DEEP; ++k)
+                v[k] = *reinterpret_cast<const Pack<T, V> *>(dy + (int64_t)__builtin_amdgcn_readlane(t, first + (j + k < n ? j + k : n - 1)) * D + cc);
 #pragma unroll
-        for (int k = 0; k < DEEP; ++k)
-            if (j + k < n) v[k].add_to(sum);
+            for (int k = 0; k < DEEP; ++k)
+                if (j + k < n) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sum[i] += to_f<IO>(v[k].v[i]);
+                }
+        }
+    }
+    if (D % V != 0) {
+        float one[V] = {};
+        for (int j = 0; j < n; ++j) {
+            const T *row = dy + (int64_t)__builtin_amdgcn_readlane(t, first + j) * D;
+#pragma unroll
+            for (int i = 0; i < V; ++i) one[i] += to_f<IO>(row[c + i < D ? c + i : D - 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[i] = c + V <= D ? sum[i] : one[i];
     }
 }
 
