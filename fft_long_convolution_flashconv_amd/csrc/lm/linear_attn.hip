@@ -180,6 +180,27 @@ __device__ __forceinline__ int near_2_14(float m) {
     return e < -100 ? -100 : (e > 100 ? 100 : e);
 }
 __device__ __forceinline__ float pow2(int e) { return __builtin_amdgcn_ldexpf(1.f, e); }
+// Sum over the lanes up to this one, in 64 bits: within 16 lanes and then across them by DPP.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_from(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+    return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double sum_up_to(double v) {
+    v = add_from<0x111, 0xf>(v);  // one lane before, two, four, eight
+    v = add_from<0x112, 0xf>(v);
+    v = add_from<0x114, 0xf>(v);
+    v = add_from<0x118, 0xf>(v);
+    v = add_from<0x142, 0xa>(v);  // the sixteenth's of rows 0 and 2 to rows 1 and 3
+    return add_from<0x143, 0xc>(v);  // the thirty-second's to rows 2 and 3
+}
+__device__ __forceinline__ double lane_of(double v, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 // 2^x of a 64-bit exponent, to 32 bits
 __device__ __forceinline__ float exp2_of(double x) {
     const float d = (float)x;
@@ -218,10 +239,13 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
     static_assert(C * LK::CH % TH == 0 && C * LM::CH % TH == 0 && NT <= 4, "whole units, a wave per 16 steps");
     // pieces of weights and states in the output's products (24 bits where the decays' gradients take them); fragments of weights
     constexpr int NP = IO == IO_F32 ? 1 : IO == IO_F16 || DO == FORWARD ? 2 : 3, WF = NT == 4 ? 6 : 2;
-    __shared__ __attribute__((aligned(16))) char la[OUT ? LK::kBytes : 16], lb[LK::kBytes], lc[LM::kBytes];
-    __shared__ __attribute__((aligned(16))) float decays[2][4 * C + 4];  // of a chunk [hi, lo, into, upd][C] and its factor in two parts
+    // Two places for tiles where the LDS has room for them without giving up a block: a chunk's are then written while
+    // the last one's are still read.
+    constexpr int TWO = OUT && WV == 8 && KP <= 128 ? 2 : 1;
+    __shared__ __attribute__((aligned(16))) char tile_a[OUT ? TWO * LK::kBytes : 16], tile_b[TWO * LK::kBytes], tile_c[TWO * LM::kBytes];
+    __shared__ __attribute__((aligned(16))) float decays[2][4 * C + 4];  // of a chunk [hi, lo, into, upd][C] and its factor
     __shared__ Frag weights[OUT ? WF * NP * 64 : 1];                     // [fragment][piece][lane]
-    __shared__ float owns[OUT ? C : 1], downs[OUT ? C : 1];              // a step's weight of itself, what its weights were scaled by
+    __shared__ float owns[OUT ? C : 1], downs[OUT ? NU * C : 1];         // a step's weight of itself, what its weights of 32 steps were scaled by
     __shared__ float dots[OUT ? WV * C : 1];                             // [wave][C]
     // (read once: the compiler keeps a struct of a launch's arguments that varies by block in memory)
     const Role *role = &roles.r[blockIdx.y];
@@ -328,7 +352,7 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
         return g;
     };
     double all = 0.0;  // (of wave EW) the segment's decay, as an exponent of two
-    const auto keep = [&]() INLINE {
+    const auto keep = [&](char *la, char *lb, char *lc) INLINE {
 #pragma unroll
         for (int q = 0; q < NA; ++q) {
             const int u = q * TH + tid;
@@ -342,16 +366,12 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
         }
     };
     // (wave EW) Exponents of two from the chunk's start on, in 64 bits: with the step's own decay where time runs
-    // on, without it where it runs back.
+    // on, without it where it runs back.  The state is multiplied by the chunk's factor in 32 bits, and what that loses
+    // is given to the next chunk's: the product of all stays within one rounding of what it should be.
+    double lost = 1.0;
     const auto exponents = [&](float *dec, float g) INLINE {
         const double own = (double)fmaxf(g, kLeast) * 1.4426950408889634;
-        double sum = own;
-#pragma unroll
-        for (int d = 1; d < C; d <<= 1) {
-            const double u = __shfl_up(sum, d);
-            if (lane >= d) sum += u;
-        }
-        const double total = __shfl(sum, C - 1), e = back ? sum - own : sum;
+        const double sum = sum_up_to(own), total = lane_of(sum, C - 1), e = back ? sum - own : sum;
         all += total;
         if (lane < C) {
             const float hi = (float)e;
@@ -360,11 +380,20 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
             dec[2 * C + lane] = exp2_of(e);
             dec[3 * C + lane] = exp2_of(total - e) * upd;
         }
-        if (lane == 0) {
-            const double f = exp2(total);
-            dec[4 * C] = (float)f;
-            dec[4 * C + 1] = (float)(f - (double)(float)f);
-        }
+        const double f = exp2(total) * lost;
+        const float f1 = (float)f;
+        lost = f1 > 1e-30f ? 1.0 + (double)((float)(f - (double)f1) * __builtin_amdgcn_rcpf(f1)) : 1.0;
+        if (lane == 0) dec[4 * C] = f1;
+    };
+
+    // the dot products of the chunk of i0
+    const auto put_dots = [&](int i0) INLINE {
+        const int cnt = count(i0);
+        if (tid >= cnt) return;
+        float e = dots[tid];
+#pragma unroll
+        for (int q = 1; q < WV; ++q) e += dots[q * C + tid];
+        dot_to[(tile * BH + bh) * s.N + (low(i0, cnt) - b * s.N) + at(tid, cnt)] = e;
     };
 
     int turn = 0;
@@ -377,60 +406,61 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
     }
     for (int i0 = i_lo; i0 < i_hi; i0 += C, turn ^= 1) {
         const float *dec = decays[turn];
+        const int place = TWO == 2 ? turn : 0;
+        char *la = tile_a + place * LK::kBytes, *lb = tile_b + place * LK::kBytes, *lc = tile_c + place * LM::kBytes;
         const int cnt = count(i0);
         const int64_t row0 = low(i0, cnt);
-        __syncthreads();  // (the last chunk has been read)
-        keep();
+        if constexpr (TWO == 1) __syncthreads();  // (the last chunk has been read)
+        keep(la, lb, lc);
         __syncthreads();
-        if constexpr (!OUT)
-            if (i0 + C < i_hi) load(i0 + C);
+        if (dot && i0 > i_lo) put_dots(i0 - C);
+        if (i0 + C < i_hi) load(i0 + C);
         if constexpr (OUT) {
-            // the chunk's weights, once for all columns: 16 steps t by a wave, transposed, as they are operands
-            if (wave < NT) {
-                const int t = wave;
+            // the chunk's weights, once for all columns: of 16 steps t and 32 steps u by a wave (or of all u, where waves are
+            // few), transposed, as they are operands
+            constexpr int SPLIT = WV == 8 ? NU : 1;
+            if (wave < NT * SPLIT && 2 * (wave % SPLIT) <= wave / SPLIT) {
+                const int t = wave / SPLIT;
                 Frag a[KS];
 #pragma unroll
                 for (int p = 0; p < KS; ++p) a[p] = LK::along(la, 16 * t, 32 * p);
                 const float hi = dec[16 * t + li], lo = dec[C + 16 * t + li];
-                float w[NT][4];  // of steps 16 q + 4 g + j
-                float m = 0.f, own = 0.f;
 #pragma unroll
-                for (int q = 0; q < NT; ++q) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) w[q][j] = 0.f;
-                    if (q > t) continue;
-                    f4 d = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int p = 0; p < KS; ++p) d = X::mul(LK::along(lb, 16 * q, 32 * p), a[p], d);
-                    const f4 h2 = *(const f4 *)(dec + 16 * q + 4 * lg), l2 = *(const f4 *)(dec + C + 16 * q + 4 * lg);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float x = d[j] * (out * upd) * __builtin_amdgcn_exp2f((hi - h2[j]) + (lo - l2[j]));
-                        w[q][j] = q < t || 4 * lg + j <= li ? x : 0.f;
-                        if (dot && q == t && 4 * lg + j == li) {
-                            own = x;
-                            w[q][j] = 0.f;
-                        }
-                        if constexpr (X::SCALE) m = fmaxf(m, fabsf(w[q][j]));
-                    }
-                }
-                if (dot && (li >> 2) == lg) owns[16 * t + li] = own;
-                float up_w = 1.f;
-                if constexpr (X::SCALE) {
-                    const int e = near_2_14(lanes_max(m, 16));
-                    up_w = pow2(e);
-                    if (lg == 0) downs[16 * t + li] = pow2(-e);
-                }
-#pragma unroll
-                for (int u = 0; u < NU; ++u) {
+                for (int v = 0; v < NU / SPLIT; ++v) {
+                    const int u = SPLIT > 1 ? wave % SPLIT : v;
                     if (2 * u > t) continue;
-                    float x[8];
+                    float x[8], m = 0.f, own = 0.f;  // of steps 32 u + 16 q + 4 g + j
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = X::SCALE ? w[2 * u + (j >> 2)][j & 3] * up_w : w[2 * u + (j >> 2)][j & 3];
+                    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[4 * q + j] = 0.f;
+                        if (2 * u + q > t) continue;
+                        f4 d = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int p = 0; p < KS; ++p) d = X::mul(LK::along(lb, 32 * u + 16 * q, 32 * p), a[p], d);
+                        const float *from = dec + 32 * u + 16 * q + 4 * lg;
+                        const f4 h2 = *(const f4 *)from, l2 = *(const f4 *)(from + C);
+                        const bool edge = 2 * u + q == t;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float w = d[j] * (out * upd) * __builtin_amdgcn_exp2f((hi - h2[j]) + (lo - l2[j]));
+                            const bool self = edge && 4 * lg + j == li;
+                            x[4 * q + j] = (edge && 4 * lg + j > li) || (dot && self) ? 0.f : w;
+                            if (dot && self) own = w;
+                            if constexpr (X::SCALE) m = fmaxf(m, fabsf(x[4 * q + j]));
+                        }
+                    }
+                    if (dot && 2 * u <= t && t <= 2 * u + 1 && (li >> 2) == lg) owns[16 * t + li] = own;
+                    if constexpr (X::SCALE) {
+                        const int e = near_2_14(lanes_max(m, 16));
+                        const float up_w = pow2(e);
+                        if (lg == 0) downs[u * C + 16 * t + li] = pow2(-e);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] *= up_w;
+                    }
                     Frag *to = weights + (t < 2 ? t : 2 * t - 2 + u) * NP * 64 + lane;
 #pragma unroll
-                    for (int q = 0; q < NP; ++q)
-                        to[q * 64] = X::piece(x, q == NP - 1);
+                    for (int q = 0; q < NP; ++q) to[q * 64] = X::piece(x, q == NP - 1);
                 }
             }
         }
@@ -441,12 +471,12 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
         Frag cf[NU];
 #pragma unroll
         for (int u = 0; u < NU; ++u) cf[u] = LM::template across<false>(lc, 32 * u, wave * 16);
+        f4 acc[OUT ? NT : 1];
+        int se = 0;
         if constexpr (OUT) {
-            f4 acc[NT];
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[t] = f4{0.f, 0.f, 0.f, 0.f};
             // the state's part: o^T = X^T a^T, the pieces of X straight from the accumulators
-            int se = 0;
             if constexpr (X::SCALE) {
                 float m = 0.f;
 #pragma unroll
@@ -465,35 +495,97 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
 #pragma unroll
                 for (int q = 0; q < NP; ++q)
                     x[q] = X::piece(w, q == NP - 1);
+                Frag a[NT];  // (products in chains side by side: one waits for the last of its own chain)
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const Frag a = LK::along(la, 16 * t, 32 * p);
+                for (int t = 0; t < NT; ++t) a[t] = LK::along(la, 16 * t, 32 * p);
 #pragma unroll
-                    for (int q = 0; q < NP; ++q)
-                        acc[t] = X::mul(x[q], a, acc[t]);
+                for (int q = 0; q < NP; ++q)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) acc[t] = X::mul(x[q], a[t], acc[t]);
+            }
+        }
+        // the state: decayed, and the chunk's products added
+        const float factor = dec[4 * C];
+        Frag x[NU][X::UPD];
+        float w[NU][8], m = 0.f, down = 1.f;
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const f4 d = *(const f4 *)(dec + 3 * C + 32 * u + 16 * q + 4 * lg);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    w[u][4 * q + j] = X::get(cf[u], 4 * q + j) * d[j];
+                    if constexpr (X::SCALE) m = fmaxf(m, fabsf(w[u][4 * q + j]));
                 }
             }
-            if (i0 + C < i_hi) load(i0 + C);  // (here and not before: 24 registers for a part of the chunk only)
+        if constexpr (X::SCALE) {
+            const int e = near_2_14(lanes_max(m, 16));
+            const float up_v = pow2(e);
+            down = pow2(-e);
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[u][j] *= up_v;
+        }
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+#pragma unroll
+            for (int q = 0; q < X::UPD; ++q) x[u][q] = X::piece(w[u], q == X::UPD - 1);
+#pragma unroll
+        for (int p = 0; p < KS; ++p) {
+            f4 add[2] = {f4{0.f, 0.f, 0.f, 0.f}, f4{0.f, 0.f, 0.f, 0.f}};
+            Frag k[2][NU];
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) k[i][u] = LK::template across<true>(lb, 32 * u, 32 * p + 4 * i);
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+                for (int q = 0; q < X::UPD; ++q)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) add[i] = X::mul(k[i][u], x[u][q], add[i]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    st[2 * p + i][j] = fmaf(st[2 * p + i][j], factor, X::SCALE ? add[i][j] * down : add[i][j]);
+        }
+        if constexpr (OUT) {
             __syncthreads();  // (the weights are there)
             // the chunk's own part, 16 steps at a time
             const int eo = wide ? 4 : EB;
             const __amdgpu_buffer_rsrc_t wo = window((char *)o + (row0 * ldo + h * M) * eo, ldo, M, cnt, eo);
             const int vo = lane_at(li, ldo, col0 + 4 * lg, M, eo);
+            f4 in[NT][X::SCALE ? NU : 1];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int u = 0; u < (X::SCALE ? NU : 1); ++u) in[t][u] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+                for (int q = 0; q < NP; ++q)
+#pragma unroll
+                    for (int t = 2 * u; t < NT; ++t)
+                        in[t][X::SCALE ? u : 0] = X::mul(cf[u], weights[((t < 2 ? t : 2 * t - 2 + u) * NP + q) * 64 + lane],
+                                                         in[t][X::SCALE ? u : 0]);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const float mid = dec[2 * C + 16 * t + li] * out * (X::SCALE ? pow2(-se) : 1.f);
-                const float down = X::SCALE ? downs[16 * t + li] : 1.f;
-                f4 in = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int u = 0; u <= t / 2; ++u)
-#pragma unroll
-                    for (int q = 0; q < NP; ++q)
-                        in = X::mul(cf[u], weights[((t < 2 ? t : 2 * t - 2 + u) * NP + q) * 64 + lane], in);
-                const int j0 = 16 * t + li, c = col0 + 4 * lg;
-                const uint32_t row = (uint32_t)at(j0, cnt);
                 float y[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = fmaf(in[j], down, acc[t][j] * mid);
+                for (int j = 0; j < 4; ++j) y[j] = acc[t][j] * mid;
+#pragma unroll
+                for (int u = 0; u < (X::SCALE ? NU : 1); ++u) {
+                    if (2 * u > t) continue;
+                    const float down = X::SCALE ? downs[u * C + 16 * t + li] : 1.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[j] = fmaf(in[t][u][j], down, y[j]);
+                }
+                const int j0 = 16 * t + li, c = col0 + 4 * lg;
+                const uint32_t row = (uint32_t)at(j0, cnt);
                 if (dot) {  // and then the step's own product
                     float z[4], e = 0.f;
                     ld_row<IO, 4>(pe + row0 * lde + (row * (uint32_t)lde + c), z, M - c);
@@ -527,58 +619,10 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
                 }
             }
         }
-        // the state: decayed, and the chunk's products added
-        const float f1 = dec[4 * C], f2 = dec[4 * C + 1];
-        Frag x[NU][X::UPD];
-        float w[NU][8], m = 0.f, down = 1.f;
-#pragma unroll
-        for (int u = 0; u < NU; ++u)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const f4 d = *(const f4 *)(dec + 3 * C + 32 * u + 16 * q + 4 * lg);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    w[u][4 * q + j] = X::get(cf[u], 4 * q + j) * d[j];
-                    if constexpr (X::SCALE) m = fmaxf(m, fabsf(w[u][4 * q + j]));
-                }
-            }
-        if constexpr (X::SCALE) {
-            const int e = near_2_14(lanes_max(m, 16));
-            const float up_v = pow2(e);
-            down = pow2(-e);
-#pragma unroll
-            for (int u = 0; u < NU; ++u)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[u][j] *= up_v;
-        }
-#pragma unroll
-        for (int u = 0; u < NU; ++u)
-#pragma unroll
-            for (int q = 0; q < X::UPD; ++q) x[u][q] = X::piece(w[u], q == X::UPD - 1);
-#pragma unroll
-        for (int p = 0; p < 2 * KS; ++p) {
-            f4 add = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                const Frag k = LK::template across<true>(lb, 32 * u, 16 * (p & ~1) + 4 * (p & 1));
-#pragma unroll
-                for (int q = 0; q < X::UPD; ++q) add = X::mul(k, x[u][q], add);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float old = st[p][j];
-                st[p][j] = fmaf(old, f1, fmaf(old, f2, X::SCALE ? add[j] * down : add[j]));
-            }
-        }
-        if (dot) {
-            __syncthreads();
-            if (tid < cnt) {
-                float e = dots[tid];
-#pragma unroll
-                for (int q = 1; q < WV; ++q) e += dots[q * C + tid];
-                dot_to[(tile * BH + bh) * s.N + (row0 - b * s.N) + at(tid, cnt)] = e;
-            }
-        }
+    }
+    if (dot && i_lo < i_hi) {
+        __syncthreads();
+        put_dots(i_lo + (i_hi - i_lo - 1) / C * C);
     }
     int rows = K;
     asm volatile("" : "+s"(rows));  // (else the choices made for the state that entered are kept for this one)
