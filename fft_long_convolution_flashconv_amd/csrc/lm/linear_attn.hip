@@ -69,7 +69,7 @@ typedef int i2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) s4 lds_s4;
 
 // What a type's products need.  An operand fragment is 8 values of k per lane,
-// k = 8 (lane >> 4) + j of 32, of the row (column) lane & 15.
+// of the row (column) lane & 15; which of 32 they are is up to both operands alike.
 template <int IO>
 struct Mx {  // 16-bit elements
     static constexpr int C = 64;                       // steps of a chunk
@@ -126,43 +126,57 @@ struct Mx<IO_F32> {
     }
 };
 
-// A tile of steps in LDS, rows of COLS elements and 16 bytes: 16 lanes that read a unit of 16 consecutive rows
-// each, or the four-row blocks of a transposed read, then meet all banks, and every address is one of the lane plus a
-// constant.
-template <int IO, int COLS>
+// A tile of steps in LDS, rows of COLS elements and PAD bytes.  With 32 bytes of padding the reads across 8 rows, of 8
+// bytes per lane, meet every bank once.  A tile that is only read along its rows (TURNED, 16-bit) has the halves of its
+// units where a fragment wants them side by side, so that this is a read of 16 bytes, for which 16 bytes of padding do
+// the same.  Every address is one of the lane plus a constant.
+template <int IO, int COLS, int PAD, bool TURNED>
 struct Lds {
     using T = typename io_elem<IO>::T;
-    static constexpr int E = 16 / (int)sizeof(T), CH = COLS / E, ROWS = Mx<IO>::C, STRIDE = (CH + 1) * 16, kBytes = ROWS * STRIDE;
+    static constexpr int E = 16 / (int)sizeof(T), CH = COLS / E, ROWS = Mx<IO>::C, STRIDE = CH * 16 + PAD, kBytes = ROWS * STRIDE;
     using Frag = typename Mx<IO>::Frag;
     __device__ __forceinline__ static int at(int row, int chunk) { return row * STRIDE + chunk * 16; }
-    // the row `row` + lane & 15, its 32 elements from k on, 8 of them per lane
-    __device__ __forceinline__ static Frag along(const char *p, int row, int k) {
-        const int i = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
-        Frag f;
-        if constexpr (IO != IO_F32) {
-            f.v = *(const u4 *)(p + at(i, g) + at(row, k / E));
+    // the unit `chunk` of a row to its place
+    __device__ __forceinline__ static void keep(char *p, int row, int chunk, u4 v) {
+        if constexpr (TURNED) {  // elements 8 q + 4 h of 32: group 2 q + h (mod 4), its first half below 16
+            char *to = p + at(row, (chunk & ~3) + 2 * (chunk & 1)) + 8 * ((chunk >> 1) & 1);
+            *(u2 *)to = u2{v.x, v.y};
+            *(u2 *)(to + 16) = u2{v.z, v.w};
         } else {
-            const f4 a = *(const f4 *)(p + at(i, 2 * g) + at(row, k / E)), b = *(const f4 *)(p + at(i, 2 * g) + at(row, k / E + 1));
+            *(u4 *)(p + at(row, chunk)) = v;
+        }
+    }
+    // 32 elements of k of a row per lane & 15: k + 4 g + j and k + 16 + 4 g + j, the order in which accumulators hold rows
+    __device__ __forceinline__ static Frag along(const char *p, int row, int k) {
+        constexpr int B = (int)sizeof(T);
+        const int i = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
+        const char *mine = p + at(i, 0) + 4 * g * B + at(row, 0) + k * B;
+        Frag f;
+        if constexpr (TURNED) {
+            f.v = *(const u4 *)(mine + 4 * g * B);
+        } else if constexpr (IO != IO_F32) {
+            const u2 a = *(const u2 *)mine, b = *(const u2 *)(mine + 16 * B);
+            f.v = u4{a.x, a.y, b.x, b.y};
+        } else {
+            const f4 a = *(const f4 *)mine, b = *(const f4 *)(mine + 16 * B);
 #pragma unroll
             for (int j = 0; j < 4; ++j) f.v[j] = a[j], f.v[4 + j] = b[j];
         }
         return f;
     }
-    // one column per lane, the steps 4 g + j and 16 + 4 g + j from `row` on.  spread: columns
-    // col + 8 (i >> 2) + (i & 3), the order in which the state's rows lie; else col + i.
-    template <bool SPREAD>
+    // the column col + lane & 15, the steps 4 g + j and 16 + 4 g + j from `row` on
     __device__ __forceinline__ static Frag across(const char *p, int row, int col) {
         const int i = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
         Frag f;
         if constexpr (IO != IO_F32) {
-            const char *mine = p + at(4 * g + (i >> 2), 0) + (SPREAD ? 16 : 8) * (i & 3);
+            const char *mine = p + at(4 * g + (i >> 2), 0) + 8 * (i & 3);
             i2 h[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q)
                 h[q] = __builtin_bit_cast(i2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(mine + at(row + 16 * q, 0) + col * 2)));
             f.v = u4{(uint32_t)h[0].x, (uint32_t)h[0].y, (uint32_t)h[1].x, (uint32_t)h[1].y};
         } else {
-            const char *mine = p + at(4 * g, 0) + (SPREAD ? 8 * (i >> 2) + (i & 3) : i) * 4;
+            const char *mine = p + at(4 * g, 0) + i * 4;
 #pragma unroll
             for (int j = 0; j < 8; ++j) f.v[j] = *(const float *)(mine + at(row + 16 * (j >> 2) + (j & 3), 0) + col * 4);
         }
@@ -209,6 +223,9 @@ __device__ __forceinline__ float exp2_of(double x) {
 
 enum { STATES, FORWARD, BACKWARD };  // what a launch of chunks is for
 
+// Segments whose states each block joins for itself: that reads a state per segment before it, and saves a launch.
+constexpr int64_t kFew = 8;
+
 // Where the segments of the rows meet.
 struct Segs {
     int64_t len, n;      // steps of one, number
@@ -232,8 +249,9 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
     using Frag = typename X::Frag;
     constexpr bool OUT = DO != STATES;
     constexpr int C = X::C, TH = WV * 64, MB = WV * 16, KS = KP / 32, NT = C / 16, NU = C / 32;
-    using LK = Lds<IO, KP>;
-    using LM = Lds<IO, MB>;
+    using LA = Lds<IO, KP, 16, IO != IO_F32>;
+    using LK = Lds<IO, KP, 32, false>;
+    using LM = Lds<IO, MB, 32, false>;
     constexpr int E = LK::E;
     constexpr int NA = C * LK::CH / TH, NC = C * LM::CH / TH;  // units of 16 bytes per thread
     static_assert(C * LK::CH % TH == 0 && C * LM::CH % TH == 0 && NT <= 4, "whole units, a wave per 16 steps");
@@ -242,7 +260,7 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
     // Two places for tiles where the LDS has room for them without giving up a block: a chunk's are then written while
     // the last one's are still read.
     constexpr int TWO = OUT && WV == 8 && KP <= 128 ? 2 : 1;
-    __shared__ __attribute__((aligned(16))) char tile_a[OUT ? TWO * LK::kBytes : 16], tile_b[TWO * LK::kBytes], tile_c[TWO * LM::kBytes];
+    __shared__ __attribute__((aligned(16))) char tile_a[OUT ? TWO * LA::kBytes : 16], tile_b[TWO * LK::kBytes], tile_c[TWO * LM::kBytes];
     __shared__ __attribute__((aligned(16))) float decays[2][4 * C + 4];  // of a chunk [hi, lo, into, upd][C] and its factor
     __shared__ Frag weights[OUT ? WF * NP * 64 : 1];                     // [fragment][piece][lane]
     __shared__ float owns[OUT ? C : 1], downs[OUT ? NU * C : 1];         // a step's weight of itself, what its weights of 32 steps were scaled by
@@ -276,17 +294,29 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
     const T *pa = OUT ? base(role->a) : nullptr, *pb = base(role->b), *pc = base(role->c), *pe = dot ? base(role->e) : nullptr;
     const int lda = (int)role->a.ld, ldb = (int)role->b.ld, ldc = (int)role->c.ld, lde = (int)role->e.ld, ldo = (int)s.H * M;
 
-    f4 st[2 * KS];  // the state: rows 32 p + 8 g + 4 (m & 1) + j of tile m = 2 p, 2 p + 1, column lane & 15
+    f4 st[2 * KS];  // the state: rows 16 m + 4 g + j of tile m, column lane & 15
     const int64_t slot = ((int64_t)blockIdx.y * sg.n + seg) * BH + bh;
-    const float *enter = OUT ? (seg == 0 && sg.n == 1 ? (s0 ? s0 + bh * K * M : nullptr) : sg.state + slot * sg.plane) : nullptr;
+    const bool few = sg.n <= kFew;  // (segments: their states are joined here, else by k_lin_enter)
+    const float *enter = !OUT ? nullptr : sg.n == 1 || few ? (s0 ? s0 + bh * K * M : nullptr) : sg.state + slot * sg.plane;
+    const auto state_at = [&](int m, int j) INLINE { return std::min(16 * m + 4 * lg + j, K - 1) * rs + std::min(col0 + li, M - 1) * cs; };
 #pragma unroll
     for (int m = 0; m < 2 * KS; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int k = 16 * (m & ~1) + 8 * lg + 4 * (m & 1) + j, c = col0 + li;
-            st[m][j] = enter ? enter[std::min(k, K - 1) * rs + std::min(c, M - 1) * cs] : 0.f;
-            if (k >= K || c >= M) st[m][j] = 0.f;
+        for (int j = 0; j < 4; ++j) st[m][j] = enter ? enter[state_at(m, j)] : 0.f;
+    if (OUT && few)
+        for (int64_t q = 0; q < seg; ++q) {
+            const int64_t at_q = ((int64_t)blockIdx.y * sg.n + q) * BH + bh;
+            const float f1 = sg.factor[at_q * 2], f2 = sg.factor[at_q * 2 + 1], *add = sg.state + at_q * sg.plane;
+#pragma unroll
+            for (int m = 0; m < 2 * KS; ++m)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) st[m][j] = fmaf(st[m][j], f1, fmaf(st[m][j], f2, add[state_at(m, j)]));
         }
+#pragma unroll
+    for (int m = 0; m < 2 * KS; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (16 * m + 4 * lg + j >= K || col0 + li >= M) st[m][j] = 0.f;
 
     // the next chunk's units, on their way
     u4 ga[OUT ? NA : 1], gb[NA], gc[NC];
@@ -356,13 +386,13 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
 #pragma unroll
         for (int q = 0; q < NA; ++q) {
             const int u = q * TH + tid;
-            if constexpr (OUT) *(u4 *)(la + LK::at(u / LK::CH, u % LK::CH)) = ga[q];
-            *(u4 *)(lb + LK::at(u / LK::CH, u % LK::CH)) = gb[q];
+            if constexpr (OUT) LA::keep(la, u / LK::CH, u % LK::CH, ga[q]);
+            LK::keep(lb, u / LK::CH, u % LK::CH, gb[q]);
         }
 #pragma unroll
         for (int q = 0; q < NC; ++q) {
             const int u = q * TH + tid;
-            *(u4 *)(lc + LM::at(u / LM::CH, u % LM::CH)) = gc[q];
+            LM::keep(lc, u / LM::CH, u % LM::CH, gc[q]);
         }
     };
     // (wave EW) Exponents of two from the chunk's start on, in 64 bits: with the step's own decay where time runs
@@ -407,7 +437,7 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
     for (int i0 = i_lo; i0 < i_hi; i0 += C, turn ^= 1) {
         const float *dec = decays[turn];
         const int place = TWO == 2 ? turn : 0;
-        char *la = tile_a + place * LK::kBytes, *lb = tile_b + place * LK::kBytes, *lc = tile_c + place * LM::kBytes;
+        char *la = tile_a + place * LA::kBytes, *lb = tile_b + place * LK::kBytes, *lc = tile_c + place * LM::kBytes;
         const int cnt = count(i0);
         const int64_t row0 = low(i0, cnt);
         if constexpr (TWO == 1) __syncthreads();  // (the last chunk has been read)
@@ -423,7 +453,7 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
                 const int t = wave / SPLIT;
                 Frag a[KS];
 #pragma unroll
-                for (int p = 0; p < KS; ++p) a[p] = LK::along(la, 16 * t, 32 * p);
+                for (int p = 0; p < KS; ++p) a[p] = LA::along(la, 16 * t, 32 * p);
                 const float hi = dec[16 * t + li], lo = dec[C + 16 * t + li];
 #pragma unroll
                 for (int v = 0; v < NU / SPLIT; ++v) {
@@ -470,7 +500,7 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
         }
         Frag cf[NU];
 #pragma unroll
-        for (int u = 0; u < NU; ++u) cf[u] = LM::template across<false>(lc, 32 * u, wave * 16);
+        for (int u = 0; u < NU; ++u) cf[u] = LM::across(lc, 32 * u, wave * 16);
         f4 acc[OUT ? NT : 1];
         int se = 0;
         if constexpr (OUT) {
@@ -497,7 +527,7 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
                     x[q] = X::piece(w, q == NP - 1);
                 Frag a[NT];  // (products in chains side by side: one waits for the last of its own chain)
 #pragma unroll
-                for (int t = 0; t < NT; ++t) a[t] = LK::along(la, 16 * t, 32 * p);
+                for (int t = 0; t < NT; ++t) a[t] = LA::along(la, 16 * t, 32 * p);
 #pragma unroll
                 for (int q = 0; q < NP; ++q)
 #pragma unroll
@@ -539,7 +569,7 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
 #pragma unroll
             for (int u = 0; u < NU; ++u)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) k[i][u] = LK::template across<true>(lb, 32 * u, 32 * p + 4 * i);
+                for (int i = 0; i < 2; ++i) k[i][u] = LK::across(lb, 32 * u, 32 * p + 16 * i);
 #pragma unroll
             for (int u = 0; u < NU; ++u)
 #pragma unroll
@@ -631,7 +661,7 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
         for (int m = 0; m < 2 * KS; ++m)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int k = 16 * (m & ~1) + 8 * lg + 4 * (m & 1) + j, c = col0 + li;
+                const int k = 16 * m + 4 * lg + j, c = col0 + li;
                 if (k < rows && c < M) to[k * rs + c * cs] = st[m][j];
             }
     };
@@ -670,62 +700,55 @@ __global__ __launch_bounds__(256) void k_lin_enter(Roles roles, Segs sg, int64_t
 }
 
 // dg of one sequence and head from the dot products, from the end on, in 64 bits.
-__global__ __launch_bounds__(256) void k_lin_dg(const float *__restrict__ dq, const float *__restrict__ dk, int tiles_q,
-                                                int tiles_k, const float *__restrict__ s_end,
-                                                const float *__restrict__ ds_end, int64_t kv, Shape s, float *dg,
-                                                double *sums) {
-    __shared__ double lds[256];
+constexpr int kDg = 1024;
+__device__ __forceinline__ double block_sum(double v, double *lds) {
+    v = lane_of(sum_up_to(v), 63);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0;
+    for (int w = 0; w < kDg / 64; ++w) v += lds[w];
+    return v;
+}
+__global__ __launch_bounds__(kDg) void k_lin_dg(const float *__restrict__ dq, const float *__restrict__ dk, int tiles,
+                                                const float *__restrict__ s_end, const float *__restrict__ ds_end, int64_t kv,
+                                                Shape s, float *dg, double *sums) {
+    __shared__ double lds[kDg / 64];
     const int64_t bh = block_id();
     if (bh >= s.B * s.H) return;
     const int64_t b = bh / s.H, h = bh - b * s.H, n = row_len(s.lengths, b, s.N), plane = s.B * s.H * s.N;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, wave = tid >> 6;
     double carry = 0.0, total = 0.0;
     if (ds_end) {
-        double v = 0.0;
-        for (int64_t i = tid; i < kv; i += 256) v += (double)s_end[bh * kv + i] * ds_end[bh * kv + i];
-        lds[tid] = v;
-        __syncthreads();
-        for (int d = 128; d > 0; d >>= 1) {
-            if (tid < d) lds[tid] += lds[tid + d];
-            __syncthreads();
-        }
-        carry = lds[0];
-        __syncthreads();
+        for (int64_t i = tid; i < kv; i += kDg) carry += (double)s_end[bh * kv + i] * ds_end[bh * kv + i];
+        carry = block_sum(carry, lds);
     }
-    for (int64_t i0 = 0; i0 < n; i0 += 256) {  // from the end
+    for (int64_t i0 = 0; i0 < n; i0 += kDg) {  // from the end
         const int64_t t = n - 1 - i0 - tid;
         double v = 0.0;
-        if (t >= 0) {
-            for (int i = 0; i < tiles_q; ++i) v += dq[i * plane + bh * s.N + t];
-            for (int i = 0; i < tiles_k; ++i) v -= dk[i * plane + bh * s.N + t];
-        }
-        lds[tid] = v;
+        if (t >= 0)
+            for (int i = 0; i < tiles; ++i) v += (double)dq[i * plane + bh * s.N + t] - (double)dk[i * plane + bh * s.N + t];
+        const double sum = sum_up_to(v);
         __syncthreads();
-        for (int d = 1; d < 256; d <<= 1) {
-            const double u = tid >= d ? lds[tid - d] : 0.0;
-            __syncthreads();
-            lds[tid] += u;
-            __syncthreads();
+        if ((tid & 63) == 63) lds[wave] = sum;
+        __syncthreads();
+        double before = carry;
+        for (int w = 0; w < kDg / 64; ++w) {
+            before += w < wave ? lds[w] : 0.0;
+            carry += lds[w];
         }
         if (t >= 0) {
             const float g = s.per_token ? s.g[(b * s.N + t) * s.H + h] : s.g[h];
-            const double d = g < kZeroBelow ? 0.0 : carry + lds[tid];
+            const double d = g < kZeroBelow ? 0.0 : before + sum;
             if (s.per_token) dg[(b * s.N + t) * s.H + h] = (float)d;
             else total += d;
         }
-        carry += lds[255];
-        __syncthreads();
     }
     if (s.per_token) {
-        for (int64_t t = n + tid; t < s.N; t += 256) dg[(b * s.N + t) * s.H + h] = 0.f;
+        for (int64_t t = n + tid; t < s.N; t += kDg) dg[(b * s.N + t) * s.H + h] = 0.f;
     } else {
-        lds[tid] = total;
-        __syncthreads();
-        for (int d = 128; d > 0; d >>= 1) {
-            if (tid < d) lds[tid] += lds[tid + d];
-            __syncthreads();
-        }
-        if (tid == 0) sums[bh] = lds[0];
+        total = block_sum(total, lds);
+        if (tid == 0) sums[bh] = total;
     }
 }
 
@@ -822,7 +845,7 @@ hipError_t run_chunks(const Roles &r, int n, const Shape &s, const Segs &g, int 
         hipError_t e = launch(k_lin_chunk<IO, KP, WV, STATES, WHOLE>, grid_of((g.n - 1) * BH * tiles, (unsigned)n), dim3(WV * 64), 0, st, r,
                               s, g, tiles);
         if (e != hipSuccess) return e;
-        e = launch(k_lin_enter, grid_of((BH * g.plane + 255) / 256, (unsigned)n), dim3(256), 0, st, r, g, BH);
+        if (g.n > kFew) e = launch(k_lin_enter, grid_of((BH * g.plane + 255) / 256, (unsigned)n), dim3(256), 0, st, r, g, BH);
         if (e != hipSuccess) return e;
     }
     return launch(k_lin_chunk<IO, KP, WV, DO, WHOLE>, grid_of(g.n * BH * tiles, (unsigned)n), dim3(WV * 64), 0, st, r, s, g, tiles);
@@ -937,8 +960,7 @@ hipError_t bwd_io(const LinAttnArgs &a, const void *dy_, const float *dx_out, co
     if (!o.dg) return hipSuccess;
     double *sums = (double *)(base + w.sums);
     if (a.B > 0)
-        e = launch(k_lin_dg, grid_of(a.B * a.H), dim3(256), 0, st, row, col, dot_tiles(a.dk, a.dv),
-                   dot_tiles(a.dk, a.dv), s_end, dx_out,
+        e = launch(k_lin_dg, grid_of(a.B * a.H), dim3(kDg), 0, st, row, col, dot_tiles(a.dk, a.dv), s_end, dx_out,
                    (int64_t)a.dk * a.dv, s, o.dg, sums);
     if (e != hipSuccess || a.per_token) return e;
     return launch(k_lin_dg_heads, dim3((unsigned)((a.H + 255) / 256)), dim3(256), 0, st, sums, o.dg, a.B, a.H);
