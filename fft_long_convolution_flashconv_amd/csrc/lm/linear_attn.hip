@@ -234,9 +234,10 @@ struct Segs {
     int64_t plane;       // K*M
 };
 
-// Waves of a SIMD that the registers are to leave room for: as many as the LDS does.
+// Waves of a SIMD that the registers are to leave room for: as many as the LDS does (heads of more than 128 take what
+// they need).
 constexpr int waves_per_simd(int io, int KP, int WV, bool whole_heads) {
-    return io == IO_F32 || KP > 64 || !whole_heads || WV == 8 ? 2 : KP == 32 ? 4 : 3;
+    return KP > 128 && WV == 4 ? 1 : io == IO_F32 || KP > 64 || !whole_heads || WV == 8 ? 2 : KP == 32 ? 4 : 3;
 }
 
 // (a lambda left as a call would keep all that it captures in memory)
@@ -444,6 +445,29 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
         keep(la, lb, lc);
         __syncthreads();
         if (dot && i0 > i_lo) put_dots(i0 - C);
+        // what the outputs are multiplied by for the decays' gradients, on its way before the next chunk's tiles
+        u4 ge[DO == BACKWARD ? NT : 1];
+        if constexpr (DO == BACKWARD)
+            if (dot) {
+                const int c = col0 + 4 * lg;
+                const T *qe = pe + row0 * lde;
+                const __amdgpu_buffer_rsrc_t we = window(qe, lde, M, cnt, EB);
+                const int ve = lane_at(li, lde, c, M, EB);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if constexpr (!WHOLE) {
+                        float z[4];
+                        ld_row<IO, 4>(qe + ((uint32_t)at(16 * t + li, cnt) * (uint32_t)lde + c), z, M - c);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) ge[t][j] = __float_as_uint(z[j]);
+                    } else if constexpr (IO == IO_F32) {
+                        ge[t] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(we, ve + rows_at(16 * t, lde, cnt, EB), 0, 0));
+                    } else {
+                        const u2 v = __builtin_bit_cast(u2, __builtin_amdgcn_raw_buffer_load_b64(we, ve + rows_at(16 * t, lde, cnt, EB), 0, 0));
+                        ge[t] = u4{v.x, v.y, 0, 0};
+                    }
+                }
+            }
         if (i0 + C < i_hi) load(i0 + C);
         if constexpr (OUT) {
             // the chunk's weights, once for all columns: of 16 steps t and 32 steps u by a wave (or of all u, where waves are
@@ -537,7 +561,7 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
         // the state: decayed, and the chunk's products added
         const float factor = dec[4 * C];
         Frag x[NU][X::UPD];
-        float w[NU][8], m = 0.f, down = 1.f;
+        float vw[NU][8], vm = 0.f, vdown = 1.f;
 #pragma unroll
         for (int u = 0; u < NU; ++u)
 #pragma unroll
@@ -545,23 +569,23 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
                 const f4 d = *(const f4 *)(dec + 3 * C + 32 * u + 16 * q + 4 * lg);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    w[u][4 * q + j] = X::get(cf[u], 4 * q + j) * d[j];
-                    if constexpr (X::SCALE) m = fmaxf(m, fabsf(w[u][4 * q + j]));
+                    vw[u][4 * q + j] = X::get(cf[u], 4 * q + j) * d[j];
+                    if constexpr (X::SCALE) vm = fmaxf(vm, fabsf(vw[u][4 * q + j]));
                 }
             }
         if constexpr (X::SCALE) {
-            const int e = near_2_14(lanes_max(m, 16));
+            const int e = near_2_14(lanes_max(vm, 16));
             const float up_v = pow2(e);
-            down = pow2(-e);
+            vdown = pow2(-e);
 #pragma unroll
             for (int u = 0; u < NU; ++u)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) w[u][j] *= up_v;
+                for (int j = 0; j < 8; ++j) vw[u][j] *= up_v;
         }
 #pragma unroll
         for (int u = 0; u < NU; ++u)
 #pragma unroll
-            for (int q = 0; q < X::UPD; ++q) x[u][q] = X::piece(w[u], q == X::UPD - 1);
+            for (int q = 0; q < X::UPD; ++q) x[u][q] = X::piece(vw[u], q == X::UPD - 1);
 #pragma unroll
         for (int p = 0; p < KS; ++p) {
             f4 add[2] = {f4{0.f, 0.f, 0.f, 0.f}, f4{0.f, 0.f, 0.f, 0.f}};
@@ -580,7 +604,7 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    st[2 * p + i][j] = fmaf(st[2 * p + i][j], factor, X::SCALE ? add[i][j] * down : add[i][j]);
+                    st[2 * p + i][j] = fmaf(st[2 * p + i][j], factor, X::SCALE ? add[i][j] * vdown : add[i][j]);
         }
         if constexpr (OUT) {
             __syncthreads();  // (the weights are there)
@@ -618,9 +642,13 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
                 const uint32_t row = (uint32_t)at(j0, cnt);
                 if (dot) {  // and then the step's own product
                     float z[4], e = 0.f;
-                    ld_row<IO, 4>(pe + row0 * lde + (row * (uint32_t)lde + c), z, M - c);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) e = fmaf(z[j], y[j], e);
+                    for (int j = 0; j < 4; ++j) {
+                        const u4 w = ge[DO == BACKWARD ? t : 0];
+                        if constexpr (IO == IO_F32 || !WHOLE) z[j] = __uint_as_float(w[j]);
+                        else z[j] = to_f<IO>(__builtin_bit_cast(T, (uint16_t)(w[j >> 1] >> (16 * (j & 1)))));
+                        e = fmaf(z[j], y[j], e);
+                    }
                     e += __shfl_xor(e, 16);
                     e += __shfl_xor(e, 32);
                     if (lg == 0) dots[wave * C + 16 * t + li] = e;
@@ -699,7 +727,9 @@ __global__ __launch_bounds__(256) void k_lin_enter(Roles roles, Segs sg, int64_t
     }
 }
 
-// dg of one sequence and head from the dot products, from the end on, in 64 bits.
+// dg of one sequence and head from the dot products, from the end on, in 64 bits.  The dot products are fp32, and what
+// they are off by adds up along the sequence; but before the first step it has to come to <x_in, dx_in>, so what it
+// misses that by is taken back evenly over the steps (a third of the squared error on average is left).
 constexpr int kDg = 1024;
 __device__ __forceinline__ double block_sum(double v, double *lds) {
     v = lane_of(sum_up_to(v), 63);
@@ -711,7 +741,8 @@ __device__ __forceinline__ double block_sum(double v, double *lds) {
     return v;
 }
 __global__ __launch_bounds__(kDg) void k_lin_dg(const float *__restrict__ dq, const float *__restrict__ dk, int tiles,
-                                                const float *__restrict__ s_end, const float *__restrict__ ds_end, int64_t kv,
+                                                const float *__restrict__ s_end, const float *__restrict__ ds_end,
+                                                const float *__restrict__ x_in, const float *__restrict__ dx_in, int64_t kv,
                                                 Shape s, float *dg, double *sums) {
     __shared__ double lds[kDg / 64];
     const int64_t bh = block_id();
@@ -723,11 +754,22 @@ __global__ __launch_bounds__(kDg) void k_lin_dg(const float *__restrict__ dq, co
         for (int64_t i = tid; i < kv; i += kDg) carry += (double)s_end[bh * kv + i] * ds_end[bh * kv + i];
         carry = block_sum(carry, lds);
     }
-    for (int64_t i0 = 0; i0 < n; i0 += kDg) {  // from the end
-        const int64_t t = n - 1 - i0 - tid;
+    const auto step = [&](int64_t t) {
         double v = 0.0;
         if (t >= 0)
             for (int i = 0; i < tiles; ++i) v += (double)dq[i * plane + bh * s.N + t] - (double)dk[i * plane + bh * s.N + t];
+        return v;
+    };
+    double missed = 0.0;
+    if (!x_in || dx_in) {
+        for (int64_t t = tid; t < n; t += kDg) missed += step(t);
+        if (x_in)
+            for (int64_t i = tid; i < kv; i += kDg) missed -= (double)x_in[bh * kv + i] * dx_in[bh * kv + i];
+        missed = (block_sum(missed, lds) + carry) / (double)(n > 0 ? n : 1);
+    }
+    for (int64_t i0 = 0; i0 < n; i0 += kDg) {  // from the end
+        const int64_t t = n - 1 - i0 - tid;
+        const double v = step(t);
         const double sum = sum_up_to(v);
         __syncthreads();
         if ((tid & 63) == 63) lds[wave] = sum;
@@ -739,7 +781,7 @@ __global__ __launch_bounds__(kDg) void k_lin_dg(const float *__restrict__ dq, co
         }
         if (t >= 0) {
             const float g = s.per_token ? s.g[(b * s.N + t) * s.H + h] : s.g[h];
-            const double d = g < kZeroBelow ? 0.0 : before + sum;
+            const double d = g < kZeroBelow ? 0.0 : before + sum - missed * (double)(n - t);
             if (s.per_token) dg[(b * s.N + t) * s.H + h] = (float)d;
             else total += d;
         }
@@ -960,7 +1002,7 @@ hipError_t bwd_io(const LinAttnArgs &a, const void *dy_, const float *dx_out, co
     if (!o.dg) return hipSuccess;
     double *sums = (double *)(base + w.sums);
     if (a.B > 0)
-        e = launch(k_lin_dg, grid_of(a.B * a.H), dim3(kDg), 0, st, row, col, dot_tiles(a.dk, a.dv), s_end, dx_out,
+        e = launch(k_lin_dg, grid_of(a.B * a.H), dim3(kDg), 0, st, row, col, dot_tiles(a.dk, a.dv), s_end, dx_out, a.x_in, o.dx_in,
                    (int64_t)a.dk * a.dv, s, o.dg, sums);
     if (e != hipSuccess || a.per_token) return e;
     return launch(k_lin_dg_heads, dim3((unsigned)((a.H + 255) / 256)), dim3(256), 0, st, sums, o.dg, a.B, a.H);
