@@ -10,11 +10,15 @@
 //   dz = dm fh w_out silu'(z),  dn = dm silu(z),  dw_out = sum dn fh,
 //   df = ra (dn w_out - fh mean(dn w_out fh)),  dw_in = sum dy rh
 // Five or eight tensors are touched once for some twenty to sixty operations per
-// element: HBM bound.  A row stays in the registers of one to four waves from the
+// element: HBM bound.  A row stays in the registers of one to eight waves from the
 // loads to the stores, so each tensor is read once; the backward pass forms r
 // again from f, z and res instead of reading what the forward pass rounded.
 // Squares, sums and all values between are fp32; y is the norm of r before r is
 // rounded.
+// Forward and backward, bf16: 8192 rows of 2560 take 43.6 and 122 us (4.8 and 2.8
+// TB/s; 545 MB, 106 us together at a copy's rate), of 768 15 and 35 us.  The
+// backward kernel waits for the row's sums, three rounds of them one behind
+// another, with 20 waves a CU at most to cover that.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -31,29 +35,30 @@ constexpr int block_rows(int W) { return W == 1 ? 4 : W <= 3 ? 2 : 1; }
 
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
-// A row of n elements at p.  Where rows are whole vectors at whole dwords they are read and written through a buffer
-// resource that ends with the row: a lane has one offset for all tensors, past the row it loads zeros and stores
-// nothing.  (With an address per tensor and lane the backward kernel waits for spilled addresses before every load: 215
-// us and 99 for 8192 x 2560 in bf16.)  ODD, every element is loaded by itself.
-template <int IO, bool ODD>
+// A row of n elements at p.  Where rows are whole dwords at whole dwords they are read and written through a buffer
+// resource that ends with the row: a lane has one offset for all tensors, and of a vector that passes the row's end the
+// dwords past it load zeros and store nothing.  (With an address per tensor and lane the backward kernel waits for
+// spilled addresses before every load: 215 us and 99 for 8192 x 2560 in bf16.)  SINGLE, every element is loaded by
+// itself: SINGLE_FIGURE
+template <int IO, bool SINGLE>
 struct Line {
     using T = typename io_elem<IO>::T;
     T *p;
     __amdgpu_buffer_rsrc_t b;
     int n;
     __device__ __forceinline__ Line(const T *q, int64_t at, int n_) : p(const_cast<T *>(q) + at), n(n_) {
-        if constexpr (!ODD) b = __builtin_amdgcn_make_buffer_rsrc(p, (short)0, n * (int)sizeof(T), 0x00020000);
+        if constexpr (!SINGLE) b = __builtin_amdgcn_make_buffer_rsrc(p, (short)0, n * (int)sizeof(T), 0x00020000);
     }
 };
 
 // A vector as loaded, in whole words: elements one by one would take a register each.
-template <int IO, bool ODD>
+template <int IO, bool SINGLE>
 struct Vec {
     using T = typename io_elem<IO>::T;
     static constexpr int WORDS = V * (int)sizeof(T) / 4;
     uint32_t w[WORDS];
-    __device__ __forceinline__ void load(const Line<IO, ODD> &l, uint32_t c) {
-        if constexpr (!ODD) {
+    __device__ __forceinline__ void load(const Line<IO, SINGLE> &l, uint32_t c) {
+        if constexpr (!SINGLE) {
 #pragma unroll
             for (int q = 0; q < WORDS / 4; ++q) {
                 const u4 r = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(l.b, (int)(c * sizeof(T)) + 16 * q, 0, 0));
@@ -82,16 +87,16 @@ struct Vec {
         for (int i = 0; i < WORDS; ++i) asm volatile("" : "+v"(w[i]));
     }
 };
-template <bool ODD>
+
 __device__ __forceinline__ void ld_par(const float *p, uint32_t c, int D, float (&o)[V]) {
-    Vec<IO_F32, ODD> v;
-    v.load(Line<IO_F32, ODD>(p, 0, D), c);
+    Vec<IO_F32, false> v;
+    v.load(Line<IO_F32, false>(p, 0, D), c);
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = v[i];
 }
-template <int IO, bool ODD>
-__device__ __forceinline__ void st_vec(const Line<IO, ODD> &l, uint32_t c, const float (&o)[V]) {
-    if constexpr (!ODD) {
+template <int IO, bool SINGLE>
+__device__ __forceinline__ void st_vec(const Line<IO, SINGLE> &l, uint32_t c, const float (&o)[V]) {
+    if constexpr (!SINGLE) {
         using T = typename io_elem<IO>::T;
         T e[V];
 #pragma unroll
@@ -224,7 +229,7 @@ struct Ptr {
     float *part;  // [blocks][3][D]: sums of dw_out, dscale, dw_in
 };
 
-template <int IO, int W, int NV, bool ODD, bool BWD>
+template <int IO, int W, int NV, bool ODD, bool SINGLE, bool BWD>
 __global__ __launch_bounds__(Row<W>::kThreads, ODD || W * NV >= 16 ? 2 : BWD && IO == IO_F32 ? 3 : 4) void k_block_norm(Ptr<IO> p, int64_t T_, int D, Groups g, float eps) {
     using R = Row<W>;
     extern __shared__ float wide[];
@@ -246,16 +251,16 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W * NV >= 16 ? 2 : BWD && 
         const bool on = t0 + row.sub < T_;
         const int64_t at = (on ? t0 + row.sub : T_ - 1) * D;
         const int n = on ? D : 0;
-        Vec<IO, ODD> f[NV], res[NV], z[NV], dr[BWD ? NV : 1], dy[BWD ? NV : 1];
+        Vec<IO, SINGLE> f[NV], res[NV], z[NV], dr[BWD ? NV : 1], dy[BWD ? NV : 1];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const uint32_t c = (j * R::kLanes + row.lane) * V;
-            f[j].load(Line<IO, ODD>(p.f, at, n), c);
-            if (p.res) res[j].load(Line<IO, ODD>(p.res, at, n), c);
-            if (p.z) z[j].load(Line<IO, ODD>(p.z, at, n), c);
+            f[j].load(Line<IO, SINGLE>(p.f, at, n), c);
+            if (p.res) res[j].load(Line<IO, SINGLE>(p.res, at, n), c);
+            if (p.z) z[j].load(Line<IO, SINGLE>(p.z, at, n), c);
             if constexpr (BWD) {
-                if (p.dr) dr[j].load(Line<IO, ODD>(p.dr, at, n), c);
-                if (p.dy) dy[j].load(Line<IO, ODD>(p.dy, at, n), c);
+                if (p.dr) dr[j].load(Line<IO, SINGLE>(p.dr, at, n), c);
+                if (p.dy) dy[j].load(Line<IO, SINGLE>(p.dy, at, n), c);
             }
         }
         float ra[NV][ODD ? V : 1];
@@ -274,7 +279,7 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W * NV >= 16 ? 2 : BWD && 
             for (int i = 0; i < V; ++i) nf[i] = f[j][i];
             if (out_norm) {
                 float w[V];
-                ld_par<ODD>(p.w_out, c, D, w);
+                ld_par(p.w_out, c, D, w);
 #pragma unroll
                 for (int i = 0; i < V; ++i) nf[i] *= ra_of(j, i) * w[i];
             }
@@ -286,7 +291,7 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W * NV >= 16 ? 2 : BWD && 
             }
             if (p.scale) {
                 float s[V];
-                ld_par<ODD>(p.scale, c, D, s);
+                ld_par(p.scale, c, D, s);
 #pragma unroll
                 for (int i = 0; i < V; ++i) r[i] *= s[i];
             }
@@ -303,7 +308,7 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W * NV >= 16 ? 2 : BWD && 
             if (in_norm) {
                 float w[V];
                 if constexpr (BWD)
-                    if (p.dy) ld_par<ODD>(p.w_in, (j * R::kLanes + row.lane) * V, D, w);
+                    if (p.dy) ld_par(p.w_in, (j * R::kLanes + row.lane) * V, D, w);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     ss = fmaf(r[j][i], r[j][i], ss);
@@ -321,13 +326,13 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W * NV >= 16 ? 2 : BWD && 
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const uint32_t c = (j * R::kLanes + row.lane) * V;
-                st_vec<IO, ODD>(Line<IO, ODD>(p.r, at, n), c, r[j]);
+                st_vec<IO, SINGLE>(Line<IO, SINGLE>(p.r, at, n), c, r[j]);
                 if (in_norm) {
                     float w[V], o[V];
-                    ld_par<ODD>(p.w_in, c, D, w);
+                    ld_par(p.w_in, c, D, w);
 #pragma unroll
                     for (int i = 0; i < V; ++i) o[i] = r[j][i] * rb * w[i];
-                    st_vec<IO, ODD>(Line<IO, ODD>(p.y, at, n), c, o);
+                    st_vec<IO, SINGLE>(Line<IO, SINGLE>(p.y, at, n), c, o);
                 }
             }
         } else {
@@ -346,7 +351,7 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W * NV >= 16 ? 2 : BWD && 
                 for (int i = 0; i < V; ++i) t[i] = p.dr ? dr[j][i] : 0.f;
                 if (in_norm && p.dy) {
                     float w[V];
-                    ld_par<ODD>(p.w_in, c, D, w);
+                    ld_par(p.w_in, c, D, w);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         const float rh = r[j][i] * rb;
@@ -354,10 +359,10 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W * NV >= 16 ? 2 : BWD && 
                         if (on) ai[j][i] = fmaf(dy[j][i], rh, ai[j][i]);
                     }
                 }
-                if (p.dres) st_vec<IO, ODD>(Line<IO, ODD>(p.dres, at, n), c, t);
+                if (p.dres) st_vec<IO, SINGLE>(Line<IO, SINGLE>(p.dres, at, n), c, t);
                 if (p.scale) {
                     float s[V];
-                    ld_par<ODD>(p.scale, c, D, s);
+                    ld_par(p.scale, c, D, s);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         if (on) as[j][i] = fmaf(t[i], m[i], as[j][i]);
@@ -372,18 +377,18 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W * NV >= 16 ? 2 : BWD && 
                         dz[i] = t[i] * nf[i] * sg[i] * fmaf(zz, 1.f - sg[i], 1.f);
                         t[i] *= zz * sg[i];
                     }
-                    st_vec<IO, ODD>(Line<IO, ODD>(p.dz, at, n), c, dz);
+                    st_vec<IO, SINGLE>(Line<IO, SINGLE>(p.dz, at, n), c, dz);
                 }
                 if (out_norm) {
                     float w[V];
-                    ld_par<ODD>(p.w_out, c, D, w);
+                    ld_par(p.w_out, c, D, w);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         if (on) aw[j][i] = fmaf(t[i], f[j][i] * ra_of(j, i), aw[j][i]);
                         dn[j][i] = t[i] * w[i];
                     }
                 } else {
-                    st_vec<IO, ODD>(Line<IO, ODD>(p.df, at, n), c, t);
+                    st_vec<IO, SINGLE>(Line<IO, SINGLE>(p.df, at, n), c, t);
                 }
             }
             if (out_norm) {
@@ -396,7 +401,7 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W * NV >= 16 ? 2 : BWD && 
 #pragma unroll
                     for (int i = 0; i < V; ++i)
                         o[i] = ra_of(j, i) * fmaf(-f[j][i] * ra_of(j, i), c2[j][ODD ? i : 0] * g.inv, dn[j][i]);
-                    st_vec<IO, ODD>(Line<IO, ODD>(p.df, at, n), c, o);
+                    st_vec<IO, SINGLE>(Line<IO, SINGLE>(p.df, at, n), c, o);
                 }
             }
         }
@@ -429,7 +434,7 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W * NV >= 16 ? 2 : BWD && 
 }
 
 // Column sums of the blocks' parts, in order: 64 columns per block, its sixteen
-// waves a share of the parts each, eight loads on their way.
+// waves a share of the parts each, eight loads on their way (6 to 8 us for 768 parts of 3 x 2560).
 constexpr int kJoin = 1024;
 __global__ __launch_bounds__(kJoin) void k_join_parts(const float *__restrict__ part, int parts, int D, float *dw_out,
                                                       float *dscale, float *dw_in) {
@@ -451,13 +456,15 @@ __global__ __launch_bounds__(kJoin) void k_join_parts(const float *__restrict__ 
     }
 }
 
-// Blocks whose sums of weights' gradients are joined by k_join_parts: as many as run at once, 16 waves per CU.
+// Blocks whose sums of weights' gradients are joined by k_join_parts: as many as run at once, 16 waves per CU (rows of
+// 2560: 122 us with 768 blocks, 144 with 1024).
 constexpr int64_t kParts = 1024;
 int64_t parts_of(int W) { return 256 * (16 / (block_rows(W) * W)); }
 
 // Waves of a row and vectors per thread.  Forward: as few waves as hold the row in three vectors per thread (eight of
 // them four).  Backward a vector's sums, gradients and inputs take some 120 registers, so one vector per thread and as
-// many waves as that takes, up to eight.  Odd rows and groups have four shapes only.
+// many waves as that takes, up to eight (rows of 2560: five waves 122 us, two of three vectors each 140, eight 179).
+// Odd rows and groups have four shapes only.
 struct Shape {
     int W, NV;
 };
@@ -480,10 +487,9 @@ Groups groups_of(int64_t D, int64_t n) {
     return g;
 }
 
-// Whether a call takes the kernels for odd rows: rows that are not whole vectors, groups that are not a power of two of
-// them, or a tensor that does not begin at a dword.
-bool is_odd(const BlockNormArgs &a, const Groups &g, std::initializer_list<const void *> tensors) {
-    if (a.D % V != 0 || (a.w_out && g.n > 1 && !g.lanes)) return true;
+// Whether elements are read one by one: rows that are not whole dwords, or a tensor that does not begin at one.
+bool is_single(int64_t row_bytes, std::initializer_list<const void *> tensors) {
+    if (row_bytes % 4 != 0) return true;
     for (const void *p : tensors)
         if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return true;
     return false;
@@ -497,28 +503,32 @@ int64_t blocks_of(int64_t T, int W, bool bwd) {
 template <int IO, bool BWD>
 hipError_t run(const Ptr<IO> &p, const BlockNormArgs &a, hipStream_t s, int &blocks) {
     const Groups g = groups_of(a.D, a.groups);
-    const bool odd = is_odd(a, g, {p.f, p.res, p.z, p.dr, p.dy, p.r, p.y, p.df, p.dres, p.dz});
+    const bool single = is_single(a.D * (int64_t)sizeof(*p.f), {p.f, p.res, p.z, p.dr, p.dy, p.r, p.y, p.df, p.dres, p.dz});
+    const bool odd = single || (a.w_out && g.n > 1 && !g.lanes);
     const Shape sh = shape_of(a.D, odd, BWD);
     const int rows = block_rows(sh.W);
     const int64_t n = blocks_of(a.T, sh.W, BWD);
     blocks = (int)std::min<int64_t>(n, kParts);
     const size_t lds = std::max(odd && g.n > 1 ? (size_t)rows * (a.D + g.n) * 4 : 0, BWD ? (size_t)a.D * 4 : 0);
     using std::integral_constant;
-    const auto go = [&](auto w, auto nv, auto odds) {
+    const auto go = [&](auto w, auto nv, auto odds, auto singles) {
         constexpr int W = decltype(w)::value, NV = decltype(nv)::value;
-        return launch(k_block_norm<IO, W, NV, decltype(odds)::value, BWD>, grid_of(n), dim3(Row<W>::kThreads), lds, s, p, a.T,
+        return launch(k_block_norm<IO, W, NV, decltype(odds)::value, decltype(singles)::value, BWD>, grid_of(n), dim3(Row<W>::kThreads), lds, s, p, a.T,
                       (int)a.D, g, a.eps);
     };
-    const auto whole = [&](auto w, auto nv) { return go(w, nv, std::false_type{}); };
+    const auto whole = [&](auto w, auto nv) { return go(w, nv, std::false_type{}, std::false_type{}); };
     constexpr integral_constant<int, 1> one{};
     constexpr integral_constant<int, 2> two{};
     constexpr integral_constant<int, 3> three{};
     constexpr integral_constant<int, 4> four{};
     constexpr integral_constant<int, 8> eight{};
     if (odd) {
-        constexpr std::true_type yes{};
-        if (sh.W == 1 && sh.NV == 1) return go(one, one, yes);
-        return sh.W == 1 ? go(one, three, yes) : sh.W == 4 ? go(four, three, yes) : go(eight, four, yes);
+        const auto shape = [&](auto singles) {
+            constexpr std::true_type yes{};
+            if (sh.W == 1 && sh.NV == 1) return go(one, one, yes, singles);
+            return sh.W == 1 ? go(one, three, yes, singles) : sh.W == 4 ? go(four, three, yes, singles) : go(eight, four, yes, singles);
+        };
+        return single ? shape(std::true_type{}) : shape(std::false_type{});
     }
     if constexpr (BWD) {
         switch (sh.W) {

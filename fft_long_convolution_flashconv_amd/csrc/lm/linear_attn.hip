@@ -12,6 +12,29 @@
 // From <S_t, D_t> = dg_t + k_t.dk_t = q_t.dq_t + dg_{t+1} the decays' gradients are
 // sums over time, dg_t = dg_{t+1} + q_t.dq_t - k_t.dk_t, where the step's own
 // products are in both and are left out of both.
+//
+// Steps are taken in chunks of 64 (fp32: 32), with L the decays' exponents summed
+// from the chunk's first step on:
+//   o_t = out (e^{L_t} X_in^T a_t + sum_{j<=t} e^{L_t - L_j} (a_t.b_j) upd c_j)
+//   X_out = e^{L_end} X_in + sum_j (e^{L_end - L_j} upd b_j) c_j^T
+// which are four matrix products.  What is multiplied is either as it was given
+// or held in pieces that come to 22 bits or more (the matrix cores' 16-bit types
+// would round weights and states to 8 or 11), sums and states are fp32, exponents
+// 64 bits.  A wave has 16 of the state's columns, in its accumulators from the
+// first chunk to the last; a block's waves share the tiles of a and b and the
+// chunk's weights in LDS.  A row is cut into segments where sequences times heads
+// do not fill the chip: STATES finds what each segment adds to a state, the
+// segments are joined, and the last launch goes through each from the state that
+// enters it.
+//
+// What bounds it: neither memory (64K steps of 8 heads of 128 in bf16 read and
+// write 539 MB, 105 us at a copy's rate, and take 245) nor the matrix cores (a
+// quarter busy), but the chain of a chunk: scan, weights, products, update, with a
+// barrier or two between.  One block of eight waves per CU is all that 220
+// registers a lane allow (two at 128 registers spill 30 to 77 and are no faster:
+// 76 us against 75 forward, 314 against 286 backward); a sixth to a quarter of
+// the time goes by without loads, a tenth without the exponents, none without the
+// stores or with the weights formed elsewhere.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -72,7 +95,7 @@ typedef __attribute__((address_space(3))) s4 lds_s4;
 // of the row (column) lane & 15; which of 32 they are is up to both operands alike.
 template <int IO>
 struct Mx {  // 16-bit elements
-    static constexpr int C = 64;                       // steps of a chunk
+    static constexpr int C = 64;                       // steps of a chunk: more need more weights, fewer more updates
     static constexpr int UPD = IO == IO_BF16 ? 3 : 2;  // pieces of a weighted value: 24 or 22 bits
     static constexpr bool SCALE = IO == IO_F16;        // pieces are of values brought near 2^14
     struct Frag {
@@ -223,7 +246,8 @@ __device__ __forceinline__ float exp2_of(double x) {
 
 enum { STATES, FORWARD, BACKWARD };  // what a launch of chunks is for
 
-// Segments whose states each block joins for itself: that reads a state per segment before it, and saves a launch.
+// Segments whose states each block joins for itself: that reads a state per segment before it, and saves a launch (eight
+// prompts of 1024 steps: 31.5 us, with the launch 35.7).
 constexpr int64_t kFew = 8;
 
 // Where the segments of the rows meet.
@@ -236,15 +260,18 @@ struct Segs {
 
 // Waves of a SIMD that the registers are to leave room for: as many as the LDS does (heads of more than 128 take what
 // they need).
-constexpr int waves_per_simd(int io, int KP, int WV, bool whole_heads) {
-    return KP > 128 && WV == 4 ? 1 : io == IO_F32 || KP > 64 || !whole_heads || WV == 8 ? 2 : KP == 32 ? 4 : 3;
+constexpr int waves_per_simd(int io, int KP, int WV, int what, bool whole_heads) {
+    return KP > 128 && WV == 4                                           ? 1
+           : io == IO_F32 || KP > 64 || !whole_heads || WV == 8          ? 2
+           : KP == 32 && !(io == IO_BF16 && what == BACKWARD)            ? 4
+                                                                         : 3;
 }
 
 // (a lambda left as a call would keep all that it captures in memory)
 #define INLINE __attribute__((always_inline))
 
 template <int IO, int KP, int WV, int DO, bool WHOLE>
-__global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_lin_chunk(Roles roles, Shape s, Segs sg, int tiles) {
+__global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, DO, WHOLE)) void k_lin_chunk(Roles roles, Shape s, Segs sg, int tiles) {
     using T = typename io_elem<IO>::T;
     using X = Mx<IO>;
     using Frag = typename X::Frag;
@@ -711,7 +738,8 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, WHOLE)) void k_
     }
 }
 
-// The states that enter the segments, from what each segment adds.
+// The states that enter the segments, from what each segment adds.  One pass over the segments' states: 14 us for 32
+// segments of each of 8 heads of 128 x 128, in order, so that equal calls give equal bits.
 __global__ __launch_bounds__(256) void k_lin_enter(Roles roles, Segs sg, int64_t BH) {
     const int64_t i = block_id() * 256 + threadIdx.x;
     if (i >= BH * sg.plane) return;
@@ -729,7 +757,8 @@ __global__ __launch_bounds__(256) void k_lin_enter(Roles roles, Segs sg, int64_t
 
 // dg of one sequence and head from the dot products, from the end on, in 64 bits.  The dot products are fp32, and what
 // they are off by adds up along the sequence; but before the first step it has to come to <x_in, dx_in>, so what it
-// misses that by is taken back evenly over the steps (a third of the squared error on average is left).
+// misses that by is taken back evenly over the steps (a third of the squared error on average is left).  Two or three
+// passes over N numbers and two over a state by one block: 7 us beside 310 for four sequences of 2048 steps and 20 heads.
 constexpr int kDg = 1024;
 __device__ __forceinline__ double block_sum(double v, double *lds) {
     v = lane_of(sum_up_to(v), 63);
@@ -815,11 +844,15 @@ __global__ __launch_bounds__(256) void k_lin_share(const float *__restrict__ wid
     o[i] = from_f<IO>(s);
 }
 
-// One token of each sequence: a block per sequence and head.
-template <int IO>
+// One token of each sequence: a block per sequence and head, which reads and writes every state once: HBM bound, and by
+// the launch where the states are few.  A thread has VEC columns side by side and every 256 / (64 / VEC)-th row.
+// 25.5 MB of states and tokens (64 sequences of 12 heads of 64 x 64, fp16): STEP_FIGURE
+template <int IO, int VEC>
 __global__ __launch_bounds__(256) void k_lin_step(LinStepArgs s) {
     using T = typename io_elem<IO>::T;
-    __shared__ float lds[256];
+    typedef float fv __attribute__((ext_vector_type(VEC)));
+    constexpr int CG = 64 / VEC, RG = 256 / CG;  // threads across 64 columns, and down the rows
+    __shared__ float lds[RG][64];
     const int64_t bh = block_id();
     if (bh >= s.B * s.H) return;
     const int64_t b = bh / s.H, h = bh - b * s.H, grp = h / (s.H / s.G);
@@ -834,24 +867,35 @@ __global__ __launch_bounds__(256) void k_lin_step(LinStepArgs s) {
     const float e = __builtin_amdgcn_exp2f((s.per_token ? s.g[b * s.H + h] : s.g[h]) * kLog2e);
     const float *from = s.x_in + (slot * s.H + h) * s.dk * s.dv;
     float *to = s.x_out + (slot * s.H + h) * s.dk * s.dv;
-    const int rg = threadIdx.x >> 6;
+    const int rg = threadIdx.x / CG, cl = threadIdx.x % CG * VEC;
     for (int c0 = 0; c0 < s.dv; c0 += 64) {
-        const int c = c0 + (threadIdx.x & 63);
-        float sum = 0.f;
-        if (c < s.dv) {
-            const float vc = to_f<IO>(v[c]);
-            for (int i = rg; i < s.dk; i += 4) {
-                const float x = fmaf(to_f<IO>(k[i]), vc, e * from[(int64_t)i * s.dv + c]);
-                to[(int64_t)i * s.dv + c] = x;
-                sum = fmaf(to_f<IO>(q[i]), x, sum);
+        const int c = c0 + cl;
+        fv sum = {};
+        if (c < s.dv) {  // (and so are all VEC)
+            fv vc;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) vc[j] = to_f<IO>(v[c + j]);
+#pragma unroll 4
+            for (int i = rg; i < s.dk; i += RG) {
+                const float ki = to_f<IO>(k[i]), qi = to_f<IO>(q[i]);
+                fv x = *(const fv *)(from + i * s.dv + c);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    x[j] = fmaf(ki, vc[j], e * x[j]);
+                    sum[j] = fmaf(qi, x[j], sum[j]);
+                }
+                *(fv *)(to + i * s.dv + c) = x;
             }
         }
         __syncthreads();
-        lds[threadIdx.x] = sum;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) lds[rg][cl + j] = sum[j];
         __syncthreads();
-        if (rg == 0 && c < s.dv) {
-            const float o = ((lds[threadIdx.x] + lds[threadIdx.x + 64]) + lds[threadIdx.x + 128]) + lds[threadIdx.x + 192];
-            y[c] = from_f<IO>(o * s.scale);
+        if (threadIdx.x < 64 && c0 + (int)threadIdx.x < s.dv) {
+            float o = lds[0][threadIdx.x];
+#pragma unroll
+            for (int r = 1; r < RG; ++r) o += lds[r][threadIdx.x];
+            y[c0 + threadIdx.x] = from_f<IO>(o * s.scale);
         }
     }
 }
@@ -862,7 +906,9 @@ int64_t up(int64_t n) { return (n + 255) & ~(int64_t)255; }
 int cols_of(int M) { return M > 64 ? 128 : 64; }
 int tiles_of(int M) { return (M + cols_of(M) - 1) / cols_of(M); }
 
-// Blocks that the chip holds at once.
+// Blocks that the chip holds at once.  A row has segments for that many: with half as many blocks the chip is half
+// empty, with twice as many every segment's state is found twice over (eight waves: 377 us with 256, 469 with 512; four
+// waves and small states: 35.9 with 768, 38 with 512).
 int64_t at_once(int K, int M) { return cols_of(M) == 64 && K <= 64 ? 768 : cols_of(M) == 64 && K <= 128 ? 512 : 256; }
 
 // Segments of a row of N steps where `blocks` work on each.
@@ -1035,11 +1081,18 @@ hipError_t launch_linear_attn_bwd(const LinAttnArgs &a, const void *dy, const fl
     }
 }
 
+template <int IO>
+static hipError_t step_io(const LinStepArgs &a, hipStream_t s) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.x_in) | reinterpret_cast<uintptr_t>(a.x_out);
+    if (a.dv % 4 == 0 && at % 16 == 0) return launch(k_lin_step<IO, 4>, grid_of(a.B * a.H), dim3(256), 0, s, a);
+    return launch(k_lin_step<IO, 1>, grid_of(a.B * a.H), dim3(256), 0, s, a);
+}
+
 hipError_t launch_linear_attn_step(const LinStepArgs &a, int io, hipStream_t s) {
     switch (io) {
-        case IO_F32: return launch(k_lin_step<IO_F32>, grid_of(a.B * a.H), dim3(256), 0, s, a);
-        case IO_F16: return launch(k_lin_step<IO_F16>, grid_of(a.B * a.H), dim3(256), 0, s, a);
-        default: return launch(k_lin_step<IO_BF16>, grid_of(a.B * a.H), dim3(256), 0, s, a);
+        case IO_F32: return step_io<IO_F32>(a, s);
+        case IO_F16: return step_io<IO_F16>(a, s);
+        default: return step_io<IO_BF16>(a, s);
     }
 }
 
