@@ -39,7 +39,7 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 // resource that ends with the row: a lane has one offset for all tensors, and of a vector that passes the row's end the
 // dwords past it load zeros and store nothing.  (With an address per tensor and lane the backward kernel waits for
 // spilled addresses before every load: 215 us and 99 for 8192 x 2560 in bf16.)  SINGLE, every element is loaded by
-// itself: SINGLE_FIGURE
+// itself (8192 x 1031 in bf16 takes 49 and 166 us, more than 2560 channels read whole).
 template <int IO, bool SINGLE>
 struct Line {
     using T = typename io_elem<IO>::T;
@@ -160,13 +160,15 @@ struct Row {
 
 // How the channels fall into groups.
 struct Groups {
-    int n, size, lanes;  // groups, channels of one, vectors of one if they are a power of two (else 0)
-    float inv;           // 1 / size
+    int n, size;      // groups, channels of one
+    int vecs, lanes;  // vectors of one if it is whole ones, at most 64 (else 0); the same if they are a power of two
+    float inv;        // 1 / size
 };
 
 // Per vector the sums of its elements' values over their group.  A group of a
-// power of two of vectors lies in the lanes of one wave; any other (ODD) goes
-// through LDS, element by element.
+// power of two of vectors lies in the lanes of one wave; one of other whole
+// vectors goes through LDS, a sum per vector (8192 x 2560 in 32 heads, bf16:
+// 41 us and 148, by elements 97 and 470); any other (ODD) element by element.
 template <int W, int NV, bool ODD, class F>
 __device__ __forceinline__ void group_sums(const Row<W> &row, const Groups &g, int D, F value, float (&out)[NV][ODD ? V : 1],
                                            float *small, float *wide) {
@@ -185,9 +187,26 @@ __device__ __forceinline__ void group_sums(const Row<W> &row, const Groups &g, i
             all = row.sum(all, small);
 #pragma unroll
             for (int j = 0; j < NV; ++j) v[j] = all;
-        } else {
+        } else if (g.lanes) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) v[j] = seg_sum(v[j], g.lanes);
+        } else {
+            float *mine = wide + row.sub * (D / V);
+            __syncthreads();  // (what the last sums read of it has been read)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int i = j * Row<W>::kLanes + row.lane;
+                if (i * V < D) mine[i] = v[j];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int i = j * Row<W>::kLanes + row.lane, first = i / g.vecs * g.vecs;
+                v[j] = 0.f;
+                if (i * V < D)
+#pragma unroll 1  // (rows that do not come here pay for its code: 8192 x 2560 both ways 171 us without, 174, unrolled 176)
+                    for (int k = 0; k < g.vecs; ++k) v[j] += mine[first + k];
+            }
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -464,7 +483,7 @@ int64_t parts_of(int W) { return 256 * (16 / (block_rows(W) * W)); }
 // Waves of a row and vectors per thread.  Forward: as few waves as hold the row in three vectors per thread (eight of
 // them four).  Backward a vector's sums, gradients and inputs take some 120 registers, so one vector per thread and as
 // many waves as that takes, up to eight (rows of 2560: five waves 122 us, two of three vectors each 140, eight 179).
-// Odd rows and groups have four shapes only.
+// Odd groups and rows read by elements have four shapes only.
 struct Shape {
     int W, NV;
 };
@@ -482,8 +501,8 @@ Groups groups_of(int64_t D, int64_t n) {
     g.n = (int)n;
     g.size = (int)(D / n);
     g.inv = 1.f / (float)g.size;
-    const int lanes = g.size / V;
-    g.lanes = (g.size % V == 0 && (lanes & (lanes - 1)) == 0 && lanes <= 64) ? lanes : 0;
+    g.vecs = g.size % V == 0 && g.size <= 64 * V ? g.size / V : 0;
+    g.lanes = (g.vecs & (g.vecs - 1)) == 0 ? g.vecs : 0;
     return g;
 }
 
@@ -504,12 +523,13 @@ template <int IO, bool BWD>
 hipError_t run(const Ptr<IO> &p, const BlockNormArgs &a, hipStream_t s, int &blocks) {
     const Groups g = groups_of(a.D, a.groups);
     const bool single = is_single(a.D * (int64_t)sizeof(*p.f), {p.f, p.res, p.z, p.dr, p.dy, p.r, p.y, p.df, p.dres, p.dz});
-    const bool odd = single || (a.w_out && g.n > 1 && !g.lanes);
+    const bool odd = single || (a.w_out && g.n > 1 && !g.vecs);
     const Shape sh = shape_of(a.D, odd, BWD);
     const int rows = block_rows(sh.W);
     const int64_t n = blocks_of(a.T, sh.W, BWD);
     blocks = (int)std::min<int64_t>(n, kParts);
-    const size_t lds = std::max(odd && g.n > 1 ? (size_t)rows * (a.D + g.n) * 4 : 0, BWD ? (size_t)a.D * 4 : 0);
+    const size_t lds = std::max(g.n == 1 ? 0 : odd ? (size_t)rows * (a.D + g.n) * 4 : g.lanes ? 0 : (size_t)rows * (a.D / V) * 4,
+                                BWD ? (size_t)a.D * 4 : 0);
     using std::integral_constant;
     const auto go = [&](auto w, auto nv, auto odds, auto singles) {
         constexpr int W = decltype(w)::value, NV = decltype(nv)::value;

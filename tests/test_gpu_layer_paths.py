@@ -104,9 +104,24 @@ def test_slices_at_dwords(io):
 @pytest.mark.parametrize("D,groups", [(48, 1), (512, 8), (768, 12), (1600, 1), (2560, 20), (3600, 1), (4096, 2), (6000, 1), (16256, 127), (16380, 4)])
 @pytest.mark.parametrize("off", [0, 1, 2])
 def test_norm_at_any_element(io, D, groups, off):
-    """Rows at a unit, at a dword and at any element, forward and backward: the same to rounding, and right."""
+    """Rows at a unit, at a dword and at any element, forward and backward."""
     say("norm at any element", io, D, groups, off)
-    T, dev = 3, device()
+    _norm_against_definition(io, 3, D, groups, off)
+
+
+# heads of whole vectors that are not a power of two of them, of one to 64 and more; rows of whole dwords that are not
+# whole vectors; rows that are not whole dwords in 16 bits
+@pytest.mark.parametrize("io", IOS)
+@pytest.mark.parametrize("T,D,groups", [(5, 48, 2), (7, 768, 8), (3, 1536, 64), (2, 2560, 32), (3, 3600, 10), (2, 1040, 2),
+                                        (1, 1008, 2), (4, 1050, 1), (3, 1050, 5), (2, 2, 1), (9, 6, 3), (3, 14, 1), (2, 4002, 1),
+                                        (2, 9002, 1), (1, 16382, 1), (3, 1031, 1), (2, 15, 5), (2, 8040, 15)])
+def test_norm_heads_and_row_ends(io, T, D, groups):
+    say("norm heads and row ends", io, T, D, groups)
+    _norm_against_definition(io, T, D, groups, 0)
+
+
+def _norm_against_definition(io, T, D, groups, off):
+    dev = device()
     gen = torch.Generator().manual_seed(D + off)
     flat = [torch.randn(T * D + 2, generator=gen).to(ref.DT[io]).to(dev) for _ in range(5)]
     f, res, z, dr, dy = (t[off:off + T * D].view(T, D) for t in flat)
@@ -157,3 +172,17 @@ def test_embed_many_of_one_and_few_of_all(io, D):
     dw = pkg.embed_bwd(tok.to(device()), dy.to(device()), len(counts), scale=0.7)
     want = torch.zeros(len(counts), D, dtype=torch.float64).index_add_(0, tok, dy.double()) * 0.7
     ref.close(dw, want, io, what="dw")
+
+
+@pytest.mark.parametrize("io", IOS)
+@pytest.mark.parametrize("D", [14, 50, 1050, 1031, 1537])
+def test_norm_leaves_what_is_behind(io, D):
+    """What lies behind the last row, which ends inside a vector, stays as it was."""
+    say("norm leaves what is behind", io, D)
+    T, dev, t = 5, device(), ref.DT[io]
+    f, w = torch.randn(T, D, device=dev).to(t), torch.randn(D, device=dev)
+    flat = [torch.full((T * D + 16,), 3.0, dtype=t, device=dev) for _ in range(2)]
+    pkg.block_norm(f, w_in=w, out=tuple(x[:T * D].view(T, D) for x in flat))
+    r, y = pkg.block_norm(f, w_in=w)
+    for x, want in zip(flat, (r, y)):
+        assert torch.equal(x[:T * D].view(T, D), want) and bool((x[T * D:] == 3.0).all())
