@@ -15,8 +15,8 @@
 // again from f, z and res instead of reading what the forward pass rounded.
 // Squares, sums and all values between are fp32; y is the norm of r before r is
 // rounded.
-// Forward and backward, bf16: 8192 rows of 2560 take 43.6 and 122 us (4.8 and 2.8
-// TB/s; 545 MB, 106 us together at a copy's rate), of 768 15 and 35 us.  The
+// Forward and backward, bf16: 8192 rows of 2560 take 45 and 126 us (4.7 and 2.7
+// TB/s; 545 MB, 106 us together at a copy's rate), of 768 15 and 36 us.  The
 // backward kernel waits for the row's sums, three rounds of them one behind
 // another, with 20 waves a CU at most to cover that.
 #include <hip/hip_runtime.h>
