@@ -779,7 +779,7 @@ class LinearAttnGrads(NamedTuple):
 def linear_attn_bwd(q, k, v, g, dy, scale: float = 1.0, x_in=None, lengths=None, dx_out=None,
                     workspace=None) -> LinearAttnGrads:
     """Gradients of linear_attn (same arguments) for dy [B,N,H,dv] and dx_out [B,H,dk,dv] f32 (upstream of the
-    final state, or None)."""
+    final state, or None).  dg is found as a running difference, to within fp32's rounding of q.dq and k.dk."""
     dev, io, (B, N), H, G, dk, dv, lds, per_token = _attn_args(q, k, v, g, 4)
     f32 = torch.float32
     _tensors(dev, ("dy", dy, v.dtype, (B, N, H, dv)), ("x_in?", x_in, f32, (B, H, dk, dv)),
@@ -805,7 +805,8 @@ def linear_attn_step(q, k, v, g, x, scale: float = 1.0, slots=None, x_out=None, 
     q, k [B,G,dk]; v [B,H,dv]; g [H] or [B,H]; x [P,H,dk,dv] f32, a pool of
     states, updated in place (or into ``x_out``, of which only the slots in use
     are written); slots [B] int32, the slot of each sequence (sequence b in slot
-    b if None).  A slot outside the pool marks an idle row: its output is zero.
+    b if None).  Slots in use must differ; one outside the pool
+    marks an idle row: its output is zero.
     Returns y [B,H,dv]."""
     dev, io, (B,), H, G, dk, dv, lds, per_token = _attn_args(q, k, v, g, 3)
     P = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 4 else 0
