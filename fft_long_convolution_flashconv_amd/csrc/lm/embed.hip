@@ -2,8 +2,9 @@
 //
 //   y[t] = scale w[tok[t]],   dw[v] = scale sum_{t: tok[t] = v} dy[t]
 // A token outside the table gives a zero row and no gradient.  Both are copies
-// with a little arithmetic: HBM bound.  A row's sum runs over its tokens in
-// order, in fp32, and is rounded once: equal calls give equal bits.
+// with a little arithmetic: HBM bound.  A row's sum runs over its tokens in a
+// fixed order (that of time, or by units of it), in fp32, and is rounded once:
+// equal calls give equal bits.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
