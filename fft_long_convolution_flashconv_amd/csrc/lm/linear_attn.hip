@@ -263,7 +263,7 @@ struct Segs {
 constexpr int waves_per_simd(int io, int KP, int WV, int what, bool whole_heads) {
     return KP > 128 && WV == 4                                           ? 1
            : io == IO_F32 || KP > 64 || !whole_heads || WV == 8          ? 2
-           : KP == 32 && !(io == IO_BF16 && what == BACKWARD)            ? 4
+           : KP == 32 && !(io == IO_BF16 && what != STATES)              ? 4
                                                                          : 3;
 }
 
@@ -283,8 +283,8 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, DO, WHOLE)) voi
     constexpr int E = LK::E;
     constexpr int NA = C * LK::CH / TH, NC = C * LM::CH / TH;  // units of 16 bytes per thread
     static_assert(C * LK::CH % TH == 0 && C * LM::CH % TH == 0 && NT <= 4, "whole units, a wave per 16 steps");
-    // pieces of weights and states in the output's products (24 bits where the decays' gradients take them); fragments of weights
-    constexpr int NP = IO == IO_F32 ? 1 : IO == IO_F16 || DO == FORWARD ? 2 : 3, WF = NT == 4 ? 6 : 2;
+    // pieces of weights and states in the output's products: 22 bits in fp16, 24 in bf16; fragments of weights
+    constexpr int NP = X::UPD, WF = NT == 4 ? 6 : 2;
     // Two places for tiles where the LDS has room for them without giving up a block: a chunk's are then written while
     // the last one's are still read.
     constexpr int TWO = OUT && WV == 8 && KP <= 128 ? 2 : 1;
