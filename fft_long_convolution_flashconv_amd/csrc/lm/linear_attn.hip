@@ -250,11 +250,31 @@ enum { STATES, FORWARD, BACKWARD };  // what a launch of chunks is for
 // prompts of 1024 steps: 31.5 us, with the launch 35.7).
 constexpr int64_t kFew = 8;
 
+// The decay over a segment, 2^up (hi + lo).  A segment is longer than the 64 steps whose factor has to be within fp32, so
+// its own may be far outside (e^96 over 128 steps of +0.75) while the states at both its ends are not.  Past 2^96 either
+// way hi is 1 to 2, so that a state times 2^up is within fp32 where what it comes to is.
+struct Factor {
+    float hi, lo;
+    int up, unused;
+};
+__device__ __forceinline__ Factor factor_of(double e) {  // 2^e
+    double up = 0.0;
+    if (!(fabs(e) <= 96.0)) up = fmin(fmax(floor(e), -512.0), 512.0);  // (2^512 of any state but zero is infinite, 2^-512 zero)
+    const double f = exp2(e - up);
+    const float hi = (float)f;
+    return {hi, (float)(f - (double)hi), (int)up, 0};
+}
+// (without a choice: one for each number keeps the loads apart, 51 us instead of 33 for eight prompts of 1024 steps)
+__device__ __forceinline__ float carried(float x, const Factor &f, float add) {
+    x = __builtin_amdgcn_ldexpf(x, f.up);
+    return fmaf(x, f.hi, fmaf(x, f.lo, add));
+}
+
 // Where the segments of the rows meet.
 struct Segs {
     int64_t len, n;      // steps of one, number
     float *state;        // [role][seg][B*H][K*M]: what a segment adds, then the state that enters it
-    float *factor;       // [role][seg][B*H][2]: the decay over it, in two parts
+    Factor *factor;      // [role][seg][B*H]: the decay over it
     int64_t plane;       // K*M
 };
 
@@ -334,11 +354,12 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, DO, WHOLE)) voi
     if (OUT && few)
         for (int64_t q = 0; q < seg; ++q) {
             const int64_t at_q = ((int64_t)blockIdx.y * sg.n + q) * BH + bh;
-            const float f1 = sg.factor[at_q * 2], f2 = sg.factor[at_q * 2 + 1], *add = sg.state + at_q * sg.plane;
+            const Factor f = sg.factor[at_q];
+            const float *add = sg.state + at_q * sg.plane;
 #pragma unroll
             for (int m = 0; m < 2 * KS; ++m)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) st[m][j] = fmaf(st[m][j], f1, fmaf(st[m][j], f2, add[state_at(m, j)]));
+                for (int j = 0; j < 4; ++j) st[m][j] = carried(st[m][j], f, add[state_at(m, j)]);
         }
 #pragma unroll
     for (int m = 0; m < 2 * KS; ++m)
@@ -730,11 +751,7 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, DO, WHOLE)) voi
             }
     } else {
         put(sg.state + slot * sg.plane);
-        if (tile == 0 && wave == EW && lane == 0) {
-            const double f = exp2(all);
-            sg.factor[slot * 2] = (float)f;
-            sg.factor[slot * 2 + 1] = (float)(f - (double)(float)f);
-        }
+        if (tile == 0 && wave == EW && lane == 0) sg.factor[slot] = factor_of(all);
     }
 }
 
@@ -751,7 +768,7 @@ __global__ __launch_bounds__(256) void k_lin_enter(Roles roles, Segs sg, int64_t
         float *p = sg.state + slot * sg.plane + e;
         const float add = j + 1 < sg.n ? *p : 0.f;
         *p = x;
-        if (j + 1 < sg.n) x = fmaf(x, sg.factor[slot * 2], fmaf(x, sg.factor[slot * 2 + 1], add));
+        if (j + 1 < sg.n) x = carried(x, sg.factor[slot], add);
     }
 }
 
@@ -923,7 +940,7 @@ Segs segs_of(int64_t N, int64_t blocks, int64_t at_once) {
     return g;
 }
 int64_t seg_bytes(const Segs &g, int64_t BH, int roles, int64_t plane) {
-    return g.n == 1 ? 0 : up(roles * g.n * BH * plane * 4) + up(roles * g.n * BH * 8);
+    return g.n == 1 ? 0 : up(roles * g.n * BH * plane * 4) + up(roles * g.n * BH * (int64_t)sizeof(Factor));
 }
 
 template <int IO, int KP, int WV, int DO, bool WHOLE>
@@ -957,7 +974,7 @@ hipError_t run_roles(const Roles &r, int n, const Shape &s, int K, int M, Segs g
     const int tiles = tiles_of(M);
     g.plane = plane;
     g.state = (float *)ws;
-    g.factor = (float *)((char *)ws + up(n * g.n * s.B * s.H * plane * 4));
+    g.factor = (Factor *)((char *)ws + up(n * g.n * s.B * s.H * plane * 4));
     if (!whole<IO>(r, n)) {
         const bool few = cols_of(M) == 64;
         if (K <= 64) return few ? run_chunks<IO, 64, 4, DO, false>(r, n, s, g, tiles, st) : run_chunks<IO, 64, 8, DO, false>(r, n, s, g, tiles, st);

@@ -443,8 +443,9 @@ h3conv_status h3conv_selective_step(const void *u, const void *dt, const float *
  *   v, y      [B,N,H,dv]   io dtype   v likewise with ldv (>= H dv); y is contiguous
  *   g         [H]          fp32       log of the decay factor of each head, or, if per_token,
  *             [B,N,H]                 of each token and head.  Usually <= 0; -infinity starts the
- *                                     state anew.  A state that grows is right while it and the
- *                                     factors over any 64 steps are within fp32.
+ *                                     state anew.  A state that grows is right while it, S_t^T q_t
+ *                                     and the factors over any 64 steps are within fp32, however
+ *                                     large the factor over more steps is.
  *   x_in      [B,H,dk,dv]  fp32       initial state, or NULL for zero
  *   lengths   [B]          int32      valid steps of every row (clamped to 0 .. N), or NULL = N:
  *                                     later steps leave the state alone, their y is zero and
