@@ -774,8 +774,11 @@ __global__ __launch_bounds__(256) void k_lin_enter(Roles roles, Segs sg, int64_t
 
 // dg of one sequence and head from the dot products, from the end on, in 64 bits.  The dot products are fp32, and what
 // they are off by adds up along the sequence; but before the first step it has to come to <x_in, dx_in>, so what it
-// misses that by is taken back evenly over the steps (a third of the squared error on average is left).  Two or three
-// passes over N numbers and two over a state by one block: 7 us beside 310 for four sequences of 2048 steps and 20 heads.
+// misses that by is taken back evenly over the steps (a third of the squared error on average is left).  Before a step
+// whose factor is 0 it has to come to 0: the sum begins anew there and is corrected for itself, so that nothing of a
+// document reaches the one before it (a document before one of 1e4 times its gradients: 1e-3 of dg without).  Two or
+// three passes over N numbers and two over a state by one block: 7 us beside 310 for four sequences of 2048 steps and
+// 20 heads.
 constexpr int kDg = 1024;
 __device__ __forceinline__ double block_sum(double v, double *lds) {
     v = lane_of(sum_up_to(v), 63);
@@ -786,57 +789,126 @@ __device__ __forceinline__ double block_sum(double v, double *lds) {
     for (int w = 0; w < kDg / 64; ++w) v += lds[w];
     return v;
 }
-__global__ __launch_bounds__(kDg) void k_lin_dg(const float *__restrict__ dq, const float *__restrict__ dk, int tiles,
-                                                const float *__restrict__ s_end, const float *__restrict__ ds_end,
-                                                const float *__restrict__ x_in, const float *__restrict__ dx_in, int64_t kv,
-                                                Shape s, float *dg, double *sums) {
-    __shared__ double lds[kDg / 64];
+// The sum over the lanes from the last one in `starts` up to this one (or from the wave's first, where there is none).
+__device__ __forceinline__ double sum_from_start(double v, uint64_t starts) {
+    if (starts == 0) return sum_up_to(v);
+    const int lane = threadIdx.x & 63;
+    int from = 63 - __builtin_clzll((starts & (~0ull >> (63 - lane))) | 1);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const double u = __shfl_up(v, d);
+        if (lane - d >= from) v += u;
+    }
+    return v;
+}
+__global__ __launch_bounds__(kDg) void k_lin_dg(float *dq, float *dk, int tiles, const float *__restrict__ s_end,
+                                                const float *__restrict__ ds_end, const float *__restrict__ x_in,
+                                                const float *__restrict__ dx_in, int64_t kv, Shape s, float *dg, double *sums) {
+    constexpr int W = kDg / 64;
+    __shared__ double lds[W];
+    __shared__ int edge[W];
     const int64_t bh = block_id();
     if (bh >= s.B * s.H) return;
-    const int64_t b = bh / s.H, h = bh - b * s.H, n = row_len(s.lengths, b, s.N), plane = s.B * s.H * s.N;
-    const int tid = threadIdx.x, wave = tid >> 6;
-    double carry = 0.0, total = 0.0;
+    const int64_t b = bh / s.H, h = bh - b * s.H, plane = s.B * s.H * s.N;
+    const int n = (int)row_len(s.lengths, b, s.N), tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    dq += bh * s.N, dk += bh * s.N;
+    double carry = 0.0, front = 0.0;  // <S, D> behind the last step, and before the first
     if (ds_end) {
         for (int64_t i = tid; i < kv; i += kDg) carry += (double)s_end[bh * kv + i] * ds_end[bh * kv + i];
         carry = block_sum(carry, lds);
     }
-    const auto step = [&](int64_t t) {
+    if (x_in && dx_in) {
+        for (int64_t i = tid; i < kv; i += kDg) front += (double)x_in[bh * kv + i] * dx_in[bh * kv + i];
+        front = block_sum(front, lds);
+    }
+    const bool known = !x_in || dx_in;  // (front)
+    const auto step = [&](int t) {
         double v = 0.0;
-        if (t >= 0)
-            for (int i = 0; i < tiles; ++i) v += (double)dq[i * plane + bh * s.N + t] - (double)dk[i * plane + bh * s.N + t];
+        for (int i = 0; i < tiles; ++i) v += (double)dq[i * plane + t] - (double)dk[i * plane + t];
         return v;
     };
-    double missed = 0.0;
-    if (!x_in || dx_in) {
-        for (int64_t t = tid; t < n; t += kDg) missed += step(t);
-        if (x_in)
-            for (int64_t i = tid; i < kv; i += kDg) missed -= (double)x_in[bh * kv + i] * dx_in[bh * kv + i];
-        missed = (block_sum(missed, lds) + carry) / (double)(n > 0 ? n : 1);
-    }
-    for (int64_t i0 = 0; i0 < n; i0 += kDg) {  // from the end
-        const int64_t t = n - 1 - i0 - tid;
+    dg += s.per_token ? b * s.N * s.H + h : 0;
+    const auto clears = [&](int t) { return (s.per_token ? s.g[(b * s.N + t) * s.H + h] : s.g[h]) < kZeroBelow; };
+    double all = 0.0, weighted = 0.0;  // sums of all steps, and of all of their sums
+    bool any = false;
+    for (int t = tid; t < n; t += kDg) {
         const double v = step(t);
-        const double sum = sum_up_to(v);
+        all += v;
+        weighted += v * (double)(t + 1);
+        any |= clears(t);
+    }
+    const double missed = known && n > 0 ? (block_sum(all, lds) + carry - front) / (double)n : 0.0;
+    if (!s.per_token) {
+        weighted = block_sum(weighted, lds) + carry * (double)n - missed * 0.5 * (double)n * (double)(n + 1);
+        if (tid == 0) sums[bh] = any || n == 0 ? 0.0 : weighted;
+        return;
+    }
+    for (int t = n + tid; t < s.N; t += kDg) dg[t * s.H] = 0.f;
+    if (!__syncthreads_or(any)) {  // one part: 9 us for rows of 2048, as below 16
+        for (int i0 = 0; i0 < n; i0 += kDg) {
+            const int t = n - 1 - i0 - tid;
+            const double sum = sum_up_to(t >= 0 ? step(t) : 0.0);
+            __syncthreads();
+            if (lane == 63) lds[wave] = sum;
+            __syncthreads();
+            double before = carry;
+            for (int w = 0; w < W; ++w) {
+                before += w < wave ? lds[w] : 0.0;
+                carry += lds[w];
+            }
+            if (t >= 0) dg[t * s.H] = (float)(before + sum - missed * (double)(n - t));
+        }
+        return;
+    }
+    // From the end: the sums, in two parts in the place of the dot products, and where each began, in that of dg.
+    int last = n;
+    for (int i0 = 0; i0 < n; i0 += kDg) {
+        const int t = n - 1 - i0 - tid;
+        const bool start = t >= 0 && t + 1 < n && clears(t + 1);
+        const uint64_t starts = __ballot(start), mine = starts & (~0ull >> (63 - lane));
+        double sum = sum_from_start(t >= 0 ? step(t) : 0.0, starts);
+        int end = mine ? t + 1 + lane - (63 - __builtin_clzll(mine)) : -1;
         __syncthreads();
-        if ((tid & 63) == 63) lds[wave] = sum;
+        if (lane == 63) lds[wave] = sum, edge[wave] = end;
         __syncthreads();
-        double before = carry;
-        for (int w = 0; w < kDg / 64; ++w) {
-            before += w < wave ? lds[w] : 0.0;
-            carry += lds[w];
+        for (int w = 0; w < W; ++w) {
+            if (w == wave && end < 0) sum += carry, end = last;
+            carry = edge[w] < 0 ? carry + lds[w] : lds[w];
+            last = edge[w] < 0 ? last : edge[w];
         }
         if (t >= 0) {
-            const float g = s.per_token ? s.g[(b * s.N + t) * s.H + h] : s.g[h];
-            const double d = g < kZeroBelow ? 0.0 : before + sum - missed * (double)(n - t);
-            if (s.per_token) dg[(b * s.N + t) * s.H + h] = (float)d;
-            else total += d;
+            const float hi = (float)sum;
+            dq[t] = hi, dk[t] = (float)(sum - (double)hi);
+            dg[t * s.H] = __int_as_float(end);
         }
     }
-    if (s.per_token) {
-        for (int64_t t = n + tid; t < s.N; t += kDg) dg[(b * s.N + t) * s.H + h] = 0.f;
-    } else {
-        total = block_sum(total, lds);
-        if (tid == 0) sums[bh] = total;
+    __syncthreads();
+    // From the front: what each sum misses at its first step (one that clears, or the row's first) is spread over its steps.
+    int first = -1;
+    for (int t0 = 0; t0 < n; t0 += kDg) {
+        const int t = t0 + tid;
+        double sum = 0.0;
+        int end = 0, from = -1;
+        bool clear = false;
+        if (t < n) {
+            clear = clears(t);
+            sum = (double)dq[t] + (double)dk[t];
+            end = __float_as_int(dg[t * s.H]);
+        }
+        const uint64_t mine = __ballot(clear) & (~0ull >> (63 - lane));
+        if (mine) from = t - lane + (63 - __builtin_clzll(mine));
+        __syncthreads();
+        if (lane == 63) edge[wave] = from;
+        __syncthreads();
+        for (int w = 0; w < W; ++w) {
+            if (w == wave && from < 0) from = first;
+            first = edge[w] < 0 ? first : edge[w];
+        }
+        if (t < n) {
+            const int at = from < 0 ? 0 : from;
+            const double there = (double)dq[at] + (double)dk[at], off = from >= 0 ? there : known ? there - front : 0.0;
+            dg[t * s.H] = clear ? 0.f : (float)(sum - off * ((double)(end - t) / (double)(end - at)));
+        }
     }
 }
 

@@ -479,8 +479,10 @@ size_t h3conv_linear_attn_workspace_size(int64_t B, int64_t N, int64_t H, int64_
  *   ws        at least h3conv_linear_attn_bwd_workspace_size bytes
  * Gradients are contiguous, written, and zero past a row's length; all sums run in a
  * fixed order.  Nothing is kept from the forward pass: the states are formed again.
- * dg_t is a running difference of q_t.dq_t and k_t.dk_t: it is within fp32's rounding
- * of those, also where e^{g_t} makes it much smaller (and 0 where e^{g_t} is 0 in fp32).
+ * dg_t is a running difference of q_t.dq_t and k_t.dk_t over the steps behind t, up to the
+ * next whose e^g is 0 in fp32 (there dg is 0 and the difference begins anew: packed documents
+ * do not meet): n steps lose about sqrt(n) of fp32's rounding of those products, also where
+ * e^{g_t} makes dg_t much smaller than they are.
  */
 h3conv_status h3conv_linear_attn_bwd(const void *q, const void *k, const void *v, const float *g, const float *x_in,
                                      const int32_t *lengths, const void *dy, const float *dx_out, void *dq, void *dk_,
