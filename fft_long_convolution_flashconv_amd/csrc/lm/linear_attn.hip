@@ -46,7 +46,7 @@
 namespace h3c {
 namespace {
 
-// A factor e^g of g below this is zero in fp32, and so is what follows from it.
+// A factor e^g of g below this is zero in fp32, and so is what follows from it.  (A g that is NaN is below neither.)
 constexpr float kLeast = -200.f, kZeroBelow = -104.f;
 
 // One tensor of tokens and heads, [B,N,heads,dim] with `ld` elements between tokens.
@@ -449,7 +449,7 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, DO, WHOLE)) voi
     // is given to the next chunk's: the product of all stays within one rounding of what it should be.
     double lost = 1.0;
     const auto exponents = [&](float *dec, float g) INLINE {
-        const double own = (double)fmaxf(g, kLeast) * 1.4426950408889634;
+        const double own = (double)(g < kLeast ? kLeast : g) * 1.4426950408889634;
         const double sum = sum_up_to(own), total = lane_of(sum, C - 1), e = back ? sum - own : sum;
         all += total;
         if (lane < C) {

@@ -446,6 +446,7 @@ h3conv_status h3conv_selective_step(const void *u, const void *dt, const float *
  *                                     state anew.  A state that grows is right while it, S_t^T q_t
  *                                     and the factors over any 64 steps are within fp32, however
  *                                     large the factor over more steps is.
+ *                                     NaN makes what is behind it NaN.
  *   x_in      [B,H,dk,dv]  fp32       initial state, or NULL for zero
  *   lengths   [B]          int32      valid steps of every row (clamped to 0 .. N), or NULL = N:
  *                                     later steps leave the state alone, their y is zero and

@@ -1,0 +1,45 @@
+"""Linear attention at the edges of what it takes: decays that are no number."""
+import pytest
+import torch
+
+import fft_long_convolution_flashconv_amd as pkg
+import lm_reference as ref
+from parity_util import device, say
+
+pytestmark = pytest.mark.gpu
+DT = ref.DT
+
+
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+def test_nan_decay(io):
+    """A decay that is NaN shows in everything behind it, in a prompt as in steps, and nowhere else."""
+    say("linear_attn nan decay", io)
+    B, N, H, d, at = 2, 150, 2, 16, 70
+    gen = torch.Generator().manual_seed(1)
+    q, k, v, dy = (torch.randn(B, N, H, d, generator=gen).to(DT[io]).to(device()) for _ in range(4))
+    g = (-0.1 * torch.rand(B, N, H, generator=gen)).to(device())
+    y0, x0 = pkg.linear_attn(q, k, v, g, return_state=True)
+    g[1, at, 1] = float("nan")
+    y, x = pkg.linear_attn(q, k, v, g, return_state=True)
+    hit = torch.zeros(B, N, H, dtype=torch.bool, device=device())
+    hit[1, at:, 1] = True
+    assert bool(torch.isnan(y[hit]).all()) and torch.equal(y[~hit], y0[~hit])
+    assert bool(torch.isnan(x[1, 1]).all()) and torch.equal(x[0], x0[0]) and torch.equal(x[1, 0], x0[1, 0])
+    pool = torch.zeros(B, H, d, d, device=device())
+    for t in (at - 1, at, at + 1):
+        s = pkg.linear_attn_step(*(m[:, t].contiguous() for m in (q, k, v, g)), pool)
+        assert torch.equal(torch.isnan(s), torch.isnan(y[:, t]))
+    o = pkg.linear_attn_bwd(q, k, v, g, dy)
+    assert bool(torch.isnan(o.dq[1, at:, 1]).all()) and bool(torch.isnan(o.dv[1, :at, 1]).all())
+    assert bool(torch.isnan(o.dk[1, :at, 1]).all()) and bool(torch.isnan(o.dg[1, at, 1]))
+    for t in (o.dq, o.dk, o.dv, o.dg):
+        assert bool(torch.isfinite(t[0]).all()) and bool(torch.isfinite(t[1, :, 0]).all())
+
+
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+def test_nan_decay_of_a_head(io):
+    gen = torch.Generator().manual_seed(1)
+    q, k, v = (torch.randn(2, 40, 3, 8, generator=gen).to(DT[io]).to(device()) for _ in range(3))
+    g = torch.tensor([-0.1, float("nan"), -0.2], device=device())
+    y = pkg.linear_attn(q, k, v, g)
+    assert bool(torch.isnan(y[:, :, 1]).all()) and bool(torch.isfinite(y[:, :, ::2]).all())
