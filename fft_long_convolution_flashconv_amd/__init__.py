@@ -786,8 +786,8 @@ def linear_attn_bwd(q, k, v, g, dy, scale: float = 1.0, x_in=None, lengths=None,
              ("lengths?", lengths, torch.int32, (B,)), ("dx_out?", dx_out, f32, (B, H, dk, dv)))
     ws = _scratch(workspace, _size("h3conv_linear_attn_bwd_workspace_size", B, N, H, G, dk, dv), v)
 
-    def new(*shape, dtype=v.dtype):
-        return torch.empty(shape, device=v.device, dtype=dtype)
+    def new(*shape, dtype=v.dtype):  # (no heads: the sums over them are not written)
+        return (torch.empty if H else torch.zeros)(shape, device=v.device, dtype=dtype)
 
     o = LinearAttnGrads(new(B, N, G, dk), new(B, N, G, dk), new(B, N, H, dv), torch.empty_like(g),
                         new(B, H, dk, dv, dtype=f32))

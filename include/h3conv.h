@@ -479,7 +479,8 @@ size_t h3conv_linear_attn_workspace_size(int64_t B, int64_t N, int64_t H, int64_
  *   dx_in     [B,H,dk,dv]  fp32       may be NULL
  *   ws        at least h3conv_linear_attn_bwd_workspace_size bytes
  * Gradients are contiguous, written, and zero past a row's length; all sums run in a
- * fixed order.  Nothing is kept from the forward pass: the states are formed again.
+ * fixed order.  H = 0 does nothing: dq and dk, sums over no heads, are left to the caller.
+ * Nothing is kept from the forward pass: the states are formed again.
  * dg_t is a running difference of q_t.dq_t and k_t.dk_t over the steps behind t, up to the
  * next whose e^g is 0 in fp32 (there dg is 0 and the difference begins anew: packed documents
  * do not meet): n steps lose about sqrt(n) of fp32's rounding of those products, also where

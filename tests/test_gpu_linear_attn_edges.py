@@ -1,4 +1,4 @@
-"""Linear attention at the edges of what it takes: decays that are no number."""
+"""Linear attention at the edges of what it takes: decays that are no number, no heads."""
 import pytest
 import torch
 
@@ -43,3 +43,18 @@ def test_nan_decay_of_a_head(io):
     g = torch.tensor([-0.1, float("nan"), -0.2], device=device())
     y = pkg.linear_attn(q, k, v, g)
     assert bool(torch.isnan(y[:, :, 1]).all()) and bool(torch.isfinite(y[:, :, ::2]).all())
+
+
+@pytest.mark.parametrize("per_token", [False, True])
+def test_no_heads(per_token):
+    """Without heads q and k have gradients all the same: sums over no heads."""
+    dev = device()
+    junk = torch.full((3, 5, 2, 8), 7.0, device=dev)
+    del junk  # (what the gradients' memory may hold)
+    q, k, v = torch.randn(3, 5, 2, 8).to(dev), torch.randn(3, 5, 2, 8).to(dev), torch.empty(3, 5, 0, 4, device=dev)
+    g = torch.empty((3, 5, 0) if per_token else (0,), device=dev)
+    o = pkg.linear_attn_bwd(q, k, v, g, v)
+    assert o.dq.shape == q.shape and o.dk.shape == k.shape and not o.dq.any() and not o.dk.any()
+    assert o.dv.shape == v.shape and o.dg.shape == g.shape and o.dx_in.shape == (3, 0, 8, 4)
+    y, x = pkg.linear_attn(q, k, v, g, return_state=True)
+    assert y.shape == v.shape and x.shape == (3, 0, 8, 4)
