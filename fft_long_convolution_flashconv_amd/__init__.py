@@ -662,8 +662,9 @@ def selective_scan_bwd(u, dt, A, Bm, C, dy, saved, D=None, z=None, dt_bias=None,
              ("saved", saved, f32, (_size("h3conv_selective_saved_size", B, H, N, S) // 4,)),
              ("lengths?", lengths, torch.int32, (B,)), ("dx_out?", dx_out, f32, (B, H, S)))
     ws = _scratch(workspace, _size("h3conv_selective_scan_bwd_workspace_size", B, H, N, S, G), u)
+    sums = torch.empty_like if H else torch.zeros_like  # (no channels: the sums over them are not written)
     g = SelectiveScanGrads(
-        torch.empty_like(u), torch.empty_like(dt), torch.empty_like(A), torch.empty_like(Bm), torch.empty_like(C),
+        torch.empty_like(u), torch.empty_like(dt), torch.empty_like(A), sums(Bm), sums(C),
         None if D is None else torch.empty_like(D), None if z is None else torch.empty_like(z),
         None if dt_bias is None else torch.empty_like(dt_bias), torch.empty((B, H, S), device=u.device, dtype=f32))
     _check(load().h3conv_selective_scan_bwd(

@@ -402,7 +402,8 @@ size_t h3conv_selective_saved_size(int64_t B, int64_t H, int64_t N, int64_t S);
  *   dD, ddt_bias [H]     fp32       likewise; may be NULL
  *   dx_in     [B,H,S]    fp32       may be NULL
  *   ws        at least h3conv_selective_scan_bwd_workspace_size bytes
- * Gradients are written, not accumulated into; all sums run in a fixed order.
+ * Gradients are written, not accumulated into; all sums run in a fixed order.  H = 0 does
+ * nothing: dB and dC, sums over no channels, are left to the caller.
  */
 h3conv_status h3conv_selective_scan_bwd(const void *u, const void *dt, const float *A, const void *Bm, const void *C,
                                         const float *D, const void *z, const float *dt_bias, const int32_t *lengths,
