@@ -1,8 +1,10 @@
-"""Linear attention at the edges of what it takes: decays that are no number, no heads."""
+"""Linear attention at the edges of what it takes: decays that are no number, no heads, states near fp32's
+largest."""
 import pytest
 import torch
 
 import fft_long_convolution_flashconv_amd as pkg
+import layer_reference as lref
 import lm_reference as ref
 from parity_util import device, say
 
@@ -58,3 +60,19 @@ def test_no_heads(per_token):
     assert o.dv.shape == v.shape and o.dg.shape == g.shape and o.dx_in.shape == (3, 0, 8, 4)
     y, x = pkg.linear_attn(q, k, v, g, return_state=True)
     assert y.shape == v.shape and x.shape == (3, 0, 8, 4)
+
+
+@pytest.mark.parametrize("io,size", [(io, size) for io in ("f32", "f16", "bf16") for size in (117, 120, 124) if size < 124 or io == "f16"])
+def test_large_states(io, size):
+    """States near fp32's largest, read with a small scale.  (Of 2^124 times normal numbers q . S is 2^(124 + 2.5) times
+    such, above 2^128 for a few of 8320: outside fp32 before the scale, which only fp16 forms of scaled states.)"""
+    say("linear_attn large states", io, size)
+    gen = torch.Generator().manual_seed(6)
+    B, N, H, d = 1, 130, 2, 32
+    q, k, v = (torch.randn(B, N, H, d, generator=gen).to(DT[io]) for _ in range(3))
+    g, x = torch.tensor([-0.01, 0.0]), torch.randn(B, H, d, d, generator=gen) * 2.0 ** size
+    scale = 2.0 ** -size
+    y, xo = pkg.linear_attn(*(t.to(device()) for t in (q, k, v, g)), scale=scale, x_in=x.to(device()), return_state=True)
+    ry, rx = lref.linear_attn(q.double(), k.double(), v.double(), g.double(), scale, x.double())
+    ref.close(y, ry, io, what="y")
+    ref.close(xo, rx, what="x_out")
