@@ -136,6 +136,13 @@ __device__ __forceinline__ float seg_sum(float v, int n) {
     return v;
 }
 
+// x^-1/2; the instruction alone takes numbers below fp32's least normal one, which eps = 0 leaves of small rows, for zeros.
+__device__ __forceinline__ float inv_root(float x) {
+    float r = __builtin_amdgcn_rsqf(x);
+    if (__ballot(x < 0x1p-100f)) r = x < 0x1p-100f ? __builtin_amdgcn_rsqf(x * 0x1p+80f) * 0x1p+40f : r;  // (a choice of the wave)
+    return r;
+}
+
 // The threads of a row: W waves of a block of one, two or four rows.
 template <int W>
 struct Row {
@@ -289,7 +296,7 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W * NV >= 16 ? 2 : BWD && 
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int i = 0; i < (ODD ? V : 1); ++i) ra[j][i] = __builtin_amdgcn_rsqf(fmaf(ra[j][i], g.inv, eps));
+                for (int i = 0; i < (ODD ? V : 1); ++i) ra[j][i] = inv_root(fmaf(ra[j][i], g.inv, eps));
         }
         // m and r of one vector
         const auto middle = [&](int j, float (&m)[V], float (&r)[V], float (&nf)[V], float (&sg)[V]) {
@@ -337,7 +344,7 @@ __global__ __launch_bounds__(Row<W>::kThreads, ODD || W * NV >= 16 ? 2 : BWD && 
             }
         }
         if (in_norm) {
-            rb = __builtin_amdgcn_rsqf(fmaf(row.sum(ss, small[1]), invD, eps));
+            rb = inv_root(fmaf(row.sum(ss, small[1]), invD, eps));
             if constexpr (BWD)
                 if (p.dy) c1 = row.sum(er, small[2]) * rb * invD;
         }

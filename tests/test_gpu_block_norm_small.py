@@ -1,0 +1,50 @@
+"""The norms around a block of rows whose squares are at fp32's lower end, with an eps of zero or next to nothing."""
+import pytest
+import torch
+
+import fft_long_convolution_flashconv_amd as pkg
+import layer_reference as lref
+import lm_reference as ref
+from parity_util import device, say
+
+pytestmark = pytest.mark.gpu
+DT = ref.DT
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("power", [-60, -63, -64])
+@pytest.mark.parametrize("D,groups", [(64, 1), (768, 1), (770, 1), (201, 1)])
+def test_small_rows(io, power, D, groups):
+    """Squares of 2^-128 and more are held to 2^-150, 2^-22 of them: within the tolerance of fp32 results."""
+    say("block_norm small rows", io, power, D, groups)
+    gen = torch.Generator().manual_seed(3)
+
+    def n(*s, dtype=DT[io]):
+        return ((1.0 + torch.rand(*s, generator=gen)) * (1 - 2 * torch.randint(0, 2, s, generator=gen))).to(dtype)
+
+    T, size = 6, 2.0 ** power
+    f, dr, dy = n(T, D) * size, n(T, D) * size, n(T, D)
+    w_out, w_in = n(D, dtype=torch.float32) * size, n(D, dtype=torch.float32)
+    a = dict(f=f, w_out=w_out, w_in=w_in)
+    g = {k: v.to(device()) for k, v in a.items()}
+    # both norms: the second one of r = norm(f) w_out, as small as f
+    r, y = pkg.block_norm(g["f"], w_out=g["w_out"], w_in=g["w_in"], groups=groups, eps=0.0)
+    o = pkg.block_norm_bwd(g["f"], dr=dr.to(device()), dy=dy.to(device()), w_out=g["w_out"], w_in=g["w_in"], groups=groups, eps=0.0)
+    leaf = {k: ref.leaf(v) for k, v in a.items()}
+    rr, ry = lref.block_norm(leaf["f"], w_out=leaf["w_out"], w_in=leaf["w_in"], groups=groups, eps=0.0)
+    ((rr * dr.double()).sum() + (ry * dy.double()).sum()).backward()
+    ref.close(r.double() / size, rr / size, io, what="r")
+    ref.close(y, ry, io, what="y")
+    ref.close(o.df.double() * size, leaf["f"].grad * size, io, what="df")
+    ref.close(o.dw_out.double() * size, leaf["w_out"].grad * size, what="dw_out")
+    ref.close(o.dw_in, leaf["w_in"].grad, what="dw_in")
+
+
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 201])
+def test_zeros_with_the_least_eps(io, D):
+    f, w = torch.zeros(3, D, dtype=DT[io], device=device()), torch.ones(D, device=device())
+    r, y = pkg.block_norm(f, w_out=w, w_in=w, eps=1e-40)
+    assert not r.any() and not y.any()
+    o = pkg.block_norm_bwd(f, dr=torch.zeros_like(f), dy=torch.zeros_like(f), w_out=w, w_in=w, eps=1e-40)
+    assert not o.df.any() and not o.dw_out.any() and not o.dw_in.any()
