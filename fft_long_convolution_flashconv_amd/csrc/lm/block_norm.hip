@@ -534,6 +534,9 @@ hipError_t run(const Ptr<IO> &p, const BlockNormArgs &a, hipStream_t s, int &blo
     const Shape sh = shape_of(a.D, odd, BWD);
     const int rows = block_rows(sh.W);
     const int64_t n = blocks_of(a.T, sh.W, BWD);
+    // (the root of nothing at all is infinite: lanes past a row's end, whose group is empty, would put 0 times that into
+    // the row's sums)
+    const float eps = std::max(a.eps, 0x1p-149f);
     blocks = (int)std::min<int64_t>(n, kParts);
     const size_t lds = std::max(g.n == 1 ? 0 : odd ? (size_t)rows * (a.D + g.n) * 4 : g.lanes ? 0 : (size_t)rows * (a.D / V) * 4,
                                 BWD ? (size_t)a.D * 4 : 0);
@@ -541,7 +544,7 @@ hipError_t run(const Ptr<IO> &p, const BlockNormArgs &a, hipStream_t s, int &blo
     const auto go = [&](auto w, auto nv, auto odds, auto singles) {
         constexpr int W = decltype(w)::value, NV = decltype(nv)::value;
         return launch(k_block_norm<IO, W, NV, decltype(odds)::value, decltype(singles)::value, BWD>, grid_of(n), dim3(Row<W>::kThreads), lds, s, p, a.T,
-                      (int)a.D, g, a.eps);
+                      (int)a.D, g, eps);
     };
     const auto whole = [&](auto w, auto nv) { return go(w, nv, std::false_type{}, std::false_type{}); };
     constexpr integral_constant<int, 1> one{};

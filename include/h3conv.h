@@ -522,7 +522,8 @@ h3conv_status h3conv_linear_attn_step(const void *q, const void *k, const void *
  *   w_out, scale, w_in  [D]    fp32       NULL = without that norm (m = f silu(gate), no y), scale 1
  * Rows need only the alignment of their elements; squares and sums are fp32, and y
  * is the norm of r before r is rounded.
- * With eps = 0 a row's squares have to be above 2^-128 to keep 22 bits.
+ * With eps = 0 a row's squares have to be above 2^-128 to keep 22 bits; an eps below 2^-149 is
+ * taken as that, so that the norm of a row of zeros is zero.
  * Supported: D <= H3CONV_MAX_NORM, groups divides D, with groups > 1 also
  * D + groups <= H3CONV_MAX_NORM; T <= 2^30; eps >= 0.
  */

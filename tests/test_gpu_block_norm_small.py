@@ -13,7 +13,7 @@ DT = ref.DT
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("power", [-60, -63, -64])
-@pytest.mark.parametrize("D,groups", [(64, 1), (768, 1), (770, 1), (201, 1)])
+@pytest.mark.parametrize("D,groups", [(64, 1), (768, 1), (770, 1), (201, 1), (768, 12), (400, 5), (770, 11)])
 def test_small_rows(io, power, D, groups):
     """Squares of 2^-128 and more are held to 2^-150, 2^-22 of them: within the tolerance of fp32 results."""
     say("block_norm small rows", io, power, D, groups)
@@ -48,3 +48,40 @@ def test_zeros_with_the_least_eps(io, D):
     assert not r.any() and not y.any()
     o = pkg.block_norm_bwd(f, dr=torch.zeros_like(f), dy=torch.zeros_like(f), w_out=w, w_in=w, eps=1e-40)
     assert not o.df.any() and not o.dw_out.any() and not o.dw_in.any()
+
+
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,D,groups", [(5, 768, 12), (3, 400, 5), (6, 770, 11), (3, 201, 3), (2, 2560, 32), (3, 1600, 50), (4, 24, 3), (2, 5001, 3)])
+def test_heads_without_an_eps(io, T, D, groups):
+    """Lanes past a row's end have no head, and nothing of theirs is in the row's sums."""
+    say("block_norm without an eps", io, T, D, groups)
+    gen = torch.Generator().manual_seed(5)
+
+    def n(*s, dtype=DT[io]):
+        return torch.randn(*s, generator=gen).to(dtype)
+
+    a = dict(f=n(T, D), res=n(T, D), w_out=n(D, dtype=torch.float32), scale=n(D, dtype=torch.float32), w_in=n(D, dtype=torch.float32))
+    dr, dy = n(T, D), n(T, D)
+    g = {k: v.to(device()) for k, v in a.items()}
+    r, y = pkg.block_norm(**g, groups=groups, eps=0.0)
+    o = pkg.block_norm_bwd(g["f"], dr=dr.to(device()), dy=dy.to(device()), groups=groups, eps=0.0, **{k: g[k] for k in g if k != "f"})
+    leaf = {k: ref.leaf(v) for k, v in a.items()}
+    rr, ry = lref.block_norm(**leaf, groups=groups, eps=0.0)
+    ((rr * dr.double()).sum() + (ry * dy.double()).sum()).backward()
+    ref.close(r, rr, io, what="r")
+    ref.close(y, ry, io, what="y")
+    for k in leaf:
+        ref.close(getattr(o, "d" + k), leaf[k].grad, io if k in ("f", "res") else "f32", what="d" + k)
+
+
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D,groups", [(64, 1), (768, 12), (201, 3)])
+def test_zeros_without_an_eps(io, D, groups):
+    """A row of zeros, beside one that is not."""
+    f, w = torch.zeros(2, D, dtype=DT[io], device=device()), torch.ones(D, device=device())
+    f[1] = 1.0
+    r, y = pkg.block_norm(f, w_out=w, w_in=w, groups=groups, eps=0.0)
+    assert not r[0].any() and not y[0].any()
+    one = torch.ones(D, dtype=torch.float64)
+    ref.close(r[1], one, io, what="r")
+    ref.close(y[1], one, io, what="y")
