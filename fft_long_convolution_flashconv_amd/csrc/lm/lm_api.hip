@@ -71,9 +71,9 @@ bool xent_sizes_ok(int64_t T, int64_t D, int64_t V) {
            product_ok({(T > V ? T : V) / 64 + 2, D / 64 + 1}, (int64_t)1 << 27);
 }
 
-bool attn_sizes_ok(int64_t B, int64_t N, int64_t H, int64_t G, int64_t dk, int64_t dv) {
-    return N <= ((int64_t)1 << 30) && dk <= H3CONV_MAX_HEAD && dv <= H3CONV_MAX_HEAD && H <= H3CONV_MAX_LD / (dk > dv ? dk : dv) && product_ok({B, H}, (int64_t)1 << 28) &&
-           product_ok({B, N, H * (dk > dv ? dk : dv)}, kElems) && product_ok({B, H, dk, dv}, kElems);
+bool attn_sizes_ok(int64_t B, int64_t N, int64_t H, int64_t dk, int64_t dv) {
+    return N <= ((int64_t)1 << 30) && dk <= H3CONV_MAX_HEAD && dv <= H3CONV_MAX_HEAD && H <= H3CONV_MAX_LD / (dk > dv ? dk : dv) &&
+           product_ok({B, H}, (int64_t)1 << 28) && product_ok({B, N, H * (dk > dv ? dk : dv)}, kElems) && product_ok({B, H, dk, dv}, kElems);
 }
 // Elements from the first to the last of n tokens' rows, ld apart.
 int64_t extent(int64_t n, int64_t ld, int64_t row) { return n == 0 ? 0 : (n - 1) * ld + row; }
@@ -280,7 +280,7 @@ h3conv_status h3conv_linear_xent_bwd(const void *x, const void *w, const int64_t
 }
 
 size_t h3conv_linear_attn_workspace_size(int64_t B, int64_t N, int64_t H, int64_t dk, int64_t dv) {
-    if (B < 0 || N < 0 || H < 0 || dk < 1 || dv < 1 || !attn_sizes_ok(B, N, H, 1, dk, dv)) return (size_t)-1;
+    if (B < 0 || N < 0 || H < 0 || dk < 1 || dv < 1 || !attn_sizes_ok(B, N, H, dk, dv)) return (size_t)-1;
     return h3c::linear_attn_workspace(B, N, H, dk, dv);
 }
 
@@ -290,7 +290,7 @@ h3conv_status h3conv_linear_attn(const void *q, const void *k, const void *v, co
                                  int per_token, int io, void *ws, size_t ws_bytes, void *stream) {
     if (B < 0 || N < 0 || H < 0 || G < 1 || H % G != 0 || dk < 1 || dv < 1 || !valid_io(io)) return H3CONV_ERR_INVALID_ARG;
     if (B == 0 || H == 0 || (N == 0 && !x_out)) return H3CONV_OK;
-    if (!attn_sizes_ok(B, N, H, G, dk, dv)) return H3CONV_ERR_UNSUPPORTED;
+    if (!attn_sizes_ok(B, N, H, dk, dv)) return H3CONV_ERR_UNSUPPORTED;
     const int64_t n = B * N;
     if (ldq < G * dk || ldk < G * dk || ldv < H * dv) return H3CONV_ERR_INVALID_ARG;
     if (!ld_small(n, ldq) || !ld_small(n, ldk) || !ld_small(n, ldv)) return H3CONV_ERR_UNSUPPORTED;
@@ -310,7 +310,7 @@ h3conv_status h3conv_linear_attn(const void *q, const void *k, const void *v, co
 }
 
 size_t h3conv_linear_attn_bwd_workspace_size(int64_t B, int64_t N, int64_t H, int64_t G, int64_t dk, int64_t dv) {
-    if (B < 0 || N < 0 || H < 0 || G < 1 || H % G != 0 || dk < 1 || dv < 1 || !attn_sizes_ok(B, N, H, G, dk, dv))
+    if (B < 0 || N < 0 || H < 0 || G < 1 || H % G != 0 || dk < 1 || dv < 1 || !attn_sizes_ok(B, N, H, dk, dv))
         return (size_t)-1;
     return h3c::linear_attn_bwd_workspace(B, N, H, G, dk, dv);
 }
@@ -322,7 +322,7 @@ h3conv_status h3conv_linear_attn_bwd(const void *q, const void *k, const void *v
                                      int per_token, int io, void *ws, size_t ws_bytes, void *stream) {
     if (B < 0 || N < 0 || H < 0 || G < 1 || H % G != 0 || dk < 1 || dv < 1 || !valid_io(io)) return H3CONV_ERR_INVALID_ARG;
     if (H == 0) return H3CONV_OK;
-    if (!attn_sizes_ok(B, N, H, G, dk, dv)) return H3CONV_ERR_UNSUPPORTED;
+    if (!attn_sizes_ok(B, N, H, dk, dv)) return H3CONV_ERR_UNSUPPORTED;
     const int64_t n = B * N;
     if (ldq < G * dk || ldk < G * dk || ldv < H * dv) return H3CONV_ERR_INVALID_ARG;
     if (!ld_small(n, ldq) || !ld_small(n, ldk) || !ld_small(n, ldv)) return H3CONV_ERR_UNSUPPORTED;
@@ -350,7 +350,7 @@ h3conv_status h3conv_linear_attn_step(const void *q, const void *k, const void *
     if (B < 0 || H < 0 || P < 0 || G < 1 || H % G != 0 || dk < 1 || dv < 1 || !valid_io(io) || (!slots && P < B))
         return H3CONV_ERR_INVALID_ARG;
     if (B == 0 || H == 0) return H3CONV_OK;
-    if (B > 65535 || !attn_sizes_ok(B, 1, H, G, dk, dv) || !product_ok({P, H, dk, dv}, kElems)) return H3CONV_ERR_UNSUPPORTED;
+    if (B > 65535 || !attn_sizes_ok(B, 1, H, dk, dv) || !product_ok({P, H, dk, dv}, kElems)) return H3CONV_ERR_UNSUPPORTED;
     if (ldq < G * dk || ldk < G * dk || ldv < H * dv) return H3CONV_ERR_INVALID_ARG;
     if (!ld_small(B, ldq) || !ld_small(B, ldk) || !ld_small(B, ldv)) return H3CONV_ERR_UNSUPPORTED;
     const int64_t e = esize(io), st = P * H * dk * dv * 4;
