@@ -780,7 +780,8 @@ class LinearAttnGrads(NamedTuple):
 def linear_attn_bwd(q, k, v, g, dy, scale: float = 1.0, x_in=None, lengths=None, dx_out=None,
                     workspace=None) -> LinearAttnGrads:
     """Gradients of linear_attn (same arguments) for dy [B,N,H,dv] and dx_out [B,H,dk,dv] f32 (upstream of the
-    final state, or None).  dg is found as a running difference, to within fp32's rounding of q.dq and k.dk."""
+    final state, or None).  dg is a running difference of q.dq and k.dk over the steps behind, up to the next that
+    clears the state: n steps lose about sqrt(n) of fp32's rounding of those."""
     dev, io, (B, N), H, G, dk, dv, lds, per_token = _attn_args(q, k, v, g, 4)
     f32 = torch.float32
     _tensors(dev, ("dy", dy, v.dtype, (B, N, H, dv)), ("x_in?", x_in, f32, (B, H, dk, dv)),

@@ -17,8 +17,10 @@
 // rounded.
 // Forward and backward, bf16: 8192 rows of 2560 take 45 and 126 us (4.7 and 2.7
 // TB/s; 545 MB, 106 us together at a copy's rate), of 768 15 and 36 us.  The
-// backward kernel waits for the row's sums, three rounds of them one behind
-// another, with 20 waves a CU at most to cover that.
+// backward kernel waits for the row's sums, four rounds of them one behind
+// another (f^2, r^2, e r, dn fh; the second and third could be one), with 20 waves
+// a CU at most to cover that.  Rows of few channels leave lanes idle (a wave at
+// least per row: 65536 rows of 64 take 32 and 97 us for 8 and 13 at a copy's rate).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -174,8 +176,9 @@ struct Groups {
 
 // Per vector the sums of its elements' values over their group.  A group of a
 // power of two of vectors lies in the lanes of one wave; one of other whole
-// vectors goes through LDS, a sum per vector (8192 x 2560 in 32 heads, bf16:
-// 41 us and 148, by elements 97 and 470); any other (ODD) element by element.
+// vectors, up to 64, goes through LDS, a sum per vector (8192 x 2560 in 32 heads,
+// bf16: 41 us and 149, by elements 97 and 470); any other (ODD) element by element
+// (4 heads of 640: 92 and 449; 128 of 20: 140 and 569).
 template <int W, int NV, bool ODD, class F>
 __device__ __forceinline__ void group_sums(const Row<W> &row, const Groups &g, int D, F value, float (&out)[NV][ODD ? V : 1],
                                            float *small, float *wide) {

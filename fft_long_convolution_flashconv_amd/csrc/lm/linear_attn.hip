@@ -28,11 +28,12 @@
 // enters it.
 //
 // What bounds it: neither memory (64K steps of 8 heads of 128 in bf16 read and
-// write 539 MB, 105 us at a copy's rate, and take 245) nor the matrix cores (a
-// quarter busy), but the chain of a chunk: scan, weights, products, update, with a
+// write 539 MB, 105 us at a copy's rate, and take 255 to 280) nor the matrix cores
+// (a quarter busy), but the chain of a chunk: scan, weights, products, update, with a
 // barrier or two between.  One block of eight waves per CU is all that 220
 // registers a lane allow (two at 128 registers spill 30 to 77 and are no faster:
-// 76 us against 75 forward, 314 against 286 backward); a sixth to a quarter of
+// 76 us against 75 forward, with two pieces, and 314 against 286 backward; two of
+// four waves and half the columns have not been measured); a sixth to a quarter of
 // the time goes by without loads, a tenth without the exponents, none without the
 // stores or with the weights formed elsewhere.
 #include <hip/hip_runtime.h>
@@ -280,7 +281,7 @@ struct Segs {
 };
 
 // Waves of a SIMD that the registers are to leave room for: as many as the LDS does (heads of more than 128 take what
-// they need).
+// they need, and more than there is: 68 to 159 registers are spilled where blocks have eight waves).
 constexpr int waves_per_simd(int io, int KP, int WV, int what, bool whole_heads) {
     return KP > 128 && WV == 4                                           ? 1
            : io == IO_F32 || KP > 64 || !whole_heads || WV == 8          ? 2
@@ -304,7 +305,8 @@ __global__ __launch_bounds__(WV * 64, waves_per_simd(IO, KP, WV, DO, WHOLE)) voi
     constexpr int E = LK::E;
     constexpr int NA = C * LK::CH / TH, NC = C * LM::CH / TH;  // units of 16 bytes per thread
     static_assert(C * LK::CH % TH == 0 && C * LM::CH % TH == 0 && NT <= 4, "whole units, a wave per 16 steps");
-    // pieces of weights and states in the output's products: 22 bits in fp16, 24 in bf16; fragments of weights
+    // pieces of weights and states in the output's products: 22 bits in fp16, 24 in bf16 (two pieces, 17 bits, would take 91
+    // us forward down to 85 for 4 x 2048 steps of 20 heads of 128); fragments of weights
     constexpr int NP = X::UPD, WF = NT == 4 ? 6 : 2;
     // Two places for tiles where the LDS has room for them without giving up a block: a chunk's are then written while
     // the last one's are still read.

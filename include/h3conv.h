@@ -446,7 +446,8 @@ h3conv_status h3conv_selective_step(const void *u, const void *dt, const float *
  *             [B,N,H]                 of each token and head.  Usually <= 0; -infinity starts the
  *                                     state anew.  A state that grows is right while it, S_t^T q_t
  *                                     and the factors over any 64 steps are within fp32, however
- *                                     large the factor over more steps is.
+ *                                     large the factor over more steps is; a factor over 64 steps
+ *                                     below fp32's normal numbers (e^-87) has fewer bits, or is 0.
  *                                     NaN makes what is behind it NaN.
  *   x_in      [B,H,dk,dv]  fp32       initial state, or NULL for zero
  *   lengths   [B]          int32      valid steps of every row (clamped to 0 .. N), or NULL = N:
