@@ -212,7 +212,8 @@ __device__ __forceinline__ float lanes_max(float v, int from) {
     for (int d = from; d < 64; d <<= 1) v = fmaxf(v, __shfl_xor(v, d));
     return v;
 }
-// The power of two that brings a largest magnitude m to 2^13 .. 2^14, as an exponent (fp32's largest takes 2^-114; from
+// The power of two that brings a largest magnitude m to 2^13 .. 2^14 (two pieces then hold a number to 22 bits, or to
+// 2^-25, which is 2^-39 of the largest), as an exponent (fp32's largest takes 2^-114; from
 // 2^-86 down less than 2^14 is reached, and what the pieces lose is below 2^-125).
 __device__ __forceinline__ int near_2_14(float m) {
     const int e = 14 - __builtin_amdgcn_frexp_expf(m);

@@ -460,7 +460,8 @@ h3conv_status h3conv_selective_step(const void *u, const void *dt, const float *
  * infinity in v or k reaches the others of its 64, also those before it.
  * Products run on the matrix cores, fp32 elements on the fp32 ones; sums and
  * states are fp32, and what multiplies an input again (weights, states) keeps 22
- * bits or more where inputs have 16.
+ * bits or more where inputs have 16; in fp16 down to 2^-39 of the largest such
+ * number of a step or a head.
  * Supported: dk, dv <= H3CONV_MAX_HEAD, G divides H, ld and H*max(dk,dv) <=
  * H3CONV_MAX_LD, N <= 2^30, B*H <= 2^28, B*N*H*max(dk,dv), B*H*dk*dv and B*N*ld <= 2^40.
  */
